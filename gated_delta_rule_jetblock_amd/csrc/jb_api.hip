@@ -91,6 +91,17 @@ jb_status hip_status(const char* fn, hipError_t e) {
 
 }  // namespace
 
+namespace jb {
+int api_fail(int st, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+  return st;
+}
+int api_ok() { return ok(); }
+}  // namespace jb
+
 extern "C" {
 
 const char* jb_status_string(jb_status st) {
@@ -109,7 +120,7 @@ const char* jb_status_string(jb_status st) {
 
 const char* jb_last_error(void) { return g_err; }
 
-int32_t jb_version(void) { return 1 * 10000 + 0 * 100 + 0; }
+int32_t jb_version(void) { return 1 * 10000 + 1 * 100 + 0; }
 
 jb_status jb_prefill_workspace_size(const jb_shape* s, size_t* bytes) {
   const char* fn = "jb_prefill_workspace_size";

@@ -1,0 +1,830 @@
+// jb_attn.hip -- attention of each sequence's new tokens over its paged cache.
+//
+// A sequence has kv rows in the cache, the last T of them its new tokens.  New
+// token i sits at row p = kv - T + i and sees rows max(0, p - window + 1) .. p
+// (window 0: from row 0).  With x_j = scale q.k_j over those rows:
+//     m = max x_j,  l = sum e^{x_j - m},  o = sum e^{x_j - m} v_j / l,
+//     lse = m + ln l;   no row seen (or every x_j = -inf): o = 0, lse = -inf.
+// The G = H / Hkv query heads of a key head share its rows, so a sequence's
+// queries are the T G rows r = i G + g of a matrix that multiplies the same K
+// and V.  One pass over the cache rows carries m, l and o (rescaled when m
+// grows); nothing of size T x kv exists.
+//
+// Both kernels for bf16 form S^T = K Q^T with 32x32x16 matrix-core products, so
+// that a lane holds one query (column lane % 32) and 16 of 32 cache rows: the
+// softmax runs inside a lane but for one exchange with lane + 32, and the
+// accumulators, rounded to bf16, are the B operand of O^T += V^T P^T as they
+// stand (K order kperm32: slots 0..3 are rows 4 g .. 4 g + 3, slots 4..7 rows
+// 8 + 4 g ..).  V's A operand is read down its columns from LDS.
+// Rounding: scores, m, l and o are fp32; P is rounded to bf16 (half a step,
+// 2^-9 of each weight at random) for the matrix cores; o is rounded once.
+//   attn_tile_kernel  many queries: 4 waves x 32 rows of one key head walk the
+//                     same 64-row cache tiles through two LDS buffers.
+//   attn_row_kernel   at most 32 rows (decode): every wave takes its own 32-row
+//                     cache tiles, no barrier in the loop, joined in LDS.
+// The cache range of a tile of queries may be cut into nsplit pieces; each
+// writes its unnormalised o, m and l, and attn_join_kernel adds them up.
+// fp32 inputs take attn_f32_kernel, the same tiles on fp32 matrix cores.
+//
+// Reading the cache: 16 consecutive rows lie in one page, so a wave fetches
+// them with one page index (a scalar load) and one buffer descriptor that ends
+// behind the last row any query of the workgroup sees: rows behind it, and
+// pages whose index is out of range, arrive as zeros whatever memory holds.
+// A masked weight is 0, and 0 times an inf or NaN is NaN, so a tile that some
+// queries see in part only is looked over first: a value in V that is not
+// finite counts as 0 on the matrix cores, and is added for the queries that do
+// see it by itself.
+#include <limits.h>
+#include <math.h>
+
+#include "jb_attn.h"
+#include "jb_device.h"
+#include "jb_dma.h"
+
+namespace jb {
+
+namespace {
+
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) bf16x8_t lds_bf16x8;
+typedef short s4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s4_t lds_s4;
+typedef unsigned int u4_t __attribute__((ext_vector_type(4)));
+typedef unsigned int u2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) f4_t lds_f4;
+typedef __attribute__((address_space(3))) u4_t lds_u4;
+typedef __attribute__((address_space(3))) u2_t lds_u2;
+typedef __attribute__((address_space(3))) uint32_t lds_u32;
+typedef __attribute__((address_space(3))) float lds_float;
+typedef float f16_t __attribute__((ext_vector_type(16)));
+typedef const __attribute__((address_space(4))) int* const_int_p;
+
+constexpr float LN2 = 0.6931471805599453f;
+
+struct Args {
+  int B, T, H, Hkv, G, pshift, max_pages, num_pages, window, nsplit;
+  int64_t total, rows, q_stride, page_stride;  // rows: total H
+  const int* cu;                               // NULL: dense, B x T tokens
+  const int* kv_lens;
+  const int* table;
+  const void *q, *k, *v;
+  void* o;
+  float* lse;
+  float* part_o;   // [nsplit][rows][D]
+  float2* part_ml; // [nsplit][rows]
+  float scale;     // times log2 e
+};
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// first token and length of sequence b, and its cache rows; all clamped to the
+// tensors (they come from device memory)
+struct Seq {
+  int64_t tok0;
+  int T, kv;
+};
+__device__ __forceinline__ Seq seq_of(const Args& a, int b) {
+  Seq s;
+  if (a.cu) {
+    const_int_p cu = (const_int_p)a.cu;
+    clamp_span(cu[b], cu[b + 1], a.T, a.total, s.tok0, s.T);
+  } else {
+    s.tok0 = (int64_t)b * a.T;
+    s.T = a.T;
+  }
+  const int cap = (int)min((int64_t)a.max_pages << a.pshift, (int64_t)0x7fffffff);
+  s.kv = min(max(((const_int_p)a.kv_lens)[b], 0), cap);
+  return s;
+}
+
+// Sequence and first row (of its T G) of slot s.  Packed sequences: sequence
+// b's tiles of R rows start at slot base(b) = cu[b] G / R + b, which leaves
+// room for all of them and never decreases, so the sequence is the last one
+// whose base is not behind s (every thread looks at one base at a time).
+__device__ __forceinline__ void slot_of(const Args& a, int64_t s, int R, int& b, int64_t& r0) {
+  if (!a.cu) {
+    const int64_t per = ((int64_t)a.T * a.G + R - 1) / R;
+    b = (int)(s / per);
+    r0 = (s - b * per) * R;
+    return;
+  }
+  int n = 0;
+  for (int i = 0; i < a.B; i += blockDim.x) {
+    const int j = i + threadIdx.x;
+    const bool in = j < a.B && min(max((int64_t)a.cu[j], (int64_t)0), a.total) * a.G / R + j <= s;
+    const int c = __syncthreads_count(in);
+    n += c;
+    if (c < (int)blockDim.x) break;
+  }
+  b = uniform(max(n - 1, 0));
+  const int64_t base = min(max((int64_t)((const_int_p)a.cu)[b], (int64_t)0), a.total) * a.G / R + b;
+  r0 = (s - base) * R;
+}
+
+// ---------------------------------------------------------------- bf16 tiles
+
+// LDS image of a tile: rows of D bf16, their 16-byte pieces permuted by row so
+// that the reads below meet distinct banks: K fragments read one piece of 32
+// rows, V fragments two neighbouring pieces of 4 rows.
+template <int D> struct Img {
+  static constexpr int PR = D / 8, ROWB = D * 2;
+  __device__ static int fk(int r) { return r & (PR < 16 ? PR - 1 : 15); }
+  __device__ static int fv(int r) { return PR < 16 ? (r & 3) << 1 : (r & 3) << 2; }
+};
+
+// 16 cache rows from row0 (a multiple of 16) of one key head into LDS.
+template <int D> struct Loader {
+  using I = Img<D>;
+  static constexpr int N = I::PR / 4;  // 1 KB transfers for 16 rows
+  int vk[N], vv[N];
+  __device__ Loader() {
+    const int lane = lane_id();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int s = i * 64 + lane, r = s / I::PR, c = s % I::PR;
+      vk[i] = r * I::ROWB + ((c ^ I::fk(r)) * 16);
+      vv[i] = r * I::ROWB + ((c ^ I::fv(r)) * 16);
+    }
+  }
+  // page index for row0 (loaded a tile ahead of its use)
+  static __device__ int page(const Args& a, int b, int row0, int hi) {
+    return row0 < hi ? ((const_int_p)a.table)[(int64_t)b * a.max_pages + (row0 >> a.pshift)] : -1;
+  }
+  __device__ void load(const Args& a, const void* cache, bool value, int pid, int kvh, int row0, int lo, int hi,
+                       uint32_t lds) const {
+    int n = min(hi - row0, 16);
+    if (pid < 0 || pid >= a.num_pages || row0 + 16 <= lo || n < 0) n = 0, pid = 0;
+    const int in_page = row0 & ((1 << a.pshift) - 1);
+    const bf16_t* p = (const bf16_t*)cache + pid * a.page_stride + ((int64_t)kvh << a.pshift) * D + in_page * D;
+    const v4i_t desc = buf_desc(p, (uint32_t)n * I::ROWB);
+#pragma unroll
+    for (int i = 0; i < N; ++i) dma16(desc, value ? vv[i] : vk[i], 0, lds + i * 1024);
+  }
+};
+
+__device__ __forceinline__ f16_t mfma32(bf16x8_t a, bf16x8_t b, f16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// a value and lane + 32's (lane - 32's)
+__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32, WAVE); }
+
+// One wave's 32 queries and what they have gathered so far.
+template <int D> struct Wave {
+  using I = Img<D>;
+  bf16x8_t q[D / 16];
+  f16_t o[D / 32];  // O^T: o[db][i] is d = 32 db + 8 (i / 4) + 4 g + i % 4
+  float m, l;       // m as the exponent base 2 subtracts it; l of this lane's half of the rows
+  int p, lw;        // sees rows lw < j <= p
+  int phi, plo;     // of the wave's real rows: the last row seen, and the least p
+  int lwlo, lwhi;   // and the least and the largest lw
+
+  __device__ void init(const Args& a, const Seq& s, int kvh, int64_t r0) {
+    const int lane = lane_id();
+    const int64_t nr = (int64_t)s.T * a.G, r = r0 + (lane & 31);
+    const int base = s.kv - s.T;
+    const bool real = r < nr;
+    const int i = real ? (int)(r / a.G) : 0, g = real ? (int)(r - (int64_t)i * a.G) : 0;
+    p = real ? base + i : -1;
+    lw = a.window ? p - a.window : -1;
+    const int64_t last = min(r0 + 32, nr) - 1;
+    plo = phi = lwlo = lwhi = -1;
+    if (r0 < nr) {
+      plo = uniform(base + (int)(r0 / a.G));
+      phi = uniform(base + (int)(last / a.G));
+      if (a.window) lwlo = plo - a.window, lwhi = phi - a.window;
+    }
+    const bf16_t* src = (const bf16_t*)a.q + (s.tok0 + i) * a.q_stride + (int64_t)(kvh * a.G + g) * D + 8 * (lane >> 5);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (real) w = *reinterpret_cast<const uint4*>(src + 16 * k);
+      q[k] = __builtin_bit_cast(bf16x8_t, w);
+    }
+#pragma unroll
+    for (int db = 0; db < D / 32; ++db)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[db][e] = 0.f;
+    m = -INFINITY;
+    l = 0.f;
+  }
+
+  // The weights of NB x 32 cache rows from j0 (their K image at lk), into s;
+  // false: no query sees any of them.
+  template <int NB>
+  __device__ bool weights(const Args& a, const lds_char* lk, int j0, f16_t (&s)[NB]) {
+    const int lane = lane_id(), c = lane & 31, g = lane >> 5;
+    if (j0 > phi || j0 + NB * 32 - 1 <= lwlo) return false;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[n][e] = 0.f;
+    const int kb = c * I::ROWB + ((g ^ I::fk(c)) << 4);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      const lds_char* at = lk + (kb ^ (k << 5));
+#pragma unroll
+      for (int n = 0; n < NB; ++n) s[n] = mfma32(*(const lds_bf16x8*)(at + n * 32 * I::ROWB), q[k], s[n]);
+    }
+    if (in_part(j0, NB * 32)) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int j = j0 + 32 * n + 8 * (e >> 2) + 4 * g + (e & 3);
+          if (j > p || j <= lw) s[n][e] = -INFINITY;
+        }
+    }
+    float mx = -INFINITY;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[n][e]);
+    mx = fmaxf(mx, other_half(mx)) * a.scale;
+    // The subtracted maximum may lag behind the true one: weights up to 2^8 lose
+    // nothing in fp32 sums or in bf16's relative precision, and the rescaling
+    // of o is left out for all but the first tiles.
+    if (__any(mx > m + 8.f)) {
+      const float mn = fmaxf(m, mx);
+      const float f = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
+#pragma unroll
+      for (int db = 0; db < D / 32; ++db)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[db][e] *= f;
+      l *= f;
+      m = mn;
+    }
+    const float ms = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        s[n][e] = fast_exp2(fmaf(s[n][e], a.scale, -ms));
+        l += s[n][e];
+      }
+    return true;
+  }
+  // whether some query sees some of the n rows from j0, but not every query all
+  __device__ bool in_part(int j0, int n) const { return j0 + n - 1 > plo || j0 <= lwhi; }
+
+  // O^T += V^T P^T
+  template <int NB> __device__ void values(const f16_t (&s)[NB], const lds_char* lv) {
+    const int lane = lane_id(), g = lane >> 5;
+    const int n16 = lane & 15, row = 4 * g + (n16 >> 2), pc = 2 * ((lane >> 4) & 1) + ((n16 & 3) >> 1);
+    const int vb = row * I::ROWB + ((pc ^ I::fv(row)) << 4) + (n16 & 1) * 8;
+#pragma unroll
+    for (int k = 0; k < 2 * NB; ++k) {
+      bf16x8_t w;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = (__bf16)s[k >> 1][8 * (k & 1) + e];
+#pragma unroll
+      for (int db = 0; db < D / 32; ++db) {
+        const lds_char* at = lv + (vb ^ (db << 6)) + k * 16 * I::ROWB;
+        const s4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)at);
+        const s4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(at + 8 * I::ROWB));
+        o[db] = mfma32(__builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)), w, o[db]);
+      }
+    }
+  }
+
+  // o += weight times value for the values that are not finite, of rows that are seen
+  template <int NB> __device__ void by_row(const f16_t (&s)[NB], const lds_char* lv, int j0) {
+    const int g = lane_id() >> 5;
+    for (int r = 0; r < NB * 32; ++r) {
+      const int e0 = ((r & 31) >> 3) * 4 + (r & 3);
+      float w = 0.f;
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w = n * 16 + e == (r >> 5) * 16 + e0 ? s[n][e] : w;
+      const float x = other_half(w);
+      if (((r >> 2) & 1) != g) w = x;
+      const bool seen = j0 + r <= p && j0 + r > lw;
+#pragma unroll
+      for (int db = 0; db < D / 32; ++db)
+#pragma unroll
+        for (int e4 = 0; e4 < 4; ++e4) {
+          const int d = 32 * db + 8 * e4 + 4 * g;
+          const u2_t u = *(const lds_u2*)(lv + r * I::ROWB + (((d >> 3) ^ I::fv(r)) << 4) + (d & 4) * 2);
+          const float v[4] = {__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                              __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u)};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (seen && !isfinite(v[e])) o[db][4 * e4 + e] = fmaf(w, v[e], o[db][4 * e4 + e]);
+        }
+    }
+  }
+};
+
+// whether a 16-byte aligned part of a V image holds a value that is not finite
+// (exponent all ones); clean_part sets those to 0
+__device__ __forceinline__ bool odd_bits(uint32_t u) {
+  return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ bool odd_part(const lds_char* v, int bytes) {
+  bool odd = false;
+#pragma unroll 4
+  for (int i = lane_id() * 16; i < bytes; i += 1024) {
+    const u4_t w = *(const lds_u4*)(v + i);
+    odd |= odd_bits(w[0]) || odd_bits(w[1]) || odd_bits(w[2]) || odd_bits(w[3]);
+  }
+  return __any(odd);
+}
+__device__ __forceinline__ void clean_part(lds_char* v, int bytes) {
+  for (int i = lane_id() * 4; i < bytes; i += 256) {
+    uint32_t u = *(const lds_u32*)(v + i);
+    if ((u & 0x7f80u) == 0x7f80u) u &= 0xffff0000u;
+    if ((u & 0x7f800000u) == 0x7f800000u) u &= 0xffffu;
+    *(lds_u32*)(v + i) = u;
+  }
+}
+
+// the cache rows [lo, hi) that queries r0 .. r1 (of one sequence) see, and the
+// part of their R-row tiles that piece `split` of `n` takes
+struct Span {
+  int lo, hi, t0, t1;
+};
+__device__ __forceinline__ Span span_of(const Args& a, const Seq& s, int64_t r0, int64_t r1, int R, int split) {
+  Span x;
+  const int base = s.kv - s.T, first = base + (int)(r0 / a.G);
+  x.hi = max(base + (int)(r1 / a.G) + 1, 0);
+  x.lo = a.window ? min(max(first - a.window + 1, 0), x.hi) : 0;
+  const int n0 = x.lo / R, n1 = (x.hi + R - 1) / R;
+  const int per = (n1 - n0 + a.nsplit - 1) / a.nsplit;
+  x.t0 = min(n0 + split * per, n1);
+  x.t1 = min(x.t0 + per, n1);
+  return x;
+}
+
+// element (row r, d .. d + 3) of a wave's staged 32 x D fp32 rows: 16-byte
+// pieces permuted by row
+template <int D> __device__ __forceinline__ lds_f4* stage_at(lds_char* st, int r, int d) {
+  return (lds_f4*)(st + r * D * 4 + (((d >> 2) ^ (r & 15)) << 4));
+}
+
+template <typename OUT> __device__ __forceinline__ void store4(OUT* p, f4_t v);
+template <> __device__ __forceinline__ void store4<float>(float* p, f4_t v) { *reinterpret_cast<f4_t*>(p) = v; }
+template <> __device__ __forceinline__ void store4<bf16_t>(bf16_t* p, f4_t v) {
+  uint2 u;
+  u.x = f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16;
+  u.y = f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16;
+  *reinterpret_cast<uint2*>(p) = u;
+}
+
+// where row r (of a sequence's T G) of key head kvh goes: row index of o, lse
+__device__ __forceinline__ int64_t out_row(const Args& a, const Seq& s, int kvh, int64_t r) {
+  const int64_t i = r / a.G;
+  return (s.tok0 + i) * a.H + kvh * a.G + (r - i * a.G);
+}
+
+template <int D, typename OUT>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a) {
+  constexpr int NW = 4, R = 64, IMG = R * D * 2;
+  __shared__ __attribute__((aligned(1024))) char ring[4 * IMG];  // K, V of an even tile, K, V of an odd one
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int combo = blockIdx.x % (unsigned)(a.Hkv * a.nsplit), kvh = combo % a.Hkv, split = combo / a.Hkv;
+  const int64_t nslot = gridDim.x / (unsigned)(a.Hkv * a.nsplit);
+  // the longest ranges first: they end last
+  const int64_t slot = nslot - 1 - blockIdx.x / (unsigned)(a.Hkv * a.nsplit);
+  int b;
+  int64_t r0;
+  slot_of(a, slot, NW * 32, b, r0);
+  const Seq s = seq_of(a, b);
+  const int64_t nr = (int64_t)s.T * a.G;
+  if (r0 < 0 || r0 >= nr) return;  // (r0 < 0: offsets that decrease)
+  if (a.cu && nr <= 32 && a.T * (int64_t)a.G > 32) return;  // attn_row_kernel's
+  const int64_t r1 = min(r0 + NW * 32, nr) - 1;
+  const Span x = span_of(a, s, r0, r1, R, split);
+  // cache rows of the first and (with a window) the last query
+  const int first = s.kv - s.T + (int)(r0 / a.G), last = a.window ? s.kv - s.T + (int)(r1 / a.G) : INT_MIN / 2;
+  Wave<D> w;
+  w.init(a, s, kvh, r0 + wave * 32);
+  const Loader<D> ld;
+  lds_char* const base = (lds_char*)ring;
+  auto issue = [&](int t, int pid) {
+    const int row0 = t * R + wave * 16;
+    const uint32_t at = (uint32_t)(uintptr_t)(base + (t & 1) * 2 * IMG + wave * 16 * D * 2);
+    ld.load(a, a.k, false, pid, kvh, row0, x.lo, x.hi, at);
+    ld.load(a, a.v, true, pid, kvh, row0, x.lo, x.hi, at + IMG);
+  };
+  if (x.t0 < x.t1) issue(x.t0, Loader<D>::page(a, b, x.t0 * R + wave * 16, x.hi));
+  int pid = x.t0 + 1 < x.t1 ? Loader<D>::page(a, b, (x.t0 + 1) * R + wave * 16, x.hi) : -1;
+  for (int t = x.t0; t < x.t1; ++t) {
+    // every wave's transfers of tile t have landed, and every wave has left tile t - 1
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (t + 1 < x.t1) {
+      issue(t + 1, pid);
+      pid = Loader<D>::page(a, b, (t + 2) * R + wave * 16, x.hi);
+    }
+    lds_char* const k = base + (t & 1) * 2 * IMG;
+    lds_char* const v = k + IMG;
+    // some rows of the tile are some queries' only (the same answer in every wave)
+    bool odd = false;
+    if ((t + 1) * R - 1 > first || t * R <= last - a.window)
+      odd = __syncthreads_or(odd_part(v + wave * (IMG / 4), IMG / 4));
+    f16_t s2[2];
+    const bool live = w.template weights<2>(a, k, t * R, s2);
+    if (odd) {
+      if (live) w.template by_row<2>(s2, v, t * R);
+      __syncthreads();
+      clean_part(v + wave * (IMG / 4), IMG / 4);
+      __syncthreads();
+    }
+    if (live) w.template values<2>(s2, v);
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  // O through LDS (each wave its own rows) so that whole rows leave
+  const float l = w.l + other_half(w.l);
+  const int c = lane & 31, g = lane >> 5;
+  const int64_t r = r0 + wave * 32 + c;
+  const bool split_out = a.nsplit > 1;
+  if (g == 0 && r < nr) {
+    const int64_t at = out_row(a, s, kvh, r);
+    if (split_out) a.part_ml[split * a.rows + at] = make_float2(w.m, l);
+    else if (a.lse) a.lse[at] = l == 0.f ? -INFINITY : (w.m + fast_log2(l)) * LN2;
+  }
+  const float f = split_out ? 1.f : l == 0.f ? 0.f : 1.f / l;
+  static_assert(NW * 32 * D * 4 <= 4 * IMG, "staging fits");
+  lds_char* st = base + wave * 32 * D * 4;
+#pragma unroll
+  for (int db = 0; db < D / 32; ++db)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *stage_at<D>(st, c, 32 * db + 8 * e + 4 * g) =
+          f4_t{w.o[db][4 * e] * f, w.o[db][4 * e + 1] * f, w.o[db][4 * e + 2] * f, w.o[db][4 * e + 3] * f};
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  constexpr int LPR = D / 4;  // lanes a row
+  for (int i = lane / LPR; i < 32; i += 64 / LPR) {
+    const int64_t rr = r0 + wave * 32 + i;
+    if (rr >= nr) break;
+    const int64_t at = out_row(a, s, kvh, rr);
+    const int d = (lane % LPR) * 4;
+    const f4_t v = *stage_at<D>(st, i, d);
+    if (split_out) *reinterpret_cast<f4_t*>(a.part_o + (split * a.rows + at) * D + d) = v;
+    else store4((OUT*)a.o + at * D + d, v);
+  }
+}
+
+// At most 32 query rows: the waves share them and split the cache.
+template <int D, int NW, typename OUT>
+__global__ __launch_bounds__(NW * 64, 1) void attn_row_kernel(Args a) {
+  constexpr int R = 32, IMG = R * D * 2;
+  __shared__ __attribute__((aligned(1024))) char ring[NW * 4 * IMG];
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int combo = blockIdx.x % (unsigned)(a.Hkv * a.nsplit), kvh = combo % a.Hkv, split = combo / a.Hkv;
+  const int b = blockIdx.x / (unsigned)(a.Hkv * a.nsplit);
+  const Seq s = seq_of(a, b);
+  const int64_t nr = (int64_t)s.T * a.G;
+  if (nr == 0 || nr > 32) return;  // none, or attn_tile_kernel's
+  const Span x = span_of(a, s, 0, nr - 1, R, split);
+  Wave<D> w;
+  w.init(a, s, kvh, 0);
+  const Loader<D> ld;
+  lds_char* const base = (lds_char*)ring + wave * 4 * IMG;
+  constexpr int NT = 4 * Loader<D>::N;  // transfers a tile
+  auto issue = [&](int t, int par, int p0, int p1) {
+    const uint32_t at = (uint32_t)(uintptr_t)(base + par * 2 * IMG);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's reads of the buffer are done
+    ld.load(a, a.k, false, p0, kvh, t * R, x.lo, x.hi, at);
+    ld.load(a, a.k, false, p1, kvh, t * R + 16, x.lo, x.hi, at + 16 * D * 2);
+    ld.load(a, a.v, true, p0, kvh, t * R, x.lo, x.hi, at + IMG);
+    ld.load(a, a.v, true, p1, kvh, t * R + 16, x.lo, x.hi, at + IMG + 16 * D * 2);
+  };
+  auto page = [&](int t, int h) { return t < x.t1 ? Loader<D>::page(a, b, t * R + 16 * h, x.hi) : -1; };
+  int t = x.t0 + wave, par = 0;
+  if (t < x.t1) issue(t, 0, page(t, 0), page(t, 1));
+  int p0 = page(t + NW, 0), p1 = page(t + NW, 1);
+  for (; t < x.t1; t += NW, par ^= 1) {
+    if (t + NW < x.t1) {
+      issue(t + NW, par ^ 1, p0, p1);
+      p0 = page(t + 2 * NW, 0), p1 = page(t + 2 * NW, 1);
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NT) : "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    lds_char* const k = base + par * 2 * IMG;
+    lds_char* const v = k + IMG;
+    f16_t s1[1];
+    if (!w.template weights<1>(a, k, t * R, s1)) continue;
+    if (w.in_part(t * R, R) && odd_part(v, IMG)) {
+      w.template by_row<1>(s1, v, t * R);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      clean_part(v, IMG);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+    w.template values<1>(s1, v);
+  }
+  // join the waves: O and (m, l) of each in LDS
+  const int c = lane & 31, g = lane >> 5;
+  const float l = w.l + other_half(w.l);
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  lds_char* const all = (lds_char*)ring;
+  constexpr int ST = 32 * D * 4;
+  static_assert(NW * ST + NW * 32 * 8 <= NW * 4 * IMG, "staging fits");
+  lds_char* st = all + wave * ST;
+#pragma unroll
+  for (int db = 0; db < D / 32; ++db)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *stage_at<D>(st, c, 32 * db + 8 * e + 4 * g) =
+          f4_t{w.o[db][4 * e], w.o[db][4 * e + 1], w.o[db][4 * e + 2], w.o[db][4 * e + 3]};
+  lds_float* ml = (lds_float*)(all + NW * ST);  // [2][NW][32]
+  if (g == 0) {
+    ml[wave * 32 + c] = w.m;
+    ml[NW * 32 + wave * 32 + c] = l;
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  constexpr int LPR = D / 4;
+  for (int i = threadIdx.x / LPR; i < nr; i += NW * 64 / LPR) {
+    const int d = (threadIdx.x % LPR) * 4;
+    float m = -INFINITY;
+#pragma unroll
+    for (int n = 0; n < NW; ++n) m = fmaxf(m, ml[n * 32 + i]);
+    f4_t sum = zero4();
+    float lt = 0.f;
+#pragma unroll
+    for (int n = 0; n < NW; ++n) {
+      const float mn = ml[n * 32 + i];
+      // (a wave that saw nothing holds zeros, or NaN that stays)
+      const float f = mn == -INFINITY ? 1.f : fast_exp2(mn - m);
+      const f4_t v = *stage_at<D>(all + n * ST, i, d);
+      lt = fmaf(ml[NW * 32 + n * 32 + i], f, lt);
+      sum += v * f;
+    }
+    const int64_t at = out_row(a, s, kvh, i);
+    if (a.nsplit > 1) {
+      if (d == 0) a.part_ml[split * a.rows + at] = make_float2(m, lt);
+      *reinterpret_cast<f4_t*>(a.part_o + (split * a.rows + at) * D + d) = sum;
+    } else {
+      const float f = lt == 0.f ? 0.f : 1.f / lt;
+      if (d == 0 && a.lse) a.lse[at] = lt == 0.f ? -INFINITY : (m + fast_log2(lt)) * LN2;
+      store4((OUT*)a.o + at * D + d, sum * f);
+    }
+  }
+}
+
+// Adds up the pieces of every row.  Rows no sequence owns stay as they are.
+template <int D, typename OUT>
+__global__ __launch_bounds__(256) void attn_join_kernel(Args a) {
+  constexpr int LPR = D / 4, RPB = 256 / LPR;
+  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
+  const int d = (threadIdx.x % LPR) * 4;
+  if (a.cu) {
+    // the sequence of the block's first token, then on from there
+    const int64_t t0 = (int64_t)blockIdx.x * RPB / a.H;
+    int n = 0;
+    for (int i = 0; i < a.B; i += 256) {
+      const int j = i + threadIdx.x;
+      const int c = __syncthreads_count(j < a.B && a.cu[j] <= t0);
+      n += c;
+      if (c < 256) break;
+    }
+    if (row >= a.rows) return;
+    const int64_t t = row / a.H;
+    int b = max(n - 1, 0);
+    while (b + 1 < a.B && a.cu[b + 1] <= t) ++b;
+    int64_t tok0;
+    int T;
+    clamp_span(a.cu[b], a.cu[b + 1], a.T, a.total, tok0, T);
+    if (t < tok0 || t >= tok0 + T) return;
+  } else if (row >= a.rows) {
+    return;
+  }
+  float m = -INFINITY, l = 0.f;
+  f4_t sum = zero4();
+  for (int s = 0; s < a.nsplit; ++s) {
+    const float2 ml = a.part_ml[s * a.rows + row];
+    const f4_t v = *reinterpret_cast<const f4_t*>(a.part_o + (s * a.rows + row) * D + d);
+    const float mn = fmaxf(m, ml.x);
+    const float f = m == -INFINITY ? 1.f : fast_exp2(m - mn), h = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - mn);
+    m = mn;
+    l = fmaf(l, f, ml.y * h);
+    sum = sum * f + v * h;
+  }
+  const float f = l == 0.f ? 0.f : 1.f / l;
+  if (d == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + fast_log2(l)) * LN2;
+  store4((OUT*)a.o + row * D + d, sum * f);
+}
+
+// ------------------------------------------------------------------ fp32 mode
+// 4 waves x 16 query rows; S^T = K Q^T and O^T += V^T P^T on 16x16x4 fp32
+// matrix cores, 32 cache rows at a time in LDS.  Lane: query lane % 16, cache
+// rows 4 g + i of each 16.  Everything stays fp32.
+template <int D, typename OUT>
+__global__ __launch_bounds__(256, 1) void attn_f32_kernel(Args a) {
+  constexpr int R = 32, LD = D + 4, NW = 4;
+  __shared__ __attribute__((aligned(16))) float sk[R * LD], sv[R * LD];
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const int combo = blockIdx.x % (unsigned)(a.Hkv * a.nsplit), kvh = combo % a.Hkv, split = combo / a.Hkv;
+  const int64_t nslot = gridDim.x / (unsigned)(a.Hkv * a.nsplit);
+  const int64_t slot = nslot - 1 - blockIdx.x / (unsigned)(a.Hkv * a.nsplit);
+  int b;
+  int64_t r0;
+  slot_of(a, slot, NW * 16, b, r0);
+  const Seq s = seq_of(a, b);
+  const int64_t nr = (int64_t)s.T * a.G;
+  if (r0 < 0 || r0 >= nr) return;
+  const Span x = span_of(a, s, r0, min(r0 + NW * 16, nr) - 1, R, split);
+  const int64_t r = r0 + wave * 16 + c;
+  const bool real = r < nr;
+  const int i0 = real ? (int)(r / a.G) : 0, g0 = real ? (int)(r - (int64_t)i0 * a.G) : 0;
+  const int p = real ? s.kv - s.T + i0 : -1, lw = a.window ? p - a.window : -1;
+  const float* src = (const float*)a.q + (s.tok0 + i0) * a.q_stride + (int64_t)(kvh * a.G + g0) * D + 4 * g;
+  float4 q[D / 16];
+  f4_t o[D / 16];
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) {
+    q[k] = real ? *reinterpret_cast<const float4*>(src + 16 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+    o[k] = zero4();
+  }
+  float m = -INFINITY, l = 0.f;
+  for (int t = x.t0; t < x.t1; ++t) {
+    __syncthreads();
+    bool bad = false;
+    for (int e = threadIdx.x; e < R * (D / 4); e += 256) {
+      const int rr = e / (D / 4), d = (e % (D / 4)) * 4, j = t * R + rr;
+      float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
+      if (j >= x.lo && j < x.hi) {
+        const int pid = a.table[(int64_t)b * a.max_pages + (j >> a.pshift)];
+        if (pid >= 0 && pid < a.num_pages) {
+          const int64_t at =
+              pid * a.page_stride + (((int64_t)kvh << a.pshift) + (j & ((1 << a.pshift) - 1))) * D + d;
+          kx = *reinterpret_cast<const float4*>((const float*)a.k + at);
+          vx = *reinterpret_cast<const float4*>((const float*)a.v + at);
+        }
+      }
+      bad |= !(isfinite(vx.x) && isfinite(vx.y) && isfinite(vx.z) && isfinite(vx.w));
+      *reinterpret_cast<float4*>(sk + rr * LD + d) = kx;
+      *reinterpret_cast<float4*>(sv + rr * LD + d) = vx;
+    }
+    const bool slow = __syncthreads_or(bad);
+    f4_t y[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      y[n] = zero4();
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const float4 kx = *reinterpret_cast<const float4*>(sk + (16 * n + c) * LD + 16 * k + 4 * g);
+        y[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(kx.x, q[k].x, y[n], 0, 0, 0);
+        y[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(kx.y, q[k].y, y[n], 0, 0, 0);
+        y[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(kx.z, q[k].z, y[n], 0, 0, 0);
+        y[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(kx.w, q[k].w, y[n], 0, 0, 0);
+      }
+    }
+    float mx = -INFINITY;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = t * R + 16 * n + 4 * g + e;
+        y[n][e] = j > p || j <= lw ? -INFINITY : y[n][e] * a.scale;
+        mx = fmaxf(mx, y[n][e]);
+      }
+    mx = fmaxf(mx, __shfl_xor(mx, 16, WAVE));
+    mx = fmaxf(mx, __shfl_xor(mx, 32, WAVE));
+    const float mn = fmaxf(m, mx), ms = mn == -INFINITY ? 0.f : mn;
+    const float f = m == -INFINITY ? 0.f : fast_exp2(m - ms);
+    m = mn;
+    l *= f;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[n][e] = fast_exp2(y[n][e] - ms);
+        l += y[n][e];
+      }
+    if (mn != -INFINITY)
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[k][e] *= f;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float v = sv[(16 * n + 4 * g + e) * LD + 16 * k + c];
+          if (slow && !isfinite(v)) v = 0.f;
+          o[k] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, y[n][e], o[k], 0, 0, 0);
+        }
+    if (slow) {
+      for (int rr = 0; rr < R; ++rr) {
+        float w = 0.f;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w = n * 16 + e == (rr & 16) + (rr & 3) ? y[n][e] : w;
+        w = __shfl(w, ((rr >> 2) & 3) * 16 + c, WAVE);
+        const int j = t * R + rr;
+        if (j <= p && j > lw)
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float v = sv[rr * LD + 16 * k + 4 * g + e];
+              if (!isfinite(v)) o[k][e] = fmaf(w, v, o[k][e]);
+            }
+      }
+    }
+  }
+  l += __shfl_xor(l, 16, WAVE);
+  l += __shfl_xor(l, 32, WAVE);
+  if (!real) return;
+  const int64_t at = out_row(a, s, kvh, r);
+  const bool split_out = a.nsplit > 1;
+  if (g == 0) {
+    if (split_out) a.part_ml[split * a.rows + at] = make_float2(m, l);
+    else if (a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + fast_log2(l)) * LN2;
+  }
+  const float f = split_out ? 1.f : l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) {
+    const f4_t v = o[k] * f;
+    if (split_out) *reinterpret_cast<f4_t*>(a.part_o + (split * a.rows + at) * D + 16 * k + 4 * g) = v;
+    else store4((OUT*)a.o + at * D + 16 * k + 4 * g, v);
+  }
+}
+
+// ------------------------------------------------------------------ launches
+
+struct Plan {
+  bool tiles, rows;   // which of the bf16 kernels run
+  int64_t slots;      // row tiles, over all sequences
+  int nsplit;
+};
+
+int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
+
+Plan plan(const AttnCall& c) {
+  Plan p;
+  const int64_t G = c.H / c.Hkv, per = (int64_t)c.T * G;
+  const bool f32 = c.io == IO_F32;
+  const int R = f32 ? 64 : 128;
+  // bf16 sequences of at most 32 rows go to attn_row_kernel; a packed batch may hold both kinds
+  p.tiles = f32 || per > 32;
+  p.rows = !f32 && (per <= 32 || (c.packed && c.total < (int64_t)c.B * c.T));
+  p.slots = c.packed ? c.total * G / R + c.B : c.B * cdiv(per, R);
+  // Pieces of the cache range: enough workgroups for the chip, none shorter
+  // than a few tiles.
+  const int64_t units = (p.tiles ? p.slots : c.B) * c.Hkv;
+  const int64_t range = c.window ? std::min<int64_t>(c.max_kv, c.window + (p.tiles ? R / G : 0)) : c.max_kv;
+  const int64_t want = cdiv(p.tiles ? 1024 : 512, units), most = cdiv(range, p.tiles ? 512 : 128);
+  p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 128));
+  return p;
+}
+
+template <int D, typename OUT>
+hipError_t launch(const AttnCall& c, const Plan& p, const Args& a, hipStream_t stream) {
+  const int combos = c.Hkv * p.nsplit;
+  if (c.io == IO_F32) {
+    attn_f32_kernel<D, OUT><<<dim3((unsigned)(p.slots * combos)), dim3(256), 0, stream>>>(a);
+  } else {
+    constexpr int NW = D == 256 ? 2 : 4;
+    if (p.tiles) attn_tile_kernel<D, OUT><<<dim3((unsigned)(p.slots * combos)), dim3(256), 0, stream>>>(a);
+    if (p.rows) attn_row_kernel<D, NW, OUT><<<dim3((unsigned)(c.B * combos)), dim3(NW * 64), 0, stream>>>(a);
+  }
+  if (p.nsplit > 1)
+    attn_join_kernel<D, OUT><<<dim3((unsigned)cdiv(a.rows, 256 / (D / 4))), dim3(256), 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t attn_workgroups(const AttnCall& c) {
+  const Plan p = plan(c);
+  const int64_t units = std::max<int64_t>(p.tiles ? p.slots : 0, p.rows ? c.B : 0);
+  return std::max<int64_t>(units * c.Hkv * p.nsplit, cdiv(c.total * c.H, 4));
+}
+
+size_t attn_workspace_bytes(const AttnCall& c) {
+  const Plan p = plan(c);
+  if (p.nsplit == 1) return 0;
+  const size_t rows = (size_t)c.total * c.H * p.nsplit;
+  return ((rows * c.D * sizeof(float) + 255) & ~(size_t)255) + ((rows * sizeof(float2) + 255) & ~(size_t)255);
+}
+
+hipError_t launch_attn(const AttnCall& c, hipStream_t stream) {
+  const Plan p = plan(c);
+  Args a;
+  a.B = c.B, a.T = c.T, a.H = c.H, a.Hkv = c.Hkv, a.G = c.H / c.Hkv;
+  a.pshift = __builtin_ctz((unsigned)c.page), a.max_pages = c.max_pages, a.num_pages = c.num_pages;
+  a.window = c.window, a.nsplit = p.nsplit;
+  a.total = c.total, a.rows = c.total * c.H, a.q_stride = c.q_stride, a.page_stride = c.page_stride;
+  a.cu = c.packed ? c.cu_seqlens : nullptr;
+  a.kv_lens = c.kv_lens, a.table = c.page_table;
+  a.q = c.q, a.k = c.k_cache, a.v = c.v_cache, a.o = c.o, a.lse = c.lse;
+  const size_t rows = (size_t)a.rows * p.nsplit;
+  a.part_o = static_cast<float*>(c.workspace);
+  a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(c.workspace) + ((rows * c.D * sizeof(float) + 255) & ~(size_t)255));
+  a.scale = c.scale * 1.4426950408889634f;
+  const bool bf = c.out == IO_BF16;
+  switch (c.D) {
+    case 64: return bf ? launch<64, bf16_t>(c, p, a, stream) : launch<64, float>(c, p, a, stream);
+    case 128: return bf ? launch<128, bf16_t>(c, p, a, stream) : launch<128, float>(c, p, a, stream);
+    case 256: return bf ? launch<256, bf16_t>(c, p, a, stream) : launch<256, float>(c, p, a, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace jb

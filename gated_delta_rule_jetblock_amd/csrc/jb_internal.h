@@ -12,6 +12,11 @@ namespace jb {
 
 enum IoType { IO_BF16 = 0, IO_F32 = 1 };
 
+// Sets jb_last_error()'s message and returns the status (jb_api.hip); api_ok
+// clears the message.
+int api_fail(int status, const char* fmt, ...);
+int api_ok();
+
 // Kernel generator over n rows of x [n][D] -> taps [n][H*4] f32 (and, when
 // pre_out is given, the hidden layer before SiLU [n][32] f32).
 hipError_t launch_gen_taps(int io, int64_t n, int D, int H, const void* x, const void* W1,

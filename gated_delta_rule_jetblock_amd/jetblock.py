@@ -36,6 +36,16 @@ class Shape(ctypes.Structure):
                  "io_dtype", "out_dtype", "flags")]
 
 
+class AttnShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("B", "T", "H", "Hkv", "D", "rot", "page", "max_pages", "num_pages", "max_kv", "window",
+                 "io_dtype", "out_dtype", "flags")] + \
+               [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "page_stride")]
+
+
+ROPE_INTERLEAVED, ROPE_NO_NORM = 1, 2
+
+
 def flag_segment(n: int) -> int:
     return (int(n) & 0xFFFF) << 8
 
@@ -77,7 +87,17 @@ _lib.jb_prefill_varlen_workspace_size.argtypes = [_S, ctypes.c_int64, ctypes.POI
 _lib.jb_prefill_varlen.argtypes = [_S, ctypes.c_int64] + [_P] * 16 + [_P, _SZ, _P]
 _lib.jb_backward_workspace_size.argtypes = [_S, ctypes.POINTER(_SZ)]
 _lib.jb_backward.argtypes = [_S] + [_P] * 27 + [_P, _SZ, _P]
-for _f in ("jb_prefill_workspace_size", "jb_decode_workspace_size", "jb_prefill", "jb_prefill_noalloc",
+_A = ctypes.POINTER(AttnShape)
+_L, _F = ctypes.c_int64, ctypes.c_float
+_lib.jb_qk_norm_rope.argtypes = [_A] + [_P] * 6 + [_F] + [_P] * 3
+_lib.jb_qk_norm_rope_backward_workspace_size.argtypes = [_A, ctypes.POINTER(_SZ)]
+_lib.jb_qk_norm_rope_backward.argtypes = [_A] + [_P] * 6 + [_F] + [_P] * 7 + [_SZ, _P]
+_lib.jb_qk_norm_rope_paged.argtypes = [_A, _L] + [_P] * 10 + [_F] + [_P] * 4
+_lib.jb_attn_paged_workspace_size.argtypes = [_A, _L, ctypes.c_int32, ctypes.POINTER(_SZ)]
+_lib.jb_attn_paged.argtypes = [_A, _L] + [_P] * 6 + [_F] + [_P] * 3 + [_SZ, _P]
+for _f in ("jb_qk_norm_rope", "jb_qk_norm_rope_backward_workspace_size", "jb_qk_norm_rope_backward",
+           "jb_qk_norm_rope_paged", "jb_attn_paged_workspace_size", "jb_attn_paged",
+           "jb_prefill_workspace_size", "jb_decode_workspace_size", "jb_prefill", "jb_prefill_noalloc",
            "jb_decode_step",
            "jb_gen_taps", "jb_gen_conv", "jb_prologue", "jb_probe_mfma", "jb_decode_update",
            "jb_project_workspace_size", "jb_prefill_from_x_workspace_size", "jb_project", "jb_prefill_from_x",
@@ -134,9 +154,13 @@ def make_shape(B, T, H, dk, dv, d_model, io_dtype=JB_BF16, out_dtype=JB_F32, fla
 
 
 def _io_code(t: torch.Tensor) -> int:
-    if t.dtype not in _DT:
-        raise TypeError(f"unsupported dtype {t.dtype}")
-    return _DT[t.dtype]
+    return _code(t.dtype)
+
+
+def _code(dtype) -> int:
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return _DT[dtype]
 
 
 def prefill_workspace_size(shape: Shape) -> int:
@@ -509,3 +533,237 @@ def backward(x, q, k, v, alpha, beta, W1, W2, dout, b1=None, b2=None, S0=None, c
                                                      "db2", "dS0", "dconv_in")],
                             _ptr(ws), ws.numel(), _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------- softmax-attention layers
+
+
+def _rows(t, name: str):
+    """Pointer, tokens and token stride of [..., heads, D] whose tokens lie at one distance."""
+    if t.stride(-1) != 1 or t.stride(-2) != t.shape[-1]:
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    if t.dim() == 3:
+        n, stride = t.shape[0], t.stride(0)
+    elif t.dim() == 4:
+        n, stride = t.shape[0] * t.shape[1], t.stride(1) if t.shape[1] > 1 else t.stride(0)
+        if t.shape[0] > 1 and t.shape[1] > 1 and t.stride(0) != t.shape[1] * stride:
+            raise ValueError(f"{name}: tokens must lie at one distance")
+    else:
+        raise ValueError(f"{name}: expected [tokens, heads, D] or [B, T, heads, D], got {tuple(t.shape)}")
+    if n > 1 and stride < t.shape[-2] * t.shape[-1]:
+        raise ValueError(f"{name}: tokens overlap (token stride {stride})")
+    return t.data_ptr(), n, stride if n > 1 else 0
+
+
+def _same(dev, **tensors):
+    """Every tensor on device `dev`; those with a dtype to match, of that dtype."""
+    for name, (t, dtype) in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, q on {dev}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+
+
+def _flat(t, name: str, *shape):
+    """Pointer of a contiguous tensor of the given shape (None: no pointer)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of shape {shape}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _on(dev, stream):
+    """The stream to launch on, and whether `dev` has to be made current for it."""
+    if dev.type != "cuda":
+        raise ValueError("libjetblock takes device tensors; got a tensor on " + str(dev))
+    if stream is None:
+        handle = torch.cuda.current_stream(dev).cuda_stream
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return handle, dev.index is not None and dev.index != torch.cuda.current_device()
+
+
+def _launch(dev, other: bool, fn, *args):
+    if other:
+        with torch.cuda.device(dev):
+            _check(fn(*args))
+    else:
+        _check(fn(*args))
+
+
+def _rope_flags(interleaved, normalize):
+    return (ROPE_INTERLEAVED if interleaved else 0) | (0 if normalize else ROPE_NO_NORM)
+
+
+def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, *, eps=1e-6, interleaved=False, normalize=True,
+                 out_dtype=None, q_out=None, k_out=None, stream=None):
+    """jb_qk_norm_rope.  q [tokens,H,D] or [B,T,H,D], k likewise with Hkv heads (any distance
+    between tokens), positions int32 [tokens], inv_freq f32 [rot/2], wq, wk [D].  Returns
+    (q_out, k_out), contiguous, of out_dtype (default: q's)."""
+    dev, io = q.device, q.dtype
+    handle, other = _on(dev, stream)
+    out_dtype = out_dtype or (q_out.dtype if q_out is not None else io)
+    _same(dev, k=(k, io), wq=(wq, io), wk=(wk, io), positions=(positions, torch.int32),
+          inv_freq=(inv_freq, torch.float32), q_out=(q_out, out_dtype), k_out=(k_out, out_dtype))
+    H, D = q.shape[-2:]
+    Hkv = k.shape[-2]
+    qp, n, qs = _rows(q, "q")
+    kp, nk, ks = _rows(k, "k")
+    if nk != n or k.shape[-1] != D:
+        raise ValueError(f"k {tuple(k.shape)} does not go with q {tuple(q.shape)}")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=out_dtype, device=dev)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=out_dtype, device=dev)
+    shape = AttnShape(1, n, H, Hkv, D, 2 * inv_freq.numel(), 0, 0, 0, 0, 0, _io_code(q), _code(out_dtype),
+                      _rope_flags(interleaved, normalize), qs, ks, 0, 0)
+    _launch(dev, other, _lib.jb_qk_norm_rope, shape, qp, kp, _flat(wq, "wq", D), _flat(wk, "wk", D),
+            _flat(inv_freq, "inv_freq", inv_freq.numel()), _flat(positions.reshape(-1), "positions", n), eps,
+            _flat(q_out, "q_out", *q.shape), _flat(k_out, "k_out", *k.shape), handle)
+    return q_out, k_out
+
+
+def qk_norm_rope_backward_workspace_size(shape: AttnShape) -> int:
+    n = _SZ(0)
+    _check(_lib.jb_qk_norm_rope_backward_workspace_size(shape, n))
+    return n.value
+
+
+def qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, wq=None, wk=None, *, eps=1e-6,
+                          interleaved=False, normalize=True, dq=None, dk=None, ws=None, stream=None):
+    """jb_qk_norm_rope_backward: gradients of qk_norm_rope from those of its outputs (contiguous,
+    bf16 or f32).  Returns dict(dq, dk, dwq, dwk): dq, dk of dq_out's dtype, dwq, dwk f32 [D]
+    (None without the norm)."""
+    dev, io, gr = q.device, q.dtype, dq_out.dtype
+    handle, other = _on(dev, stream)
+    _same(dev, k=(k, io), wq=(wq, io), wk=(wk, io), positions=(positions, torch.int32),
+          inv_freq=(inv_freq, torch.float32), dq_out=(dq_out, gr), dk_out=(dk_out, gr), dq=(dq, gr), dk=(dk, gr))
+    H, D = q.shape[-2:]
+    Hkv = k.shape[-2]
+    qp, n, qs = _rows(q, "q")
+    kp, nk, ks = _rows(k, "k")
+    if nk != n or k.shape[-1] != D:
+        raise ValueError(f"k {tuple(k.shape)} does not go with q {tuple(q.shape)}")
+    dq = torch.empty(q.shape, dtype=gr, device=dev) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=gr, device=dev) if dk is None else dk
+    dwq = dwk = None
+    if normalize:
+        dwq = torch.empty(D, dtype=torch.float32, device=dev)
+        dwk = torch.empty(D, dtype=torch.float32, device=dev)
+    shape = AttnShape(1, n, H, Hkv, D, 2 * inv_freq.numel(), 0, 0, 0, 0, 0, _io_code(q), _code(gr),
+                      _rope_flags(interleaved, normalize), qs, ks, 0, 0)
+    if ws is None:
+        ws = workspace(qk_norm_rope_backward_workspace_size(shape), dev)
+    _launch(dev, other, _lib.jb_qk_norm_rope_backward, shape, qp, kp, _flat(wq, "wq", D), _flat(wk, "wk", D),
+            _flat(inv_freq, "inv_freq", inv_freq.numel()), _flat(positions.reshape(-1), "positions", n), eps,
+            _flat(dq_out, "dq_out", *q.shape), _flat(dk_out, "dk_out", *k.shape), _flat(dq, "dq", *q.shape),
+            _flat(dk, "dk", *k.shape), _flat(dwq, "dwq", D), _flat(dwk, "dwk", D), ws.data_ptr(), ws.numel(), handle)
+    return dict(dq=dq, dk=dk, dwq=dwq, dwk=dwk)
+
+
+def _batch(q, cu_seqlens, max_seqlen):
+    """B and T of q: packed [tokens,H,D] with cu_seqlens, [B,T,H,D], or [B,H,D] (one token each)."""
+    if cu_seqlens is not None:
+        if q.dim() != 3 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("packed: q is [tokens, H, D] and cu_seqlens [B + 1]")
+        return cu_seqlens.numel() - 1, q.shape[0] if max_seqlen is None else int(max_seqlen)
+    return (q.shape[0], q.shape[1]) if q.dim() == 4 else (q.shape[0], 1)
+
+
+def _pages(k_cache, v_cache, page_table, kv_lens, B, D):
+    """num_pages, Hkv, page, page stride and max_pages of a cache."""
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache are [pages, Hkv, page, D] alike")
+    P, Hkv, page, d = k_cache.shape
+    st = k_cache.stride()
+    if d != D or st[3] != 1 or st[2] != D or (Hkv > 1 and st[1] != page * D):
+        raise ValueError("a page of the caches must be contiguous, of q's head size")
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table: expected [{B}, max_pages], got {tuple(page_table.shape)}")
+    if kv_lens.dim() != 1 or kv_lens.numel() != B:
+        raise ValueError(f"kv_lens: expected [{B}], got {tuple(kv_lens.shape)}")
+    if P > 1 and st[0] < Hkv * page * D:
+        raise ValueError(f"pages of the caches overlap (page stride {st[0]})")
+    return P, Hkv, page, st[0] if P > 1 else 0, page_table.shape[1]
+
+
+def qk_norm_rope_paged(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq, wq=None, wk=None, *,
+                       cu_seqlens=None, max_seqlen: int | None = None, positions=None, eps=1e-6, interleaved=False,
+                       normalize=True, q_out=None, stream=None):
+    """jb_qk_norm_rope_paged: rotated queries out, rotated keys and values into the caches
+    [pages,Hkv,page,D] (in place).  q [B,T,H,D], [B,H,D] (one token each) or packed [tokens,H,D]
+    with cu_seqlens int32 [B+1]; page_table int32 [B,max_pages], kv_lens int32 [B] (the new tokens
+    among the rows).  Returns dict(q, k_cache, v_cache)."""
+    dev, io, i32 = q.device, q.dtype, torch.int32
+    handle, other = _on(dev, stream)
+    _same(dev, k=(k, io), v=(v, io), k_cache=(k_cache, io), v_cache=(v_cache, io), wq=(wq, io), wk=(wk, io),
+          page_table=(page_table, i32), kv_lens=(kv_lens, i32), cu_seqlens=(cu_seqlens, i32),
+          positions=(positions, i32), inv_freq=(inv_freq, torch.float32), q_out=(q_out, io))
+    H, D = q.shape[-2:]
+    qp, n, qs = _rows(q, "q")
+    kp, nk, ks = _rows(k, "k")
+    vp, nv, vs = _rows(v, "v")
+    B, T = _batch(q, cu_seqlens, max_seqlen)
+    P, Hkv, page, ps, max_pages = _pages(k_cache, v_cache, page_table, kv_lens, B, D)
+    if nk != n or nv != n or k.shape[-2:] != (Hkv, D) or v.shape[-2:] != (Hkv, D):
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} do not go with q {tuple(q.shape)} and the caches")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=io, device=dev)
+    code = _io_code(q)
+    shape = AttnShape(B, T, H, Hkv, D, 2 * inv_freq.numel(), page, max_pages, P, 0, 0, code, code,
+                      _rope_flags(interleaved, normalize), qs, ks, vs, ps)
+    _launch(dev, other, _lib.jb_qk_norm_rope_paged, shape, n,
+            None if cu_seqlens is None else _flat(cu_seqlens, "cu_seqlens", B + 1), _flat(kv_lens, "kv_lens", B),
+            _flat(page_table, "page_table", B, max_pages), qp, kp, vp, _flat(wq, "wq", D), _flat(wk, "wk", D),
+            _flat(inv_freq, "inv_freq", inv_freq.numel()),
+            None if positions is None else _flat(positions.reshape(-1), "positions", n), eps,
+            _flat(q_out, "q_out", *q.shape), k_cache.data_ptr(), v_cache.data_ptr(), handle)
+    return dict(q=q_out, k_cache=k_cache, v_cache=v_cache)
+
+
+def attn_paged_workspace_size(shape: AttnShape, total_tokens: int, packed: bool) -> int:
+    n = _SZ(0)
+    _check(_lib.jb_attn_paged_workspace_size(shape, int(total_tokens), int(packed), n))
+    return n.value
+
+
+def attn_paged(q, k_cache, v_cache, page_table, kv_lens, *, cu_seqlens=None, max_seqlen: int | None = None,
+               max_kv: int | None = None, window: int = 0, scale: float | None = None, out_dtype=None, o=None,
+               want_lse=False, lse=None, ws=None, stream=None):
+    """jb_attn_paged: attention of each sequence's new tokens over its paged cache (which holds
+    them already).  q [B,T,H,D], [B,H,D] (decode) or packed [tokens,H,D] with cu_seqlens int32
+    [B+1]; caches, page_table and kv_lens as for qk_norm_rope_paged.  max_seqlen and max_kv, host
+    integers, are the longest sequence's new tokens (packed; default: all) and cache rows (default:
+    the table's capacity); they plan the launch, nothing is read back from the device.  Returns
+    dict(o, lse): o of q's shape and out_dtype (default: q's), lse f32 [..., H] or None."""
+    dev, io, i32 = q.device, q.dtype, torch.int32
+    handle, other = _on(dev, stream)
+    out_dtype = out_dtype or (o.dtype if o is not None else io)
+    _same(dev, k_cache=(k_cache, io), v_cache=(v_cache, io), page_table=(page_table, i32), kv_lens=(kv_lens, i32),
+          cu_seqlens=(cu_seqlens, i32), o=(o, out_dtype), lse=(lse, torch.float32), ws=(ws, torch.uint8))
+    H, D = q.shape[-2:]
+    qp, n, qs = _rows(q, "q")
+    B, T = _batch(q, cu_seqlens, max_seqlen)
+    P, Hkv, page, ps, max_pages = _pages(k_cache, v_cache, page_table, kv_lens, B, D)
+    if o is None:
+        o = torch.empty(q.shape, dtype=out_dtype, device=dev)
+    if lse is None and want_lse:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+    packed = cu_seqlens is not None
+    shape = AttnShape(B, T, H, Hkv, D, 0, page, max_pages, P, 0 if max_kv is None else int(max_kv), int(window),
+                      _io_code(q), _code(out_dtype), 0, qs, 0, 0, ps)
+    if ws is None:
+        need = attn_paged_workspace_size(shape, n, packed)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _launch(dev, other, _lib.jb_attn_paged, shape, n, _flat(cu_seqlens, "cu_seqlens", B + 1),
+            _flat(kv_lens, "kv_lens", B), _flat(page_table, "page_table", B, max_pages), qp, k_cache.data_ptr(),
+            v_cache.data_ptr(), 0.0 if scale is None else float(scale), _flat(o, "o", *q.shape),
+            _flat(lse, "lse", *q.shape[:-1]), None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel(), handle)
+    return dict(o=o, lse=lse)

@@ -378,6 +378,128 @@ jb_status jb_backward(const jb_shape* shape, const void* x, const void* q, const
                       void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The softmax-attention layers of a hybrid stack.  The pages' models keep a few
+ * full-attention and sliding-window layers (grouped queries, windows 1152 and
+ * 2048) beside the JetBlock layers (Jet-Nemotron csdn translation, section 3.1
+ * and appendix A.1), served by chunked prefill and decode like them.  These
+ * calls are such a layer's operators between its projections: the norm and
+ * position rotation of queries and keys, the paged cache's append, and the
+ * attention of new tokens over it.
+ *
+ * Layouts (H query heads on Hkv key heads, G = H / Hkv; head size D)
+ *   q, q_out, o    [tokens][H][D]      query head h reads key head h / G
+ *   k, v, k_out    [tokens][Hkv][D]
+ *   k_cache, v_cache [num_pages][Hkv][page][D]
+ *   page_table     [B][max_pages] int32: row j of sequence b's cache is row
+ *                  j % page of page page_table[b][j / page]
+ *   kv_lens        [B] int32: rows of sequence b's cache, its new tokens the
+ *                  last of them
+ *   lse            [tokens][H] float32
+ * Tokens are B x T (cu_seqlens NULL), or packed: sequence b is rows
+ * cu_seqlens[b] .. cu_seqlens[b+1] - 1 of total_tokens, at most its first
+ * shape.T of them; rows that no sequence owns are left as they are.
+ * q, k and v may have any distance between tokens (the strides below, for
+ * slices of one projection's output); the caches any distance between pages.
+ * Device-side values cannot be checked on the host, and none makes a call
+ * reach outside the tensors: offsets are clamped as in jb_prefill_varlen,
+ * kv_lens to [0, max_pages * page], and a page index outside [0, num_pages)
+ * reads as rows of zeros and is not written to.  Two sequences (or an append
+ * and anything else) must not write the same page.
+ *
+ * Supported: D in {64, 128, 256}; H <= 256, a multiple of Hkv; page a power of
+ * two in [16, 4096]; max_pages * page <= 2^30; both dtypes; 1 <= B <= 65535;
+ * 0 <= T <= 2^30; total_tokens < 2^31; fewer than 2^40 elements in any tensor.
+ * Pointers 16-byte aligned (cu_seqlens, kv_lens, page_table, positions,
+ * inv_freq and lse: 4-byte).
+ * ------------------------------------------------------------------------- */
+
+typedef struct {
+  int32_t B, T;         /* sequences, tokens of each (packed: of the longest) */
+  int32_t H, Hkv, D;
+  int32_t rot;          /* rotated values of a head: a multiple of 16 in [0, D] */
+  int32_t page, max_pages, num_pages;  /* the cache (0 where a call has none) */
+  int32_t max_kv;       /* longest kv_lens[b] the launch is planned for (longer
+                           ones are right too); 0: max_pages * page */
+  int32_t window;       /* rows a query sees, itself among them; 0: all before it */
+  int32_t io_dtype;     /* jb_dtype of q, k, v, the caches and norm weights */
+  int32_t out_dtype;    /* jb_dtype of q_out, k_out, o and the gradients */
+  int32_t flags;        /* JB_ROPE_* or 0 */
+  int64_t q_stride, k_stride, v_stride;  /* elements between tokens, 0: contiguous */
+  int64_t page_stride;  /* elements between pages of a cache, 0: contiguous */
+} jb_attn_shape;
+
+/* Pairs of the rotation are (2i, 2i+1) instead of (i, i + rot/2). */
+#define JB_ROPE_INTERLEAVED ((int32_t)1)
+/* Rotation only: no norm, wq and wk NULL. */
+#define JB_ROPE_NO_NORM ((int32_t)2)
+
+/*
+ * jb_qk_norm_rope -- every head row x of q and k (B T tokens):
+ *     y = R (w x / sqrt(mean(x^2) + eps))
+ * with w = wq or wk [D] (nullable: 1) and R the rotation of each pair of the
+ * first rot values by positions[token] * inv_freq[pair] radians: (a, b) to
+ * (a cos - b sin, b cos + a sin).  positions [tokens] int32, inv_freq [rot/2]
+ * float32; the angle is formed in 64 bits, so far positions keep theirs.
+ * q_out, k_out are contiguous; q_out may be q and k_out may be k (contiguous,
+ * same dtype).  Norm, rotation and sums are fp32; outputs are rounded once.
+ */
+jb_status jb_qk_norm_rope(const jb_attn_shape* shape, const void* q, const void* k, const void* wq,
+                          const void* wk, const float* inv_freq, const int32_t* positions, float eps,
+                          void* q_out, void* k_out, void* stream);
+
+/* Workspace bytes of jb_qk_norm_rope_backward for `shape`. */
+jb_status jb_qk_norm_rope_backward_workspace_size(const jb_attn_shape* shape, size_t* bytes);
+
+/*
+ * jb_qk_norm_rope_backward -- its gradient: from q, k (the inputs) and dq_out,
+ * dk_out (contiguous, out_dtype) writes dq, dk (contiguous, out_dtype; dq may
+ * be dq_out, dk may be dk_out) and the weights' gradients dwq, dwk [D] float32
+ * (nullable; must be NULL with JB_ROPE_NO_NORM; formed also where wq, wk are
+ * NULL: the gradient with respect to ones).  Sums run in a fixed order.
+ * workspace: jb_qk_norm_rope_backward_workspace_size() bytes, 256-byte aligned.
+ */
+jb_status jb_qk_norm_rope_backward(const jb_attn_shape* shape, const void* q, const void* k, const void* wq,
+                                   const void* wk, const float* inv_freq, const int32_t* positions,
+                                   float eps, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                                   float* dwq, float* dwk, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * jb_qk_norm_rope_paged -- jb_qk_norm_rope for serving: token i of sequence b
+ * (T_b new ones) is row kv_lens[b] - T_b + i of its cache; its rotated keys
+ * and its values (as they are) are written there, its rotated queries to
+ * q_out.  positions is nullable: the cache row.  out_dtype must be io_dtype.
+ * A token whose row is negative (kv_lens[b] < T_b) is not stored.
+ */
+jb_status jb_qk_norm_rope_paged(const jb_attn_shape* shape, int64_t total_tokens, const int32_t* cu_seqlens,
+                                const int32_t* kv_lens, const int32_t* page_table, const void* q,
+                                const void* k, const void* v, const void* wq, const void* wk,
+                                const float* inv_freq, const int32_t* positions, float eps, void* q_out,
+                                void* k_cache, void* v_cache, void* stream);
+
+/* Workspace bytes of jb_attn_paged (packed: whether cu_seqlens will be given). */
+jb_status jb_attn_paged_workspace_size(const jb_attn_shape* shape, int64_t total_tokens, int32_t packed,
+                                       size_t* bytes);
+
+/*
+ * jb_attn_paged -- attention of new tokens over the paged cache that holds
+ * them: token i of sequence b, at cache row p = kv_lens[b] - T_b + i, sees rows
+ * j <= p, with a window those with j > p - window:
+ *     o = sum_j softmax_j(scale q.k_j) v_j,   lse = ln sum_j e^{scale q.k_j}
+ * scale 0 selects 1 / sqrt(D); it must not be negative.  A token that sees no
+ * row (p < 0) gets o = 0 and lse = -inf.  Rows that a token does not see have
+ * no part in it, whatever they hold.  One token per sequence (T = 1) is the
+ * decode step.  lse is nullable.  bf16: scores, statistics and sums are fp32,
+ * the softmax weights are rounded to bf16 for their product with v, o is
+ * rounded once.  fp32 inputs: fp32 throughout.
+ * workspace: jb_attn_paged_workspace_size() bytes (NULL if 0), 256-byte aligned.
+ */
+jb_status jb_attn_paged(const jb_attn_shape* shape, int64_t total_tokens, const int32_t* cu_seqlens,
+                        const int32_t* kv_lens, const int32_t* page_table, const void* q,
+                        const void* k_cache, const void* v_cache, float scale, void* o, float* lse,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Single-stage entry points.  Each runs one stage of the path by itself so
  * that it can be checked on its own; the two calls above fuse these stages.
  * ------------------------------------------------------------------------- */
