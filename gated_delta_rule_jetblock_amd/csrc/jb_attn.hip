@@ -34,8 +34,7 @@
 // queries see in part only is looked over first: a value in V that is not
 // finite counts as 0 on the matrix cores, and is added for the queries that do
 // see it by itself.
-#include <limits.h>
-#include <math.h>
+#include <cmath>
 
 #include "jb_attn.h"
 #include "jb_device.h"
@@ -166,8 +165,13 @@ __device__ __forceinline__ f16_t mfma32(bf16x8_t a, bf16x8_t b, f16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// a value and lane + 32's (lane - 32's)
+// lane + 32's (lane - 32's) value
 __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32, WAVE); }
+// the larger of a value and lane + 32's (lane - 32's), without LDS
+__device__ __forceinline__ float half_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
 
 // One wave's 32 queries and what they have gathered so far.
 template <int D> struct Wave {
@@ -176,8 +180,7 @@ template <int D> struct Wave {
   f16_t o[D / 32];  // O^T: o[db][i] is d = 32 db + 8 (i / 4) + 4 g + i % 4
   float m, l;       // m as the exponent base 2 subtracts it; l of this lane's half of the rows
   int p, lw;        // sees rows lw < j <= p
-  int phi, plo;     // of the wave's real rows: the last row seen, and the least p
-  int lwlo, lwhi;   // and the least and the largest lw
+  int phi, lwlo;    // of the wave's real rows: the last row seen, and the least lw
 
   __device__ void init(const Args& a, const Seq& s, int kvh, int64_t r0) {
     const int lane = lane_id();
@@ -188,11 +191,10 @@ template <int D> struct Wave {
     p = real ? base + i : -1;
     lw = a.window ? p - a.window : -1;
     const int64_t last = min(r0 + 32, nr) - 1;
-    plo = phi = lwlo = lwhi = -1;
+    phi = lwlo = -1;
     if (r0 < nr) {
-      plo = uniform(base + (int)(r0 / a.G));
       phi = uniform(base + (int)(last / a.G));
-      if (a.window) lwlo = plo - a.window, lwhi = phi - a.window;
+      if (a.window) lwlo = uniform(base + (int)(r0 / a.G)) - a.window;
     }
     const bf16_t* src = (const bf16_t*)a.q + (s.tok0 + i) * a.q_stride + (int64_t)(kvh * a.G + g) * D + 8 * (lane >> 5);
 #pragma unroll
@@ -209,41 +211,42 @@ template <int D> struct Wave {
     l = 0.f;
   }
 
-  // The weights of NB x 32 cache rows from j0 (their K image at lk), into s;
-  // false: no query sees any of them.
-  template <int NB>
-  __device__ bool weights(const Args& a, const lds_char* lk, int j0, f16_t (&s)[NB]) {
+  // S^T of NB x 32 cache rows, their K image at lk
+  template <int NB> __device__ void scores(const lds_char* lk, f16_t (&s)[NB]) const {
     const int lane = lane_id(), c = lane & 31, g = lane >> 5;
-    if (j0 > phi || j0 + NB * 32 - 1 <= lwlo) return false;
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s[n][e] = 0.f;
     const int kb = c * I::ROWB + ((g ^ I::fk(c)) << 4);
+    constexpr int AHEAD = 4;  // steps whose fragments are on their way
+    bf16x8_t f[D / 16][NB];
+    f16_t z;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) z[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+      for (int n = 0; n < NB; ++n) f[k][n] = *(const lds_bf16x8*)(lk + (kb ^ (k << 5)) + n * 32 * I::ROWB);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+      for (int n = 0; n < NB; ++n) s[n] = mfma32(f[k][n], q[k], k ? s[n] : z);
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD * NB, 0);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      const lds_char* at = lk + (kb ^ (k << 5));
-#pragma unroll
-      for (int n = 0; n < NB; ++n) s[n] = mfma32(*(const lds_bf16x8*)(at + n * 32 * I::ROWB), q[k], s[n]);
+      __builtin_amdgcn_sched_group_barrier(0x8, NB, 0);
+      if (k + AHEAD < D / 16) __builtin_amdgcn_sched_group_barrier(0x100, NB, 0);
     }
-    if (in_part(j0, NB * 32)) {
-#pragma unroll
-      for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int j = j0 + 32 * n + 8 * (e >> 2) + 4 * g + (e & 3);
-          if (j > p || j <= lw) s[n][e] = -INFINITY;
-        }
-    }
-    float mx = -INFINITY;
+  }
+
+  // Takes the tile's scores into the running maximum; returns what the
+  // exponents subtract.  The maximum subtracted may lag behind the true one:
+  // weights up to 2^8 lose nothing in fp32 sums or in bf16's relative
+  // precision, and the rescaling of o is left out for all but the first tiles.
+  template <int NB> __device__ float take_max(const Args& a, const f16_t (&s)[NB]) {
+    float mx = s[0][0];
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
       for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[n][e]);
-    mx = fmaxf(mx, other_half(mx)) * a.scale;
-    // The subtracted maximum may lag behind the true one: weights up to 2^8 lose
-    // nothing in fp32 sums or in bf16's relative precision, and the rescaling
-    // of o is left out for all but the first tiles.
+    mx = half_max(mx) * a.scale;
     if (__any(mx > m + 8.f)) {
       const float mn = fmaxf(m, mx);
       const float f = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
@@ -254,36 +257,84 @@ template <int D> struct Wave {
       l *= f;
       m = mn;
     }
-    const float ms = m == -INFINITY ? 0.f : m;
+    return m == -INFINITY ? 0.f : m;
+  }
+
+  // Weights from scores; O^T += V^T P^T, 16 cache rows at a time: the
+  // exponentials of the next 16 go between the products of these.
+  template <int NB> __device__ void weights(const Args& a, f16_t (&s)[NB], float ms, int k) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      s[k >> 1][8 * (k & 1) + e] = fast_exp2(fmaf(s[k >> 1][8 * (k & 1) + e], a.scale, -ms));
+      l += s[k >> 1][8 * (k & 1) + e];
+    }
+  }
+
+  // A tile that every query sees whole
+  template <int NB> __device__ void full(const Args& a, const lds_char* lk, const lds_char* lv) {
+    f16_t s[NB];
+    scores<NB>(lk, s);
+    const float ms = take_max<NB>(a, s);
+    values<NB, true>(a, lv, s, ms);
+  }
+
+  // NB x 32 cache rows from j0 that some queries see in part; false: none sees any
+  template <int NB>
+  __device__ bool part(const Args& a, const lds_char* lk, int j0, f16_t (&s)[NB]) {
+    const int g = lane_id() >> 5;
+    if (j0 > phi || j0 + NB * 32 - 1 <= lwlo) return false;
+    scores<NB>(lk, s);
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        s[n][e] = fast_exp2(fmaf(s[n][e], a.scale, -ms));
-        l += s[n][e];
+        const int j = j0 + 32 * n + 8 * (e >> 2) + 4 * g + (e & 3);
+        if (j > p || j <= lw) s[n][e] = -INFINITY;
       }
+    const float ms = take_max<NB>(a, s);
+#pragma unroll
+    for (int k = 0; k < 2 * NB; ++k) weights<NB>(a, s, ms, k);
     return true;
   }
-  // whether some query sees some of the n rows from j0, but not every query all
-  __device__ bool in_part(int j0, int n) const { return j0 + n - 1 > plo || j0 <= lwhi; }
-
-  // O^T += V^T P^T
-  template <int NB> __device__ void values(const f16_t (&s)[NB], const lds_char* lv) {
+  // O^T += V^T P^T; EXP: s holds scores yet
+  template <int NB, bool EXP> __device__ void values(const Args& a, const lds_char* lv, f16_t (&s)[NB], float ms) {
     const int lane = lane_id(), g = lane >> 5;
     const int n16 = lane & 15, row = 4 * g + (n16 >> 2), pc = 2 * ((lane >> 4) & 1) + ((n16 & 3) >> 1);
     const int vb = row * I::ROWB + ((pc ^ I::fv(row)) << 4) + (n16 & 1) * 8;
+    constexpr int DB = D / 32;
+    if constexpr (EXP) weights<NB>(a, s, ms, 0);
 #pragma unroll
     for (int k = 0; k < 2 * NB; ++k) {
-      bf16x8_t w;
+      bf16x8_t w, v[DB];
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = (__bf16)s[k >> 1][8 * (k & 1) + e];
 #pragma unroll
-      for (int db = 0; db < D / 32; ++db) {
+      for (int db = 0; db < DB; ++db) {
         const lds_char* at = lv + (vb ^ (db << 6)) + k * 16 * I::ROWB;
         const s4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)at);
         const s4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(at + 8 * I::ROWB));
-        o[db] = mfma32(__builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)), w, o[db]);
+        v[db] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
       }
+#pragma unroll
+      for (int db = 0; db < DB; ++db) o[db] = mfma32(v[db], w, o[db]);
+      if constexpr (EXP)
+        if (k + 1 < 2 * NB) weights<NB>(a, s, ms, k + 1);
+    }
+    if constexpr (EXP) {
+      // the first step's reads and weights, then between any two products the
+      // reads and a part of the weights (28 instructions) of the next step
+      __builtin_amdgcn_sched_group_barrier(0x100, 2 * DB, 0);
+      __builtin_amdgcn_sched_group_barrier(0x2, 28, 0);
+#pragma unroll
+      for (int k = 0; k < 2 * NB; ++k)
+#pragma unroll
+        for (int db = 0; db < DB; ++db) {
+          __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+          if (k + 1 < 2 * NB) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            __builtin_amdgcn_sched_group_barrier(0x2, 28 / DB, 0);
+          }
+        }
     }
   }
 
@@ -311,6 +362,7 @@ template <int D> struct Wave {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             if (seen && !isfinite(v[e])) o[db][4 * e4 + e] = fmaf(w, v[e], o[db][4 * e4 + e]);
+          asm volatile("" ::: "memory");  // (a rare path: its reads take no registers from the others)
         }
     }
   }
@@ -356,6 +408,21 @@ __device__ __forceinline__ Span span_of(const Args& a, const Seq& s, int64_t r0,
   return x;
 }
 
+// The order in which a workgroup takes its tiles: those that every query r0 ..
+// r1 sees whole first (f0 .. f0 + nf - 1), then those before and behind them.
+struct Order {
+  int t0, f0, nf, nt;
+  __device__ Order(const Args& a, const Seq& s, const Span& x, int64_t r0, int64_t r1, int R) {
+    // whole: ends by the first query's row and begins behind the last one's window
+    const int first = s.kv - s.T + (int)(r0 / a.G), cut = s.kv - s.T + (int)(r1 / a.G) - a.window;
+    t0 = x.t0;
+    nt = x.t1 - x.t0;
+    f0 = min(a.window && cut >= 0 ? max(x.t0, cut / R + 1) : x.t0, x.t1);
+    nf = max(min(x.t1, first < 0 ? 0 : (first + 1) / R) - f0, 0);
+  }
+  __device__ int tile(int n) const { return n < nf ? f0 + n : n - nf < f0 - t0 ? t0 + n - nf : t0 + n; }
+};
+
 // element (row r, d .. d + 3) of a wave's staged 32 x D fp32 rows: 16-byte
 // pieces permuted by row
 template <int D> __device__ __forceinline__ lds_f4* stage_at(lds_char* st, int r, int d) {
@@ -395,42 +462,48 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
   if (a.cu && nr <= 32 && a.T * (int64_t)a.G > 32) return;  // attn_row_kernel's
   const int64_t r1 = min(r0 + NW * 32, nr) - 1;
   const Span x = span_of(a, s, r0, r1, R, split);
-  // cache rows of the first and (with a window) the last query
-  const int first = s.kv - s.T + (int)(r0 / a.G), last = a.window ? s.kv - s.T + (int)(r1 / a.G) : INT_MIN / 2;
   Wave<D> w;
   w.init(a, s, kvh, r0 + wave * 32);
   const Loader<D> ld;
   lds_char* const base = (lds_char*)ring;
-  auto issue = [&](int t, int pid) {
-    const int row0 = t * R + wave * 16;
-    const uint32_t at = (uint32_t)(uintptr_t)(base + (t & 1) * 2 * IMG + wave * 16 * D * 2);
+  const Order ord(a, s, x, r0, r1, R);
+  const int nf = ord.nf, nt = ord.nt;
+  auto tile = [&](int n) { return ord.tile(n); };
+  auto page = [&](int n) { return n < nt ? Loader<D>::page(a, b, tile(n) * R + wave * 16, x.hi) : -1; };
+  auto issue = [&](int n, int pid) {
+    const int row0 = tile(n) * R + wave * 16;
+    const uint32_t at = (uint32_t)(uintptr_t)(base + (n & 1) * 2 * IMG + wave * 16 * D * 2);
     ld.load(a, a.k, false, pid, kvh, row0, x.lo, x.hi, at);
     ld.load(a, a.v, true, pid, kvh, row0, x.lo, x.hi, at + IMG);
   };
-  if (x.t0 < x.t1) issue(x.t0, Loader<D>::page(a, b, x.t0 * R + wave * 16, x.hi));
-  int pid = x.t0 + 1 < x.t1 ? Loader<D>::page(a, b, (x.t0 + 1) * R + wave * 16, x.hi) : -1;
-  for (int t = x.t0; t < x.t1; ++t) {
-    // every wave's transfers of tile t have landed, and every wave has left tile t - 1
+  if (nt > 0) issue(0, page(0));
+  int pid = page(1);
+  auto next = [&](int n) {
+    // every wave's transfers of tile n have landed, and every wave has left tile n - 1
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (t + 1 < x.t1) {
-      issue(t + 1, pid);
-      pid = Loader<D>::page(a, b, (t + 2) * R + wave * 16, x.hi);
+    if (n + 1 < nt) {
+      issue(n + 1, pid);
+      pid = page(n + 2);
     }
-    lds_char* const k = base + (t & 1) * 2 * IMG;
+    return base + (n & 1) * 2 * IMG;
+  };
+  for (int n = 0; n < nf; ++n) {
+    const lds_char* k = next(n);
+    w.template full<2>(a, k, k + IMG);
+  }
+  for (int n = nf; n < nt; ++n) {
+    lds_char* const k = next(n);
     lds_char* const v = k + IMG;
-    // some rows of the tile are some queries' only (the same answer in every wave)
-    bool odd = false;
-    if ((t + 1) * R - 1 > first || t * R <= last - a.window)
-      odd = __syncthreads_or(odd_part(v + wave * (IMG / 4), IMG / 4));
+    const bool odd = __syncthreads_or(odd_part(v + wave * (IMG / 4), IMG / 4));
     f16_t s2[2];
-    const bool live = w.template weights<2>(a, k, t * R, s2);
+    const bool live = w.template part<2>(a, k, tile(n) * R, s2);
     if (odd) {
-      if (live) w.template by_row<2>(s2, v, t * R);
+      if (live) w.template by_row<2>(s2, v, tile(n) * R);
       __syncthreads();
       clean_part(v + wave * (IMG / 4), IMG / 4);
       __syncthreads();
     }
-    if (live) w.template values<2>(s2, v);
+    if (live) w.template values<2, false>(a, v, s2, 0.f);
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   // O through LDS (each wave its own rows) so that whole rows leave
@@ -490,29 +563,42 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_row_kernel(Args a) {
     ld.load(a, a.v, true, p0, kvh, t * R, x.lo, x.hi, at + IMG);
     ld.load(a, a.v, true, p1, kvh, t * R + 16, x.lo, x.hi, at + IMG + 16 * D * 2);
   };
-  auto page = [&](int t, int h) { return t < x.t1 ? Loader<D>::page(a, b, t * R + 16 * h, x.hi) : -1; };
-  int t = x.t0 + wave, par = 0;
-  if (t < x.t1) issue(t, 0, page(t, 0), page(t, 1));
-  int p0 = page(t + NW, 0), p1 = page(t + NW, 1);
-  for (; t < x.t1; t += NW, par ^= 1) {
-    if (t + NW < x.t1) {
-      issue(t + NW, par ^ 1, p0, p1);
-      p0 = page(t + 2 * NW, 0), p1 = page(t + 2 * NW, 1);
+  const Order ord(a, s, x, 0, nr - 1, R);
+  const int nf = ord.nf, nt = ord.nt;
+  auto page = [&](int n, int h) { return n < nt ? Loader<D>::page(a, b, ord.tile(n) * R + 16 * h, x.hi) : -1; };
+  int par = 0, p0 = -1, p1 = -1;
+  // tile n has landed, and the wave's next one is on its way into the other buffer
+  auto next = [&](int n) {
+    if (n + NW < nt) {
+      issue(ord.tile(n + NW), par ^ 1, p0, p1);
+      p0 = page(n + 2 * NW, 0), p1 = page(n + 2 * NW, 1);
       asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NT) : "memory");
     } else {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
     lds_char* const k = base + par * 2 * IMG;
+    par ^= 1;
+    return k;
+  };
+  if (wave < nt) issue(ord.tile(wave), 0, page(wave, 0), page(wave, 1));
+  p0 = page(wave + NW, 0), p1 = page(wave + NW, 1);
+  int n = wave;
+  for (; n < nf; n += NW) {
+    const lds_char* k = next(n);
+    w.template full<1>(a, k, k + IMG);
+  }
+  for (; n < nt; n += NW) {
+    lds_char* const k = next(n);
     lds_char* const v = k + IMG;
     f16_t s1[1];
-    if (!w.template weights<1>(a, k, t * R, s1)) continue;
-    if (w.in_part(t * R, R) && odd_part(v, IMG)) {
-      w.template by_row<1>(s1, v, t * R);
+    if (!w.template part<1>(a, k, ord.tile(n) * R, s1)) continue;
+    if (odd_part(v, IMG)) {
+      w.template by_row<1>(s1, v, ord.tile(n) * R);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       clean_part(v, IMG);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
-    w.template values<1>(s1, v);
+    w.template values<1, false>(a, v, s1, 0.f);
   }
   // join the waves: O and (m, l) of each in LDS
   const int c = lane & 31, g = lane >> 5;
@@ -563,12 +649,14 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_row_kernel(Args a) {
   }
 }
 
-// Adds up the pieces of every row.  Rows no sequence owns stay as they are.
-template <int D, typename OUT>
+// Adds up the pieces of every row, SG lane groups a row.  Rows no sequence owns
+// stay as they are.
+template <int D, int SG, typename OUT>
 __global__ __launch_bounds__(256) void attn_join_kernel(Args a) {
-  constexpr int LPR = D / 4, RPB = 256 / LPR;
-  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
-  const int d = (threadIdx.x % LPR) * 4;
+  constexpr int LPR = D / 4, RPB = 256 / (LPR * SG);
+  const int d = (threadIdx.x % LPR) * 4, sg = threadIdx.x / LPR % SG;
+  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / (LPR * SG);
+  bool own = row < a.rows;
   if (a.cu) {
     // the sequence of the block's first token, then on from there
     const int64_t t0 = (int64_t)blockIdx.x * RPB / a.H;
@@ -579,28 +667,42 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Args a) {
       n += c;
       if (c < 256) break;
     }
-    if (row >= a.rows) return;
     const int64_t t = row / a.H;
     int b = max(n - 1, 0);
     while (b + 1 < a.B && a.cu[b + 1] <= t) ++b;
     int64_t tok0;
     int T;
     clamp_span(a.cu[b], a.cu[b + 1], a.T, a.total, tok0, T);
-    if (t < tok0 || t >= tok0 + T) return;
-  } else if (row >= a.rows) {
-    return;
+    own = own && t >= tok0 && t < tok0 + T;
   }
   float m = -INFINITY, l = 0.f;
   f4_t sum = zero4();
-  for (int s = 0; s < a.nsplit; ++s) {
-    const float2 ml = a.part_ml[s * a.rows + row];
-    const f4_t v = *reinterpret_cast<const f4_t*>(a.part_o + (s * a.rows + row) * D + d);
-    const float mn = fmaxf(m, ml.x);
-    const float f = m == -INFINITY ? 1.f : fast_exp2(m - mn), h = ml.x == -INFINITY ? 1.f : fast_exp2(ml.x - mn);
+  auto add = [&](float pm, float pl, f4_t v) {
+    const float mn = fmaxf(m, pm);
+    const float f = m == -INFINITY ? 1.f : fast_exp2(m - mn), h = pm == -INFINITY ? 1.f : fast_exp2(pm - mn);
     m = mn;
-    l = fmaf(l, f, ml.y * h);
+    l = fmaf(l, f, pl * h);
     sum = sum * f + v * h;
+  };
+  if (own) {
+#pragma unroll 4
+    for (int s = sg; s < a.nsplit; s += SG) {
+      const float2 ml = a.part_ml[s * a.rows + row];
+      add(ml.x, ml.y, *reinterpret_cast<const f4_t*>(a.part_o + (s * a.rows + row) * D + d));
+    }
   }
+  if constexpr (SG > 1) {
+    __shared__ f4_t so[SG][RPB * LPR];
+    __shared__ float2 sml[SG][RPB];
+    const int r = threadIdx.x / (LPR * SG), at = r * LPR + threadIdx.x % LPR;
+    so[sg][at] = sum;
+    if (d == 0) sml[sg][r] = make_float2(m, l);
+    __syncthreads();
+    if (sg) return;
+#pragma unroll
+    for (int i = 1; i < SG; ++i) add(sml[i][r].x, sml[i][r].y, so[i][at]);
+  }
+  if (!own) return;
   const float f = l == 0.f ? 0.f : 1.f / l;
   if (d == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + fast_log2(l)) * LN2;
   store4((OUT*)a.o + row * D + d, sum * f);
@@ -638,24 +740,40 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(Args a) {
     o[k] = zero4();
   }
   float m = -INFINITY, l = 0.f;
+  // Tile t + 1 is on its way into registers while tile t is used: the two pages
+  // of its 32 rows are known a tile before that.
+  constexpr int PER = R * (D / 4) / 256;
+  float4 kn[PER], vn[PER];
+  auto fetch = [&](int t, int p0, int p1) {
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int e = u * 256 + threadIdx.x, rr = e / (D / 4), d = (e % (D / 4)) * 4, j = t * R + rr;
+      const int pid = rr < 16 ? p0 : p1;
+      kn[u] = vn[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j >= x.lo && j < x.hi && pid >= 0 && pid < a.num_pages) {
+        const int64_t at = pid * a.page_stride + (((int64_t)kvh << a.pshift) + (j & ((1 << a.pshift) - 1))) * D + d;
+        kn[u] = *reinterpret_cast<const float4*>((const float*)a.k + at);
+        vn[u] = *reinterpret_cast<const float4*>((const float*)a.v + at);
+      }
+    }
+  };
+  auto page = [&](int t, int h) { return t < x.t1 ? Loader<D>::page(a, b, t * R + 16 * h, x.hi) : -1; };
+  if (x.t0 < x.t1) fetch(x.t0, page(x.t0, 0), page(x.t0, 1));
+  int p0 = page(x.t0 + 1, 0), p1 = page(x.t0 + 1, 1);
   for (int t = x.t0; t < x.t1; ++t) {
     __syncthreads();
     bool bad = false;
-    for (int e = threadIdx.x; e < R * (D / 4); e += 256) {
-      const int rr = e / (D / 4), d = (e % (D / 4)) * 4, j = t * R + rr;
-      float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
-      if (j >= x.lo && j < x.hi) {
-        const int pid = a.table[(int64_t)b * a.max_pages + (j >> a.pshift)];
-        if (pid >= 0 && pid < a.num_pages) {
-          const int64_t at =
-              pid * a.page_stride + (((int64_t)kvh << a.pshift) + (j & ((1 << a.pshift) - 1))) * D + d;
-          kx = *reinterpret_cast<const float4*>((const float*)a.k + at);
-          vx = *reinterpret_cast<const float4*>((const float*)a.v + at);
-        }
-      }
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int e = u * 256 + threadIdx.x, rr = e / (D / 4), d = (e % (D / 4)) * 4;
+      const float4 kx = kn[u], vx = vn[u];
       bad |= !(isfinite(vx.x) && isfinite(vx.y) && isfinite(vx.z) && isfinite(vx.w));
       *reinterpret_cast<float4*>(sk + rr * LD + d) = kx;
       *reinterpret_cast<float4*>(sv + rr * LD + d) = vx;
+    }
+    if (t + 1 < x.t1) {
+      fetch(t + 1, p0, p1);
+      p0 = page(t + 2, 0), p1 = page(t + 2, 1);
     }
     const bool slow = __syncthreads_or(bad);
     f4_t y[2];
@@ -765,12 +883,31 @@ Plan plan(const AttnCall& c) {
   p.tiles = f32 || per > 32;
   p.rows = !f32 && (per <= 32 || (c.packed && c.total < (int64_t)c.B * c.T));
   p.slots = c.packed ? c.total * G / R + c.B : c.B * cdiv(per, R);
-  // Pieces of the cache range: enough workgroups for the chip, none shorter
-  // than a few tiles.
-  const int64_t units = (p.tiles ? p.slots : c.B) * c.Hkv;
-  const int64_t range = c.window ? std::min<int64_t>(c.max_kv, c.window + (p.tiles ? R / G : 0)) : c.max_kv;
-  const int64_t want = cdiv(p.tiles ? 1024 : 512, units), most = cdiv(range, p.tiles ? 512 : 128);
-  p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 128));
+  if (!p.tiles || f32) {
+    // Decode and fp32: enough workgroups for ragged lengths to even out (2048;
+    // at B = 64, up to 64K rows: 512 took 580 us, 1024 478, 2048 443, 4096 465),
+    // none shorter than one tile of each wave.
+    const int64_t units = (p.tiles ? p.slots : c.B) * c.Hkv;
+    const int64_t range = c.window ? std::min<int64_t>(c.max_kv, c.window + c.T) : c.max_kv;
+    const int64_t want = cdiv(f32 ? 1024 : 2048, units), most = cdiv(range, f32 ? 64 : 128);
+    p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 128));
+    return p;
+  }
+  // Tiles: the least of the rounds the pieces take on the chip's workgroup
+  // slots (tiles of 64 rows and some 4 tiles' worth of start and end each, 2.2
+  // us a tile at D = 128) plus the join's traffic.  At 2K new tokens on 64K
+  // rows (192 units): 6 pieces 1119 us, 8 (three whole rounds) 975, 16 1108;
+  // an 8K prompt (1024 units): 1 piece 290 us, 2 331.
+  const double units = (double)p.slots * c.Hkv, resident = 256 * (c.D == 64 ? 3 : c.D == 128 ? 2 : 1);
+  const double tiles = (double)cdiv(c.window ? std::min<int64_t>(c.max_kv, c.window + R / G) : c.max_kv, 64);
+  const double us = 2.2 * c.D / 128 * (resident / 512), rows = (double)c.total * c.H;
+  double best = 0;
+  p.nsplit = 1;
+  for (int n = 1; n <= 64 && n <= std::max(tiles / 4, 1.0); ++n) {
+    const double t = std::ceil(units * n / resident) * (tiles / n + 4) * us +
+                     (n > 1 ? 5 + rows * c.D * 8 * n / 5e6 : 0);
+    if (n == 1 || t < best) best = t, p.nsplit = n;
+  }
   return p;
 }
 
@@ -784,8 +921,10 @@ hipError_t launch(const AttnCall& c, const Plan& p, const Args& a, hipStream_t s
     if (p.tiles) attn_tile_kernel<D, OUT><<<dim3((unsigned)(p.slots * combos)), dim3(256), 0, stream>>>(a);
     if (p.rows) attn_row_kernel<D, NW, OUT><<<dim3((unsigned)(c.B * combos)), dim3(NW * 64), 0, stream>>>(a);
   }
-  if (p.nsplit > 1)
-    attn_join_kernel<D, OUT><<<dim3((unsigned)cdiv(a.rows, 256 / (D / 4))), dim3(256), 0, stream>>>(a);
+  // many pieces: a workgroup a row, its lane groups sharing the pieces
+  constexpr int SG = 256 / (D / 4);
+  if (p.nsplit > 8) attn_join_kernel<D, SG, OUT><<<dim3((unsigned)a.rows), dim3(256), 0, stream>>>(a);
+  else if (p.nsplit > 1) attn_join_kernel<D, 1, OUT><<<dim3((unsigned)cdiv(a.rows, SG)), dim3(256), 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -794,7 +933,7 @@ hipError_t launch(const AttnCall& c, const Plan& p, const Args& a, hipStream_t s
 int64_t attn_workgroups(const AttnCall& c) {
   const Plan p = plan(c);
   const int64_t units = std::max<int64_t>(p.tiles ? p.slots : 0, p.rows ? c.B : 0);
-  return std::max<int64_t>(units * c.Hkv * p.nsplit, cdiv(c.total * c.H, 4));
+  return std::max<int64_t>(units * c.Hkv * p.nsplit, c.total * c.H);
 }
 
 size_t attn_workspace_bytes(const AttnCall& c) {

@@ -250,8 +250,8 @@ __global__ __launch_bounds__(256) void rope_kernel(Args a) {
 }
 
 template <int D, typename IO, typename GR>
-__global__ __launch_bounds__(256) void rope_backward_kernel(Args a) {
-  constexpr int L = D / 8, GROUPS = 256 / L;
+__global__ __launch_bounds__(256, 3) void rope_backward_kernel(Args a) {
+  constexpr int L = D / 8, GROUPS = 256 / L, U = sizeof(IO) + sizeof(GR) > 4 ? 2 : UNROLL;
   const RopeCall& c = a.c;
   const int lane = lane_id(), s = lane % L, group = threadIdx.x / L;
   const int from = (lane & ~(L - 1)) + partner<D>(c, s);
@@ -266,18 +266,18 @@ __global__ __launch_bounds__(256) void rope_backward_kernel(Args a) {
     const Turn turn = turn_of<D>(c, s, c.positions[t]);
     const IO* q = (const IO*)c.q + t * c.q_stride + 8 * s;
     const IO* k = (const IO*)c.k + t * c.k_stride + 8 * s;
-    for (int h = h0; h < h1; h += UNROLL) {
-      Raw<IO> x[UNROLL];
-      Raw<GR> y[UNROLL];
+    for (int h = h0; h < h1; h += U) {
+      Raw<IO> x[U];
+      Raw<GR> y[U];
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
+      for (int u = 0; u < U; ++u) {
         const int i = min(h + u, h1 - 1);
         x[u] = load8(i < c.H ? q + (int64_t)i * D : k + (int64_t)(i - c.H) * D);
         y[u] = load8(i < c.H ? (const GR*)c.dq_out + (t * c.H + i) * D + 8 * s
                              : (const GR*)c.dk_out + (t * c.Hkv + i - c.H) * D + 8 * s);
       }
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
+      for (int u = 0; u < U; ++u) {
         const int i = h + u;
         if (i >= h1) break;
         const bool key = i >= c.H;
@@ -329,6 +329,7 @@ __global__ __launch_bounds__(1024) void rope_dw_kernel(const float* sums, int n,
   __shared__ float part[32][33];
   const int col = blockIdx.x * 32 + threadIdx.x % 32, y = threadIdx.x / 32;
   float sum = 0.f;
+#pragma unroll 8
   for (int i = y; i < n; i += 32) sum += sums[(int64_t)i * 2 * D + col];
   part[y][threadIdx.x % 32] = sum;
   __syncthreads();
@@ -348,7 +349,7 @@ int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
 Args args_of(const RopeCall& c, int nh) {
   Args a;
   a.c = c;
-  const int64_t groups = 4096 * (512 / c.D);  // lane groups of 4096 waves
+  const int64_t groups = 8192 * (512 / c.D);  // lane groups of 8192 waves
   int64_t parts = std::min<int64_t>(std::max<int64_t>(groups / std::max<int64_t>(c.total, 1), 1), nh);
   a.heads = (int)cdiv(nh, parts);
   a.parts = (int)cdiv(nh, a.heads);
@@ -365,7 +366,7 @@ template <int D, typename IO, typename OUT> hipError_t forward(const RopeCall& c
   return hipGetLastError();
 }
 
-constexpr int BWD_GROUPS = 1024;  // workgroups of the backward pass at most
+constexpr int BWD_GROUPS = 768;  // workgroups of the backward pass at most: 3 a CU reside
 
 int backward_blocks(const Args& a) { return (int)std::min<int64_t>(cdiv(a.units, 256 / (a.c.D / 8)), BWD_GROUPS); }
 

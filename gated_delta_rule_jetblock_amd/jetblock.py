@@ -555,45 +555,55 @@ def _rows(t, name: str):
     return t.data_ptr(), n, stride if n > 1 else 0
 
 
-def _same(dev, **tensors):
-    """Every tensor on device `dev`; those with a dtype to match, of that dtype."""
-    for name, (t, dtype) in tensors.items():
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name}: expected a torch.Tensor")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, q on {dev}")
-        if t.dtype != dtype:
-            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+def _same(di, *groups):
+    """Every tensor of each (dtype, names, tensors) group of that dtype and on device di."""
+    for dtype, names, tensors in groups:
+        for t in tensors:
+            if t is not None and (t.dtype is not dtype or t.get_device() != di):
+                name = names.split()[[x is t for x in tensors].index(True)]
+                if t.dtype is not dtype:
+                    raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+                raise ValueError(f"{name} is on {t.device}, q on cuda:{di}")
 
 
 def _flat(t, name: str, *shape):
     """Pointer of a contiguous tensor of the given shape (None: no pointer)."""
     if t is None:
         return None
-    if tuple(t.shape) != shape or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor of shape {shape}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _on(dev, stream):
-    """The stream to launch on, and whether `dev` has to be made current for it."""
-    if dev.type != "cuda":
-        raise ValueError("libjetblock takes device tensors; got a tensor on " + str(dev))
+# the handle of a device's current stream (the public accessor builds a Stream object, 2 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda di: torch.cuda.current_stream(di).cuda_stream)
+
+
+def _device(q) -> int:
+    if not q.is_cuda:
+        raise ValueError("libjetblock takes device tensors; got a tensor on " + str(q.device))
+    return q.get_device()
+
+
+def _launch(di: int, stream, fn, *args):
+    """fn(*args, stream) on device di: the given stream, or the device's current one."""
     if stream is None:
-        handle = torch.cuda.current_stream(dev).cuda_stream
+        handle = _raw_stream(di)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    return handle, dev.index is not None and dev.index != torch.cuda.current_device()
-
-
-def _launch(dev, other: bool, fn, *args):
-    if other:
-        with torch.cuda.device(dev):
-            _check(fn(*args))
+    if di == torch.cuda.current_device():
+        _check(fn(*args, handle))
     else:
-        _check(fn(*args))
+        with torch.cuda.device(di):
+            _check(fn(*args, handle))
+
+
+def _empty(like, dtype):
+    """An uninitialised contiguous tensor of `like`'s shape and device."""
+    if dtype is like.dtype and like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(like.shape, dtype=dtype, device=like.device)
 
 
 def _rope_flags(interleaved, normalize):
@@ -605,11 +615,10 @@ def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, *, eps=1e-6, inter
     """jb_qk_norm_rope.  q [tokens,H,D] or [B,T,H,D], k likewise with Hkv heads (any distance
     between tokens), positions int32 [tokens], inv_freq f32 [rot/2], wq, wk [D].  Returns
     (q_out, k_out), contiguous, of out_dtype (default: q's)."""
-    dev, io = q.device, q.dtype
-    handle, other = _on(dev, stream)
+    di, io = _device(q), q.dtype
     out_dtype = out_dtype or (q_out.dtype if q_out is not None else io)
-    _same(dev, k=(k, io), wq=(wq, io), wk=(wk, io), positions=(positions, torch.int32),
-          inv_freq=(inv_freq, torch.float32), q_out=(q_out, out_dtype), k_out=(k_out, out_dtype))
+    _same(di, (io, "k wq wk", (k, wq, wk)), (torch.int32, "positions", (positions,)),
+          (torch.float32, "inv_freq", (inv_freq,)), (out_dtype, "q_out k_out", (q_out, k_out)))
     H, D = q.shape[-2:]
     Hkv = k.shape[-2]
     qp, n, qs = _rows(q, "q")
@@ -617,14 +626,14 @@ def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, *, eps=1e-6, inter
     if nk != n or k.shape[-1] != D:
         raise ValueError(f"k {tuple(k.shape)} does not go with q {tuple(q.shape)}")
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=out_dtype, device=dev)
+        q_out = _empty(q, out_dtype)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=out_dtype, device=dev)
+        k_out = _empty(k, out_dtype)
     shape = AttnShape(1, n, H, Hkv, D, 2 * inv_freq.numel(), 0, 0, 0, 0, 0, _io_code(q), _code(out_dtype),
                       _rope_flags(interleaved, normalize), qs, ks, 0, 0)
-    _launch(dev, other, _lib.jb_qk_norm_rope, shape, qp, kp, _flat(wq, "wq", D), _flat(wk, "wk", D),
+    _launch(di, stream, _lib.jb_qk_norm_rope, shape, qp, kp, _flat(wq, "wq", D), _flat(wk, "wk", D),
             _flat(inv_freq, "inv_freq", inv_freq.numel()), _flat(positions.reshape(-1), "positions", n), eps,
-            _flat(q_out, "q_out", *q.shape), _flat(k_out, "k_out", *k.shape), handle)
+            _flat(q_out, "q_out", *q.shape), _flat(k_out, "k_out", *k.shape))
     return q_out, k_out
 
 
@@ -639,18 +648,18 @@ def qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, wq=None, wk
     """jb_qk_norm_rope_backward: gradients of qk_norm_rope from those of its outputs (contiguous,
     bf16 or f32).  Returns dict(dq, dk, dwq, dwk): dq, dk of dq_out's dtype, dwq, dwk f32 [D]
     (None without the norm)."""
-    dev, io, gr = q.device, q.dtype, dq_out.dtype
-    handle, other = _on(dev, stream)
-    _same(dev, k=(k, io), wq=(wq, io), wk=(wk, io), positions=(positions, torch.int32),
-          inv_freq=(inv_freq, torch.float32), dq_out=(dq_out, gr), dk_out=(dk_out, gr), dq=(dq, gr), dk=(dk, gr))
+    di, dev, io, gr = _device(q), q.device, q.dtype, dq_out.dtype
+    _same(di, (io, "k wq wk", (k, wq, wk)), (torch.int32, "positions", (positions,)),
+          (torch.float32, "inv_freq", (inv_freq,)), (gr, "dq_out dk_out dq dk", (dq_out, dk_out, dq, dk)),
+          (torch.uint8, "ws", (ws,)))
     H, D = q.shape[-2:]
     Hkv = k.shape[-2]
     qp, n, qs = _rows(q, "q")
     kp, nk, ks = _rows(k, "k")
     if nk != n or k.shape[-1] != D:
         raise ValueError(f"k {tuple(k.shape)} does not go with q {tuple(q.shape)}")
-    dq = torch.empty(q.shape, dtype=gr, device=dev) if dq is None else dq
-    dk = torch.empty(k.shape, dtype=gr, device=dev) if dk is None else dk
+    dq = _empty(q, gr) if dq is None else dq
+    dk = _empty(k, gr) if dk is None else dk
     dwq = dwk = None
     if normalize:
         dwq = torch.empty(D, dtype=torch.float32, device=dev)
@@ -659,10 +668,10 @@ def qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, wq=None, wk
                       _rope_flags(interleaved, normalize), qs, ks, 0, 0)
     if ws is None:
         ws = workspace(qk_norm_rope_backward_workspace_size(shape), dev)
-    _launch(dev, other, _lib.jb_qk_norm_rope_backward, shape, qp, kp, _flat(wq, "wq", D), _flat(wk, "wk", D),
+    _launch(di, stream, _lib.jb_qk_norm_rope_backward, shape, qp, kp, _flat(wq, "wq", D), _flat(wk, "wk", D),
             _flat(inv_freq, "inv_freq", inv_freq.numel()), _flat(positions.reshape(-1), "positions", n), eps,
             _flat(dq_out, "dq_out", *q.shape), _flat(dk_out, "dk_out", *k.shape), _flat(dq, "dq", *q.shape),
-            _flat(dk, "dk", *k.shape), _flat(dwq, "dwq", D), _flat(dwk, "dwk", D), ws.data_ptr(), ws.numel(), handle)
+            _flat(dk, "dk", *k.shape), _flat(dwq, "dwq", D), _flat(dwk, "dwk", D), ws.data_ptr(), ws.numel())
     return dict(dq=dq, dk=dk, dwq=dwq, dwk=dwk)
 
 
@@ -699,11 +708,10 @@ def qk_norm_rope_paged(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq,
     [pages,Hkv,page,D] (in place).  q [B,T,H,D], [B,H,D] (one token each) or packed [tokens,H,D]
     with cu_seqlens int32 [B+1]; page_table int32 [B,max_pages], kv_lens int32 [B] (the new tokens
     among the rows).  Returns dict(q, k_cache, v_cache)."""
-    dev, io, i32 = q.device, q.dtype, torch.int32
-    handle, other = _on(dev, stream)
-    _same(dev, k=(k, io), v=(v, io), k_cache=(k_cache, io), v_cache=(v_cache, io), wq=(wq, io), wk=(wk, io),
-          page_table=(page_table, i32), kv_lens=(kv_lens, i32), cu_seqlens=(cu_seqlens, i32),
-          positions=(positions, i32), inv_freq=(inv_freq, torch.float32), q_out=(q_out, io))
+    di, io = _device(q), q.dtype
+    _same(di, (io, "k v k_cache v_cache wq wk q_out", (k, v, k_cache, v_cache, wq, wk, q_out)),
+          (torch.int32, "page_table kv_lens cu_seqlens positions", (page_table, kv_lens, cu_seqlens, positions)),
+          (torch.float32, "inv_freq", (inv_freq,)))
     H, D = q.shape[-2:]
     qp, n, qs = _rows(q, "q")
     kp, nk, ks = _rows(k, "k")
@@ -713,16 +721,16 @@ def qk_norm_rope_paged(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq,
     if nk != n or nv != n or k.shape[-2:] != (Hkv, D) or v.shape[-2:] != (Hkv, D):
         raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} do not go with q {tuple(q.shape)} and the caches")
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=io, device=dev)
+        q_out = _empty(q, io)
     code = _io_code(q)
     shape = AttnShape(B, T, H, Hkv, D, 2 * inv_freq.numel(), page, max_pages, P, 0, 0, code, code,
                       _rope_flags(interleaved, normalize), qs, ks, vs, ps)
-    _launch(dev, other, _lib.jb_qk_norm_rope_paged, shape, n,
+    _launch(di, stream, _lib.jb_qk_norm_rope_paged, shape, n,
             None if cu_seqlens is None else _flat(cu_seqlens, "cu_seqlens", B + 1), _flat(kv_lens, "kv_lens", B),
             _flat(page_table, "page_table", B, max_pages), qp, kp, vp, _flat(wq, "wq", D), _flat(wk, "wk", D),
             _flat(inv_freq, "inv_freq", inv_freq.numel()),
             None if positions is None else _flat(positions.reshape(-1), "positions", n), eps,
-            _flat(q_out, "q_out", *q.shape), k_cache.data_ptr(), v_cache.data_ptr(), handle)
+            _flat(q_out, "q_out", *q.shape), k_cache.data_ptr(), v_cache.data_ptr())
     return dict(q=q_out, k_cache=k_cache, v_cache=v_cache)
 
 
@@ -741,29 +749,29 @@ def attn_paged(q, k_cache, v_cache, page_table, kv_lens, *, cu_seqlens=None, max
     integers, are the longest sequence's new tokens (packed; default: all) and cache rows (default:
     the table's capacity); they plan the launch, nothing is read back from the device.  Returns
     dict(o, lse): o of q's shape and out_dtype (default: q's), lse f32 [..., H] or None."""
-    dev, io, i32 = q.device, q.dtype, torch.int32
-    handle, other = _on(dev, stream)
+    di, io = _device(q), q.dtype
     out_dtype = out_dtype or (o.dtype if o is not None else io)
-    _same(dev, k_cache=(k_cache, io), v_cache=(v_cache, io), page_table=(page_table, i32), kv_lens=(kv_lens, i32),
-          cu_seqlens=(cu_seqlens, i32), o=(o, out_dtype), lse=(lse, torch.float32), ws=(ws, torch.uint8))
+    _same(di, (io, "k_cache v_cache", (k_cache, v_cache)),
+          (torch.int32, "page_table kv_lens cu_seqlens", (page_table, kv_lens, cu_seqlens)),
+          (out_dtype, "o", (o,)), (torch.float32, "lse", (lse,)), (torch.uint8, "ws", (ws,)))
     H, D = q.shape[-2:]
     qp, n, qs = _rows(q, "q")
     B, T = _batch(q, cu_seqlens, max_seqlen)
     P, Hkv, page, ps, max_pages = _pages(k_cache, v_cache, page_table, kv_lens, B, D)
     if o is None:
-        o = torch.empty(q.shape, dtype=out_dtype, device=dev)
+        o = _empty(q, out_dtype)
     if lse is None and want_lse:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
     packed = cu_seqlens is not None
     shape = AttnShape(B, T, H, Hkv, D, 0, page, max_pages, P, 0 if max_kv is None else int(max_kv), int(window),
                       _io_code(q), _code(out_dtype), 0, qs, 0, 0, ps)
     if ws is None:
         need = attn_paged_workspace_size(shape, n, packed)
         if need:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _launch(dev, other, _lib.jb_attn_paged, shape, n, _flat(cu_seqlens, "cu_seqlens", B + 1),
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _launch(di, stream, _lib.jb_attn_paged, shape, n, _flat(cu_seqlens, "cu_seqlens", B + 1),
             _flat(kv_lens, "kv_lens", B), _flat(page_table, "page_table", B, max_pages), qp, k_cache.data_ptr(),
             v_cache.data_ptr(), 0.0 if scale is None else float(scale), _flat(o, "o", *q.shape),
             _flat(lse, "lse", *q.shape[:-1]), None if ws is None else ws.data_ptr(),
-            0 if ws is None else ws.numel(), handle)
+            0 if ws is None else ws.numel())
     return dict(o=o, lse=lse)

@@ -159,10 +159,11 @@ def test_binding_refuses_what_does_not_fit(jb):
                  (kc[:1].expand(5, 2, 16, 64), kc[:1].expand(5, 2, 16, 64), table, kv, 3, 64)):
         with pytest.raises(ValueError):
             jb._pages(*args)
-    with pytest.raises(TypeError):
-        jb._same(q.device, kv_lens=(kv.long(), torch.int32))
-    with pytest.raises(ValueError):
-        jb._same(q.device, k=(torch.zeros(1, device="meta"), torch.float32))
+    jb._same(-1, (bf, "k v", (k, None)), (torch.int32, "kv_lens", (kv,)))
+    with pytest.raises(TypeError, match="kv_lens: expected torch.int32"):
+        jb._same(-1, (bf, "k v", (k, None)), (torch.int32, "table kv_lens", (table, kv.long())))
+    with pytest.raises(ValueError, match="v is on cpu"):
+        jb._same(0, (bf, "k v", (None, k)))
     with pytest.raises(TypeError):
         jb._code(torch.float16)
     with pytest.raises(ValueError):
