@@ -131,34 +131,74 @@ template <int D> struct Img {
   __device__ static int fv(int r) { return PR < 16 ? (r & 3) << 1 : (r & 3) << 2; }
 };
 
-// 16 cache rows from row0 (a multiple of 16) of one key head into LDS.
+// 16 rows of an image (1 KB a transfer) from a buffer descriptor: transfers i =
+// 0 .. 3 of 1 KB each; the instruction's offset counts for the buffer and LDS.
+__device__ __forceinline__ void dma4(v4i_t desc, int v0, int v1, int v2, int v3, uint32_t lds) {
+  uint32_t saved;
+  asm volatile(
+      "s_nop 4\n\ts_mov_b32 %0, m0\n\ts_mov_b32 m0, %6\n\ts_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %5, 0 offen lds\n\t"
+      "buffer_load_dwordx4 %2, %5, 0 offen offset:1024 lds\n\t"
+      "buffer_load_dwordx4 %3, %5, 0 offen offset:2048 lds\n\t"
+      "buffer_load_dwordx4 %4, %5, 0 offen offset:(1024*3) lds\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "v"(v0), "v"(v1), "v"(v2), "v"(v3), "s"(desc), "s"(lds)
+      : "memory");
+}
+__device__ __forceinline__ void dma2(v4i_t desc, int v0, int v1, uint32_t lds) {
+  uint32_t saved;
+  asm volatile(
+      "s_nop 4\n\ts_mov_b32 %0, m0\n\ts_mov_b32 m0, %4\n\ts_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %3, 0 offen lds\n\t"
+      "buffer_load_dwordx4 %2, %3, 0 offen offset:1024 lds\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "v"(v0), "v"(v1), "s"(desc), "s"(lds)
+      : "memory");
+}
+
+// Cache rows, 16 at a time, of one sequence and key head into LDS images.
 template <int D> struct Loader {
   using I = Img<D>;
   static constexpr int N = I::PR / 4;  // 1 KB transfers for 16 rows
-  int vk[N], vv[N];
-  __device__ Loader() {
+  int vk[N], vv;                       // byte in the rows, less i KB, of transfer i (the same for V's)
+  const bf16_t *k, *v;
+  const_int_p table;
+  __device__ Loader(const Args& a, int b, int kvh) {
     const int lane = lane_id();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int s = i * 64 + lane, r = s / I::PR, c = s % I::PR;
-      vk[i] = r * I::ROWB + ((c ^ I::fk(r)) * 16);
-      vv[i] = r * I::ROWB + ((c ^ I::fv(r)) * 16);
+      const int r = lane / I::PR, c = lane % I::PR;
+      vk[i] = r * I::ROWB + ((c ^ I::fk(i * 64 / I::PR + r)) * 16);
     }
+    vv = (lane / I::PR) * I::ROWB + ((lane % I::PR ^ I::fv(lane / I::PR)) * 16);
+    k = (const bf16_t*)a.k + ((int64_t)kvh << a.pshift) * D;
+    v = (const bf16_t*)a.v + ((int64_t)kvh << a.pshift) * D;
+    table = (const_int_p)a.table + (int64_t)b * a.max_pages;
   }
   // page index for row0 (loaded a tile ahead of its use)
-  static __device__ int page(const Args& a, int b, int row0, int hi) {
-    return row0 < hi ? ((const_int_p)a.table)[(int64_t)b * a.max_pages + (row0 >> a.pshift)] : -1;
-  }
-  __device__ void load(const Args& a, const void* cache, bool value, int pid, int kvh, int row0, int lo, int hi,
-                       uint32_t lds) const {
-    int n = min(hi - row0, 16);
-    if (pid < 0 || pid >= a.num_pages || row0 + 16 <= lo || n < 0) n = 0, pid = 0;
-    const int in_page = row0 & ((1 << a.pshift) - 1);
-    const bf16_t* p = (const bf16_t*)cache + pid * a.page_stride + ((int64_t)kvh << a.pshift) * D + in_page * D;
-    const v4i_t desc = buf_desc(p, (uint32_t)n * I::ROWB);
+  __device__ int page(const Args& a, int row0, int hi) const { return row0 < hi ? table[row0 >> a.pshift] : -1; }
+  // rows row0 .. row0 + 15 (row0 a multiple of 16) of K and V; zeros from row hi on
+  __device__ void load(const Args& a, int pid, int row0, int hi, uint32_t ldsk, uint32_t ldsv) const {
+    const bool ok = (unsigned)pid < (unsigned)a.num_pages;
+    const int n = ok ? min(max(hi - row0, 0), 16) : 0;
+    const int64_t at = (ok ? pid : 0) * a.page_stride + (row0 & ((1 << a.pshift) - 1)) * D;
+    const int bytes = n * I::ROWB;
+    if constexpr (N == 2) {
+      dma2(buf_desc(k + at, bytes), vk[0], vk[1], ldsk);
+      dma2(buf_desc(v + at, bytes), vv, vv, ldsv);
+    } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) dma16(desc, value ? vv[i] : vk[i], 0, lds + i * 1024);
+      for (int i = 0; i < N; i += 4) {  // (a descriptor for 4 KB: its range check sees every offset)
+        const int left = max(bytes - i * 1024, 0);
+        dma4(buf_desc(k + at + i * 512, left), vk[i], vk[i + 1], vk[i + 2], vk[i + 3], ldsk + i * 1024);
+        dma4(buf_desc(v + at + i * 512, left), vv, vv ^ fv_flip(1), vv, vv ^ fv_flip(1), ldsv + i * 1024);
+      }
+    }
   }
+  // D = 256: a transfer holds 2 rows, so V's piece order takes turns
+  static constexpr int fv_flip(int i) { return D == 256 && i ? (2 << 2) * 16 : 0; }
 };
 
 __device__ __forceinline__ f16_t mfma32(bf16x8_t a, bf16x8_t b, f16_t c) {
@@ -211,28 +251,29 @@ template <int D> struct Wave {
     l = 0.f;
   }
 
-  // S^T of NB x 32 cache rows, their K image at lk
+  // S^T of NB x 32 cache rows, their K image at lk; K fragments are read
+  // AHEAD steps before their products.
   template <int NB> __device__ void scores(const lds_char* lk, f16_t (&s)[NB]) const {
     const int lane = lane_id(), c = lane & 31, g = lane >> 5;
     const int kb = c * I::ROWB + ((g ^ I::fk(c)) << 4);
-    constexpr int AHEAD = 4;  // steps whose fragments are on their way
-    bf16x8_t f[D / 16][NB];
+    constexpr int AHEAD = 4, STEPS = D / 16;
+    bf16x8_t f[STEPS][NB];
     f16_t z;
 #pragma unroll
     for (int e = 0; e < 16; ++e) z[e] = 0.f;
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k)
+    auto read = [&](int k) {
 #pragma unroll
       for (int n = 0; n < NB; ++n) f[k][n] = *(const lds_bf16x8*)(lk + (kb ^ (k << 5)) + n * 32 * I::ROWB);
+    };
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k)
+    for (int k = 0; k < AHEAD; ++k) read(k);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+      if (k + AHEAD < STEPS) read(k + AHEAD);
 #pragma unroll
       for (int n = 0; n < NB; ++n) s[n] = mfma32(f[k][n], q[k], k ? s[n] : z);
-    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD * NB, 0);
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      __builtin_amdgcn_sched_group_barrier(0x8, NB, 0);
-      if (k + AHEAD < D / 16) __builtin_amdgcn_sched_group_barrier(0x100, NB, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 
@@ -260,13 +301,13 @@ template <int D> struct Wave {
     return m == -INFINITY ? 0.f : m;
   }
 
-  // Weights from scores; O^T += V^T P^T, 16 cache rows at a time: the
-  // exponentials of the next 16 go between the products of these.
-  template <int NB> __device__ void weights(const Args& a, f16_t (&s)[NB], float ms, int k) {
+  // weights of elements e0 .. e0 + n - 1 of the 16-row step k from its scores
+  template <int NB> __device__ void weights(const Args& a, f16_t (&s)[NB], float ms, int k, int e0 = 0, int n = 8) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      s[k >> 1][8 * (k & 1) + e] = fast_exp2(fmaf(s[k >> 1][8 * (k & 1) + e], a.scale, -ms));
-      l += s[k >> 1][8 * (k & 1) + e];
+    for (int e = e0; e < e0 + n; ++e) {
+      const float x = fast_exp2(fmaf(s[k >> 1][8 * (k & 1) + e], a.scale, -ms));
+      s[k >> 1][8 * (k & 1) + e] = x;
+      l += x;
     }
   }
 
@@ -296,45 +337,37 @@ template <int D> struct Wave {
     for (int k = 0; k < 2 * NB; ++k) weights<NB>(a, s, ms, k);
     return true;
   }
-  // O^T += V^T P^T; EXP: s holds scores yet
+  // O^T += V^T P^T, 16 cache rows a step.  EXP: s holds scores yet; the next
+  // step's exponentials and reads go between the products of this one.
   template <int NB, bool EXP> __device__ void values(const Args& a, const lds_char* lv, f16_t (&s)[NB], float ms) {
     const int lane = lane_id(), g = lane >> 5;
     const int n16 = lane & 15, row = 4 * g + (n16 >> 2), pc = 2 * ((lane >> 4) & 1) + ((n16 & 3) >> 1);
     const int vb = row * I::ROWB + ((pc ^ I::fv(row)) << 4) + (n16 & 1) * 8;
-    constexpr int DB = D / 32;
-    if constexpr (EXP) weights<NB>(a, s, ms, 0);
+    constexpr int DB = D / 32, STEPS = 2 * NB, PART = 8 / DB;
+    bf16x8_t v[2][DB];
+    auto read = [&](int k, int db) {
+      const lds_char* at = lv + (vb ^ (db << 6)) + k * 16 * I::ROWB;
+      const s4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)at);
+      const s4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(at + 8 * I::ROWB));
+      v[k & 1][db] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
 #pragma unroll
-    for (int k = 0; k < 2 * NB; ++k) {
-      bf16x8_t w, v[DB];
+    for (int db = 0; db < DB; ++db) read(0, db);
+    if constexpr (EXP) weights<NB>(a, s, ms, 0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+      bf16x8_t w;
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = (__bf16)s[k >> 1][8 * (k & 1) + e];
 #pragma unroll
       for (int db = 0; db < DB; ++db) {
-        const lds_char* at = lv + (vb ^ (db << 6)) + k * 16 * I::ROWB;
-        const s4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)at);
-        const s4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(at + 8 * I::ROWB));
-        v[db] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        if (k + 1 < STEPS) read(k + 1, db);
+        o[db] = mfma32(v[k & 1][db], w, o[db]);
+        if constexpr (EXP)
+          if (k + 1 < STEPS) weights<NB>(a, s, ms, k + 1, db * PART, PART);
+        __builtin_amdgcn_sched_barrier(0);
       }
-#pragma unroll
-      for (int db = 0; db < DB; ++db) o[db] = mfma32(v[db], w, o[db]);
-      if constexpr (EXP)
-        if (k + 1 < 2 * NB) weights<NB>(a, s, ms, k + 1);
-    }
-    if constexpr (EXP) {
-      // the first step's reads and weights, then between any two products the
-      // reads and a part of the weights (28 instructions) of the next step
-      __builtin_amdgcn_sched_group_barrier(0x100, 2 * DB, 0);
-      __builtin_amdgcn_sched_group_barrier(0x2, 28, 0);
-#pragma unroll
-      for (int k = 0; k < 2 * NB; ++k)
-#pragma unroll
-        for (int db = 0; db < DB; ++db) {
-          __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-          if (k + 1 < 2 * NB) {
-            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-            __builtin_amdgcn_sched_group_barrier(0x2, 28 / DB, 0);
-          }
-        }
     }
   }
 
@@ -464,17 +497,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
   const Span x = span_of(a, s, r0, r1, R, split);
   Wave<D> w;
   w.init(a, s, kvh, r0 + wave * 32);
-  const Loader<D> ld;
+  const Loader<D> ld(a, b, kvh);
   lds_char* const base = (lds_char*)ring;
   const Order ord(a, s, x, r0, r1, R);
   const int nf = ord.nf, nt = ord.nt;
   auto tile = [&](int n) { return ord.tile(n); };
-  auto page = [&](int n) { return n < nt ? Loader<D>::page(a, b, tile(n) * R + wave * 16, x.hi) : -1; };
+  auto page = [&](int n) { return n < nt ? ld.page(a, tile(n) * R + wave * 16, x.hi) : -1; };
   auto issue = [&](int n, int pid) {
     const int row0 = tile(n) * R + wave * 16;
     const uint32_t at = (uint32_t)(uintptr_t)(base + (n & 1) * 2 * IMG + wave * 16 * D * 2);
-    ld.load(a, a.k, false, pid, kvh, row0, x.lo, x.hi, at);
-    ld.load(a, a.v, true, pid, kvh, row0, x.lo, x.hi, at + IMG);
+    ld.load(a, pid, row0, x.hi, at, at + IMG);
   };
   if (nt > 0) issue(0, page(0));
   int pid = page(1);
@@ -552,20 +584,18 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_row_kernel(Args a) {
   const Span x = span_of(a, s, 0, nr - 1, R, split);
   Wave<D> w;
   w.init(a, s, kvh, 0);
-  const Loader<D> ld;
+  const Loader<D> ld(a, b, kvh);
   lds_char* const base = (lds_char*)ring + wave * 4 * IMG;
   constexpr int NT = 4 * Loader<D>::N;  // transfers a tile
   auto issue = [&](int t, int par, int p0, int p1) {
     const uint32_t at = (uint32_t)(uintptr_t)(base + par * 2 * IMG);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's reads of the buffer are done
-    ld.load(a, a.k, false, p0, kvh, t * R, x.lo, x.hi, at);
-    ld.load(a, a.k, false, p1, kvh, t * R + 16, x.lo, x.hi, at + 16 * D * 2);
-    ld.load(a, a.v, true, p0, kvh, t * R, x.lo, x.hi, at + IMG);
-    ld.load(a, a.v, true, p1, kvh, t * R + 16, x.lo, x.hi, at + IMG + 16 * D * 2);
+    ld.load(a, p0, t * R, x.hi, at, at + IMG);
+    ld.load(a, p1, t * R + 16, x.hi, at + 16 * D * 2, at + IMG + 16 * D * 2);
   };
   const Order ord(a, s, x, 0, nr - 1, R);
   const int nf = ord.nf, nt = ord.nt;
-  auto page = [&](int n, int h) { return n < nt ? Loader<D>::page(a, b, ord.tile(n) * R + 16 * h, x.hi) : -1; };
+  auto page = [&](int n, int h) { return n < nt ? ld.page(a, ord.tile(n) * R + 16 * h, x.hi) : -1; };
   int par = 0, p0 = -1, p1 = -1;
   // tile n has landed, and the wave's next one is on its way into the other buffer
   auto next = [&](int n) {
@@ -757,7 +787,10 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(Args a) {
       }
     }
   };
-  auto page = [&](int t, int h) { return t < x.t1 ? Loader<D>::page(a, b, t * R + 16 * h, x.hi) : -1; };
+  auto page = [&](int t, int h) {
+    const int j = t * R + 16 * h;
+    return t < x.t1 && j < x.hi ? ((const_int_p)a.table)[(int64_t)b * a.max_pages + (j >> a.pshift)] : -1;
+  };
   if (x.t0 < x.t1) fetch(x.t0, page(x.t0, 0), page(x.t0, 1));
   int p0 = page(x.t0 + 1, 0), p1 = page(x.t0 + 1, 1);
   for (int t = x.t0; t < x.t1; ++t) {
