@@ -164,7 +164,8 @@ template <int D> struct Loader {
   static constexpr int N = I::PR / 4;  // 1 KB transfers for 16 rows
   int vk[N], vv;                       // byte in the rows, less i KB, of transfer i (the same for V's)
   const bf16_t *k, *v;
-  const_int_p table;
+  const int* table;
+  int e0, ents;                        // table entries e0 + lane
   __device__ Loader(const Args& a, int b, int kvh) {
     const int lane = lane_id();
 #pragma unroll
@@ -175,12 +176,23 @@ template <int D> struct Loader {
     vv = (lane / I::PR) * I::ROWB + ((lane % I::PR ^ I::fv(lane / I::PR)) * 16);
     k = (const bf16_t*)a.k + ((int64_t)kvh << a.pshift) * D;
     v = (const bf16_t*)a.v + ((int64_t)kvh << a.pshift) * D;
-    table = (const_int_p)a.table + (int64_t)b * a.max_pages;
+    table = a.table + (int64_t)b * a.max_pages;
+    e0 = -64;
   }
-  // page index for row0 (loaded a tile ahead of its use)
-  __device__ int page(const Args& a, int row0, int hi) const { return row0 < hi ? table[row0 >> a.pshift] : -1; }
+  // Page index of row0 < hi <= max_pages * page.  64 entries of the table wait
+  // in a register, so that hardly any tile waits for one.
+  __device__ int page(const Args& a, int row0) {
+    const int e = row0 >> a.pshift;
+    if ((unsigned)(e - e0) >= 64u) {
+      e0 = e;
+      ents = table[min(e + lane_id(), a.max_pages - 1)];
+      asm volatile("" : "+v"(ents));  // waited for here
+    }
+    return __builtin_amdgcn_readlane(ents, e - e0);
+  }
   // rows row0 .. row0 + 15 (row0 a multiple of 16) of K and V; zeros from row hi on
-  __device__ void load(const Args& a, int pid, int row0, int hi, uint32_t ldsk, uint32_t ldsv) const {
+  __device__ void load(const Args& a, int row0, int hi, uint32_t ldsk, uint32_t ldsv) {
+    const int pid = row0 < hi ? page(a, row0) : -1;
     const bool ok = (unsigned)pid < (unsigned)a.num_pages;
     const int n = ok ? min(max(hi - row0, 0), 16) : 0;
     const int64_t at = (ok ? pid : 0) * a.page_stride + (row0 & ((1 << a.pshift) - 1)) * D;
@@ -243,6 +255,10 @@ template <int D> struct Wave {
       if (real) w = *reinterpret_cast<const uint4*>(src + 16 * k);
       q[k] = __builtin_bit_cast(bf16x8_t, w);
     }
+    // here, not in the loop, is where the loads are waited for (a wait there
+    // would be one for the transfers in flight)
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) asm volatile("" : "+v"(q[k]));
 #pragma unroll
     for (int db = 0; db < D / 32; ++db)
 #pragma unroll
@@ -497,26 +513,21 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
   const Span x = span_of(a, s, r0, r1, R, split);
   Wave<D> w;
   w.init(a, s, kvh, r0 + wave * 32);
-  const Loader<D> ld(a, b, kvh);
+  Loader<D> ld(a, b, kvh);
   lds_char* const base = (lds_char*)ring;
   const Order ord(a, s, x, r0, r1, R);
   const int nf = ord.nf, nt = ord.nt;
   auto tile = [&](int n) { return ord.tile(n); };
-  auto page = [&](int n) { return n < nt ? ld.page(a, tile(n) * R + wave * 16, x.hi) : -1; };
-  auto issue = [&](int n, int pid) {
+  auto issue = [&](int n) {
     const int row0 = tile(n) * R + wave * 16;
     const uint32_t at = (uint32_t)(uintptr_t)(base + (n & 1) * 2 * IMG + wave * 16 * D * 2);
-    ld.load(a, pid, row0, x.hi, at, at + IMG);
+    ld.load(a, row0, x.hi, at, at + IMG);
   };
-  if (nt > 0) issue(0, page(0));
-  int pid = page(1);
+  if (nt > 0) issue(0);
   auto next = [&](int n) {
     // every wave's transfers of tile n have landed, and every wave has left tile n - 1
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (n + 1 < nt) {
-      issue(n + 1, pid);
-      pid = page(n + 2);
-    }
+    if (n + 1 < nt) issue(n + 1);
     return base + (n & 1) * 2 * IMG;
   };
   for (int n = 0; n < nf; ++n) {
@@ -584,24 +595,22 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_row_kernel(Args a) {
   const Span x = span_of(a, s, 0, nr - 1, R, split);
   Wave<D> w;
   w.init(a, s, kvh, 0);
-  const Loader<D> ld(a, b, kvh);
+  Loader<D> ld(a, b, kvh);
   lds_char* const base = (lds_char*)ring + wave * 4 * IMG;
   constexpr int NT = 4 * Loader<D>::N;  // transfers a tile
-  auto issue = [&](int t, int par, int p0, int p1) {
+  auto issue = [&](int t, int par) {
     const uint32_t at = (uint32_t)(uintptr_t)(base + par * 2 * IMG);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's reads of the buffer are done
-    ld.load(a, p0, t * R, x.hi, at, at + IMG);
-    ld.load(a, p1, t * R + 16, x.hi, at + 16 * D * 2, at + IMG + 16 * D * 2);
+    ld.load(a, t * R, x.hi, at, at + IMG);
+    ld.load(a, t * R + 16, x.hi, at + 16 * D * 2, at + IMG + 16 * D * 2);
   };
   const Order ord(a, s, x, 0, nr - 1, R);
   const int nf = ord.nf, nt = ord.nt;
-  auto page = [&](int n, int h) { return n < nt ? ld.page(a, ord.tile(n) * R + 16 * h, x.hi) : -1; };
-  int par = 0, p0 = -1, p1 = -1;
+  int par = 0;
   // tile n has landed, and the wave's next one is on its way into the other buffer
   auto next = [&](int n) {
     if (n + NW < nt) {
-      issue(ord.tile(n + NW), par ^ 1, p0, p1);
-      p0 = page(n + 2 * NW, 0), p1 = page(n + 2 * NW, 1);
+      issue(ord.tile(n + NW), par ^ 1);
       asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NT) : "memory");
     } else {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -610,8 +619,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_row_kernel(Args a) {
     par ^= 1;
     return k;
   };
-  if (wave < nt) issue(ord.tile(wave), 0, page(wave, 0), page(wave, 1));
-  p0 = page(wave + NW, 0), p1 = page(wave + NW, 1);
+  if (wave < nt) issue(ord.tile(wave), 0);
   int n = wave;
   for (; n < nf; n += NW) {
     const lds_char* k = next(n);
