@@ -60,8 +60,16 @@ typedef const __attribute__((address_space(4))) int* const_int_p;
 
 constexpr float LN2 = 0.6931471805599453f;
 
+// the unit (sequence, key head) that begins in a run and goes on in the `more`
+// next ones; seg: its place among the run's units, 0 the first, 1 any other
+struct Shared {
+  int b, kvh, more, seg;
+};
+
 struct Args {
   int B, T, H, Hkv, G, pshift, max_pages, num_pages, window, nsplit;
+  bool few;                                    // attn_row_kernel takes sequences of at most 32 rows
+  bool direct;                                 // a unit of those is a workgroup
   int64_t total, rows, q_stride, page_stride;  // rows: total H
   const int* cu;                               // NULL: dense, B x T tokens
   const int* kv_lens;
@@ -71,6 +79,9 @@ struct Args {
   float* lse;
   float* part_o;   // [nsplit][rows][D]
   float2* part_ml; // [nsplit][rows]
+  float* run_o;    // [2 a workgroup][32][D]: attn_row_kernel's shared units
+  float2* run_ml;  // [2 a workgroup][32]
+  Shared* shared;  // [workgroups]
   float scale;     // times log2 e
 };
 
@@ -327,12 +338,16 @@ template <int D> struct Wave {
     }
   }
 
-  // A tile that every query sees whole
+  // A tile that every query sees whole.  The vector work goes before the other
+  // wave's products: at equal priority 2K tokens on 64K rows took 782 us and an
+  // 8K prompt 289, so 766 and 267.
   template <int NB> __device__ void full(const Args& a, const lds_char* lk, const lds_char* lv) {
     f16_t s[NB];
     scores<NB>(lk, s);
+    __builtin_amdgcn_s_setprio(1);
     const float ms = take_max<NB>(a, s);
     values<NB, true>(a, lv, s, ms);
+    __builtin_amdgcn_s_setprio(0);
   }
 
   // NB x 32 cache rows from j0 that some queries see in part; false: none sees any
@@ -508,7 +523,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
   const Seq s = seq_of(a, b);
   const int64_t nr = (int64_t)s.T * a.G;
   if (r0 < 0 || r0 >= nr) return;  // (r0 < 0: offsets that decrease)
-  if (a.cu && nr <= 32 && a.T * (int64_t)a.G > 32) return;  // attn_row_kernel's
+  if (a.few && nr <= 32) return;  // attn_row_kernel's
   const int64_t r1 = min(r0 + NW * 32, nr) - 1;
   const Span x = span_of(a, s, r0, r1, R, split);
   Wave<D> w;
@@ -581,110 +596,251 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
   }
 }
 
-// At most 32 query rows: the waves share them and split the cache.
+// Decode: sequences of at most 32 query rows.  A unit is one key head of one
+// such sequence; it walks its cache in steps of NW tiles, one a wave.  The steps
+// of all units, end to end, are cut into one equal run for each workgroup (the
+// chip's worth of them), so that ragged lengths leave no workgroup waiting; a
+// run's first and last units may be shared with its neighbours.
+// The lengths live in device memory: every workgroup adds them up itself, and
+// says which shared unit begins in its run.
+__device__ __forceinline__ int steps_of(const Args& a, const Seq& s, int rows_a_step) {
+  const int64_t nr = (int64_t)s.T * a.G;
+  if (nr == 0 || nr > 32) return 0;  // none, or attn_tile_kernel's
+  const int hi = s.kv, lo = a.window ? min(max(s.kv - s.T - a.window + 1, 0), hi) : 0;
+  // (a sequence without rows has its output to write)
+  return max((hi + rows_a_step - 1) / rows_a_step - lo / rows_a_step, 1);
+}
+
 template <int D, int NW, typename OUT>
 __global__ __launch_bounds__(NW * 64, 1) void attn_row_kernel(Args a) {
-  constexpr int R = 32, IMG = R * D * 2;
+  constexpr int R = 32, IMG = R * D * 2, STEP = R * NW, NTHR = NW * 64;
   __shared__ __attribute__((aligned(1024))) char ring[NW * 4 * IMG];
+  __shared__ int64_t found[2];
+  __shared__ int sums[NW];
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int combo = blockIdx.x % (unsigned)(a.Hkv * a.nsplit), kvh = combo % a.Hkv, split = combo / a.Hkv;
-  const int b = blockIdx.x / (unsigned)(a.Hkv * a.nsplit);
-  const Seq s = seq_of(a, b);
-  const int64_t nr = (int64_t)s.T * a.G;
-  if (nr == 0 || nr > 32) return;  // none, or attn_tile_kernel's
-  const Span x = span_of(a, s, 0, nr - 1, R, split);
-  Wave<D> w;
-  w.init(a, s, kvh, 0);
-  Loader<D> ld(a, b, kvh);
-  lds_char* const base = (lds_char*)ring + wave * 4 * IMG;
+  int b;
+  int64_t at, end, start;  // this run's steps, and the first sequence's first one
+  int64_t run_steps = 0;
+  if (a.direct) {         // many units: each is a run
+    b = blockIdx.x / (unsigned)a.Hkv;
+    const int n = steps_of(a, seq_of(a, b), STEP);
+    start = 0;
+    at = (int64_t)(blockIdx.x % (unsigned)a.Hkv) * n;
+    end = at + n;
+  } else {
+    // steps of 64 NW sequences at a time, added up; then this run's place
+    int64_t all = 0;
+    for (int i = 0; i < a.B; i += NTHR) {
+      int v = i + (int)threadIdx.x < a.B ? steps_of(a, seq_of(a, i + threadIdx.x), STEP) : 0;
+#pragma unroll
+      for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, WAVE);
+      if (lane == 0) sums[wave] = v;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < NW; ++w) all += sums[w];
+      __syncthreads();
+    }
+    all *= a.Hkv;
+    const int64_t per = (all + gridDim.x - 1) / gridDim.x;
+    at = min(blockIdx.x * per, all);
+    end = min(at + per, all);
+    if (threadIdx.x == 0) found[0] = found[1] = 0;
+    int64_t base = 0;
+    for (int i = 0; i < a.B; i += NTHR) {
+      const int n = i + (int)threadIdx.x < a.B ? steps_of(a, seq_of(a, i + threadIdx.x), STEP) : 0;
+      int v = n;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(v, o, WAVE);
+        if (lane >= o) v += u;
+      }
+      if (lane == 63) sums[wave] = v;
+      __syncthreads();
+      int64_t before = base + (int64_t)(v - n) * a.Hkv;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        if (w < wave) before += (int64_t)sums[w] * a.Hkv;
+        base += (int64_t)sums[w] * a.Hkv;
+      }
+      if (before <= at && at < before + (int64_t)n * a.Hkv) found[0] = i + threadIdx.x, found[1] = before;
+      __syncthreads();
+    }
+    b = uniform((int)found[0]);
+    start = found[1];
+    run_steps = per;
+  }
+  Shared shared = {0, 0, 0, 0};
+
   constexpr int NT = 4 * Loader<D>::N;  // transfers a tile
-  auto issue = [&](int t, int par) {
-    const uint32_t at = (uint32_t)(uintptr_t)(base + par * 2 * IMG);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's reads of the buffer are done
-    ld.load(a, t * R, x.hi, at, at + IMG);
-    ld.load(a, t * R + 16, x.hi, at + 16 * D * 2, at + IMG + 16 * D * 2);
-  };
-  const Order ord(a, s, x, 0, nr - 1, R);
-  const int nf = ord.nf, nt = ord.nt;
-  int par = 0;
-  // tile n has landed, and the wave's next one is on its way into the other buffer
-  auto next = [&](int n) {
-    if (n + NW < nt) {
-      issue(ord.tile(n + NW), par ^ 1);
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NT) : "memory");
-    } else {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  lds_char* const base = (lds_char*)ring + wave * 4 * IMG;
+  for (int seg = 0; at < end && b < a.B; seg = 1) {
+    const Seq s = seq_of(a, b);
+    const int steps = steps_of(a, s, STEP);
+    if (steps == 0) {  // (only behind a sequence that has some)
+      ++b;
+      continue;
     }
-    lds_char* const k = base + par * 2 * IMG;
-    par ^= 1;
-    return k;
-  };
-  if (wave < nt) issue(ord.tile(wave), 0);
-  int n = wave;
-  for (; n < nf; n += NW) {
-    const lds_char* k = next(n);
-    w.template full<1>(a, k, k + IMG);
-  }
-  for (; n < nt; n += NW) {
-    lds_char* const k = next(n);
-    lds_char* const v = k + IMG;
-    f16_t s1[1];
-    if (!w.template part<1>(a, k, ord.tile(n) * R, s1)) continue;
-    if (odd_part(v, IMG)) {
-      w.template by_row<1>(s1, v, ord.tile(n) * R);
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      clean_part(v, IMG);
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const int kvh = uniform((int)((at - start) / steps)), s0 = uniform((int)(at - start - (int64_t)kvh * steps));
+    const int s1 = uniform((int)min((int64_t)steps, s0 + end - at));
+    if (kvh >= a.Hkv) break;  // (lengths that changed meanwhile)
+    const int nr = (int)(s.T * a.G);
+    Span x;
+    x.hi = max(s.kv, 0);
+    x.lo = a.window ? min(max(s.kv - s.T - a.window + 1, 0), x.hi) : 0;
+    const int n0 = x.lo / STEP * NW;
+    x.t0 = max(n0 + s0 * NW, x.lo / R);
+    x.t1 = min(n0 + s1 * NW, (x.hi + R - 1) / R);
+    Wave<D> w;
+    w.init(a, s, kvh, 0);
+    Loader<D> ld(a, b, kvh);
+    auto issue = [&](int t, int par) {
+      const uint32_t to = (uint32_t)(uintptr_t)(base + par * 2 * IMG);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's reads of the buffer are done
+      ld.load(a, t * R, x.hi, to, to + IMG);
+      ld.load(a, t * R + 16, x.hi, to + 16 * D * 2, to + IMG + 16 * D * 2);
+    };
+    const Order ord(a, s, x, 0, nr - 1, R);
+    const int nf = ord.nf, nt = ord.nt;
+    int par = 0;
+    // tile n has landed, and the wave's next one is on its way into the other buffer
+    auto next = [&](int n) {
+      if (n + NW < nt) {
+        issue(ord.tile(n + NW), par ^ 1);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NT) : "memory");
+      } else {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      }
+      lds_char* const k = base + par * 2 * IMG;
+      par ^= 1;
+      return k;
+    };
+    if (wave < nt) issue(ord.tile(wave), 0);
+    int n = wave;
+    for (; n < nf; n += NW) {
+      const lds_char* k = next(n);
+      w.template full<1>(a, k, k + IMG);
     }
-    w.template values<1, false>(a, v, s1, 0.f);
-  }
-  // join the waves: O and (m, l) of each in LDS
-  const int c = lane & 31, g = lane >> 5;
-  const float l = w.l + other_half(w.l);
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  lds_char* const all = (lds_char*)ring;
-  constexpr int ST = 32 * D * 4;
-  static_assert(NW * ST + NW * 32 * 8 <= NW * 4 * IMG, "staging fits");
-  lds_char* st = all + wave * ST;
-#pragma unroll
-  for (int db = 0; db < D / 32; ++db)
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      *stage_at<D>(st, c, 32 * db + 8 * e + 4 * g) =
-          f4_t{w.o[db][4 * e], w.o[db][4 * e + 1], w.o[db][4 * e + 2], w.o[db][4 * e + 3]};
-  lds_float* ml = (lds_float*)(all + NW * ST);  // [2][NW][32]
-  if (g == 0) {
-    ml[wave * 32 + c] = w.m;
-    ml[NW * 32 + wave * 32 + c] = l;
-  }
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  constexpr int LPR = D / 4;
-  for (int i = threadIdx.x / LPR; i < nr; i += NW * 64 / LPR) {
-    const int d = (threadIdx.x % LPR) * 4;
-    float m = -INFINITY;
-#pragma unroll
-    for (int n = 0; n < NW; ++n) m = fmaxf(m, ml[n * 32 + i]);
-    f4_t sum = zero4();
-    float lt = 0.f;
-#pragma unroll
-    for (int n = 0; n < NW; ++n) {
-      const float mn = ml[n * 32 + i];
-      // (a wave that saw nothing holds zeros, or NaN that stays)
-      const float f = mn == -INFINITY ? 1.f : fast_exp2(mn - m);
-      const f4_t v = *stage_at<D>(all + n * ST, i, d);
-      lt = fmaf(ml[NW * 32 + n * 32 + i], f, lt);
-      sum += v * f;
+    for (; n < nt; n += NW) {
+      lds_char* const k = next(n);
+      lds_char* const v = k + IMG;
+      f16_t s1[1];
+      if (!w.template part<1>(a, k, ord.tile(n) * R, s1)) continue;
+      if (odd_part(v, IMG)) {
+        w.template by_row<1>(s1, v, ord.tile(n) * R);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        clean_part(v, IMG);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      }
+      w.template values<1, false>(a, v, s1, 0.f);
     }
-    const int64_t at = out_row(a, s, kvh, i);
-    if (a.nsplit > 1) {
-      if (d == 0) a.part_ml[split * a.rows + at] = make_float2(m, lt);
-      *reinterpret_cast<f4_t*>(a.part_o + (split * a.rows + at) * D + d) = sum;
-    } else {
-      const float f = lt == 0.f ? 0.f : 1.f / lt;
-      if (d == 0 && a.lse) a.lse[at] = lt == 0.f ? -INFINITY : (m + fast_log2(lt)) * LN2;
-      store4((OUT*)a.o + at * D + d, sum * f);
+    // join the waves: O and (m, l) of each in LDS
+    const int c = lane & 31, g = lane >> 5;
+    const float l = w.l + other_half(w.l);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    lds_char* const all = (lds_char*)ring;
+    constexpr int ST = 32 * D * 4;
+    static_assert(NW * ST + NW * 32 * 8 <= NW * 4 * IMG, "staging fits");
+    lds_char* st = all + wave * ST;
+#pragma unroll
+    for (int db = 0; db < D / 32; ++db)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *stage_at<D>(st, c, 32 * db + 8 * e + 4 * g) =
+            f4_t{w.o[db][4 * e], w.o[db][4 * e + 1], w.o[db][4 * e + 2], w.o[db][4 * e + 3]};
+    lds_float* ml = (lds_float*)(all + NW * ST);  // [2][NW][32]
+    if (g == 0) {
+      ml[wave * 32 + c] = w.m;
+      ml[NW * 32 + wave * 32 + c] = l;
     }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    const bool whole = s0 == 0 && s1 == steps;
+    if (s0 == 0 && !whole) shared = {b, kvh, (int)((at + steps - 1) / run_steps) - (int)blockIdx.x, seg};
+    const int64_t slot = 2 * (int64_t)blockIdx.x + seg;
+    constexpr int LPR = D / 4;
+    for (int i = threadIdx.x / LPR; i < nr; i += NTHR / LPR) {
+      const int d = (threadIdx.x % LPR) * 4;
+      float m = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < NW; ++n) m = fmaxf(m, ml[n * 32 + i]);
+      f4_t sum = zero4();
+      float lt = 0.f;
+#pragma unroll
+      for (int n = 0; n < NW; ++n) {
+        const float mn = ml[n * 32 + i];
+        // (a wave that saw nothing holds zeros, or NaN that stays)
+        const float f = mn == -INFINITY ? 1.f : fast_exp2(mn - m);
+        const f4_t v = *stage_at<D>(all + n * ST, i, d);
+        lt = fmaf(ml[NW * 32 + n * 32 + i], f, lt);
+        sum += v * f;
+      }
+      if (!whole) {
+        if (d == 0) a.run_ml[slot * 32 + i] = make_float2(m, lt);
+        *reinterpret_cast<f4_t*>(a.run_o + (slot * 32 + i) * D + d) = sum;
+      } else {
+        const int64_t to = out_row(a, s, kvh, i);
+        const float f = lt == 0.f ? 0.f : 1.f / lt;
+        if (d == 0 && a.lse) a.lse[to] = lt == 0.f ? -INFINITY : (m + fast_log2(lt)) * LN2;
+        store4((OUT*)a.o + to * D + d, sum * f);
+      }
+    }
+    at += s1 - s0;
+    if (at >= end) break;
+    if (kvh == a.Hkv - 1) start += (int64_t)steps * a.Hkv, ++b;
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the staging is read
   }
+  if (!a.direct && threadIdx.x == 0) a.shared[blockIdx.x] = shared;
+}
+
+// Adds up (m, l, o) pieces in the order they come.
+struct Sum {
+  float m = -INFINITY, l = 0.f;
+  f4_t o = zero4();
+  __device__ void add(float pm, float pl, f4_t v) {
+    const float mn = fmaxf(m, pm);
+    const float f = m == -INFINITY ? 1.f : fast_exp2(m - mn), h = pm == -INFINITY ? 1.f : fast_exp2(pm - mn);
+    m = mn;
+    l = fmaf(l, f, pl * h);
+    o = o * f + v * h;
+  }
+  // over the SG lane groups of a row, the others' part through LDS: the first has all
+  template <int SG, int LPR> __device__ void over(int sg, int r, int d4, f4_t (*so)[256 / SG], float2 (*sml)[256 / SG]) {
+    so[sg][r * LPR + d4] = o;
+    sml[sg][r * LPR + d4] = make_float2(m, l);
+    __syncthreads();
+    if (sg == 0)
+#pragma unroll
+      for (int i = 1; i < SG; ++i) add(sml[i][r * LPR + d4].x, sml[i][r * LPR + d4].y, so[i][r * LPR + d4]);
+  }
+  template <typename OUT, int D> __device__ void store(const Args& a, int64_t row, int d) const {
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    if (d == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + fast_log2(l)) * LN2;
+    store4((OUT*)a.o + row * D + d, o * f);
+  }
+};
+
+// The units that runs share: one workgroup for each query row of the unit that
+// begins in run blockIdx.x / rows, its lane groups sharing the runs.
+template <int D, typename OUT>
+__global__ __launch_bounds__(256) void attn_row_join_kernel(Args a, int rows) {
+  constexpr int LPR = D / 4, SG = 256 / LPR;
+  const int w0 = blockIdx.x / (unsigned)rows, r = blockIdx.x % (unsigned)rows;
+  const Shared u = a.shared[w0];
+  if (u.more == 0) return;
+  const Seq s = seq_of(a, u.b);
+  if (r >= s.T * a.G) return;
+  const int d4 = threadIdx.x % LPR, sg = threadIdx.x / LPR;
+  Sum x;
+#pragma unroll 4
+  for (int i = sg; i <= u.more; i += SG) {
+    // (it is the first unit of every run but the one it begins in)
+    const int64_t at = (2 * (int64_t)(w0 + i) + (i ? 0 : u.seg)) * 32 + r;
+    const float2 ml = a.run_ml[at];
+    x.add(ml.x, ml.y, *reinterpret_cast<const f4_t*>(a.run_o + at * D + d4 * 4));
+  }
+  __shared__ f4_t so[SG][LPR];
+  __shared__ float2 sml[SG][LPR];
+  x.template over<SG, LPR>(sg, 0, d4, so, sml);
+  if (sg == 0) x.template store<OUT, D>(a, out_row(a, s, u.kvh, r), d4 * 4);
 }
 
 // Adds up the pieces of every row, SG lane groups a row.  Rows no sequence owns
@@ -711,39 +867,22 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Args a) {
     int64_t tok0;
     int T;
     clamp_span(a.cu[b], a.cu[b + 1], a.T, a.total, tok0, T);
-    own = own && t >= tok0 && t < tok0 + T;
+    own = own && t >= tok0 && t < tok0 + T && !(a.few && (int64_t)T * a.G <= 32);
   }
-  float m = -INFINITY, l = 0.f;
-  f4_t sum = zero4();
-  auto add = [&](float pm, float pl, f4_t v) {
-    const float mn = fmaxf(m, pm);
-    const float f = m == -INFINITY ? 1.f : fast_exp2(m - mn), h = pm == -INFINITY ? 1.f : fast_exp2(pm - mn);
-    m = mn;
-    l = fmaf(l, f, pl * h);
-    sum = sum * f + v * h;
-  };
+  Sum x;
   if (own) {
 #pragma unroll 4
-    for (int s = sg; s < a.nsplit; s += SG) {
-      const float2 ml = a.part_ml[s * a.rows + row];
-      add(ml.x, ml.y, *reinterpret_cast<const f4_t*>(a.part_o + (s * a.rows + row) * D + d));
+    for (int i = sg; i < a.nsplit; i += SG) {
+      const float2 ml = a.part_ml[i * a.rows + row];
+      x.add(ml.x, ml.y, *reinterpret_cast<const f4_t*>(a.part_o + (i * a.rows + row) * D + d));
     }
   }
   if constexpr (SG > 1) {
     __shared__ f4_t so[SG][RPB * LPR];
-    __shared__ float2 sml[SG][RPB];
-    const int r = threadIdx.x / (LPR * SG), at = r * LPR + threadIdx.x % LPR;
-    so[sg][at] = sum;
-    if (d == 0) sml[sg][r] = make_float2(m, l);
-    __syncthreads();
-    if (sg) return;
-#pragma unroll
-    for (int i = 1; i < SG; ++i) add(sml[i][r].x, sml[i][r].y, so[i][at]);
+    __shared__ float2 sml[SG][RPB * LPR];
+    x.template over<SG, LPR>(sg, threadIdx.x / (LPR * SG), threadIdx.x % LPR, so, sml);
   }
-  if (!own) return;
-  const float f = l == 0.f ? 0.f : 1.f / l;
-  if (d == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + fast_log2(l)) * LN2;
-  store4((OUT*)a.o + row * D + d, sum * f);
+  if (own && sg == 0) x.template store<OUT, D>(a, row, d);
 }
 
 // ------------------------------------------------------------------ fp32 mode
@@ -910,27 +1049,42 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(Args a) {
 struct Plan {
   bool tiles, rows;   // which of the bf16 kernels run
   int64_t slots;      // row tiles, over all sequences
-  int nsplit;
+  int nsplit;         // pieces of their cache ranges
+  bool direct;        // attn_row_kernel: a unit a workgroup
+  int64_t runs;       // its workgroups
+  int rows_a_unit;    // query rows of its units, at most
 };
 
 int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
+size_t a256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+constexpr int row_waves(int D) { return D == 256 ? 2 : 4; }  // of attn_row_kernel: two tiles each in LDS
 
 Plan plan(const AttnCall& c) {
   Plan p;
   const int64_t G = c.H / c.Hkv, per = (int64_t)c.T * G;
   const bool f32 = c.io == IO_F32;
   const int R = f32 ? 64 : 128;
-  // bf16 sequences of at most 32 rows go to attn_row_kernel; a packed batch may hold both kinds
+  // bf16 sequences of at most 32 rows go to attn_row_kernel.  A packed batch may
+  // hold both kinds, and gets both kernels unless the cache range is so short
+  // that a workgroup of the tile kernel walks it while others still work (16
+  // sequences of 1 to 1024 tokens under a window of 1152: 104 us with both
+  // kernels, 93 with one).
+  const int64_t reach = c.window ? std::min(c.max_kv, c.window) : c.max_kv;
   p.tiles = f32 || per > 32;
-  p.rows = !f32 && (per <= 32 || (c.packed && c.total < (int64_t)c.B * c.T));
+  p.rows = !f32 && (per <= 32 || (c.packed && c.total < (int64_t)c.B * c.T && reach > 2048));
   p.slots = c.packed ? c.total * G / R + c.B : c.B * cdiv(per, R);
-  if (!p.tiles || f32) {
-    // Decode and fp32: enough workgroups for ragged lengths to even out (2048;
-    // at B = 64, up to 64K rows: 512 took 580 us, 1024 478, 2048 443, 4096 465),
-    // none shorter than one tile of each wave.
-    const int64_t units = (p.tiles ? p.slots : c.B) * c.Hkv;
-    const int64_t range = c.window ? std::min<int64_t>(c.max_kv, c.window + c.T) : c.max_kv;
-    const int64_t want = cdiv(f32 ? 1024 : 2048, units), most = cdiv(range, f32 ? 64 : 128);
+  p.nsplit = 1;
+  // Decode: as many workgroups as the chip holds, of a step at least; with
+  // thousands of units, or one step each, there is nothing to even out.
+  p.rows_a_unit = (int)std::min<int64_t>(per, 32);
+  const int64_t units = (int64_t)c.B * c.Hkv, range = c.window ? std::min<int64_t>(c.max_kv, c.window + 32) : c.max_kv;
+  const int step = 32 * row_waves(c.D);
+  p.direct = units >= 4096 || range <= step;
+  p.runs = p.direct ? units : std::min<int64_t>(c.D == 64 ? 512 : 256, units * cdiv(range, step));
+  if (!p.tiles) return p;
+  if (f32) {
+    const int64_t want = cdiv(1024, p.slots * c.Hkv), most = cdiv(reach, 64);
     p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 128));
     return p;
   }
@@ -939,17 +1093,32 @@ Plan plan(const AttnCall& c) {
   // us a tile at D = 128) plus the join's traffic.  At 2K new tokens on 64K
   // rows (192 units): 6 pieces 1119 us, 8 (three whole rounds) 975, 16 1108;
   // an 8K prompt (1024 units): 1 piece 290 us, 2 331.
-  const double units = (double)p.slots * c.Hkv, resident = 256 * (c.D == 64 ? 3 : c.D == 128 ? 2 : 1);
+  const double work = (double)p.slots * c.Hkv, resident = 256 * (c.D == 64 ? 3 : c.D == 128 ? 2 : 1);
   const double tiles = (double)cdiv(c.window ? std::min<int64_t>(c.max_kv, c.window + R / G) : c.max_kv, 64);
   const double us = 2.2 * c.D / 128 * (resident / 512), rows = (double)c.total * c.H;
   double best = 0;
-  p.nsplit = 1;
   for (int n = 1; n <= 64 && n <= std::max(tiles / 4, 1.0); ++n) {
-    const double t = std::ceil(units * n / resident) * (tiles / n + 4) * us +
+    const double t = std::ceil(work * n / resident) * (tiles / n + 4) * us +
                      (n > 1 ? 5 + rows * c.D * 8 * n / 5e6 : 0);
     if (n == 1 || t < best) best = t, p.nsplit = n;
   }
   return p;
+}
+
+// workspace: the tile kernels' pieces, then the decode runs'
+struct Layout {
+  size_t part_o, part_ml, run_o, run_ml, shared, bytes;
+};
+Layout layout(const AttnCall& c, const Plan& p) {
+  Layout w = {};
+  const size_t rows = p.nsplit > 1 ? (size_t)c.total * c.H * p.nsplit : 0;
+  const size_t runs = p.rows && !p.direct ? (size_t)p.runs * 2 * 32 : 0;
+  w.part_ml = w.part_o + a256(rows * c.D * sizeof(float));
+  w.run_o = w.part_ml + a256(rows * sizeof(float2));
+  w.run_ml = w.run_o + a256(runs * c.D * sizeof(float));
+  w.shared = w.run_ml + a256(runs * sizeof(float2));
+  w.bytes = w.shared + a256(runs / 64 * sizeof(Shared));
+  return w;
 }
 
 template <int D, typename OUT>
@@ -958,9 +1127,13 @@ hipError_t launch(const AttnCall& c, const Plan& p, const Args& a, hipStream_t s
   if (c.io == IO_F32) {
     attn_f32_kernel<D, OUT><<<dim3((unsigned)(p.slots * combos)), dim3(256), 0, stream>>>(a);
   } else {
-    constexpr int NW = D == 256 ? 2 : 4;
+    constexpr int NW = row_waves(D);
     if (p.tiles) attn_tile_kernel<D, OUT><<<dim3((unsigned)(p.slots * combos)), dim3(256), 0, stream>>>(a);
-    if (p.rows) attn_row_kernel<D, NW, OUT><<<dim3((unsigned)(c.B * combos)), dim3(NW * 64), 0, stream>>>(a);
+    if (p.rows) {
+      attn_row_kernel<D, NW, OUT><<<dim3((unsigned)p.runs), dim3(NW * 64), 0, stream>>>(a);
+      if (!p.direct)
+        attn_row_join_kernel<D, OUT><<<dim3((unsigned)(p.runs * p.rows_a_unit)), dim3(256), 0, stream>>>(a, p.rows_a_unit);
+    }
   }
   // many pieces: a workgroup a row, its lane groups sharing the pieces
   constexpr int SG = 256 / (D / 4);
@@ -973,30 +1146,29 @@ hipError_t launch(const AttnCall& c, const Plan& p, const Args& a, hipStream_t s
 
 int64_t attn_workgroups(const AttnCall& c) {
   const Plan p = plan(c);
-  const int64_t units = std::max<int64_t>(p.tiles ? p.slots : 0, p.rows ? c.B : 0);
-  return std::max<int64_t>(units * c.Hkv * p.nsplit, c.total * c.H);
+  return std::max(std::max(p.tiles ? p.slots * c.Hkv * p.nsplit : 0, c.total * c.H), (int64_t)c.B * c.Hkv * 32);
 }
 
-size_t attn_workspace_bytes(const AttnCall& c) {
-  const Plan p = plan(c);
-  if (p.nsplit == 1) return 0;
-  const size_t rows = (size_t)c.total * c.H * p.nsplit;
-  return ((rows * c.D * sizeof(float) + 255) & ~(size_t)255) + ((rows * sizeof(float2) + 255) & ~(size_t)255);
-}
+size_t attn_workspace_bytes(const AttnCall& c) { return layout(c, plan(c)).bytes; }
 
 hipError_t launch_attn(const AttnCall& c, hipStream_t stream) {
   const Plan p = plan(c);
   Args a;
   a.B = c.B, a.T = c.T, a.H = c.H, a.Hkv = c.Hkv, a.G = c.H / c.Hkv;
   a.pshift = __builtin_ctz((unsigned)c.page), a.max_pages = c.max_pages, a.num_pages = c.num_pages;
-  a.window = c.window, a.nsplit = p.nsplit;
+  a.window = c.window, a.nsplit = p.nsplit, a.few = p.rows;
   a.total = c.total, a.rows = c.total * c.H, a.q_stride = c.q_stride, a.page_stride = c.page_stride;
   a.cu = c.packed ? c.cu_seqlens : nullptr;
   a.kv_lens = c.kv_lens, a.table = c.page_table;
   a.q = c.q, a.k = c.k_cache, a.v = c.v_cache, a.o = c.o, a.lse = c.lse;
-  const size_t rows = (size_t)a.rows * p.nsplit;
-  a.part_o = static_cast<float*>(c.workspace);
-  a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(c.workspace) + ((rows * c.D * sizeof(float) + 255) & ~(size_t)255));
+  const Layout w = layout(c, p);
+  char* ws = static_cast<char*>(c.workspace);
+  a.part_o = reinterpret_cast<float*>(ws + w.part_o);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
+  a.run_o = reinterpret_cast<float*>(ws + w.run_o);
+  a.run_ml = reinterpret_cast<float2*>(ws + w.run_ml);
+  a.shared = reinterpret_cast<Shared*>(ws + w.shared);
+  a.direct = p.direct;
   a.scale = c.scale * 1.4426950408889634f;
   const bool bf = c.out == IO_BF16;
   switch (c.D) {
