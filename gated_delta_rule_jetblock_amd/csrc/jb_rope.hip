@@ -44,29 +44,41 @@ template <> struct Raw<float> {
   static constexpr int N = 8;
   __device__ float get(int i) const { return __uint_as_float(u[i]); }
 };
-template <typename T> __device__ __forceinline__ Raw<T> load8(const T* p) {
+typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
+// NT: a stream that no cache need keep.  Stores of q_out and of training's
+// outputs, and the backward's loads; 64K tokens took 98 and 143 us without,
+// 96 and 133 with (the forward's loads, which gain nothing, stay plain).
+template <bool NT = false, typename T> __device__ __forceinline__ Raw<T> load8(const T* p) {
   Raw<T> r;
 #pragma unroll
   for (int i = 0; i < Raw<T>::N / 4; ++i) {
-    const uint4 w = reinterpret_cast<const uint4*>(p)[i];
-    r.u[4 * i] = w.x, r.u[4 * i + 1] = w.y, r.u[4 * i + 2] = w.z, r.u[4 * i + 3] = w.w;
+    const u4_t* a = reinterpret_cast<const u4_t*>(p) + i;
+    const u4_t w = NT ? __builtin_nontemporal_load(a) : *a;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r.u[4 * i + e] = w[e];
   }
   return r;
+}
+template <bool NT> __device__ __forceinline__ void put4(void* p, u4_t v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, static_cast<u4_t*>(p));
+  else *static_cast<u4_t*>(p) = v;
 }
 template <typename T> __device__ __forceinline__ void store_raw(T* p, const Raw<T>& r) {
 #pragma unroll
   for (int i = 0; i < Raw<T>::N / 4; ++i)
-    reinterpret_cast<uint4*>(p)[i] = make_uint4(r.u[4 * i], r.u[4 * i + 1], r.u[4 * i + 2], r.u[4 * i + 3]);
+    put4<false>(reinterpret_cast<u4_t*>(p) + i, u4_t{r.u[4 * i], r.u[4 * i + 1], r.u[4 * i + 2], r.u[4 * i + 3]});
 }
-__device__ __forceinline__ void store8(float* p, const float (&y)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(y[0], y[1], y[2], y[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(y[4], y[5], y[6], y[7]);
+template <bool NT> __device__ __forceinline__ void store8(float* p, const float (&y)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    put4<NT>(p + 4 * i, u4_t{__float_as_uint(y[4 * i]), __float_as_uint(y[4 * i + 1]), __float_as_uint(y[4 * i + 2]),
+                             __float_as_uint(y[4 * i + 3])});
 }
-__device__ __forceinline__ void store8(bf16_t* p, const float (&y)[8]) {
-  uint32_t u[4];
+template <bool NT> __device__ __forceinline__ void store8(bf16_t* p, const float (&y)[8]) {
+  u4_t u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) u[i] = f32_to_bf16(y[2 * i]) | (uint32_t)f32_to_bf16(y[2 * i + 1]) << 16;
-  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+  put4<NT>(p, u);
 }
 
 // sum over a row's D / 8 lanes
@@ -88,28 +100,56 @@ template <int D> __device__ __forceinline__ int partner(const RopeCall& c, int s
   return c.interleaved ? s : s < half ? s + half : s < 2 * half ? s - half : s;
 }
 
-template <int D> __device__ __forceinline__ Turn turn_of(const RopeCall& c, int s, int position) {
+// sin and cos of 2 pi t for |t| <= 1/2 (turns): the nearest quarter turn comes
+// off (exactly), the rest, at most an eighth, goes through the Taylor series of
+// both, cut where a term falls below 2^-31 (x^9, x^10 at pi / 4).
+__device__ __forceinline__ void sincos_turn(float t, float& sn, float& cs) {
+  const float n = rintf(4.f * t), x = fmaf(-0.25f, n, t), y = x * x;
+  const float s = x * fmaf(y, fmaf(y, fmaf(y, fmaf(y, 42.0586939f, -76.7058598f), 81.6052493f), -41.3417022f), 6.28318531f);
+  const float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, fmaf(y, -26.4262568f, 60.2446414f), -85.4568172f), 64.939394f), -19.7392088f), 1.f);
+  const int q = (int)n;
+  const float a = q & 1 ? c : s, b = q & 1 ? s : c;
+  sn = q & 2 ? -a : a;
+  cs = (q + 1) & 2 ? -b : b;
+}
+
+typedef float f4u_t __attribute__((ext_vector_type(4), aligned(4)));  // four floats anywhere
+
+// the frequencies of this lane's pairs (8, or 4 interleaved); 0 where nothing turns
+__device__ __forceinline__ void frequencies(const RopeCall& c, int s, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = 0.f;
+  if (8 * s < c.rot) {
+    const float* p = c.inv_freq + (c.interleaved ? 4 * s : 8 * s < c.rot / 2 ? 8 * s : 8 * s - c.rot / 2);
+    const f4u_t u = *reinterpret_cast<const f4u_t*>(p);
+    const f4u_t v = c.interleaved ? u : *reinterpret_cast<const f4u_t*>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = u[i], f[4 + i] = v[i];
+  }
+}
+
+template <int D> __device__ __forceinline__ Turn turn_of(const RopeCall& c, int s, const float (&f)[8], int position) {
   Turn t;
   const double p = (double)position * 0.15915494309189533577;  // turns per radian
+  const bool first = 8 * s < c.rot / 2;
+  if (c.interleaved) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = 8 * s + i;
-    t.cos[i] = 1.f;
-    t.sin[i] = 0.f;
-    if (e < c.rot) {
-      if (c.interleaved) {
-        if (i & 1) {  // the pair's angle is there
-          t.cos[i] = t.cos[i - 1];
-          t.sin[i] = -t.sin[i - 1];
-          continue;
-        }
-      }
-      const int pair = c.interleaved ? e / 2 : e < c.rot / 2 ? e : e - c.rot / 2;
-      const double turns = p * (double)c.inv_freq[pair];
+    for (int i = 0; i < 4; ++i) {
+      const double turns = p * (double)f[i];
       float sn, cs;
-      sincospif(2.f * (float)(turns - rint(turns)), &sn, &cs);
+      sincos_turn((float)(turns - rint(turns)), sn, cs);
+      t.cos[2 * i] = t.cos[2 * i + 1] = cs;
+      t.sin[2 * i] = -sn;
+      t.sin[2 * i + 1] = sn;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const double turns = p * (double)f[i];
+      float sn, cs;
+      sincos_turn((float)(turns - rint(turns)), sn, cs);
       t.cos[i] = cs;
-      t.sin[i] = c.interleaved || e < c.rot / 2 ? -sn : sn;
+      t.sin[i] = first ? -sn : sn;
     }
   }
   return t;
@@ -148,10 +188,32 @@ __global__ __launch_bounds__(256) void rope_kernel(Args a) {
   const RopeCall& c = a.c;
   const int lane = lane_id(), s = lane % L, group = threadIdx.x / L;
   const int64_t unit = (int64_t)blockIdx.x * GROUPS + group;
-  int64_t t = unit / a.parts;
-  const int h0 = (int)(unit - t * a.parts) * a.heads;
   bool live = unit < a.units;
-  if (!live) t = 0;
+  // (fewer than 2^31 units where a token has several)
+  int64_t t = !live ? 0 : a.parts == 1 ? unit : (uint32_t)unit / (uint32_t)a.parts;
+  const int h0 = a.parts == 1 || !live ? 0 : (int)((uint32_t)unit % (uint32_t)a.parts) * a.heads;
+  // what does not depend on the token's place is on its way while that is found
+  const int nh = c.H + (PAGED ? 2 : 1) * c.Hkv, h1 = min(h0 + a.heads, nh);
+  const IO* q = (const IO*)c.q + t * c.q_stride + 8 * s;
+  const IO* k = (const IO*)c.k + t * c.k_stride + 8 * s;
+  const IO* v = (const IO*)c.v + (PAGED ? t * c.v_stride + 8 * s : 0);
+  Raw<IO> x[UNROLL];
+  auto fetch = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int i = min(h + u, h1 - 1);
+      x[u] = load8(i < c.H ? q + (int64_t)i * D : i < c.H + c.Hkv ? k + (int64_t)(i - c.H) * D
+                                                              : v + (int64_t)(i - c.H - c.Hkv) * D);
+    }
+  };
+  fetch(h0);
+  const int es = partner<D>(c, s) * 8, from = (lane & ~(L - 1)) + es / 8;
+  float f[8], wq[8], wqp[8], wk[8], wkp[8];
+  frequencies(c, s, f);
+  weights<IO>(c.wq, 8 * s, wq);
+  weights<IO>(c.wq, es, wqp);
+  weights<IO>(c.wk, 8 * s, wk);
+  weights<IO>(c.wk, es, wkp);
   int row = 0;          // the token's row in its sequence's cache
   int64_t slot = -1;    // and in the pool (element offset of key head 0), or -1
   if constexpr (PAGED) {
@@ -175,7 +237,7 @@ __global__ __launch_bounds__(256) void rope_kernel(Args a) {
       i = t - tok0;
       live = live && i >= 0 && i < T;
     } else {
-      b = (int)(t / c.T);
+      b = (int)((uint32_t)t / (uint32_t)c.T);
       i = t - (int64_t)b * c.T;
       T = c.T;
     }
@@ -188,39 +250,18 @@ __global__ __launch_bounds__(256) void rope_kernel(Args a) {
     }
   }
   if (!live) return;  // whole lane groups leave; the others shuffle among themselves
-  const Turn turn = turn_of<D>(c, s, c.positions ? c.positions[t] : row);
-  const int from = (lane & ~(L - 1)) + partner<D>(c, s), es = partner<D>(c, s) * 8;
+  const Turn turn = turn_of<D>(c, s, f, c.positions ? c.positions[t] : row);
   // y = r (x cw + x' sw), for queries and for keys
   float cq[8], sq[8], ck[8], sk[8];
-  {
-    float w[8], wp[8];
-    weights<IO>(c.wq, 8 * s, w);
-    weights<IO>(c.wq, es, wp);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      cq[i] = w[i] * turn.cos[i];
-      sq[i] = wp[c.interleaved ? i ^ 1 : i] * turn.sin[i];
-    }
-    weights<IO>(c.wk, 8 * s, w);
-    weights<IO>(c.wk, es, wp);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      ck[i] = w[i] * turn.cos[i];
-      sk[i] = wp[c.interleaved ? i ^ 1 : i] * turn.sin[i];
-    }
+  for (int i = 0; i < 8; ++i) {
+    cq[i] = wq[i] * turn.cos[i];
+    sq[i] = (c.interleaved ? wqp[i ^ 1] : wqp[i]) * turn.sin[i];
+    ck[i] = wk[i] * turn.cos[i];
+    sk[i] = (c.interleaved ? wkp[i ^ 1] : wkp[i]) * turn.sin[i];
   }
-  const IO* q = (const IO*)c.q + t * c.q_stride + 8 * s;
-  const IO* k = (const IO*)c.k + t * c.k_stride + 8 * s;
-  const IO* v = (const IO*)c.v + (PAGED ? t * c.v_stride + 8 * s : 0);
-  const int nh = c.H + (PAGED ? 2 : 1) * c.Hkv, h1 = min(h0 + a.heads, nh);
   for (int h = h0; h < h1; h += UNROLL) {
-    Raw<IO> x[UNROLL];
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      const int i = min(h + u, h1 - 1);
-      x[u] = load8(i < c.H ? q + (int64_t)i * D : i < c.H + c.Hkv ? k + (int64_t)(i - c.H) * D
-                                                                : v + (int64_t)(i - c.H - c.Hkv) * D);
-    }
+    if (h > h0) fetch(h);
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
       const int i = h + u;
@@ -242,9 +283,9 @@ __global__ __launch_bounds__(256) void rope_kernel(Args a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         y[e] = r * fmaf(x[u].get(e), key ? ck[e] : cq[e], xp.get(e) * (key ? sk[e] : sq[e]));
-      if (!key) store8((OUT*)c.q_out + (t * c.H + i) * D + 8 * s, y);
-      else if (!PAGED) store8((OUT*)c.k_out + (t * c.Hkv + i - c.H) * D + 8 * s, y);
-      else if (slot >= 0) store8((OUT*)c.k_out + slot + (int64_t)(i - c.H) * c.page * D + 8 * s, y);
+      if (!key) store8<true>((OUT*)c.q_out + (t * c.H + i) * D + 8 * s, y);
+      else if (!PAGED) store8<true>((OUT*)c.k_out + (t * c.Hkv + i - c.H) * D + 8 * s, y);
+      else if (slot >= 0) store8<false>((OUT*)c.k_out + slot + (int64_t)(i - c.H) * c.page * D + 8 * s, y);
     }
   }
 }
@@ -258,12 +299,14 @@ __global__ __launch_bounds__(256, 3) void rope_backward_kernel(Args a) {
   float wq[8], wk[8], dwq[8], dwk[8];
   weights<IO>(c.wq, 8 * s, wq);
   weights<IO>(c.wk, 8 * s, wk);
+  float f[8];
+  frequencies(c, s, f);
 #pragma unroll
   for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = 0.f;
   for (int64_t unit = (int64_t)blockIdx.x * GROUPS + group; unit < a.units; unit += (int64_t)gridDim.x * GROUPS) {
-    const int64_t t = unit / a.parts;
+    const int64_t t = a.parts == 1 ? unit : (uint32_t)unit / (uint32_t)a.parts;
     const int h0 = (int)(unit - t * a.parts) * a.heads, h1 = min(h0 + a.heads, c.H + c.Hkv);
-    const Turn turn = turn_of<D>(c, s, c.positions[t]);
+    const Turn turn = turn_of<D>(c, s, f, c.positions[t]);
     const IO* q = (const IO*)c.q + t * c.q_stride + 8 * s;
     const IO* k = (const IO*)c.k + t * c.k_stride + 8 * s;
     for (int h = h0; h < h1; h += U) {
@@ -272,8 +315,8 @@ __global__ __launch_bounds__(256, 3) void rope_backward_kernel(Args a) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = min(h + u, h1 - 1);
-        x[u] = load8(i < c.H ? q + (int64_t)i * D : k + (int64_t)(i - c.H) * D);
-        y[u] = load8(i < c.H ? (const GR*)c.dq_out + (t * c.H + i) * D + 8 * s
+        x[u] = load8<true>(i < c.H ? q + (int64_t)i * D : k + (int64_t)(i - c.H) * D);
+        y[u] = load8<true>(i < c.H ? (const GR*)c.dq_out + (t * c.H + i) * D + 8 * s
                              : (const GR*)c.dk_out + (t * c.Hkv + i - c.H) * D + 8 * s);
       }
 #pragma unroll
@@ -303,8 +346,8 @@ __global__ __launch_bounds__(256, 3) void rope_backward_kernel(Args a) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) g[e] = r * fmaf(-x[u].get(e) * r, dot, g[e]);
         }
-        if (!key) store8((GR*)c.dq + (t * c.H + i) * D + 8 * s, g);
-        else store8((GR*)c.dk + (t * c.Hkv + i - c.H) * D + 8 * s, g);
+        if (!key) store8<true>((GR*)c.dq + (t * c.H + i) * D + 8 * s, g);
+        else store8<true>((GR*)c.dk + (t * c.Hkv + i - c.H) * D + 8 * s, g);
       }
     }
   }
@@ -349,7 +392,7 @@ int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
 Args args_of(const RopeCall& c, int nh) {
   Args a;
   a.c = c;
-  const int64_t groups = 8192 * (512 / c.D);  // lane groups of 8192 waves
+  const int64_t groups = 4096 * (512 / c.D);  // lane groups of 4096 waves
   int64_t parts = std::min<int64_t>(std::max<int64_t>(groups / std::max<int64_t>(c.total, 1), 1), nh);
   a.heads = (int)cdiv(nh, parts);
   a.parts = (int)cdiv(nh, a.heads);
