@@ -83,9 +83,19 @@ struct Args {
   float2* run_ml;  // [2 a workgroup][32]
   Shared* shared;  // [workgroups]
   float scale;     // times log2 e
+  double inv_g, inv_h;
 };
 
+// floor(n / d) from 1 / d in 64 bits, for 0 <= n, d with n < 2^41 and
+// n / d < 2^31 (or d < 2^41 and n / d < 2^10): (n + 1/2) / d is at least
+// 1 / (2 d) away from a whole number, further than its roundings.  A 64-bit
+// division is some 150 instructions, and each stands before a kernel's first load.
+__device__ __forceinline__ int64_t quotient(int64_t n, double inv) { return (int64_t)(((double)n + 0.5) * inv); }
+
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// the token of row r of a sequence's T G
+__device__ __forceinline__ int token_of(const Args& a, int64_t r) { return (int)(((double)r + 0.5) * a.inv_g); }
 
 // first token and length of sequence b, and its cache rows; all clamped to the
 // tensors (they come from device memory)
@@ -114,7 +124,7 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
 __device__ __forceinline__ void slot_of(const Args& a, int64_t s, int R, int& b, int64_t& r0) {
   if (!a.cu) {
     const int64_t per = ((int64_t)a.T * a.G + R - 1) / R;
-    b = (int)(s / per);
+    b = (int)((uint32_t)s / (uint32_t)per);  // (both below 2^31: a grid's size, T G / R)
     r0 = (s - b * per) * R;
     return;
   }
@@ -250,14 +260,14 @@ template <int D> struct Wave {
     const int64_t nr = (int64_t)s.T * a.G, r = r0 + (lane & 31);
     const int base = s.kv - s.T;
     const bool real = r < nr;
-    const int i = real ? (int)(r / a.G) : 0, g = real ? (int)(r - (int64_t)i * a.G) : 0;
+    const int i = real ? token_of(a, r) : 0, g = real ? (int)(r - (int64_t)i * a.G) : 0;
     p = real ? base + i : -1;
     lw = a.window ? p - a.window : -1;
     const int64_t last = min(r0 + 32, nr) - 1;
     phi = lwlo = -1;
     if (r0 < nr) {
-      phi = uniform(base + (int)(last / a.G));
-      if (a.window) lwlo = uniform(base + (int)(r0 / a.G)) - a.window;
+      phi = uniform(base + token_of(a, last));
+      if (a.window) lwlo = uniform(base + token_of(a, r0)) - a.window;
     }
     const bf16_t* src = (const bf16_t*)a.q + (s.tok0 + i) * a.q_stride + (int64_t)(kvh * a.G + g) * D + 8 * (lane >> 5);
 #pragma unroll
@@ -266,16 +276,19 @@ template <int D> struct Wave {
       if (real) w = *reinterpret_cast<const uint4*>(src + 16 * k);
       q[k] = __builtin_bit_cast(bf16x8_t, w);
     }
-    // here, not in the loop, is where the loads are waited for (a wait there
-    // would be one for the transfers in flight)
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) asm volatile("" : "+v"(q[k]));
 #pragma unroll
     for (int db = 0; db < D / 32; ++db)
 #pragma unroll
       for (int e = 0; e < 16; ++e) o[db][e] = 0.f;
     m = -INFINITY;
     l = 0.f;
+  }
+
+  // The queries are here: not in the loop, where a wait for them would be one
+  // for the transfers in flight.
+  __device__ void arrived() {
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) asm volatile("" : "+v"(q[k]));
   }
 
   // S^T of NB x 32 cache rows, their K image at lk; K fragments are read
@@ -462,8 +475,8 @@ struct Span {
 };
 __device__ __forceinline__ Span span_of(const Args& a, const Seq& s, int64_t r0, int64_t r1, int R, int split) {
   Span x;
-  const int base = s.kv - s.T, first = base + (int)(r0 / a.G);
-  x.hi = max(base + (int)(r1 / a.G) + 1, 0);
+  const int base = s.kv - s.T, first = base + token_of(a, r0);
+  x.hi = max(base + token_of(a, r1) + 1, 0);
   x.lo = a.window ? min(max(first - a.window + 1, 0), x.hi) : 0;
   const int n0 = x.lo / R, n1 = (x.hi + R - 1) / R;
   const int per = (n1 - n0 + a.nsplit - 1) / a.nsplit;
@@ -478,7 +491,7 @@ struct Order {
   int t0, f0, nf, nt;
   __device__ Order(const Args& a, const Seq& s, const Span& x, int64_t r0, int64_t r1, int R) {
     // whole: ends by the first query's row and begins behind the last one's window
-    const int first = s.kv - s.T + (int)(r0 / a.G), cut = s.kv - s.T + (int)(r1 / a.G) - a.window;
+    const int first = s.kv - s.T + token_of(a, r0), cut = s.kv - s.T + token_of(a, r1) - a.window;
     t0 = x.t0;
     nt = x.t1 - x.t0;
     f0 = min(a.window && cut >= 0 ? max(x.t0, cut / R + 1) : x.t0, x.t1);
@@ -504,8 +517,8 @@ template <> __device__ __forceinline__ void store4<bf16_t>(bf16_t* p, f4_t v) {
 
 // where row r (of a sequence's T G) of key head kvh goes: row index of o, lse
 __device__ __forceinline__ int64_t out_row(const Args& a, const Seq& s, int kvh, int64_t r) {
-  const int64_t i = r / a.G;
-  return (s.tok0 + i) * a.H + kvh * a.G + (r - i * a.G);
+  const int i = token_of(a, r);
+  return (s.tok0 + i) * a.H + kvh * a.G + (r - (int64_t)i * a.G);
 }
 
 template <int D, typename OUT>
@@ -538,6 +551,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
     const uint32_t at = (uint32_t)(uintptr_t)(base + (n & 1) * 2 * IMG + wave * 16 * D * 2);
     ld.load(a, row0, x.hi, at, at + IMG);
   };
+  // the queries and the page indices arrive together, then the first tile leaves
+  if (nt > 0) ld.page(a, min(tile(0) * R + wave * 16, x.hi - 1));
+  w.arrived();
   if (nt > 0) issue(0);
   auto next = [&](int n) {
     // every wave's transfers of tile n have landed, and every wave has left tile n - 1
@@ -641,7 +657,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_row_kernel(Args a) {
       __syncthreads();
     }
     all *= a.Hkv;
-    const int64_t per = (all + gridDim.x - 1) / gridDim.x;
+    const int64_t per = quotient(all + gridDim.x - 1, 1.0 / gridDim.x);
     at = min(blockIdx.x * per, all);
     end = min(at + per, all);
     if (threadIdx.x == 0) found[0] = found[1] = 0;
@@ -680,7 +696,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_row_kernel(Args a) {
       ++b;
       continue;
     }
-    const int kvh = uniform((int)((at - start) / steps)), s0 = uniform((int)(at - start - (int64_t)kvh * steps));
+    const int kvh = uniform((int)quotient(at - start, 1.0 / steps)), s0 = uniform((int)(at - start - (int64_t)kvh * steps));
     const int s1 = uniform((int)min((int64_t)steps, s0 + end - at));
     if (kvh >= a.Hkv) break;  // (lengths that changed meanwhile)
     const int nr = (int)(s.T * a.G);
@@ -714,6 +730,8 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_row_kernel(Args a) {
       par ^= 1;
       return k;
     };
+    if (wave < nt) ld.page(a, ord.tile(wave) * R);
+    w.arrived();
     if (wave < nt) issue(ord.tile(wave), 0);
     int n = wave;
     for (; n < nf; n += NW) {
@@ -754,7 +772,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_row_kernel(Args a) {
     }
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     const bool whole = s0 == 0 && s1 == steps;
-    if (s0 == 0 && !whole) shared = {b, kvh, (int)((at + steps - 1) / run_steps) - (int)blockIdx.x, seg};
+    if (s0 == 0 && !whole) shared = {b, kvh, (int)quotient(at + steps - 1, 1.0 / run_steps) - (int)blockIdx.x, seg};
     const int64_t slot = 2 * (int64_t)blockIdx.x + seg;
     constexpr int LPR = D / 4;
     for (int i = threadIdx.x / LPR; i < nr; i += NTHR / LPR) {
@@ -853,7 +871,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Args a) {
   bool own = row < a.rows;
   if (a.cu) {
     // the sequence of the block's first token, then on from there
-    const int64_t t0 = (int64_t)blockIdx.x * RPB / a.H;
+    const int64_t t0 = quotient((int64_t)blockIdx.x * RPB, a.inv_h);
     int n = 0;
     for (int i = 0; i < a.B; i += 256) {
       const int j = i + threadIdx.x;
@@ -861,7 +879,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Args a) {
       n += c;
       if (c < 256) break;
     }
-    const int64_t t = row / a.H;
+    const int64_t t = quotient(row, a.inv_h);
     int b = max(n - 1, 0);
     while (b + 1 < a.B && a.cu[b + 1] <= t) ++b;
     int64_t tok0;
@@ -906,7 +924,7 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(Args a) {
   const Span x = span_of(a, s, r0, min(r0 + NW * 16, nr) - 1, R, split);
   const int64_t r = r0 + wave * 16 + c;
   const bool real = r < nr;
-  const int i0 = real ? (int)(r / a.G) : 0, g0 = real ? (int)(r - (int64_t)i0 * a.G) : 0;
+  const int i0 = real ? token_of(a, r) : 0, g0 = real ? (int)(r - (int64_t)i0 * a.G) : 0;
   const int p = real ? s.kv - s.T + i0 : -1, lw = a.window ? p - a.window : -1;
   const float* src = (const float*)a.q + (s.tok0 + i0) * a.q_stride + (int64_t)(kvh * a.G + g0) * D + 4 * g;
   float4 q[D / 16];
@@ -1170,6 +1188,7 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t stream) {
   a.shared = reinterpret_cast<Shared*>(ws + w.shared);
   a.direct = p.direct;
   a.scale = c.scale * 1.4426950408889634f;
+  a.inv_g = 1.0 / a.G, a.inv_h = 1.0 / a.H;
   const bool bf = c.out == IO_BF16;
   switch (c.D) {
     case 64: return bf ? launch<64, bf16_t>(c, p, a, stream) : launch<64, float>(c, p, a, stream);
