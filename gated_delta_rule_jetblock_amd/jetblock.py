@@ -540,19 +540,24 @@ def backward(x, q, k, v, alpha, beta, W1, W2, dout, b1=None, b2=None, S0=None, c
 
 def _rows(t, name: str):
     """Pointer, tokens and token stride of [..., heads, D] whose tokens lie at one distance."""
-    if t.stride(-1) != 1 or t.stride(-2) != t.shape[-1]:
-        raise ValueError(f"{name}: a token's heads must be contiguous")
-    if t.dim() == 3:
-        n, stride = t.shape[0], t.stride(0)
-    elif t.dim() == 4:
-        n, stride = t.shape[0] * t.shape[1], t.stride(1) if t.shape[1] > 1 else t.stride(0)
-        if t.shape[0] > 1 and t.shape[1] > 1 and t.stride(0) != t.shape[1] * stride:
+    shape, st = t.shape, t.stride()
+    if len(shape) == 3:
+        n, heads, d = shape
+        stride = st[0]
+    elif len(shape) == 4:
+        B, T, heads, d = shape
+        n, stride = B * T, st[1] if T > 1 else st[0]
+        if B > 1 and T > 1 and st[0] != T * stride:
             raise ValueError(f"{name}: tokens must lie at one distance")
     else:
-        raise ValueError(f"{name}: expected [tokens, heads, D] or [B, T, heads, D], got {tuple(t.shape)}")
-    if n > 1 and stride < t.shape[-2] * t.shape[-1]:
+        raise ValueError(f"{name}: expected [tokens, heads, D] or [B, T, heads, D], got {tuple(shape)}")
+    if st[-1] != 1 or st[-2] != d:
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    if n <= 1:
+        return t.data_ptr(), n, 0
+    if stride < heads * d:
         raise ValueError(f"{name}: tokens overlap (token stride {stride})")
-    return t.data_ptr(), n, stride if n > 1 else 0
+    return t.data_ptr(), n, stride
 
 
 def _same(di, *groups):
@@ -572,6 +577,12 @@ def _flat(t, name: str, *shape):
         return None
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor of shape {shape}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _positions(t, n: int):
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"positions: expected {n} contiguous values, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
@@ -632,7 +643,7 @@ def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, *, eps=1e-6, inter
     shape = AttnShape(1, n, H, Hkv, D, 2 * inv_freq.numel(), 0, 0, 0, 0, 0, _io_code(q), _code(out_dtype),
                       _rope_flags(interleaved, normalize), qs, ks, 0, 0)
     _launch(di, stream, _lib.jb_qk_norm_rope, shape, qp, kp, _flat(wq, "wq", D), _flat(wk, "wk", D),
-            _flat(inv_freq, "inv_freq", inv_freq.numel()), _flat(positions.reshape(-1), "positions", n), eps,
+            _flat(inv_freq, "inv_freq", inv_freq.numel()), _positions(positions, n), eps,
             _flat(q_out, "q_out", *q.shape), _flat(k_out, "k_out", *k.shape))
     return q_out, k_out
 
@@ -669,7 +680,7 @@ def qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, wq=None, wk
     if ws is None:
         ws = workspace(qk_norm_rope_backward_workspace_size(shape), dev)
     _launch(di, stream, _lib.jb_qk_norm_rope_backward, shape, qp, kp, _flat(wq, "wq", D), _flat(wk, "wk", D),
-            _flat(inv_freq, "inv_freq", inv_freq.numel()), _flat(positions.reshape(-1), "positions", n), eps,
+            _flat(inv_freq, "inv_freq", inv_freq.numel()), _positions(positions, n), eps,
             _flat(dq_out, "dq_out", *q.shape), _flat(dk_out, "dk_out", *k.shape), _flat(dq, "dq", *q.shape),
             _flat(dk, "dk", *k.shape), _flat(dwq, "dwq", D), _flat(dwk, "dwk", D), ws.data_ptr(), ws.numel())
     return dict(dq=dq, dk=dk, dwq=dwq, dwk=dwk)
@@ -686,19 +697,20 @@ def _batch(q, cu_seqlens, max_seqlen):
 
 def _pages(k_cache, v_cache, page_table, kv_lens, B, D):
     """num_pages, Hkv, page, page stride and max_pages of a cache."""
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+    shape, st = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != st:
         raise ValueError("k_cache and v_cache are [pages, Hkv, page, D] alike")
-    P, Hkv, page, d = k_cache.shape
-    st = k_cache.stride()
+    P, Hkv, page, d = shape
     if d != D or st[3] != 1 or st[2] != D or (Hkv > 1 and st[1] != page * D):
         raise ValueError("a page of the caches must be contiguous, of q's head size")
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError(f"page_table: expected [{B}, max_pages], got {tuple(page_table.shape)}")
-    if kv_lens.dim() != 1 or kv_lens.numel() != B:
+    table = page_table.shape
+    if len(table) != 2 or table[0] != B:
+        raise ValueError(f"page_table: expected [{B}, max_pages], got {tuple(table)}")
+    if kv_lens.shape != (B,):
         raise ValueError(f"kv_lens: expected [{B}], got {tuple(kv_lens.shape)}")
     if P > 1 and st[0] < Hkv * page * D:
         raise ValueError(f"pages of the caches overlap (page stride {st[0]})")
-    return P, Hkv, page, st[0] if P > 1 else 0, page_table.shape[1]
+    return P, Hkv, page, st[0] if P > 1 else 0, table[1]
 
 
 def qk_norm_rope_paged(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq, wq=None, wk=None, *,
@@ -729,7 +741,7 @@ def qk_norm_rope_paged(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq,
             None if cu_seqlens is None else _flat(cu_seqlens, "cu_seqlens", B + 1), _flat(kv_lens, "kv_lens", B),
             _flat(page_table, "page_table", B, max_pages), qp, kp, vp, _flat(wq, "wq", D), _flat(wk, "wk", D),
             _flat(inv_freq, "inv_freq", inv_freq.numel()),
-            None if positions is None else _flat(positions.reshape(-1), "positions", n), eps,
+            None if positions is None else _positions(positions, n), eps,
             _flat(q_out, "q_out", *q.shape), k_cache.data_ptr(), v_cache.data_ptr())
     return dict(q=q_out, k_cache=k_cache, v_cache=v_cache)
 
