@@ -49,11 +49,10 @@ typedef __attribute__((address_space(3))) bf16x8_t lds_bf16x8;
 typedef short s4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s4_t lds_s4;
 typedef unsigned int u4_t __attribute__((ext_vector_type(4)));
-typedef unsigned int u2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) f4_t lds_f4;
 typedef __attribute__((address_space(3))) u4_t lds_u4;
-typedef __attribute__((address_space(3))) u2_t lds_u2;
 typedef __attribute__((address_space(3))) uint32_t lds_u32;
+typedef __attribute__((address_space(3))) uint16_t lds_u16;
 typedef __attribute__((address_space(3))) float lds_float;
 typedef float f16_t __attribute__((ext_vector_type(16)));
 typedef const __attribute__((address_space(4))) int* const_int_p;
@@ -246,6 +245,27 @@ __device__ __forceinline__ float half_max(float x) {
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
+// o += weight times value, for the values that are not finite, of the cache rows
+// that a query sees (o: D / 2 and s: NB x 16 accumulators of a wave).  A call of
+// its own, on memory: it is rare, and inline it took the registers of the loops.
+template <int D, int NB>
+__device__ __attribute__((noinline)) void add_odd_values(float* o, const float* s, const lds_char* lv, int j0, int p,
+                                                         int lw) {
+  using I = Img<D>;
+  const int g = lane_id() >> 5;
+  for (int r = 0; r < NB * 32; ++r) {
+    const float mine = s[(r >> 5) * 16 + ((r & 31) >> 3) * 4 + (r & 3)], other = __shfl_xor(mine, 32, WAVE);
+    const float w = ((r >> 2) & 1) == g ? mine : other;
+    if (j0 + r > p || j0 + r <= lw) continue;
+    for (int e = 0; e < D / 2; ++e) {
+      const int d = 32 * (e >> 4) + 8 * ((e >> 2) & 3) + 4 * g + (e & 3);
+      const uint32_t u = *(const lds_u16*)(lv + r * I::ROWB + (((d >> 3) ^ I::fv(r)) << 4) + (d & 7) * 2);
+      const float v = __uint_as_float(u << 16);
+      if (!isfinite(v)) o[e] = fmaf(w, v, o[e]);
+    }
+  }
+}
+
 // One wave's 32 queries and what they have gathered so far.
 template <int D> struct Wave {
   using I = Img<D>;
@@ -387,16 +407,16 @@ template <int D> struct Wave {
     const int lane = lane_id(), g = lane >> 5;
     const int n16 = lane & 15, row = 4 * g + (n16 >> 2), pc = 2 * ((lane >> 4) & 1) + ((n16 & 3) >> 1);
     const int vb = row * I::ROWB + ((pc ^ I::fv(row)) << 4) + (n16 & 1) * 8;
-    constexpr int DB = D / 32, STEPS = 2 * NB, PART = 8 / DB;
-    bf16x8_t v[2][DB];
-    auto read = [&](int k, int db) {
-      const lds_char* at = lv + (vb ^ (db << 6)) + k * 16 * I::ROWB;
+    constexpr int DB = D / 32, STEPS = 2 * NB, PART = 8 / DB, AHEAD = 4;
+    bf16x8_t v[STEPS * DB];  // read AHEAD products before its own
+    auto read = [&](int i) {
+      const lds_char* at = lv + (vb ^ ((i % DB) << 6)) + (i / DB) * 16 * I::ROWB;
       const s4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)at);
       const s4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(at + 8 * I::ROWB));
-      v[k & 1][db] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      v[i] = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     };
 #pragma unroll
-    for (int db = 0; db < DB; ++db) read(0, db);
+    for (int i = 0; i < AHEAD; ++i) read(i);
     if constexpr (EXP) weights<NB>(a, s, ms, 0);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -406,8 +426,9 @@ template <int D> struct Wave {
       for (int e = 0; e < 8; ++e) w[e] = (__bf16)s[k >> 1][8 * (k & 1) + e];
 #pragma unroll
       for (int db = 0; db < DB; ++db) {
-        if (k + 1 < STEPS) read(k + 1, db);
-        o[db] = mfma32(v[k & 1][db], w, o[db]);
+        const int i = k * DB + db;
+        if (i + AHEAD < STEPS * DB) read(i + AHEAD);
+        o[db] = mfma32(v[i], w, o[db]);
         if constexpr (EXP)
           if (k + 1 < STEPS) weights<NB>(a, s, ms, k + 1, db * PART, PART);
         __builtin_amdgcn_sched_barrier(0);
@@ -416,32 +437,15 @@ template <int D> struct Wave {
   }
 
   // o += weight times value for the values that are not finite, of rows that are seen
-  template <int NB> __device__ void by_row(const f16_t (&s)[NB], const lds_char* lv, int j0) {
-    const int g = lane_id() >> 5;
-    for (int r = 0; r < NB * 32; ++r) {
-      const int e0 = ((r & 31) >> 3) * 4 + (r & 3);
-      float w = 0.f;
+  template <int NB> __device__ void odd_values(const f16_t (&s)[NB], const lds_char* lv, int j0) {
+    float so[D / 2], ss[NB * 16];
 #pragma unroll
-      for (int n = 0; n < NB; ++n)
+    for (int e = 0; e < D / 2; ++e) so[e] = o[e >> 4][e & 15];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) w = n * 16 + e == (r >> 5) * 16 + e0 ? s[n][e] : w;
-      const float x = other_half(w);
-      if (((r >> 2) & 1) != g) w = x;
-      const bool seen = j0 + r <= p && j0 + r > lw;
+    for (int e = 0; e < NB * 16; ++e) ss[e] = s[e >> 4][e & 15];
+    add_odd_values<D, NB>(so, ss, lv, j0, p, lw);
 #pragma unroll
-      for (int db = 0; db < D / 32; ++db)
-#pragma unroll
-        for (int e4 = 0; e4 < 4; ++e4) {
-          const int d = 32 * db + 8 * e4 + 4 * g;
-          const u2_t u = *(const lds_u2*)(lv + r * I::ROWB + (((d >> 3) ^ I::fv(r)) << 4) + (d & 4) * 2);
-          const float v[4] = {__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                              __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u)};
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (seen && !isfinite(v[e])) o[db][4 * e4 + e] = fmaf(w, v[e], o[db][4 * e4 + e]);
-          asm volatile("" ::: "memory");  // (a rare path: its reads take no registers from the others)
-        }
-    }
+    for (int e = 0; e < D / 2; ++e) o[e >> 4][e & 15] = so[e];
   }
 };
 
@@ -572,7 +576,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
     f16_t s2[2];
     const bool live = w.template part<2>(a, k, tile(n) * R, s2);
     if (odd) {
-      if (live) w.template by_row<2>(s2, v, tile(n) * R);
+      if (live) w.template odd_values<2>(s2, v, tile(n) * R);
       __syncthreads();
       clean_part(v + wave * (IMG / 4), IMG / 4);
       __syncthreads();
@@ -742,14 +746,15 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_row_kernel(Args a) {
       lds_char* const k = next(n);
       lds_char* const v = k + IMG;
       f16_t s1[1];
-      if (!w.template part<1>(a, k, ord.tile(n) * R, s1)) continue;
-      if (odd_part(v, IMG)) {
-        w.template by_row<1>(s1, v, ord.tile(n) * R);
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        clean_part(v, IMG);
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (w.template part<1>(a, k, ord.tile(n) * R, s1)) {
+        if (odd_part(v, IMG)) {
+          w.template odd_values<1>(s1, v, ord.tile(n) * R);
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          clean_part(v, IMG);
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+        w.template values<1, false>(a, v, s1, 0.f);
       }
-      w.template values<1, false>(a, v, s1, 0.f);
     }
     // join the waves: O and (m, l) of each in LDS
     const int c = lane & 31, g = lane >> 5;
