@@ -909,25 +909,30 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Args a) {
 }
 
 // ------------------------------------------------------------------ fp32 mode
-// 4 waves x 16 query rows; S^T = K Q^T and O^T += V^T P^T on 16x16x4 fp32
-// matrix cores, 32 cache rows at a time in LDS.  Lane: query lane % 16, cache
-// rows 4 g + i of each 16.  Everything stays fp32.
-template <int D, typename OUT>
+// S^T = K Q^T and O^T += V^T P^T on 16x16x4 fp32 matrix cores, a tile of cache
+// rows at a time in LDS.  Lane: query lane % 16, cache rows 4 g + i of each 16.
+// Everything stays fp32.  4 waves x 16 query rows share 32-row tiles; for at
+// most 16 query rows (decode, SHARE) every wave has the same queries and takes
+// 16 of a tile's 64 cache rows, joined in LDS at the end.
+template <int D, bool SHARE, typename OUT>
 __global__ __launch_bounds__(256, 1) void attn_f32_kernel(Args a) {
-  constexpr int R = 32, LD = D + 4, NW = 4;
-  __shared__ __attribute__((aligned(16))) float sk[R * LD], sv[R * LD];
+  constexpr int R = SHARE ? 64 : 32, LD = D + 4, NW = 4, QR = SHARE ? 16 : NW * 16;
+  constexpr int NB = SHARE ? 1 : 2;  // 16-row blocks of a tile that a wave takes
+  __shared__ __attribute__((aligned(16))) float kv[2 * R * LD];
+  float *const sk = kv, *const sv = kv + R * LD;
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int combo = blockIdx.x % (unsigned)(a.Hkv * a.nsplit), kvh = combo % a.Hkv, split = combo / a.Hkv;
   const int64_t nslot = gridDim.x / (unsigned)(a.Hkv * a.nsplit);
   const int64_t slot = nslot - 1 - blockIdx.x / (unsigned)(a.Hkv * a.nsplit);
   int b;
   int64_t r0;
-  slot_of(a, slot, NW * 16, b, r0);
+  slot_of(a, slot, QR, b, r0);
   const Seq s = seq_of(a, b);
   const int64_t nr = (int64_t)s.T * a.G;
   if (r0 < 0 || r0 >= nr) return;
-  const Span x = span_of(a, s, r0, min(r0 + NW * 16, nr) - 1, R, split);
-  const int64_t r = r0 + wave * 16 + c;
+  const Span x = span_of(a, s, r0, min(r0 + QR, nr) - 1, R, split);
+  const int64_t r = r0 + (SHARE ? 0 : wave * 16) + c;
+  const int block = SHARE ? wave * 16 : 0;  // of this wave's rows in a tile
   const bool real = r < nr;
   const int i0 = real ? token_of(a, r) : 0, g0 = real ? (int)(r - (int64_t)i0 * a.G) : 0;
   const int p = real ? s.kv - s.T + i0 : -1, lw = a.window ? p - a.window : -1;
@@ -940,15 +945,18 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(Args a) {
     o[k] = zero4();
   }
   float m = -INFINITY, l = 0.f;
-  // Tile t + 1 is on its way into registers while tile t is used: the two pages
-  // of its 32 rows are known a tile before that.
+  // Tile t + 1 is on its way into registers while tile t is used: the pages of
+  // its rows are known a tile before that.
   constexpr int PER = R * (D / 4) / 256;
   float4 kn[PER], vn[PER];
-  auto fetch = [&](int t, int p0, int p1) {
+  int pages[R / 16];
+  auto fetch = [&](int t) {
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
       const int e = u * 256 + threadIdx.x, rr = e / (D / 4), d = (e % (D / 4)) * 4, j = t * R + rr;
-      const int pid = rr < 16 ? p0 : p1;
+      int pid = pages[0];
+#pragma unroll
+      for (int h = 1; h < R / 16; ++h) pid = rr >= 16 * h ? pages[h] : pid;
       kn[u] = vn[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (j >= x.lo && j < x.hi && pid >= 0 && pid < a.num_pages) {
         const int64_t at = pid * a.page_stride + (((int64_t)kvh << a.pshift) + (j & ((1 << a.pshift) - 1))) * D + d;
@@ -957,12 +965,16 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(Args a) {
       }
     }
   };
-  auto page = [&](int t, int h) {
-    const int j = t * R + 16 * h;
-    return t < x.t1 && j < x.hi ? ((const_int_p)a.table)[(int64_t)b * a.max_pages + (j >> a.pshift)] : -1;
+  auto look_up = [&](int t) {
+#pragma unroll
+    for (int h = 0; h < R / 16; ++h) {
+      const int j = t * R + 16 * h;
+      pages[h] = t < x.t1 && j < x.hi ? ((const_int_p)a.table)[(int64_t)b * a.max_pages + (j >> a.pshift)] : -1;
+    }
   };
-  if (x.t0 < x.t1) fetch(x.t0, page(x.t0, 0), page(x.t0, 1));
-  int p0 = page(x.t0 + 1, 0), p1 = page(x.t0 + 1, 1);
+  look_up(x.t0);
+  if (x.t0 < x.t1) fetch(x.t0);
+  look_up(x.t0 + 1);
   for (int t = x.t0; t < x.t1; ++t) {
     __syncthreads();
     bool bad = false;
@@ -975,17 +987,17 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(Args a) {
       *reinterpret_cast<float4*>(sv + rr * LD + d) = vx;
     }
     if (t + 1 < x.t1) {
-      fetch(t + 1, p0, p1);
-      p0 = page(t + 2, 0), p1 = page(t + 2, 1);
+      fetch(t + 1);
+      look_up(t + 2);
     }
     const bool slow = __syncthreads_or(bad);
-    f4_t y[2];
+    f4_t y[NB];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int n = 0; n < NB; ++n) {
       y[n] = zero4();
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        const float4 kx = *reinterpret_cast<const float4*>(sk + (16 * n + c) * LD + 16 * k + 4 * g);
+        const float4 kx = *reinterpret_cast<const float4*>(sk + (block + 16 * n + c) * LD + 16 * k + 4 * g);
         y[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(kx.x, q[k].x, y[n], 0, 0, 0);
         y[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(kx.y, q[k].y, y[n], 0, 0, 0);
         y[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(kx.z, q[k].z, y[n], 0, 0, 0);
@@ -994,10 +1006,10 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(Args a) {
     }
     float mx = -INFINITY;
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < NB; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int j = t * R + 16 * n + 4 * g + e;
+        const int j = t * R + block + 16 * n + 4 * g + e;
         y[n][e] = j > p || j <= lw ? -INFINITY : y[n][e] * a.scale;
         mx = fmaxf(mx, y[n][e]);
       }
@@ -1008,7 +1020,7 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(Args a) {
     m = mn;
     l *= f;
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < NB; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         y[n][e] = fast_exp2(y[n][e] - ms);
@@ -1020,30 +1032,30 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(Args a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[k][e] *= f;
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < NB; ++n)
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float v = sv[(16 * n + 4 * g + e) * LD + 16 * k + c];
+          float v = sv[(block + 16 * n + 4 * g + e) * LD + 16 * k + c];
           if (slow && !isfinite(v)) v = 0.f;
           o[k] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, y[n][e], o[k], 0, 0, 0);
         }
     if (slow) {
-      for (int rr = 0; rr < R; ++rr) {
+      for (int rr = 0; rr < NB * 16; ++rr) {
         float w = 0.f;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) w = n * 16 + e == (rr & 16) + (rr & 3) ? y[n][e] : w;
         w = __shfl(w, ((rr >> 2) & 3) * 16 + c, WAVE);
-        const int j = t * R + rr;
+        const int j = t * R + block + rr;
         if (j <= p && j > lw)
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float v = sv[rr * LD + 16 * k + 4 * g + e];
+              const float v = sv[(block + rr) * LD + 16 * k + 4 * g + e];
               if (!isfinite(v)) o[k][e] = fmaf(w, v, o[k][e]);
             }
       }
@@ -1051,6 +1063,34 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(Args a) {
   }
   l += __shfl_xor(l, 16, WAVE);
   l += __shfl_xor(l, 32, WAVE);
+  if constexpr (SHARE) {
+    // the waves' parts, the first wave adding them up in its registers
+    __syncthreads();
+    float* const so = kv;                      // [NW][16][LD]
+    float* const sml = kv + NW * 16 * LD;      // [NW][2][16]
+    static_assert(NW * 16 * LD + NW * 32 <= 2 * R * LD, "staging fits");
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) *reinterpret_cast<f4_t*>(so + (wave * 16 + c) * LD + 16 * k + 4 * g) = o[k];
+    if (g == 0) sml[wave * 32 + c] = m, sml[wave * 32 + 16 + c] = l;
+    __syncthreads();
+    if (wave) return;
+    float mt = m;
+#pragma unroll
+    for (int w = 1; w < NW; ++w) mt = fmaxf(mt, sml[w * 32 + c]);
+    // (a wave that saw nothing holds zeros, or NaN that stays)
+    const float f0 = m == -INFINITY ? 1.f : fast_exp2(m - mt);
+    l *= f0;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) o[k] *= f0;
+#pragma unroll
+    for (int w = 1; w < NW; ++w) {
+      const float mw = sml[w * 32 + c], fw = mw == -INFINITY ? 1.f : fast_exp2(mw - mt);
+      l = fmaf(sml[w * 32 + 16 + c], fw, l);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) o[k] += *reinterpret_cast<const f4_t*>(so + (w * 16 + c) * LD + 16 * k + 4 * g) * fw;
+    }
+    m = mt;
+  }
   if (!real) return;
   const int64_t at = out_row(a, s, kvh, r);
   const bool split_out = a.nsplit > 1;
@@ -1073,6 +1113,7 @@ struct Plan {
   bool tiles, rows;   // which of the bf16 kernels run
   int64_t slots;      // row tiles, over all sequences
   int nsplit;         // pieces of their cache ranges
+  bool share;         // fp32 decode: the waves of attn_f32_kernel share the queries
   bool direct;        // attn_row_kernel: a unit a workgroup
   int64_t runs;       // its workgroups
   int rows_a_unit;    // query rows of its units, at most
@@ -1087,7 +1128,8 @@ Plan plan(const AttnCall& c) {
   Plan p;
   const int64_t G = c.H / c.Hkv, per = (int64_t)c.T * G;
   const bool f32 = c.io == IO_F32;
-  const int R = f32 ? 64 : 128;
+  p.share = f32 && per <= 16;
+  const int R = p.share ? 16 : f32 ? 64 : 128;
   // bf16 sequences of at most 32 rows go to attn_row_kernel.  A packed batch may
   // hold both kinds, and gets both kernels unless the cache range is so short
   // that a workgroup of the tile kernel walks it while others still work (16
@@ -1148,7 +1190,8 @@ template <int D, typename OUT>
 hipError_t launch(const AttnCall& c, const Plan& p, const Args& a, hipStream_t stream) {
   const int combos = c.Hkv * p.nsplit;
   if (c.io == IO_F32) {
-    attn_f32_kernel<D, OUT><<<dim3((unsigned)(p.slots * combos)), dim3(256), 0, stream>>>(a);
+    if (p.share) attn_f32_kernel<D, true, OUT><<<dim3((unsigned)(p.slots * combos)), dim3(256), 0, stream>>>(a);
+    else attn_f32_kernel<D, false, OUT><<<dim3((unsigned)(p.slots * combos)), dim3(256), 0, stream>>>(a);
   } else {
     constexpr int NW = row_waves(D);
     if (p.tiles) attn_tile_kernel<D, OUT><<<dim3((unsigned)(p.slots * combos)), dim3(256), 0, stream>>>(a);
