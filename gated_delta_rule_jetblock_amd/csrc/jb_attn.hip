@@ -1149,7 +1149,11 @@ Plan plan(const AttnCall& c) {
   p.runs = p.direct ? units : std::min<int64_t>(c.D == 64 ? 512 : 256, units * cdiv(range, step));
   if (!p.tiles) return p;
   if (f32) {
-    const int64_t want = cdiv(1024, p.slots * c.Hkv), most = cdiv(reach, 64);
+    // about the workgroups that the chip holds, by the LDS and registers of the
+    // head size (16 x 8K rows of decode at head size 256: 256 workgroups take
+    // 138 us, 1024 172; at 64 the other way round, 56 and 44)
+    const int64_t hold = std::min((p.share ? 65536 : 131072) / c.D, 1024);
+    const int64_t want = cdiv(hold, p.slots * c.Hkv), most = cdiv(reach, 64);
     p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 128));
     return p;
   }
@@ -1212,7 +1216,8 @@ hipError_t launch(const AttnCall& c, const Plan& p, const Args& a, hipStream_t s
 
 int64_t attn_workgroups(const AttnCall& c) {
   const Plan p = plan(c);
-  return std::max(std::max(p.tiles ? p.slots * c.Hkv * p.nsplit : 0, c.total * c.H), (int64_t)c.B * c.Hkv * 32);
+  const int64_t tiles = p.tiles ? p.slots * c.Hkv * p.nsplit : 0, join = p.nsplit > 1 ? c.total * c.H : 0;
+  return std::max(std::max(tiles, join), p.rows ? p.runs * 32 : 0);
 }
 
 size_t attn_workspace_bytes(const AttnCall& c) { return layout(c, plan(c)).bytes; }

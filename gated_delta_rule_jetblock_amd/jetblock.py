@@ -9,6 +9,7 @@ importing this module raises, and a call on CPU tensors raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -597,17 +598,27 @@ def _device(q) -> int:
     return q.get_device()
 
 
-def _launch(di: int, stream, fn, *args):
-    """fn(*args, stream) on device di: the given stream, or the device's current one."""
-    if stream is None:
-        handle = _raw_stream(di)
-    else:
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+def _launch(di: int, fn, *args):
+    """fn(*args, stream) on device di's current stream."""
     if di == torch.cuda.current_device():
-        _check(fn(*args, handle))
+        _check(fn(*args, _raw_stream(di)))
     else:
         with torch.cuda.device(di):
-            _check(fn(*args, handle))
+            _check(fn(*args, _raw_stream(di)))
+
+
+def _on_stream(fn):
+    """Adds the `stream` argument (a torch stream or a handle): the call, and what it allocates,
+    belong to that stream, so nothing it still uses is handed out on another."""
+    @functools.wraps(fn)
+    def call(q, *args, stream=None, **kw):
+        if stream is None:
+            return fn(q, *args, **kw)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=q.device)
+        with torch.cuda.stream(stream):
+            return fn(q, *args, **kw)
+    return call
 
 
 def _empty(like, dtype):
@@ -621,8 +632,9 @@ def _rope_flags(interleaved, normalize):
     return (ROPE_INTERLEAVED if interleaved else 0) | (0 if normalize else ROPE_NO_NORM)
 
 
+@_on_stream
 def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, *, eps=1e-6, interleaved=False, normalize=True,
-                 out_dtype=None, q_out=None, k_out=None, stream=None):
+                 out_dtype=None, q_out=None, k_out=None):
     """jb_qk_norm_rope.  q [tokens,H,D] or [B,T,H,D], k likewise with Hkv heads (any distance
     between tokens), positions int32 [tokens], inv_freq f32 [rot/2], wq, wk [D].  Returns
     (q_out, k_out), contiguous, of out_dtype (default: q's)."""
@@ -642,7 +654,7 @@ def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, *, eps=1e-6, inter
         k_out = _empty(k, out_dtype)
     shape = AttnShape(1, n, H, Hkv, D, 2 * inv_freq.numel(), 0, 0, 0, 0, 0, _io_code(q), _code(out_dtype),
                       _rope_flags(interleaved, normalize), qs, ks, 0, 0)
-    _launch(di, stream, _lib.jb_qk_norm_rope, shape, qp, kp, _flat(wq, "wq", D), _flat(wk, "wk", D),
+    _launch(di, _lib.jb_qk_norm_rope, shape, qp, kp, _flat(wq, "wq", D), _flat(wk, "wk", D),
             _flat(inv_freq, "inv_freq", inv_freq.numel()), _positions(positions, n), eps,
             _flat(q_out, "q_out", *q.shape), _flat(k_out, "k_out", *k.shape))
     return q_out, k_out
@@ -654,8 +666,9 @@ def qk_norm_rope_backward_workspace_size(shape: AttnShape) -> int:
     return n.value
 
 
+@_on_stream
 def qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, wq=None, wk=None, *, eps=1e-6,
-                          interleaved=False, normalize=True, dq=None, dk=None, ws=None, stream=None):
+                          interleaved=False, normalize=True, dq=None, dk=None, ws=None):
     """jb_qk_norm_rope_backward: gradients of qk_norm_rope from those of its outputs (contiguous,
     bf16 or f32).  Returns dict(dq, dk, dwq, dwk): dq, dk of dq_out's dtype, dwq, dwk f32 [D]
     (None without the norm)."""
@@ -679,7 +692,7 @@ def qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, wq=None, wk
                       _rope_flags(interleaved, normalize), qs, ks, 0, 0)
     if ws is None:
         ws = workspace(qk_norm_rope_backward_workspace_size(shape), dev)
-    _launch(di, stream, _lib.jb_qk_norm_rope_backward, shape, qp, kp, _flat(wq, "wq", D), _flat(wk, "wk", D),
+    _launch(di, _lib.jb_qk_norm_rope_backward, shape, qp, kp, _flat(wq, "wq", D), _flat(wk, "wk", D),
             _flat(inv_freq, "inv_freq", inv_freq.numel()), _positions(positions, n), eps,
             _flat(dq_out, "dq_out", *q.shape), _flat(dk_out, "dk_out", *k.shape), _flat(dq, "dq", *q.shape),
             _flat(dk, "dk", *k.shape), _flat(dwq, "dwq", D), _flat(dwk, "dwk", D), ws.data_ptr(), ws.numel())
@@ -691,7 +704,7 @@ def _batch(q, cu_seqlens, max_seqlen):
     if cu_seqlens is not None:
         if q.dim() != 3 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("packed: q is [tokens, H, D] and cu_seqlens [B + 1]")
-        return cu_seqlens.numel() - 1, q.shape[0] if max_seqlen is None else int(max_seqlen)
+        return cu_seqlens.numel() - 1, q.shape[0] if max_seqlen is None else min(int(max_seqlen), q.shape[0])
     return (q.shape[0], q.shape[1]) if q.dim() == 4 else (q.shape[0], 1)
 
 
@@ -713,9 +726,10 @@ def _pages(k_cache, v_cache, page_table, kv_lens, B, D):
     return P, Hkv, page, st[0] if P > 1 else 0, table[1]
 
 
+@_on_stream
 def qk_norm_rope_paged(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq, wq=None, wk=None, *,
                        cu_seqlens=None, max_seqlen: int | None = None, positions=None, eps=1e-6, interleaved=False,
-                       normalize=True, q_out=None, stream=None):
+                       normalize=True, q_out=None):
     """jb_qk_norm_rope_paged: rotated queries out, rotated keys and values into the caches
     [pages,Hkv,page,D] (in place).  q [B,T,H,D], [B,H,D] (one token each) or packed [tokens,H,D]
     with cu_seqlens int32 [B+1]; page_table int32 [B,max_pages], kv_lens int32 [B] (the new tokens
@@ -737,7 +751,7 @@ def qk_norm_rope_paged(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq,
     code = _io_code(q)
     shape = AttnShape(B, T, H, Hkv, D, 2 * inv_freq.numel(), page, max_pages, P, 0, 0, code, code,
                       _rope_flags(interleaved, normalize), qs, ks, vs, ps)
-    _launch(di, stream, _lib.jb_qk_norm_rope_paged, shape, n,
+    _launch(di, _lib.jb_qk_norm_rope_paged, shape, n,
             None if cu_seqlens is None else _flat(cu_seqlens, "cu_seqlens", B + 1), _flat(kv_lens, "kv_lens", B),
             _flat(page_table, "page_table", B, max_pages), qp, kp, vp, _flat(wq, "wq", D), _flat(wk, "wk", D),
             _flat(inv_freq, "inv_freq", inv_freq.numel()),
@@ -752,9 +766,10 @@ def attn_paged_workspace_size(shape: AttnShape, total_tokens: int, packed: bool)
     return n.value
 
 
+@_on_stream
 def attn_paged(q, k_cache, v_cache, page_table, kv_lens, *, cu_seqlens=None, max_seqlen: int | None = None,
                max_kv: int | None = None, window: int = 0, scale: float | None = None, out_dtype=None, o=None,
-               want_lse=False, lse=None, ws=None, stream=None):
+               want_lse=False, lse=None, ws=None):
     """jb_attn_paged: attention of each sequence's new tokens over its paged cache (which holds
     them already).  q [B,T,H,D], [B,H,D] (decode) or packed [tokens,H,D] with cu_seqlens int32
     [B+1]; caches, page_table and kv_lens as for qk_norm_rope_paged.  max_seqlen and max_kv, host
@@ -770,18 +785,21 @@ def attn_paged(q, k_cache, v_cache, page_table, kv_lens, *, cu_seqlens=None, max
     qp, n, qs = _rows(q, "q")
     B, T = _batch(q, cu_seqlens, max_seqlen)
     P, Hkv, page, ps, max_pages = _pages(k_cache, v_cache, page_table, kv_lens, B, D)
+    if not 0 <= window <= 1 << 30:
+        raise ValueError(f"window = {window} not in [0, 2^30]")
+    max_kv = 0 if max_kv is None else max(1, min(int(max_kv), max_pages * page))
     if o is None:
         o = _empty(q, out_dtype)
     if lse is None and want_lse:
         lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
     packed = cu_seqlens is not None
-    shape = AttnShape(B, T, H, Hkv, D, 0, page, max_pages, P, 0 if max_kv is None else int(max_kv), int(window),
+    shape = AttnShape(B, T, H, Hkv, D, 0, page, max_pages, P, max_kv, int(window),
                       _io_code(q), _code(out_dtype), 0, qs, 0, 0, ps)
     if ws is None:
         need = attn_paged_workspace_size(shape, n, packed)
         if need:
             ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _launch(di, stream, _lib.jb_attn_paged, shape, n, _flat(cu_seqlens, "cu_seqlens", B + 1),
+    _launch(di, _lib.jb_attn_paged, shape, n, _flat(cu_seqlens, "cu_seqlens", B + 1),
             _flat(kv_lens, "kv_lens", B), _flat(page_table, "page_table", B, max_pages), qp, k_cache.data_ptr(),
             v_cache.data_ptr(), 0.0 if scale is None else float(scale), _flat(o, "o", *q.shape),
             _flat(lse, "lse", *q.shape[:-1]), None if ws is None else ws.data_ptr(),

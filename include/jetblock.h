@@ -403,8 +403,10 @@ jb_status jb_backward(const jb_shape* shape, const void* x, const void* q, const
  * Device-side values cannot be checked on the host, and none makes a call
  * reach outside the tensors: offsets are clamped as in jb_prefill_varlen,
  * kv_lens to [0, max_pages * page], and a page index outside [0, num_pages)
- * reads as rows of zeros and is not written to.  Two sequences (or an append
- * and anything else) must not write the same page.
+ * reads as rows of zeros and is not written to.  Sequences may share pages that
+ * none of them appends to; two appends must not write the same row.  Outputs
+ * overlap no input except where a call says so, and calls that may run at the
+ * same time need workspaces of their own.
  *
  * Supported: D in {64, 128, 256}; H <= 256, a multiple of Hkv; page a power of
  * two in [16, 4096]; max_pages * page <= 2^30; both dtypes; 1 <= B <= 65535;

@@ -298,3 +298,97 @@ def test_captured_graphs(jb):
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(out["o"], e["o"]) and torch.equal(out["lse"], e["lse"]), i
+
+
+@pytest.mark.parametrize("B,packed", [(2100, False), (600, True), (300, True)])
+def test_many_sequences(jb, B, packed):
+    """Thousands of decode units (one each a workgroup), and hundreds in equal runs: sequences of
+    no, one to three tokens and 0 to 700 rows in any order."""
+    rng = np.random.RandomState(B)
+    new = rng.randint(0, 4, B).tolist() if packed else [1] * B
+    kv = rng.randint(0, 60 if B > 1000 else 700, B).tolist()
+    d = batch(new, kv, 4, 2, 64, 16, BF, seed=B, packed=packed)
+    check(d, call(jb, d, max_seqlen=3), new, kv)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [1, 3])
+def test_256_queries_to_a_key_head(jb, dtype, T):
+    """A token's rows fill two tiles of queries."""
+    new, kv = [T, T], [200, 33]
+    d = batch(new, kv, 256, 1, 64, 32, dtype, seed=15)
+    check(d, call(jb, d), new, kv)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("new", [[40, 1, 2], [2, 1, 3]])
+def test_non_finite_value_between_new_tokens(jb, D, new):
+    """A value row that only the later new tokens see (chunk and decode kernels, larger heads):
+    theirs are not finite, the others' bits stay."""
+    kv, page = [90, 70, 100], 16
+    d = batch(new, kv, 4, 2, D, page, BF, seed=D)
+    clean = call(jb, d)
+    at = 0
+    for b, (t, l) in enumerate(zip(new, kv)):
+        if t > 1:
+            j = l - 1   # the last new token's own row
+            d["v_cache"][int(d["table"][b, j // page]), :, j % page, 5] = float("inf")
+    r = call(jb, d)
+    for b, t in enumerate(new):
+        rows = slice(at, at + t - 1 if t > 1 else at + t)
+        assert torch.equal(r["o"][rows], clean["o"][rows]) and torch.equal(r["lse"][rows], clean["lse"][rows]), b
+        if t > 1:
+            last = r["o"][at + t - 1].float()
+            assert torch.isinf(last[:, 5]).all()
+            keep = torch.arange(D, device="cuda") != 5
+            assert torch.equal(last[:, keep], clean["o"][at + t - 1].float()[:, keep])
+        at += t
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_stream_argument(jb, as_handle):
+    """The stream argument, a torch stream or its handle: the call and its allocations belong to
+    it (the current stream may reuse nothing of them meanwhile)."""
+    new, kv = [1] * 4, [9000, 5000, 77, 1000]
+    d = batch(new, kv, 12, 2, 128, 64, BF, seed=16)
+    e = call(jb, d)
+    g = {k: v.cuda() for k, v in d.items()}
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(5):
+        r = jb.attn_paged(g["q"], g["k_cache"], g["v_cache"], g["table"], g["kv"], cu_seqlens=g["cu"],
+                          stream=s.cuda_stream if as_handle else s)
+        torch.full((1 << 22,), 7, dtype=torch.uint8, device="cuda")  # the current stream's own allocations
+        s.synchronize()
+        assert torch.equal(r["o"], e["o"])
+
+
+def test_two_calls_at_once(jb):
+    """Calls on two streams, each with a workspace of its own, do not touch each other."""
+    s = [torch.cuda.Stream() for _ in range(2)]
+    ds, es, gs = [], [], []
+    for i, (new, kv) in enumerate((([1] * 3, [9000, 4000, 100]), ([300, 1], [3000, 2500]))):
+        d = batch(new, kv, 12, 2, 128, 64, BF, seed=17 + i)
+        es.append(call(jb, d))
+        gs.append({k: v.cuda() for k, v in d.items()})
+    torch.cuda.synchronize()
+    for _ in range(4):
+        rs = [jb.attn_paged(g["q"], g["k_cache"], g["v_cache"], g["table"], g["kv"], cu_seqlens=g["cu"], stream=t)
+              for g, t in zip(gs, s)]
+        for t in s:
+            t.synchronize()
+        for r, e in zip(rs, es):
+            assert torch.equal(r["o"], e["o"])
+
+
+def test_first_offset_is_not_zero(jb):
+    """Rows before the first sequence belong to nobody either."""
+    new, kv = [30, 1], [100, 64]
+    for dtype in (BF, F32):
+        d = batch(new, kv, 4, 2, 64, 16, dtype, seed=19, behind=9)
+        e = call(jb, d)
+        d["q"] = torch.cat([d["q"][31:], d["q"][:31]])
+        d["cu"] = d["cu"] + 9
+        o = torch.full(d["q"].shape, 5.0, dtype=dtype, device="cuda")
+        r = call(jb, d, o=o)
+        assert torch.equal(r["o"][9:], e["o"][:31]) and (o[:9] == 5).all()
