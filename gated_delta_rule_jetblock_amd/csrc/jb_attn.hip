@@ -16,8 +16,8 @@
 // accumulators, rounded to bf16, are the B operand of O^T += V^T P^T as they
 // stand (K order kperm32: slots 0..3 are rows 4 g .. 4 g + 3, slots 4..7 rows
 // 8 + 4 g ..).  V's A operand is read down its columns from LDS.
-// Rounding: scores, m, l and o are fp32; P is rounded to bf16 (half a step,
-// 2^-9 of each weight at random) for the matrix cores; o is rounded once.
+// Rounding: scores, m, l and o are fp32; P is rounded to bf16 for the matrix
+// cores (at most 2^-8 of each weight, either way); o is rounded once.
 //   attn_tile_kernel  many queries: 4 waves x 32 rows of one key head walk the
 //                     same 64-row cache tiles through two LDS buffers.
 //   attn_row_kernel   at most 32 rows (decode): every wave takes its own 32-row
@@ -27,7 +27,7 @@
 // fp32 inputs take attn_f32_kernel, the same tiles on fp32 matrix cores.
 //
 // Reading the cache: 16 consecutive rows lie in one page, so a wave fetches
-// them with one page index (a scalar load) and one buffer descriptor that ends
+// them straight into LDS with one page index and one buffer descriptor that ends
 // behind the last row any query of the workgroup sees: rows behind it, and
 // pages whose index is out of range, arrive as zeros whatever memory holds.
 // A masked weight is 0, and 0 times an inf or NaN is NaN, so a tile that some
@@ -316,7 +316,7 @@ template <int D> struct Wave {
   template <int NB> __device__ void scores(const lds_char* lk, f16_t (&s)[NB]) const {
     const int lane = lane_id(), c = lane & 31, g = lane >> 5;
     const int kb = c * I::ROWB + ((g ^ I::fk(c)) << 4);
-    constexpr int AHEAD = 4, STEPS = D / 16;
+    constexpr int AHEAD = 2, STEPS = D / 16;
     bf16x8_t f[STEPS][NB];
     f16_t z;
 #pragma unroll
@@ -371,13 +371,15 @@ template <int D> struct Wave {
     }
   }
 
-  // A tile that every query sees whole.  The vector work goes before the other
-  // wave's products: at equal priority 2K tokens on 64K rows took 782 us and an
-  // 8K prompt 289, so 766 and 267.
+  // A tile that every query sees whole.  The maximum and the first weights, which
+  // nothing of this wave overlaps, go before the other wave's work, and the
+  // products with V, mixed with the other weights, before its products with K
+  // (at equal priority 2K tokens on 64K rows took 782 us and an 8K prompt 289; so
+  // 735 and 253).
   template <int NB> __device__ void full(const Args& a, const lds_char* lk, const lds_char* lv) {
     f16_t s[NB];
     scores<NB>(lk, s);
-    __builtin_amdgcn_s_setprio(1);
+    __builtin_amdgcn_s_setprio(2);
     const float ms = take_max<NB>(a, s);
     values<NB, true>(a, lv, s, ms);
     __builtin_amdgcn_s_setprio(0);
@@ -407,7 +409,7 @@ template <int D> struct Wave {
     const int lane = lane_id(), g = lane >> 5;
     const int n16 = lane & 15, row = 4 * g + (n16 >> 2), pc = 2 * ((lane >> 4) & 1) + ((n16 & 3) >> 1);
     const int vb = row * I::ROWB + ((pc ^ I::fv(row)) << 4) + (n16 & 1) * 8;
-    constexpr int DB = D / 32, STEPS = 2 * NB, PART = 8 / DB, AHEAD = 4;
+    constexpr int DB = D / 32, STEPS = 2 * NB, PART = 8 / DB, AHEAD = 2;
     bf16x8_t v[STEPS * DB];  // read AHEAD products before its own
     auto read = [&](int i) {
       const lds_char* at = lv + (vb ^ ((i % DB) << 6)) + (i / DB) * 16 * I::ROWB;
@@ -417,7 +419,10 @@ template <int D> struct Wave {
     };
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) read(i);
-    if constexpr (EXP) weights<NB>(a, s, ms, 0);
+    if constexpr (EXP) {
+      weights<NB>(a, s, ms, 0);
+      __builtin_amdgcn_s_setprio(1);
+    }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int k = 0; k < STEPS; ++k) {
@@ -525,6 +530,17 @@ __device__ __forceinline__ int64_t out_row(const Args& a, const Seq& s, int kvh,
   return (s.tok0 + i) * a.H + kvh * a.G + (r - (int64_t)i * a.G);
 }
 
+// Many queries: 4 waves x 32 rows of one key head walk 64-row cache tiles, two in
+// LDS: tile n + 1 arrives while n is used, one barrier a tile.
+// Bound by the matrix cores and by what feeds them in turn: a wave's tile is 1024
+// cycles of products (D = 128) and about 900 of vector work (32 exponentials at a
+// quarter of the rate, the maximum, the sums), so two waves of two workgroups
+// share a SIMD; 128 rows a workgroup keep two on a CU (64 KB of LDS, 208
+// registers) and read every K and V value once for 128 queries.  2K tokens on 64K
+// rows, 12 heads on 2: 735 us, 1105 TFLOP/s (the library's product of 8192^3
+// reaches 1226 on this card), matrix cores busy 60% of the cycles at the 1.75 GHz
+// the card then holds, no bank conflicts.  Head size 64, as much vector work for
+// half the products: 790 TFLOP/s; 256, one wave a SIMD: 970.
 template <int D, typename OUT>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a) {
   constexpr int NW = 4, R = 64, IMG = R * D * 2;
@@ -623,6 +639,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
 // run's first and last units may be shared with its neighbours.
 // The lengths live in device memory: every workgroup adds them up itself, and
 // says which shared unit begins in its run.
+// Bound by HBM: each wave keeps a 16 KB tile on its way (64 KB a CU) while it uses
+// another, without a barrier.  64 sequences of 64K rows, 2 key heads of 128: 677
+// us, 6.3 TB/s; of 1K to 64K rows: 355 us, 6.1 TB/s (cut into 16 even pieces each,
+// without regard to the others: 377); 256 of 1K rows: 47 us, 5.8 TB/s.
 __device__ __forceinline__ int steps_of(const Args& a, const Seq& s, int rows_a_step) {
   const int64_t nr = (int64_t)s.T * a.G;
   if (nr == 0 || nr > 32) return 0;  // none, or attn_tile_kernel's
@@ -913,7 +933,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Args a) {
 // rows at a time in LDS.  Lane: query lane % 16, cache rows 4 g + i of each 16.
 // Everything stays fp32.  4 waves x 16 query rows share 32-row tiles; for at
 // most 16 query rows (decode, SHARE) every wave has the same queries and takes
-// 16 of a tile's 64 cache rows, joined in LDS at the end.
+// 16 of a tile's 64 cache rows, joined in LDS at the end.  16 sequences of 8K
+// rows, 2 key heads of 128: 66 us, 4.1 TB/s; 1K tokens on 4K rows, 8 heads: 191
+// us, 79 TFLOP/s (the library's fp32 product reaches 154).
 template <int D, bool SHARE, typename OUT>
 __global__ __launch_bounds__(256, 1) void attn_f32_kernel(Args a) {
   constexpr int R = SHARE ? 64 : 32, LD = D + 4, NW = 4, QR = SHARE ? 16 : NW * 16;

@@ -18,7 +18,11 @@
 // The angles and the weight become two factors a value, y = r (x c + x' s) with
 // x' the other member of the pair, fetched from its lane as raw bits.
 // dw is summed in fp32 in a fixed order: lanes over their tokens, the
-// workgroup through LDS, then one kernel over the workgroups' sums.
+// workgroup through LDS, then one kernel over the workgroups' sums (5 us).
+// 64K tokens of 12 + 2 heads of 128, bf16: 88 us, 5.4 TB/s (the library's copy
+// reaches 5.0 on this card); backward 130 us, 5.4 TB/s, 3 workgroups a CU; the
+// append of 13K tokens in 32 chunks, 16 + 2 heads: 35 us, 3.8 TB/s, a quarter of
+// it the chain of loads that finds a token's place.
 #include "jb_attn.h"
 #include "jb_device.h"
 
@@ -45,9 +49,9 @@ template <> struct Raw<float> {
   __device__ float get(int i) const { return __uint_as_float(u[i]); }
 };
 typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
-// NT: a stream that no cache need keep.  Stores of q_out and of training's
-// outputs, and the backward's loads; 64K tokens took 98 and 143 us without,
-// 96 and 133 with (the forward's loads, which gain nothing, stay plain).
+// NT: a stream that no cache need keep: training's loads and stores and the
+// append's q_out.  64K tokens took 93 us forward and 143 backward without, 88
+// and 130 with; the append's own loads gain nothing.
 template <bool NT = false, typename T> __device__ __forceinline__ Raw<T> load8(const T* p) {
   Raw<T> r;
 #pragma unroll
@@ -180,11 +184,12 @@ template <typename T> __device__ __forceinline__ void weights(const void* w, int
   }
 }
 
-constexpr int UNROLL = 4;  // rows of a lane group in flight
-
 template <int D, typename IO, typename OUT, bool PAGED>
 __global__ __launch_bounds__(256) void rope_kernel(Args a) {
   constexpr int L = D / 8, GROUPS = 256 / L;
+  // rows in use, and as many on their way (64K tokens: 4 took 91 us, 2 93, and 96
+  // with none on their way; an append of 13K tokens: 2 take 35 us, 4 38)
+  constexpr int U = PAGED || sizeof(IO) == 4 ? 2 : 4;
   const RopeCall& c = a.c;
   const int lane = lane_id(), s = lane % L, group = threadIdx.x / L;
   const int64_t unit = (int64_t)blockIdx.x * GROUPS + group;
@@ -197,16 +202,16 @@ __global__ __launch_bounds__(256) void rope_kernel(Args a) {
   const IO* q = (const IO*)c.q + t * c.q_stride + 8 * s;
   const IO* k = (const IO*)c.k + t * c.k_stride + 8 * s;
   const IO* v = (const IO*)c.v + (PAGED ? t * c.v_stride + 8 * s : 0);
-  Raw<IO> x[UNROLL];
-  auto fetch = [&](int h) {
+  Raw<IO> x[U], next[U];
+  auto fetch = [&](Raw<IO>(&x)[U], int h) {
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int i = min(h + u, h1 - 1);
-      x[u] = load8(i < c.H ? q + (int64_t)i * D : i < c.H + c.Hkv ? k + (int64_t)(i - c.H) * D
+      x[u] = load8<!PAGED>(i < c.H ? q + (int64_t)i * D : i < c.H + c.Hkv ? k + (int64_t)(i - c.H) * D
                                                               : v + (int64_t)(i - c.H - c.Hkv) * D);
     }
   };
-  fetch(h0);
+  fetch(x, h0);
   const int es = partner<D>(c, s) * 8, from = (lane & ~(L - 1)) + es / 8;
   float f[8], wq[8], wqp[8], wk[8], wkp[8];
   frequencies(c, s, f);
@@ -260,10 +265,10 @@ __global__ __launch_bounds__(256) void rope_kernel(Args a) {
     ck[i] = wk[i] * turn.cos[i];
     sk[i] = (c.interleaved ? wkp[i ^ 1] : wkp[i]) * turn.sin[i];
   }
-  for (int h = h0; h < h1; h += UNROLL) {
-    if (h > h0) fetch(h);
+  for (int h = h0; h < h1; h += U) {
+    if (h + U < h1) fetch(next, h + U);
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int i = h + u;
       if (i >= h1) break;
       if (PAGED && i >= c.H + c.Hkv) {
@@ -287,12 +292,14 @@ __global__ __launch_bounds__(256) void rope_kernel(Args a) {
       else if (!PAGED) store8<true>((OUT*)c.k_out + (t * c.Hkv + i - c.H) * D + 8 * s, y);
       else if (slot >= 0) store8<false>((OUT*)c.k_out + slot + (int64_t)(i - c.H) * c.page * D + 8 * s, y);
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = next[u];
   }
 }
 
 template <int D, typename IO, typename GR>
 __global__ __launch_bounds__(256, 3) void rope_backward_kernel(Args a) {
-  constexpr int L = D / 8, GROUPS = 256 / L, U = sizeof(IO) + sizeof(GR) > 4 ? 2 : UNROLL;
+  constexpr int L = D / 8, GROUPS = 256 / L, U = sizeof(IO) + sizeof(GR) > 4 ? 2 : 4;
   const RopeCall& c = a.c;
   const int lane = lane_id(), s = lane % L, group = threadIdx.x / L;
   const int from = (lane & ~(L - 1)) + partner<D>(c, s);
@@ -389,10 +396,11 @@ int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
 
 // A token's heads go to one lane group, which then forms its angles once,
 // unless that leaves the chip short of waves.
-Args args_of(const RopeCall& c, int nh) {
+Args args_of(const RopeCall& c) {
+  const int nh = c.H + (c.paged ? 2 : 1) * c.Hkv;
   Args a;
   a.c = c;
-  const int64_t groups = 4096 * (512 / c.D);  // lane groups of 4096 waves
+  const int64_t groups = (c.paged ? 8192 : 4096) * (512 / c.D);  // lane groups of that many waves
   int64_t parts = std::min<int64_t>(std::max<int64_t>(groups / std::max<int64_t>(c.total, 1), 1), nh);
   a.heads = (int)cdiv(nh, parts);
   a.parts = (int)cdiv(nh, a.heads);
@@ -402,7 +410,7 @@ Args args_of(const RopeCall& c, int nh) {
 }
 
 template <int D, typename IO, typename OUT> hipError_t forward(const RopeCall& c, hipStream_t stream) {
-  const Args a = args_of(c, c.H + (c.paged ? 2 : 1) * c.Hkv);
+  const Args a = args_of(c);
   const dim3 grid((unsigned)cdiv(a.units, 256 / (D / 8)));
   if (c.paged) rope_kernel<D, IO, OUT, true><<<grid, dim3(256), 0, stream>>>(a);
   else rope_kernel<D, IO, OUT, false><<<grid, dim3(256), 0, stream>>>(a);
@@ -414,7 +422,7 @@ constexpr int BWD_GROUPS = 768;  // workgroups of the backward pass at most: 3 a
 int backward_blocks(const Args& a) { return (int)std::min<int64_t>(cdiv(a.units, 256 / (a.c.D / 8)), BWD_GROUPS); }
 
 template <int D, typename IO, typename GR> hipError_t backward(const RopeCall& c, hipStream_t stream) {
-  Args a = args_of(c, c.H + c.Hkv);
+  Args a = args_of(c);
   const int n = backward_blocks(a);
   if (c.dwq || c.dwk) a.sums = static_cast<float*>(c.workspace);
   rope_backward_kernel<D, IO, GR><<<dim3(n), dim3(256), 0, stream>>>(a);
@@ -447,11 +455,11 @@ template <int D, typename IO, typename OUT> struct Backward {
 }  // namespace
 
 int64_t rope_workgroups(const RopeCall& c) {
-  return cdiv(args_of(c, c.H + (c.paged ? 2 : 1) * c.Hkv).units, 256 / (c.D / 8));
+  return cdiv(args_of(c).units, 256 / (c.D / 8));
 }
 
 size_t rope_backward_workspace_bytes(const RopeCall& c) {
-  return c.total == 0 ? 0 : (size_t)backward_blocks(args_of(c, c.H + c.Hkv)) * 2 * c.D * sizeof(float);
+  return c.total == 0 ? 0 : (size_t)backward_blocks(args_of(c)) * 2 * c.D * sizeof(float);
 }
 
 hipError_t launch_rope(const RopeCall& c, hipStream_t stream) { return dispatch<Forward>(c, stream); }
