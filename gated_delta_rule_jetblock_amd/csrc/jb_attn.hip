@@ -538,7 +538,7 @@ __device__ __forceinline__ int64_t out_row(const Args& a, const Seq& s, int kvh,
 // share a SIMD; 128 rows a workgroup keep two on a CU (64 KB of LDS, 208
 // registers) and read every K and V value once for 128 queries.  2K tokens on 64K
 // rows, 12 heads on 2: 735 us, 1105 TFLOP/s (the library's product of 8192^3
-// reaches 1226 on this card), matrix cores busy 60% of the cycles at the 1.75 GHz
+// reaches 1226 on this card), matrix cores busy 62% of the cycles at the 1.7 GHz
 // the card then holds, no bank conflicts.  Head size 64, as much vector work for
 // half the products: 790 TFLOP/s; 256, one wave a SIMD: 970.
 template <int D, typename OUT>
