@@ -524,6 +524,27 @@ template <> __device__ __forceinline__ void store4<bf16_t>(bf16_t* p, f4_t v) {
   *reinterpret_cast<uint2*>(p) = u;
 }
 
+// A wave's staged rows 0 .. rows - 1 to memory, 16 bytes a lane; lane i (and lane
+// 32 + i) knows where row i goes.  (Found anew for every row, their places cost 2
+// us at every workgroup's end, 5% of the windowed case.)
+template <int D, typename T> __device__ __forceinline__ void leave_rows(T* out, lds_char* st, int64_t at, int rows) {
+  constexpr int N = 16 / sizeof(T), LPR = D / N;  // values a lane, lanes a row
+  const int lane = lane_id(), d = lane % LPR * N;
+#pragma unroll
+  for (int i0 = 0; i0 < 32; i0 += 64 / LPR) {
+    const int i = i0 + lane / LPR;
+    const int64_t to = (int64_t)(uint32_t)__shfl((int)at, i, WAVE) | (int64_t)__shfl((int)(at >> 32), i, WAVE) << 32;
+    const f4_t v = *stage_at<D>(st, i, d);
+    u4_t u = __builtin_bit_cast(u4_t, v);
+    if constexpr (N == 8) {
+      const f4_t x = *stage_at<D>(st, i, d + 4);
+      u = u4_t{f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16, f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16,
+               f32_to_bf16(x[0]) | (uint32_t)f32_to_bf16(x[1]) << 16, f32_to_bf16(x[2]) | (uint32_t)f32_to_bf16(x[3]) << 16};
+    }
+    if (i < rows) *reinterpret_cast<u4_t*>(out + to * D + d) = u;
+  }
+}
+
 // where row r (of a sequence's T G) of key head kvh goes: row index of o, lse
 __device__ __forceinline__ int64_t out_row(const Args& a, const Seq& s, int kvh, int64_t r) {
   const int i = token_of(a, r);
@@ -537,7 +558,7 @@ __device__ __forceinline__ int64_t out_row(const Args& a, const Seq& s, int kvh,
 // quarter of the rate, the maximum, the sums), so two waves of two workgroups
 // share a SIMD; 128 rows a workgroup keep two on a CU (64 KB of LDS, 208
 // registers) and read every K and V value once for 128 queries.  2K tokens on 64K
-// rows, 12 heads on 2: 735 us, 1105 TFLOP/s (the library's product of 8192^3
+// rows, 12 heads on 2: 722 us, 1125 TFLOP/s (the library's product of 8192^3
 // reaches 1226 on this card), matrix cores busy 62% of the cycles at the 1.7 GHz
 // the card then holds, no bank conflicts.  Head size 64, as much vector work for
 // half the products: 790 TFLOP/s; 256, one wave a SIMD: 970.
@@ -605,8 +626,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
   const int c = lane & 31, g = lane >> 5;
   const int64_t r = r0 + wave * 32 + c;
   const bool split_out = a.nsplit > 1;
+  const int64_t at = r < nr ? out_row(a, s, kvh, r) : 0;
   if (g == 0 && r < nr) {
-    const int64_t at = out_row(a, s, kvh, r);
     if (split_out) a.part_ml[split * a.rows + at] = make_float2(w.m, l);
     else if (a.lse) a.lse[at] = l == 0.f ? -INFINITY : (w.m + fast_log2(l)) * LN2;
   }
@@ -620,16 +641,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
       *stage_at<D>(st, c, 32 * db + 8 * e + 4 * g) =
           f4_t{w.o[db][4 * e] * f, w.o[db][4 * e + 1] * f, w.o[db][4 * e + 2] * f, w.o[db][4 * e + 3] * f};
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  constexpr int LPR = D / 4;  // lanes a row
-  for (int i = lane / LPR; i < 32; i += 64 / LPR) {
-    const int64_t rr = r0 + wave * 32 + i;
-    if (rr >= nr) break;
-    const int64_t at = out_row(a, s, kvh, rr);
-    const int d = (lane % LPR) * 4;
-    const f4_t v = *stage_at<D>(st, i, d);
-    if (split_out) *reinterpret_cast<f4_t*>(a.part_o + (split * a.rows + at) * D + d) = v;
-    else store4((OUT*)a.o + at * D + d, v);
-  }
+  const int rows = (int)min(max(nr - r0 - wave * 32, (int64_t)0), (int64_t)32);
+  if (split_out) leave_rows<D>(a.part_o + split * a.rows * D, st, at, rows);
+  else leave_rows<D>((OUT*)a.o, st, at, rows);
 }
 
 // Decode: sequences of at most 32 query rows.  A unit is one key head of one

@@ -9,7 +9,6 @@ importing this module raises, and a call on CPU tensors raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 import re
 
@@ -607,18 +606,15 @@ def _launch(di: int, fn, *args):
             _check(fn(*args, _raw_stream(di)))
 
 
-def _on_stream(fn):
-    """Adds the `stream` argument (a torch stream or a handle): the call, and what it allocates,
-    belong to that stream, so nothing it still uses is handed out on another."""
-    @functools.wraps(fn)
-    def call(q, *args, stream=None, **kw):
-        if stream is None:
-            return fn(q, *args, **kw)
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=q.device)
-        with torch.cuda.stream(stream):
-            return fn(q, *args, **kw)
-    return call
+def _on_stream(fn, args):
+    """fn(**args) on the stream args names (a torch stream or a handle): the call, and what it
+    allocates, belong to that stream, so nothing it still uses is handed out on another."""
+    args = dict(args)
+    stream = args.pop("stream")
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=args["q"].device)
+    with torch.cuda.stream(stream):
+        return fn(**args)
 
 
 def _empty(like, dtype):
@@ -632,18 +628,19 @@ def _rope_flags(interleaved, normalize):
     return (ROPE_INTERLEAVED if interleaved else 0) | (0 if normalize else ROPE_NO_NORM)
 
 
-@_on_stream
 def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, *, eps=1e-6, interleaved=False, normalize=True,
-                 out_dtype=None, q_out=None, k_out=None):
+                 out_dtype=None, q_out=None, k_out=None, stream=None):
     """jb_qk_norm_rope.  q [tokens,H,D] or [B,T,H,D], k likewise with Hkv heads (any distance
     between tokens), positions int32 [tokens], inv_freq f32 [rot/2], wq, wk [D].  Returns
     (q_out, k_out), contiguous, of out_dtype (default: q's)."""
+    if stream is not None:
+        return _on_stream(qk_norm_rope, locals())
     di, io = _device(q), q.dtype
     out_dtype = out_dtype or (q_out.dtype if q_out is not None else io)
     _same(di, (io, "k wq wk", (k, wq, wk)), (torch.int32, "positions", (positions,)),
           (torch.float32, "inv_freq", (inv_freq,)), (out_dtype, "q_out k_out", (q_out, k_out)))
     H, D = q.shape[-2:]
-    Hkv = k.shape[-2]
+    Hkv, pairs = k.shape[-2], inv_freq.numel()
     qp, n, qs = _rows(q, "q")
     kp, nk, ks = _rows(k, "k")
     if nk != n or k.shape[-1] != D:
@@ -652,10 +649,10 @@ def qk_norm_rope(q, k, positions, inv_freq, wq=None, wk=None, *, eps=1e-6, inter
         q_out = _empty(q, out_dtype)
     if k_out is None:
         k_out = _empty(k, out_dtype)
-    shape = AttnShape(1, n, H, Hkv, D, 2 * inv_freq.numel(), 0, 0, 0, 0, 0, _io_code(q), _code(out_dtype),
+    shape = AttnShape(1, n, H, Hkv, D, 2 * pairs, 0, 0, 0, 0, 0, _io_code(q), _code(out_dtype),
                       _rope_flags(interleaved, normalize), qs, ks, 0, 0)
     _launch(di, _lib.jb_qk_norm_rope, shape, qp, kp, _flat(wq, "wq", D), _flat(wk, "wk", D),
-            _flat(inv_freq, "inv_freq", inv_freq.numel()), _positions(positions, n), eps,
+            _flat(inv_freq, "inv_freq", pairs), _positions(positions, n), eps,
             _flat(q_out, "q_out", *q.shape), _flat(k_out, "k_out", *k.shape))
     return q_out, k_out
 
@@ -666,18 +663,19 @@ def qk_norm_rope_backward_workspace_size(shape: AttnShape) -> int:
     return n.value
 
 
-@_on_stream
 def qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, wq=None, wk=None, *, eps=1e-6,
-                          interleaved=False, normalize=True, dq=None, dk=None, ws=None):
+                          interleaved=False, normalize=True, dq=None, dk=None, ws=None, stream=None):
     """jb_qk_norm_rope_backward: gradients of qk_norm_rope from those of its outputs (contiguous,
     bf16 or f32).  Returns dict(dq, dk, dwq, dwk): dq, dk of dq_out's dtype, dwq, dwk f32 [D]
     (None without the norm)."""
+    if stream is not None:
+        return _on_stream(qk_norm_rope_backward, locals())
     di, dev, io, gr = _device(q), q.device, q.dtype, dq_out.dtype
     _same(di, (io, "k wq wk", (k, wq, wk)), (torch.int32, "positions", (positions,)),
           (torch.float32, "inv_freq", (inv_freq,)), (gr, "dq_out dk_out dq dk", (dq_out, dk_out, dq, dk)),
           (torch.uint8, "ws", (ws,)))
     H, D = q.shape[-2:]
-    Hkv = k.shape[-2]
+    Hkv, pairs = k.shape[-2], inv_freq.numel()
     qp, n, qs = _rows(q, "q")
     kp, nk, ks = _rows(k, "k")
     if nk != n or k.shape[-1] != D:
@@ -688,15 +686,15 @@ def qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, wq=None, wk
     if normalize:
         dwq = torch.empty(D, dtype=torch.float32, device=dev)
         dwk = torch.empty(D, dtype=torch.float32, device=dev)
-    shape = AttnShape(1, n, H, Hkv, D, 2 * inv_freq.numel(), 0, 0, 0, 0, 0, _io_code(q), _code(gr),
+    shape = AttnShape(1, n, H, Hkv, D, 2 * pairs, 0, 0, 0, 0, 0, _io_code(q), _code(gr),
                       _rope_flags(interleaved, normalize), qs, ks, 0, 0)
     if ws is None:
         ws = workspace(qk_norm_rope_backward_workspace_size(shape), dev)
     _launch(di, _lib.jb_qk_norm_rope_backward, shape, qp, kp, _flat(wq, "wq", D), _flat(wk, "wk", D),
-            _flat(inv_freq, "inv_freq", inv_freq.numel()), _positions(positions, n), eps,
+            _flat(inv_freq, "inv_freq", pairs), _positions(positions, n), eps,
             _flat(dq_out, "dq_out", *q.shape), _flat(dk_out, "dk_out", *k.shape), _flat(dq, "dq", *q.shape),
             _flat(dk, "dk", *k.shape), _flat(dwq, "dwq", D), _flat(dwk, "dwk", D), ws.data_ptr(), ws.numel())
-    return dict(dq=dq, dk=dk, dwq=dwq, dwk=dwk)
+    return {"dq": dq, "dk": dk, "dwq": dwq, "dwk": dwk}
 
 
 def _batch(q, cu_seqlens, max_seqlen):
@@ -726,19 +724,21 @@ def _pages(k_cache, v_cache, page_table, kv_lens, B, D):
     return P, Hkv, page, st[0] if P > 1 else 0, table[1]
 
 
-@_on_stream
 def qk_norm_rope_paged(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq, wq=None, wk=None, *,
                        cu_seqlens=None, max_seqlen: int | None = None, positions=None, eps=1e-6, interleaved=False,
-                       normalize=True, q_out=None):
+                       normalize=True, q_out=None, stream=None):
     """jb_qk_norm_rope_paged: rotated queries out, rotated keys and values into the caches
     [pages,Hkv,page,D] (in place).  q [B,T,H,D], [B,H,D] (one token each) or packed [tokens,H,D]
     with cu_seqlens int32 [B+1]; page_table int32 [B,max_pages], kv_lens int32 [B] (the new tokens
     among the rows).  Returns dict(q, k_cache, v_cache)."""
+    if stream is not None:
+        return _on_stream(qk_norm_rope_paged, locals())
     di, io = _device(q), q.dtype
     _same(di, (io, "k v k_cache v_cache wq wk q_out", (k, v, k_cache, v_cache, wq, wk, q_out)),
           (torch.int32, "page_table kv_lens cu_seqlens positions", (page_table, kv_lens, cu_seqlens, positions)),
           (torch.float32, "inv_freq", (inv_freq,)))
     H, D = q.shape[-2:]
+    pairs = inv_freq.numel()
     qp, n, qs = _rows(q, "q")
     kp, nk, ks = _rows(k, "k")
     vp, nv, vs = _rows(v, "v")
@@ -749,15 +749,15 @@ def qk_norm_rope_paged(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq,
     if q_out is None:
         q_out = _empty(q, io)
     code = _io_code(q)
-    shape = AttnShape(B, T, H, Hkv, D, 2 * inv_freq.numel(), page, max_pages, P, 0, 0, code, code,
+    shape = AttnShape(B, T, H, Hkv, D, 2 * pairs, page, max_pages, P, 0, 0, code, code,
                       _rope_flags(interleaved, normalize), qs, ks, vs, ps)
     _launch(di, _lib.jb_qk_norm_rope_paged, shape, n,
             None if cu_seqlens is None else _flat(cu_seqlens, "cu_seqlens", B + 1), _flat(kv_lens, "kv_lens", B),
             _flat(page_table, "page_table", B, max_pages), qp, kp, vp, _flat(wq, "wq", D), _flat(wk, "wk", D),
-            _flat(inv_freq, "inv_freq", inv_freq.numel()),
+            _flat(inv_freq, "inv_freq", pairs),
             None if positions is None else _positions(positions, n), eps,
             _flat(q_out, "q_out", *q.shape), k_cache.data_ptr(), v_cache.data_ptr())
-    return dict(q=q_out, k_cache=k_cache, v_cache=v_cache)
+    return {"q": q_out, "k_cache": k_cache, "v_cache": v_cache}
 
 
 def attn_paged_workspace_size(shape: AttnShape, total_tokens: int, packed: bool) -> int:
@@ -766,15 +766,16 @@ def attn_paged_workspace_size(shape: AttnShape, total_tokens: int, packed: bool)
     return n.value
 
 
-@_on_stream
 def attn_paged(q, k_cache, v_cache, page_table, kv_lens, *, cu_seqlens=None, max_seqlen: int | None = None,
                max_kv: int | None = None, window: int = 0, scale: float | None = None, out_dtype=None, o=None,
-               want_lse=False, lse=None, ws=None):
+               want_lse=False, lse=None, ws=None, stream=None):
     """jb_attn_paged: attention of each sequence's new tokens over its paged cache (which holds
     them already).  q [B,T,H,D], [B,H,D] (decode) or packed [tokens,H,D] with cu_seqlens int32
     [B+1]; caches, page_table and kv_lens as for qk_norm_rope_paged.  max_seqlen and max_kv, host
     integers, are the longest sequence's new tokens (packed; default: all) and cache rows (default:
     the table's capacity); they plan the launch, nothing is read back from the device.  Returns
+    if stream is not None:
+        return _on_stream(attn_paged, locals())
     dict(o, lse): o of q's shape and out_dtype (default: q's), lse f32 [..., H] or None."""
     di, io = _device(q), q.dtype
     out_dtype = out_dtype or (o.dtype if o is not None else io)
@@ -804,4 +805,4 @@ def attn_paged(q, k_cache, v_cache, page_table, kv_lens, *, cu_seqlens=None, max
             v_cache.data_ptr(), 0.0 if scale is None else float(scale), _flat(o, "o", *q.shape),
             _flat(lse, "lse", *q.shape[:-1]), None if ws is None else ws.data_ptr(),
             0 if ws is None else ws.numel())
-    return dict(o=o, lse=lse)
+    return {"o": o, "lse": lse}
