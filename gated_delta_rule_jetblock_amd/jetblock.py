@@ -774,9 +774,9 @@ def attn_paged(q, k_cache, v_cache, page_table, kv_lens, *, cu_seqlens=None, max
     [B+1]; caches, page_table and kv_lens as for qk_norm_rope_paged.  max_seqlen and max_kv, host
     integers, are the longest sequence's new tokens (packed; default: all) and cache rows (default:
     the table's capacity); they plan the launch, nothing is read back from the device.  Returns
+    dict(o, lse): o of q's shape and out_dtype (default: q's), lse f32 [..., H] or None."""
     if stream is not None:
         return _on_stream(attn_paged, locals())
-    dict(o, lse): o of q's shape and out_dtype (default: q's), lse f32 [..., H] or None."""
     di, io = _device(q), q.dtype
     out_dtype = out_dtype or (o.dtype if o is not None else io)
     _same(di, (io, "k_cache v_cache", (k_cache, v_cache)),

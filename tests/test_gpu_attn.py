@@ -392,3 +392,30 @@ def test_first_offset_is_not_zero(jb):
         o = torch.full(d["q"].shape, 5.0, dtype=dtype, device="cuda")
         r = call(jb, d, o=o)
         assert torch.equal(r["o"][9:], e["o"][:31]) and (o[:9] == 5).all()
+
+
+def test_a_call_waits_for_its_stream(jb):
+    """Inputs that the given stream writes late, behind long work: every call with that stream reads
+    them as written (on the current stream it would find them too early)."""
+    d = batch([1] * 3, [900, 400, 100], 12, 2, 128, 64, BF, seed=23)
+    g = {k: v.cuda() for k, v in d.items()}
+    x, k, v = g["q"], torch.randn(3, 2, 128, device="cuda").to(BF), torch.randn(3, 2, 128, device="cuda").to(BF)
+    pos, fr = torch.arange(3, dtype=torch.int32, device="cuda"), torch.rand(64, device="cuda")
+    tail = (g["k_cache"], g["v_cache"], g["table"], g["kv"])
+    runs = [lambda q, **a: jb.qk_norm_rope(q, k, pos, fr, **a)[0],
+            lambda q, **a: jb.qk_norm_rope_backward(q, k, pos, fr, torch.ones_like(q), k, **a)["dq"],
+            lambda q, **a: jb.qk_norm_rope_paged(q, k, v, g["k_cache"].clone(), g["v_cache"].clone(), *tail[2:], fr, **a)["q"],
+            lambda q, **a: jb.attn_paged(q, *tail, **a)["o"]]
+    s, busy = torch.cuda.Stream(), torch.randn(8192, 8192, device="cuda").to(BF)
+    for i, run in enumerate(runs):
+        print(f"[late input, call {i}]", flush=True)
+        want, q = run(x), torch.zeros_like(x)
+        run(q, stream=s)  # (allocations of the first call are behind us)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                busy @ busy
+            q.copy_(x)
+        got = run(q, stream=s)
+        s.synchronize()
+        assert torch.equal(got, want), i

@@ -168,3 +168,15 @@ def test_binding_refuses_what_does_not_fit(jb):
         jb._code(torch.float16)
     with pytest.raises(ValueError):
         jb._flat(q[:, :2], "q", 6, 2, 64)
+
+
+@pytest.mark.parametrize("name", ["qk_norm_rope", "qk_norm_rope_backward", "qk_norm_rope_paged", "attn_paged"])
+def test_stream_argument_is_taken(jb, monkeypatch, name):
+    """With a stream every call goes through the stream's own context, its other arguments as given;
+    the documentation holds nothing but words."""
+    import inspect
+    fn, seen = getattr(jb, name), []
+    monkeypatch.setattr(jb, "_on_stream", lambda f, args: seen.append((f, dict(args))) or "there")
+    given = {n: object() for n, p in inspect.signature(fn).parameters.items()}
+    assert fn(**given) == "there" and seen == [(fn, given)]
+    assert "return _on" not in fn.__doc__ and fn.__doc__.rstrip().endswith(".")
