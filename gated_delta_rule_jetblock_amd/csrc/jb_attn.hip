@@ -811,7 +811,10 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_row_kernel(Args a) {
     }
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     const bool whole = s0 == 0 && s1 == steps;
-    if (s0 == 0 && !whole) shared = {b, kvh, (int)quotient(at + steps - 1, 1.0 / run_steps) - (int)blockIdx.x, seg};
+    if (s0 == 0 && !whole) {  // (in the grid whatever the lengths in memory do meanwhile)
+      const int last = (int)min(quotient(at + steps - 1, 1.0 / run_steps), (int64_t)gridDim.x - 1);
+      shared = {b, kvh, last - (int)blockIdx.x, seg};
+    }
     const int64_t slot = 2 * (int64_t)blockIdx.x + seg;
     constexpr int LPR = D / 4;
     for (int i = threadIdx.x / LPR; i < nr; i += NTHR / LPR) {
