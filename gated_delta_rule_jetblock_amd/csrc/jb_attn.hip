@@ -1196,18 +1196,26 @@ Plan plan(const AttnCall& c) {
     p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 128));
     return p;
   }
-  // Tiles: the least of the rounds the pieces take on the chip's workgroup
-  // slots (tiles of 64 rows and some 4 tiles' worth of start and end each, 2.2
-  // us a tile at D = 128) plus the join's traffic.  At 2K new tokens on 64K
-  // rows (192 units): 6 pieces 1119 us, 8 (three whole rounds) 975, 16 1108;
-  // an 8K prompt (1024 units): 1 piece 290 us, 2 331.
-  const double work = (double)p.slots * c.Hkv, resident = 256 * (c.D == 64 ? 3 : c.D == 128 ? 2 : 1);
-  const double tiles = (double)cdiv(c.window ? std::min<int64_t>(c.max_kv, c.window + R / G) : c.max_kv, 64);
-  const double us = 2.2 * c.D / 128 * (resident / 512), rows = (double)c.total * c.H;
+  // Tiles: the least of the rounds the pieces take on the chip's workgroup slots
+  // (tiles of 64 rows, in the mean over the queries, and some 4 tiles' worth of
+  // start and end each; the longest range alone is a bound too) plus the join's
+  // traffic.  A workgroup alone on its CU walks a tile in 1.7 us (D = 128), 2.0
+  // with a second one there, so a last round of at most 256 costs less than a
+  // whole one.  2K tokens, 16 heads on 2 (256 units) under a window of 1152: 1
+  // piece 33 us, 2 40; 2K tokens on 64K rows (192 units): 6 pieces 1119 us, 8
+  // (three whole rounds) 975, 16 1108; an 8K prompt (1024 units): 1 piece 290
+  // us, 2 331 (the last two with an earlier form of the kernel).
+  const int cu = c.D == 64 ? 3 : c.D == 128 ? 2 : 1;  // workgroups a CU holds
+  const int64_t work = p.slots * c.Hkv;
+  auto tiles = [&](int64_t kv) { return (double)cdiv(c.window ? std::min<int64_t>(kv, c.window + R / G) : kv, 64); };
+  const double longest = tiles(c.max_kv), mean = tiles(std::max<int64_t>(c.max_kv - c.T / 2, 1));
+  const double rows = (double)c.total * c.H;
+  auto walk = [&](int64_t on_a_cu) { return on_a_cu ? 1.7 * (1 + 0.2 * (on_a_cu - 1)) * c.D / 128 : 0.; };
   double best = 0;
-  for (int n = 1; n <= 64 && n <= std::max(tiles / 4, 1.0); ++n) {
-    const double t = std::ceil(work * n / resident) * (tiles / n + 4) * us +
-                     (n > 1 ? 5 + rows * c.D * 8 * n / 5e6 : 0);
+  for (int n = 1; n <= 64 && n <= std::max(longest / 4, 1.0); ++n) {
+    const int64_t whole = work * n / (256 * cu), rest = work * n % (256 * cu);
+    const double t = std::max((mean / n + 4) * (whole * walk(cu) + walk(cdiv(rest, 256))), (longest / n + 4) * walk(1)) +
+                     (n > 1 ? 5 + rows * c.D * 8 * n / 6e6 : 0);
     if (n == 1 || t < best) best = t, p.nsplit = n;
   }
   return p;
