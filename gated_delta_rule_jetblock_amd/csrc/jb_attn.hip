@@ -682,26 +682,13 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_row_kernel(Args a) {
     at = (int64_t)(blockIdx.x % (unsigned)a.Hkv) * n;
     end = at + n;
   } else {
-    // steps of 64 NW sequences at a time, added up; then this run's place
-    int64_t all = 0;
-    for (int i = 0; i < a.B; i += NTHR) {
-      int v = i + (int)threadIdx.x < a.B ? steps_of(a, seq_of(a, i + threadIdx.x), STEP) : 0;
-#pragma unroll
-      for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, WAVE);
-      if (lane == 0) sums[wave] = v;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < NW; ++w) all += sums[w];
-      __syncthreads();
-    }
-    all *= a.Hkv;
-    const int64_t per = quotient(all + gridDim.x - 1, 1.0 / gridDim.x);
-    at = min(blockIdx.x * per, all);
-    end = min(at + per, all);
+    // The steps of 64 NW sequences at a time, added up; then this run's place
+    // among them, at once where one pass has seen them all.
     if (threadIdx.x == 0) found[0] = found[1] = 0;
-    int64_t base = 0;
-    for (int i = 0; i < a.B; i += NTHR) {
-      const int n = i + (int)threadIdx.x < a.B ? steps_of(a, seq_of(a, i + threadIdx.x), STEP) : 0;
+    int64_t base, before;  // steps of the sequences up to here, and before this thread's
+    int n;                 // this thread's
+    auto add = [&](int i) {
+      n = i + (int)threadIdx.x < a.B ? steps_of(a, seq_of(a, i + threadIdx.x), STEP) : 0;
       int v = n;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
@@ -710,15 +697,32 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_row_kernel(Args a) {
       }
       if (lane == 63) sums[wave] = v;
       __syncthreads();
-      int64_t before = base + (int64_t)(v - n) * a.Hkv;
+      before = base + (int64_t)(v - n) * a.Hkv;
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
         if (w < wave) before += (int64_t)sums[w] * a.Hkv;
         base += (int64_t)sums[w] * a.Hkv;
       }
-      if (before <= at && at < before + (int64_t)n * a.Hkv) found[0] = i + threadIdx.x, found[1] = before;
       __syncthreads();
+    };
+    auto look = [&](int i) {
+      if (before <= at && at < before + (int64_t)n * a.Hkv) found[0] = i + threadIdx.x, found[1] = before;
+    };
+    base = 0;
+    for (int i = 0; i < a.B; i += NTHR) add(i);
+    const int64_t per = quotient(base + gridDim.x - 1, 1.0 / gridDim.x);
+    at = min(blockIdx.x * per, base);
+    end = min(at + per, base);
+    if (a.B <= NTHR) {
+      look(0);
+    } else {
+      base = 0;
+      for (int i = 0; i < a.B; i += NTHR) {
+        add(i);
+        look(i);
+      }
     }
+    __syncthreads();
     b = uniform((int)found[0]);
     start = found[1];
     run_steps = per;
@@ -1206,7 +1210,8 @@ Plan plan(const AttnCall& c) {
   // (three whole rounds) 975, 16 1108; an 8K prompt (1024 units): 1 piece 290
   // us, 2 331 (the last two with an earlier form of the kernel).
   const int cu = c.D == 64 ? 3 : c.D == 128 ? 2 : 1;  // workgroups a CU holds
-  const int64_t work = p.slots * c.Hkv;
+  // (a packed batch has more slots than tiles; half a tile of each sequence is a guess)
+  const int64_t work = (c.packed ? cdiv(c.total * G, R) + c.B / 2 : p.slots) * c.Hkv;
   auto tiles = [&](int64_t kv) { return (double)cdiv(c.window ? std::min<int64_t>(kv, c.window + R / G) : kv, 64); };
   const double longest = tiles(c.max_kv), mean = tiles(std::max<int64_t>(c.max_kv - c.T / 2, 1));
   const double rows = (double)c.total * c.H;
