@@ -69,20 +69,22 @@ struct Args {
   int B, T, H, Hkv, G, pshift, max_pages, num_pages, window, nsplit;
   bool few;                                    // attn_row_kernel takes sequences of at most 32 rows
   bool direct;                                 // a unit of those is a workgroup
-  int64_t total, rows, q_stride, page_stride;  // rows: total H
+  int64_t total, q_stride, page_stride;
+  int64_t whole, tail;                         // row tiles: the first ones, and those in nsplit pieces
+  int pitch;                                   // rows of a tile's piece
   const int* cu;                               // NULL: dense, B x T tokens
   const int* kv_lens;
   const int* table;
   const void *q, *k, *v;
   void* o;
   float* lse;
-  float* part_o;   // [nsplit][rows][D]
-  float2* part_ml; // [nsplit][rows]
+  float* part_o;   // [nsplit][tail][Hkv][pitch][D]
+  float2* part_ml; // [nsplit][tail][Hkv][pitch]
   float* run_o;    // [2 a workgroup][32][D]: attn_row_kernel's shared units
   float2* run_ml;  // [2 a workgroup][32]
   Shared* shared;  // [workgroups]
   float scale;     // times log2 e
-  double inv_g, inv_h;
+  double inv_g;
 };
 
 // floor(n / d) from 1 / d in 64 bits, for 0 <= n, d with n < 2^41 and
@@ -116,29 +118,48 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
   return s;
 }
 
-// Sequence and first row (of its T G) of slot s.  Packed sequences: sequence
-// b's tiles of R rows start at slot base(b) = cu[b] G / R + b, which leaves
+// Sequence and first row (of its T G) of slot s, tiles of R = 2^rshift rows.
+// Packed sequences: sequence b's tiles start at slot base(b) = cu[b] G / R + b, which leaves
 // room for all of them and never decreases, so the sequence is the last one
 // whose base is not behind s (every thread looks at one base at a time).
-__device__ __forceinline__ void slot_of(const Args& a, int64_t s, int R, int& b, int64_t& r0) {
+__device__ __forceinline__ void slot_of(const Args& a, int64_t s, int rshift, int& b, int64_t& r0) {
   if (!a.cu) {
-    const int64_t per = ((int64_t)a.T * a.G + R - 1) / R;
+    const int64_t per = ((int64_t)a.T * a.G + (1 << rshift) - 1) >> rshift;
     b = (int)((uint32_t)s / (uint32_t)per);  // (both below 2^31: a grid's size, T G / R)
-    r0 = (s - b * per) * R;
+    r0 = (s - b * per) << rshift;
     return;
   }
   int n = 0;
   for (int i = 0; i < a.B; i += blockDim.x) {
     const int j = i + threadIdx.x;
-    const bool in = j < a.B && min(max((int64_t)a.cu[j], (int64_t)0), a.total) * a.G / R + j <= s;
+    const bool in = j < a.B && (min(max((int64_t)a.cu[j], (int64_t)0), a.total) * a.G >> rshift) + j <= s;
     const int c = __syncthreads_count(in);
     n += c;
     if (c < (int)blockDim.x) break;
   }
   b = uniform(max(n - 1, 0));
-  const int64_t base = min(max((int64_t)((const_int_p)a.cu)[b], (int64_t)0), a.total) * a.G / R + b;
-  r0 = (s - base) * R;
+  const int64_t base = (min(max((int64_t)((const_int_p)a.cu)[b], (int64_t)0), a.total) * a.G >> rshift) + b;
+  r0 = (s - base) * (1 << rshift);
 }
+
+// What a workgroup of the tile kernels takes: a slot's key head, and the piece
+// `split` of n of its cache range.  The longest ranges first: they end last.
+struct Place {
+  int kvh, split, n;
+  int64_t slot;
+  __device__ __forceinline__ explicit Place(const Args& a) {
+    const int64_t head = a.whole * a.Hkv;
+    n = blockIdx.x < head ? 1 : a.nsplit;
+    const uint32_t i = blockIdx.x < head ? blockIdx.x : (uint32_t)(blockIdx.x - head), q = i / (uint32_t)(a.Hkv * n);
+    const int combo = i - q * (uint32_t)(a.Hkv * n);
+    kvh = combo % a.Hkv, split = combo / a.Hkv;
+    slot = (n == 1 && a.whole ? a.whole + a.tail : a.tail) - 1 - q;
+  }
+  // index of row 0 in the pieces
+  __device__ __forceinline__ int64_t part(const Args& a) const {
+    return (((int64_t)split * a.tail + slot) * a.Hkv + kvh) * a.pitch;
+  }
+};
 
 // ---------------------------------------------------------------- bf16 tiles
 
@@ -482,13 +503,13 @@ __device__ __forceinline__ void clean_part(lds_char* v, int bytes) {
 struct Span {
   int lo, hi, t0, t1;
 };
-__device__ __forceinline__ Span span_of(const Args& a, const Seq& s, int64_t r0, int64_t r1, int R, int split) {
+__device__ __forceinline__ Span span_of(const Args& a, const Seq& s, int64_t r0, int64_t r1, int R, int split, int n) {
   Span x;
   const int base = s.kv - s.T, first = base + token_of(a, r0);
   x.hi = max(base + token_of(a, r1) + 1, 0);
   x.lo = a.window ? min(max(first - a.window + 1, 0), x.hi) : 0;
   const int n0 = x.lo / R, n1 = (x.hi + R - 1) / R;
-  const int per = (n1 - n0 + a.nsplit - 1) / a.nsplit;
+  const int per = (n1 - n0 + n - 1) / n;
   x.t0 = min(n0 + split * per, n1);
   x.t1 = min(x.t0 + per, n1);
   return x;
@@ -567,19 +588,17 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
   constexpr int NW = 4, R = 64, IMG = R * D * 2;
   __shared__ __attribute__((aligned(1024))) char ring[4 * IMG];  // K, V of an even tile, K, V of an odd one
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int combo = blockIdx.x % (unsigned)(a.Hkv * a.nsplit), kvh = combo % a.Hkv, split = combo / a.Hkv;
-  const int64_t nslot = gridDim.x / (unsigned)(a.Hkv * a.nsplit);
-  // the longest ranges first: they end last
-  const int64_t slot = nslot - 1 - blockIdx.x / (unsigned)(a.Hkv * a.nsplit);
+  const Place at(a);
+  const int kvh = at.kvh;
   int b;
   int64_t r0;
-  slot_of(a, slot, NW * 32, b, r0);
+  slot_of(a, at.slot, 7, b, r0);
   const Seq s = seq_of(a, b);
   const int64_t nr = (int64_t)s.T * a.G;
   if (r0 < 0 || r0 >= nr) return;  // (r0 < 0: offsets that decrease)
   if (a.few && nr <= 32) return;  // attn_row_kernel's
   const int64_t r1 = min(r0 + NW * 32, nr) - 1;
-  const Span x = span_of(a, s, r0, r1, R, split);
+  const Span x = span_of(a, s, r0, r1, R, at.split, at.n);
   Wave<D> w;
   w.init(a, s, kvh, r0 + wave * 32);
   Loader<D> ld(a, b, kvh);
@@ -589,8 +608,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
   auto tile = [&](int n) { return ord.tile(n); };
   auto issue = [&](int n) {
     const int row0 = tile(n) * R + wave * 16;
-    const uint32_t at = (uint32_t)(uintptr_t)(base + (n & 1) * 2 * IMG + wave * 16 * D * 2);
-    ld.load(a, row0, x.hi, at, at + IMG);
+    const uint32_t to = (uint32_t)(uintptr_t)(base + (n & 1) * 2 * IMG + wave * 16 * D * 2);
+    ld.load(a, row0, x.hi, to, to + IMG);
   };
   // the queries and the page indices arrive together, then the first tile leaves
   if (nt > 0) ld.page(a, min(tile(0) * R + wave * 16, x.hi - 1));
@@ -625,11 +644,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
   const float l = w.l + other_half(w.l);
   const int c = lane & 31, g = lane >> 5;
   const int64_t r = r0 + wave * 32 + c;
-  const bool split_out = a.nsplit > 1;
-  const int64_t at = r < nr ? out_row(a, s, kvh, r) : 0;
+  const bool split_out = at.n > 1;
+  const int64_t to = r >= nr ? 0 : split_out ? at.part(a) + wave * 32 + c : out_row(a, s, kvh, r);
   if (g == 0 && r < nr) {
-    if (split_out) a.part_ml[split * a.rows + at] = make_float2(w.m, l);
-    else if (a.lse) a.lse[at] = l == 0.f ? -INFINITY : (w.m + fast_log2(l)) * LN2;
+    if (split_out) a.part_ml[to] = make_float2(w.m, l);
+    else if (a.lse) a.lse[to] = l == 0.f ? -INFINITY : (w.m + fast_log2(l)) * LN2;
   }
   const float f = split_out ? 1.f : l == 0.f ? 0.f : 1.f / l;
   static_assert(NW * 32 * D * 4 <= 4 * IMG, "staging fits");
@@ -642,8 +661,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
           f4_t{w.o[db][4 * e] * f, w.o[db][4 * e + 1] * f, w.o[db][4 * e + 2] * f, w.o[db][4 * e + 3] * f};
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   const int rows = (int)min(max(nr - r0 - wave * 32, (int64_t)0), (int64_t)32);
-  if (split_out) leave_rows<D>(a.part_o + split * a.rows * D, st, at, rows);
-  else leave_rows<D>((OUT*)a.o, st, at, rows);
+  if (split_out) leave_rows<D>(a.part_o, st, to, rows);
+  else leave_rows<D>((OUT*)a.o, st, to, rows);
 }
 
 // Decode: sequences of at most 32 query rows.  A unit is one key head of one
@@ -907,46 +926,37 @@ __global__ __launch_bounds__(256) void attn_row_join_kernel(Args a, int rows) {
   if (sg == 0) x.template store<OUT, D>(a, out_row(a, s, u.kvh, r), d4 * 4);
 }
 
-// Adds up the pieces of every row, SG lane groups a row.  Rows no sequence owns
-// stay as they are.
+// Adds up the pieces of every row of the tiles (of 2^rshift rows) that are in
+// pieces, SG lane groups a row; a workgroup's rows are of one tile (the pitch is
+// a multiple of 16).
 template <int D, int SG, typename OUT>
-__global__ __launch_bounds__(256) void attn_join_kernel(Args a) {
+__global__ __launch_bounds__(256) void attn_join_kernel(Args a, int rshift) {
   constexpr int LPR = D / 4, RPB = 256 / (LPR * SG);
-  const int d = (threadIdx.x % LPR) * 4, sg = threadIdx.x / LPR % SG;
-  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / (LPR * SG);
-  bool own = row < a.rows;
-  if (a.cu) {
-    // the sequence of the block's first token, then on from there
-    const int64_t t0 = quotient((int64_t)blockIdx.x * RPB, a.inv_h);
-    int n = 0;
-    for (int i = 0; i < a.B; i += 256) {
-      const int j = i + threadIdx.x;
-      const int c = __syncthreads_count(j < a.B && a.cu[j] <= t0);
-      n += c;
-      if (c < 256) break;
-    }
-    const int64_t t = quotient(row, a.inv_h);
-    int b = max(n - 1, 0);
-    while (b + 1 < a.B && a.cu[b + 1] <= t) ++b;
-    int64_t tok0;
-    int T;
-    clamp_span(a.cu[b], a.cu[b + 1], a.T, a.total, tok0, T);
-    own = own && t >= tok0 && t < tok0 + T && !(a.few && (int64_t)T * a.G <= 32);
-  }
+  const int d = (threadIdx.x % LPR) * 4, sg = threadIdx.x / LPR % SG, i = threadIdx.x / (LPR * SG);
+  const uint32_t each = (uint32_t)a.pitch / RPB, unit = blockIdx.x / each, slot = unit / (uint32_t)a.Hkv;
+  const int kvh = unit - slot * (uint32_t)a.Hkv, row = (blockIdx.x - unit * each) * RPB + i;
+  int b;
+  int64_t r0;
+  slot_of(a, slot, rshift, b, r0);
+  const Seq s = seq_of(a, b);
+  const int64_t nr = (int64_t)s.T * a.G, r = r0 + row;
+  if (r0 < 0 || (a.few && nr <= 32)) return;
+  const bool own = r < nr;
   Sum x;
   if (own) {
+    const int64_t n = a.tail * a.Hkv * a.pitch, at = (int64_t)unit * a.pitch + row;
 #pragma unroll 4
     for (int i = sg; i < a.nsplit; i += SG) {
-      const float2 ml = a.part_ml[i * a.rows + row];
-      x.add(ml.x, ml.y, *reinterpret_cast<const f4_t*>(a.part_o + (i * a.rows + row) * D + d));
+      const float2 ml = a.part_ml[i * n + at];
+      x.add(ml.x, ml.y, *reinterpret_cast<const f4_t*>(a.part_o + (i * n + at) * D + d));
     }
   }
   if constexpr (SG > 1) {
     __shared__ f4_t so[SG][RPB * LPR];
     __shared__ float2 sml[SG][RPB * LPR];
-    x.template over<SG, LPR>(sg, threadIdx.x / (LPR * SG), threadIdx.x % LPR, so, sml);
+    x.template over<SG, LPR>(sg, i, threadIdx.x % LPR, so, sml);
   }
-  if (own && sg == 0) x.template store<OUT, D>(a, row, d);
+  if (own && sg == 0) x.template store<OUT, D>(a, out_row(a, s, kvh, r), d);
 }
 
 // ------------------------------------------------------------------ fp32 mode
@@ -964,16 +974,15 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(Args a) {
   __shared__ __attribute__((aligned(16))) float kv[2 * R * LD];
   float *const sk = kv, *const sv = kv + R * LD;
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-  const int combo = blockIdx.x % (unsigned)(a.Hkv * a.nsplit), kvh = combo % a.Hkv, split = combo / a.Hkv;
-  const int64_t nslot = gridDim.x / (unsigned)(a.Hkv * a.nsplit);
-  const int64_t slot = nslot - 1 - blockIdx.x / (unsigned)(a.Hkv * a.nsplit);
+  const Place at(a);
+  const int kvh = at.kvh;
   int b;
   int64_t r0;
-  slot_of(a, slot, QR, b, r0);
+  slot_of(a, at.slot, SHARE ? 4 : 6, b, r0);
   const Seq s = seq_of(a, b);
   const int64_t nr = (int64_t)s.T * a.G;
   if (r0 < 0 || r0 >= nr) return;
-  const Span x = span_of(a, s, r0, min(r0 + QR, nr) - 1, R, split);
+  const Span x = span_of(a, s, r0, min(r0 + QR, nr) - 1, R, at.split, at.n);
   const int64_t r = r0 + (SHARE ? 0 : wave * 16) + c;
   const int block = SHARE ? wave * 16 : 0;  // of this wave's rows in a tile
   const bool real = r < nr;
@@ -1135,18 +1144,18 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(Args a) {
     m = mt;
   }
   if (!real) return;
-  const int64_t at = out_row(a, s, kvh, r);
-  const bool split_out = a.nsplit > 1;
+  const bool split_out = at.n > 1;
+  const int64_t to = split_out ? at.part(a) + r - r0 : out_row(a, s, kvh, r);
   if (g == 0) {
-    if (split_out) a.part_ml[split * a.rows + at] = make_float2(m, l);
-    else if (a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m + fast_log2(l)) * LN2;
+    if (split_out) a.part_ml[to] = make_float2(m, l);
+    else if (a.lse) a.lse[to] = l == 0.f ? -INFINITY : (m + fast_log2(l)) * LN2;
   }
   const float f = split_out ? 1.f : l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int k = 0; k < D / 16; ++k) {
     const f4_t v = o[k] * f;
-    if (split_out) *reinterpret_cast<f4_t*>(a.part_o + (split * a.rows + at) * D + 16 * k + 4 * g) = v;
-    else store4((OUT*)a.o + at * D + 16 * k + 4 * g, v);
+    if (split_out) *reinterpret_cast<f4_t*>(a.part_o + to * D + 16 * k + 4 * g) = v;
+    else store4((OUT*)a.o + to * D + 16 * k + 4 * g, v);
   }
 }
 
@@ -1155,7 +1164,9 @@ __global__ __launch_bounds__(256, 1) void attn_f32_kernel(Args a) {
 struct Plan {
   bool tiles, rows;   // which of the bf16 kernels run
   int64_t slots;      // row tiles, over all sequences
-  int nsplit;         // pieces of their cache ranges
+  int64_t tail;       // those, the last to run, whose cache ranges are in pieces
+  int nsplit;         // pieces
+  int rshift, pitch;  // rows of a tile (2^rshift), and of its piece
   bool share;         // fp32 decode: the waves of attn_f32_kernel share the queries
   bool direct;        // attn_row_kernel: a unit a workgroup
   int64_t runs;       // its workgroups
@@ -1172,7 +1183,9 @@ Plan plan(const AttnCall& c) {
   const int64_t G = c.H / c.Hkv, per = (int64_t)c.T * G;
   const bool f32 = c.io == IO_F32;
   p.share = f32 && per <= 16;
-  const int R = p.share ? 16 : f32 ? 64 : 128;
+  p.rshift = p.share ? 4 : f32 ? 6 : 7;
+  const int R = 1 << p.rshift;
+  p.pitch = (int)std::min<int64_t>(R, (per + 15) & ~(int64_t)15);
   // bf16 sequences of at most 32 rows go to attn_row_kernel.  A packed batch may
   // hold both kinds, and gets both kernels unless the cache range is so short
   // that a workgroup of the tile kernel walks it while others still work (16
@@ -1183,6 +1196,7 @@ Plan plan(const AttnCall& c) {
   p.rows = !f32 && (per <= 32 || (c.packed && c.total < (int64_t)c.B * c.T && reach > 2048));
   p.slots = c.packed ? c.total * G / R + c.B : c.B * cdiv(per, R);
   p.nsplit = 1;
+  p.tail = 0;
   // Decode: as many workgroups as the chip holds, of a step at least; with
   // thousands of units, or one step each, there is nothing to even out.
   p.rows_a_unit = (int)std::min<int64_t>(per, 32);
@@ -1198,6 +1212,7 @@ Plan plan(const AttnCall& c) {
     const int64_t hold = std::min((p.share ? 65536 : 131072) / c.D, 1024);
     const int64_t want = cdiv(hold, p.slots * c.Hkv), most = cdiv(reach, 64);
     p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 128));
+    p.tail = p.nsplit > 1 ? p.slots : 0;
     return p;
   }
   // Tiles: the least of the rounds the pieces take on the chip's workgroup slots
@@ -1216,12 +1231,25 @@ Plan plan(const AttnCall& c) {
   const double longest = tiles(c.max_kv), mean = tiles(std::max<int64_t>(c.max_kv - c.T / 2, 1));
   const double rows = (double)c.total * c.H;
   auto walk = [&](int64_t on_a_cu) { return on_a_cu ? 1.7 * (1 + 0.2 * (on_a_cu - 1)) * c.D / 128 : 0.; };
+  auto rounds = [&](int64_t n) { return n / (256 * cu) * walk(cu) + walk(cdiv(n % (256 * cu), 256)); };
+  auto join = [&](double rows, int n) { return n > 1 ? 5 + rows * c.D * 8 * n / 6e6 : 0.; };
   double best = 0;
   for (int n = 1; n <= 64 && n <= std::max(longest / 4, 1.0); ++n) {
-    const int64_t whole = work * n / (256 * cu), rest = work * n % (256 * cu);
-    const double t = std::max((mean / n + 4) * (whole * walk(cu) + walk(cdiv(rest, 256))), (longest / n + 4) * walk(1)) +
-                     (n > 1 ? 5 + rows * c.D * 8 * n / 6e6 : 0);
+    const double t = std::max((mean / n + 4) * rounds(work * n), (longest / n + 4) * walk(1)) + join(rows, n);
     if (n == 1 || t < best) best = t, p.nsplit = n;
+  }
+  p.tail = p.nsplit > 1 ? p.slots : 0;
+  // Whole ranges in more than one round: those of the last, partial round (the
+  // shortest) may be in pieces (12 heads on 2 of 128: 528 units under a window of
+  // 1152 take 64 us so, 76 whole; 600 under one of 2304 108, 126).
+  const int64_t rest = work % (256 * cu);
+  if (p.nsplit == 1 && work > 256 * cu && rest) {
+    const double shortest = tiles(std::max<int64_t>(c.max_kv - c.T, 1));
+    best = (shortest + 4) * rounds(rest);
+    for (int n = 2; n <= 16 && n <= shortest / 4; ++n) {
+      const double t = (shortest / n + 4) * rounds(rest * n) + join((double)rest * R, n);
+      if (t < best) best = t, p.nsplit = n, p.tail = std::min(cdiv(rest, c.Hkv), p.slots);
+    }
   }
   return p;
 }
@@ -1232,7 +1260,7 @@ struct Layout {
 };
 Layout layout(const AttnCall& c, const Plan& p) {
   Layout w = {};
-  const size_t rows = p.nsplit > 1 ? (size_t)c.total * c.H * p.nsplit : 0;
+  const size_t rows = (size_t)p.tail * c.Hkv * p.pitch * p.nsplit;
   const size_t runs = p.rows && !p.direct ? (size_t)p.runs * 2 * 32 : 0;
   w.part_ml = w.part_o + a256(rows * c.D * sizeof(float));
   w.run_o = w.part_ml + a256(rows * sizeof(float2));
@@ -1242,15 +1270,17 @@ Layout layout(const AttnCall& c, const Plan& p) {
   return w;
 }
 
+int64_t tile_workgroups(const AttnCall& c, const Plan& p) { return (p.slots + p.tail * (p.nsplit - 1)) * c.Hkv; }
+
 template <int D, typename OUT>
 hipError_t launch(const AttnCall& c, const Plan& p, const Args& a, hipStream_t stream) {
-  const int combos = c.Hkv * p.nsplit;
+  const dim3 tiles((unsigned)tile_workgroups(c, p));
   if (c.io == IO_F32) {
-    if (p.share) attn_f32_kernel<D, true, OUT><<<dim3((unsigned)(p.slots * combos)), dim3(256), 0, stream>>>(a);
-    else attn_f32_kernel<D, false, OUT><<<dim3((unsigned)(p.slots * combos)), dim3(256), 0, stream>>>(a);
+    if (p.share) attn_f32_kernel<D, true, OUT><<<tiles, dim3(256), 0, stream>>>(a);
+    else attn_f32_kernel<D, false, OUT><<<tiles, dim3(256), 0, stream>>>(a);
   } else {
     constexpr int NW = row_waves(D);
-    if (p.tiles) attn_tile_kernel<D, OUT><<<dim3((unsigned)(p.slots * combos)), dim3(256), 0, stream>>>(a);
+    if (p.tiles) attn_tile_kernel<D, OUT><<<tiles, dim3(256), 0, stream>>>(a);
     if (p.rows) {
       attn_row_kernel<D, NW, OUT><<<dim3((unsigned)p.runs), dim3(NW * 64), 0, stream>>>(a);
       if (!p.direct)
@@ -1259,8 +1289,9 @@ hipError_t launch(const AttnCall& c, const Plan& p, const Args& a, hipStream_t s
   }
   // many pieces: a workgroup a row, its lane groups sharing the pieces
   constexpr int SG = 256 / (D / 4);
-  if (p.nsplit > 8) attn_join_kernel<D, SG, OUT><<<dim3((unsigned)a.rows), dim3(256), 0, stream>>>(a);
-  else if (p.nsplit > 1) attn_join_kernel<D, 1, OUT><<<dim3((unsigned)cdiv(a.rows, SG)), dim3(256), 0, stream>>>(a);
+  const int64_t rows = p.tail * c.Hkv * p.pitch;
+  if (p.nsplit > 8) attn_join_kernel<D, SG, OUT><<<dim3((unsigned)rows), dim3(256), 0, stream>>>(a, p.rshift);
+  else if (p.nsplit > 1) attn_join_kernel<D, 1, OUT><<<dim3((unsigned)(rows / SG)), dim3(256), 0, stream>>>(a, p.rshift);
   return hipGetLastError();
 }
 
@@ -1268,7 +1299,7 @@ hipError_t launch(const AttnCall& c, const Plan& p, const Args& a, hipStream_t s
 
 int64_t attn_workgroups(const AttnCall& c) {
   const Plan p = plan(c);
-  const int64_t tiles = p.tiles ? p.slots * c.Hkv * p.nsplit : 0, join = p.nsplit > 1 ? c.total * c.H : 0;
+  const int64_t tiles = p.tiles ? tile_workgroups(c, p) : 0, join = p.tail * c.Hkv * p.pitch;
   return std::max(std::max(tiles, join), p.rows ? p.runs * 32 : 0);
 }
 
@@ -1280,7 +1311,7 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t stream) {
   a.B = c.B, a.T = c.T, a.H = c.H, a.Hkv = c.Hkv, a.G = c.H / c.Hkv;
   a.pshift = __builtin_ctz((unsigned)c.page), a.max_pages = c.max_pages, a.num_pages = c.num_pages;
   a.window = c.window, a.nsplit = p.nsplit, a.few = p.rows;
-  a.total = c.total, a.rows = c.total * c.H, a.q_stride = c.q_stride, a.page_stride = c.page_stride;
+  a.total = c.total, a.q_stride = c.q_stride, a.page_stride = c.page_stride;
   a.cu = c.packed ? c.cu_seqlens : nullptr;
   a.kv_lens = c.kv_lens, a.table = c.page_table;
   a.q = c.q, a.k = c.k_cache, a.v = c.v_cache, a.o = c.o, a.lse = c.lse;
@@ -1293,7 +1324,8 @@ hipError_t launch_attn(const AttnCall& c, hipStream_t stream) {
   a.shared = reinterpret_cast<Shared*>(ws + w.shared);
   a.direct = p.direct;
   a.scale = c.scale * 1.4426950408889634f;
-  a.inv_g = 1.0 / a.G, a.inv_h = 1.0 / a.H;
+  a.inv_g = 1.0 / a.G;
+  a.whole = p.slots - p.tail, a.tail = p.tail, a.pitch = p.pitch;
   const bool bf = c.out == IO_BF16;
   switch (c.D) {
     case 64: return bf ? launch<64, bf16_t>(c, p, a, stream) : launch<64, float>(c, p, a, stream);

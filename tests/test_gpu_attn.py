@@ -419,3 +419,26 @@ def test_a_call_waits_for_its_stream(jb):
         got = run(q, stream=s)
         s.synchronize()
         assert torch.equal(got, want), i
+
+
+@pytest.mark.parametrize("D,H,Hkv", [(256, 8, 8), (128, 32, 16), (64, 24, 24)])
+@pytest.mark.parametrize("behind", [0, 77])
+def test_last_round_in_pieces(jb, D, H, Hkv, behind):
+    """A few more tiles than the chip takes at once, under a window: the ranges of the last ones
+    are in pieces, the others whole.  Tokens from all over each sequence, and rows of nobody."""
+    G = H // Hkv
+    new, kv, window = [1500 // G, 0, 1300 // G, 1424 // G], [2600, 40, 1300, 1900], 1000
+    d = batch(new, kv, H, Hkv, D, 64, BF, seed=D + behind, behind=behind)
+    o = torch.full(d["q"].shape, 5.0, dtype=BF, device="cuda")
+    shape = jb.AttnShape(4, max(new), H, Hkv, D, 0, 64, 41, d["k_cache"].shape[0], 2600, window,
+                         jb.JB_BF16, jb.JB_BF16, 0, 0, 0, 0, 0)
+    pieces = jb.attn_paged_workspace_size(shape, sum(new) + behind, True)
+    assert 0 < pieces < 2 * (sum(new) + behind) * H * D * 4  # (all rows in pieces: that at least)
+    r = call(jb, d, window=window, max_seqlen=max(new), max_kv=2600, o=o)
+    assert (o[sum(new):] == 5).all()
+    at = 0
+    for b, t in enumerate(new):
+        for i in sorted({0, 1, 63 // G, 126 // G, 200, t // 2, t - 131, t - 3}) if t else ():
+            one = dict(d, q=d["q"][at + i:at + i + 3], table=d["table"][b:b + 1])
+            check(one, dict(o=r["o"][at + i:at + i + 3], lse=r["lse"][at + i:at + i + 3]), [3], [kv[b] - t + i + 3], window)
+        at += t
