@@ -47,7 +47,12 @@ int main(void) {
                       jb_status st = jb_attn_paged_workspace_size(&s, total, packed, &bytes);
                       EXPECT(good || st != JB_OK, "a shape past the limits was accepted");
                       if (st == JB_OK && bytes && total) {
-                        EXPECT(bytes >= (size_t)total * s.H * s.D * 8, "workspace %zu below two pieces", bytes);
+                        /* two pieces of every row; or only those of a last round: at least 16 rows, at most
+                         * 16 pieces of the 128 rows of 3 tiles a CU (and what rounds them up to whole heads) */
+                        const size_t row = (size_t)s.D * 4 + 8;
+                        EXPECT(bytes >= (size_t)total * s.H * s.D * 8 ||
+                                   (bytes >= 2 * 16 * row && bytes <= (size_t)(768 + 255) * 128 * 16 * row + 65536 * row),
+                               "workspace %zu is neither of all rows nor of a last round", bytes);
                         st = jb_attn_paged(&s, total, packed ? p : NULL, p, p, p, p, p, 0.f, p, p, p, bytes - 1, NULL);
                         EXPECT(st == JB_ERR_WORKSPACE, "short workspace gave %s", jb_status_string(st));
                       }
