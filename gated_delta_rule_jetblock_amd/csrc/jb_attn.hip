@@ -16,8 +16,14 @@
 // accumulators, rounded to bf16, are the B operand of O^T += V^T P^T as they
 // stand (K order kperm32: slots 0..3 are rows 4 g .. 4 g + 3, slots 4..7 rows
 // 8 + 4 g ..).  V's A operand is read down its columns from LDS.
-// Rounding: scores, m, l and o are fp32; P is rounded to bf16 for the matrix
-// cores (at most 2^-8 of each weight, either way); o is rounded once.
+// Rounding: scores, m, l and o are fp32, o is rounded once.  The matrix cores
+// take P as bf16, because V is: where o is bf16 and there are many queries, P is
+// rounded to it, half a step of each weight (2^-8) next to the half step that o
+// itself loses (together 2.0-2.4e-3 of o's norm, o's rounding alone 1.65e-3).
+// Where the caller wants o in fp32, and in decode, P is two parts, hi + lo
+// (within 2^-15), and their products with V are two: nothing in decode (64
+// sequences of 64K rows 365 us either way), but a third more with many queries (2K
+// tokens on 64K rows 766 us, in two parts 1030; an 8K prompt 258 and 346).
 //   attn_tile_kernel  many queries: 4 waves x 32 rows of one key head walk the
 //                     same 64-row cache tiles through two LDS buffers.
 //   attn_row_kernel   at most 32 rows (decode): every wave takes its own 32-row
@@ -397,12 +403,12 @@ template <int D> struct Wave {
   // products with V, mixed with the other weights, before its products with K
   // (at equal priority 2K tokens on 64K rows took 782 us and an 8K prompt 289; so
   // 735 and 253).
-  template <int NB> __device__ void full(const Args& a, const lds_char* lk, const lds_char* lv) {
+  template <int NB, bool TWO> __device__ void full(const Args& a, const lds_char* lk, const lds_char* lv) {
     f16_t s[NB];
     scores<NB>(lk, s);
     __builtin_amdgcn_s_setprio(2);
     const float ms = take_max<NB>(a, s);
-    values<NB, true>(a, lv, s, ms);
+    values<NB, true, TWO>(a, lv, s, ms);
     __builtin_amdgcn_s_setprio(0);
   }
 
@@ -425,8 +431,10 @@ template <int D> struct Wave {
     return true;
   }
   // O^T += V^T P^T, 16 cache rows a step.  EXP: s holds scores yet; the next
-  // step's exponentials and reads go between the products of this one.
-  template <int NB, bool EXP> __device__ void values(const Args& a, const lds_char* lv, f16_t (&s)[NB], float ms) {
+  // step's exponentials and reads go between the products of this one.  TWO: P
+  // as its upper 16 bits and what they leave, rounded to bf16 (cutting hi off takes
+  // fewer operations than rounding it: 2K tokens on 64K rows 1030 us, 1053).
+  template <int NB, bool EXP, bool TWO> __device__ void values(const Args& a, const lds_char* lv, f16_t (&s)[NB], float ms) {
     const int lane = lane_id(), g = lane >> 5;
     const int n16 = lane & 15, row = 4 * g + (n16 >> 2), pc = 2 * ((lane >> 4) & 1) + ((n16 & 3) >> 1);
     const int vb = row * I::ROWB + ((pc ^ I::fv(row)) << 4) + (n16 & 1) * 8;
@@ -447,14 +455,24 @@ template <int D> struct Wave {
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int k = 0; k < STEPS; ++k) {
-      bf16x8_t w;
+      bf16x8_t w, lo;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = (__bf16)s[k >> 1][8 * (k & 1) + e];
+      for (int e = 0; e < 8; ++e) {
+        const float x = s[k >> 1][8 * (k & 1) + e];
+        if constexpr (TWO) {
+          const uint32_t hi = __float_as_uint(x) & 0xffff0000u;
+          w[e] = __builtin_bit_cast(__bf16, (uint16_t)(hi >> 16));
+          lo[e] = (__bf16)(x - __uint_as_float(hi));
+        } else {
+          w[e] = (__bf16)x;
+        }
+      }
 #pragma unroll
       for (int db = 0; db < DB; ++db) {
         const int i = k * DB + db;
         if (i + AHEAD < STEPS * DB) read(i + AHEAD);
         o[db] = mfma32(v[i], w, o[db]);
+        if constexpr (TWO) o[db] = mfma32(v[i], lo, o[db]);
         if constexpr (EXP)
           if (k + 1 < STEPS) weights<NB>(a, s, ms, k + 1, db * PART, PART);
         __builtin_amdgcn_sched_barrier(0);
@@ -586,6 +604,7 @@ __device__ __forceinline__ int64_t out_row(const Args& a, const Seq& s, int kvh,
 template <int D, typename OUT>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a) {
   constexpr int NW = 4, R = 64, IMG = R * D * 2;
+  constexpr bool TWO = sizeof(OUT) == 4;  // P in two parts
   __shared__ __attribute__((aligned(1024))) char ring[4 * IMG];  // K, V of an even tile, K, V of an odd one
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const Place at(a);
@@ -623,7 +642,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
   };
   for (int n = 0; n < nf; ++n) {
     const lds_char* k = next(n);
-    w.template full<2>(a, k, k + IMG);
+    w.template full<2, TWO>(a, k, k + IMG);
   }
   for (int n = nf; n < nt; ++n) {
     lds_char* const k = next(n);
@@ -637,7 +656,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
       clean_part(v + wave * (IMG / 4), IMG / 4);
       __syncthreads();
     }
-    if (live) w.template values<2, false>(a, v, s2, 0.f);
+    if (live) w.template values<2, false, TWO>(a, v, s2, 0.f);
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   // O through LDS (each wave its own rows) so that whole rows leave
@@ -797,7 +816,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_row_kernel(Args a) {
     int n = wave;
     for (; n < nf; n += NW) {
       const lds_char* k = next(n);
-      w.template full<1>(a, k, k + IMG);
+      w.template full<1, true>(a, k, k + IMG);
     }
     for (; n < nt; n += NW) {
       lds_char* const k = next(n);
@@ -810,7 +829,7 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_row_kernel(Args a) {
           clean_part(v, IMG);
           asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
-        w.template values<1, false>(a, v, s1, 0.f);
+        w.template values<1, false, true>(a, v, s1, 0.f);
       }
     }
     // join the waves: O and (m, l) of each in LDS

@@ -491,9 +491,11 @@ jb_status jb_attn_paged_workspace_size(const jb_attn_shape* shape, int64_t total
  * scale 0 selects 1 / sqrt(D); it must not be negative.  A token that sees no
  * row (p < 0) gets o = 0 and lse = -inf.  Rows that a token does not see have
  * no part in it, whatever they hold.  One token per sequence (T = 1) is the
- * decode step.  lse is nullable.  bf16: scores, statistics and sums are fp32,
- * the softmax weights are rounded to bf16 for their product with v, o is
- * rounded once.  fp32 inputs: fp32 throughout.
+ * decode step.  lse is nullable.  bf16: scores, statistics and sums are fp32, o
+ * is rounded once.  The softmax weights meet v as two bf16 parts (within 2^-15 of
+ * each) where out_dtype is fp32, and where T H / Hkv <= 32 (decode); elsewhere they
+ * may be rounded to bf16, the type of o (within 2^-8).  fp32 inputs: fp32
+ * throughout.
  * workspace: jb_attn_paged_workspace_size() bytes (NULL if 0), 256-byte aligned.
  */
 jb_status jb_attn_paged(const jb_attn_shape* shape, int64_t total_tokens, const int32_t* cu_seqlens,
