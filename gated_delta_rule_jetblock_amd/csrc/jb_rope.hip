@@ -159,9 +159,11 @@ template <int D> __device__ __forceinline__ Turn turn_of(const RopeCall& c, int 
   return t;
 }
 
-// the other members of this lane's pairs
+// the other members of this lane's pairs; zeros where the rotation does not reach
+// (rot is a multiple of 16, so a lane's values turn or do not together): their sine
+// is 0, but 0 times an inf or NaN would not be
 template <typename T>
-__device__ __forceinline__ Raw<T> others(const Raw<T>& x, bool interleaved, int lane) {
+__device__ __forceinline__ Raw<T> others(const Raw<T>& x, bool interleaved, int lane, bool turns) {
   Raw<T> y;
   if (interleaved) {
 #pragma unroll
@@ -171,6 +173,8 @@ __device__ __forceinline__ Raw<T> others(const Raw<T>& x, bool interleaved, int 
 #pragma unroll
     for (int i = 0; i < Raw<T>::N; ++i) y.u[i] = (uint32_t)__shfl((int)x.u[i], lane, WAVE);
   }
+#pragma unroll
+  for (int i = 0; i < Raw<T>::N; ++i) y.u[i] = turns ? y.u[i] : 0u;
   return y;
 }
 
@@ -282,7 +286,7 @@ __global__ __launch_bounds__(256) void rope_kernel(Args a) {
         for (int e = 0; e < 8; ++e) sum = fmaf(x[u].get(e), x[u].get(e), sum);
         r = 1.f / sqrtf(row_sum<L>(sum) * (1.f / D) + c.eps);
       }
-      const Raw<IO> xp = others(x[u], c.interleaved, from);
+      const Raw<IO> xp = others(x[u], c.interleaved, from, 8 * s < c.rot);
       const bool key = i >= c.H;
       float y[8];
 #pragma unroll
@@ -331,7 +335,7 @@ __global__ __launch_bounds__(256, 3) void rope_backward_kernel(Args a) {
         const int i = h + u;
         if (i >= h1) break;
         const bool key = i >= c.H;
-        const Raw<GR> yp = others(y[u], c.interleaved, from);
+        const Raw<GR> yp = others(y[u], c.interleaved, from, 8 * s < c.rot);
         float g[8];  // R^T dy: the same turn backwards
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = fmaf(y[u].get(e), turn.cos[e], -yp.get(e) * turn.sin[e]);

@@ -1,12 +1,13 @@
 """GPU tests of the attention-layer operators at their edges: what the softmax weights' rounding
-leaves of an fp32 output and of a decode step."""
+leaves of an fp32 output and of a decode step, values that are not finite next to the rotation."""
 import numpy as np
 import pytest
 import torch
 
-from layer_checks import numbers
+from layer_checks import numbers, same_kind
 from oracle import attention as ref
 from test_gpu_attn import BF, F32, batch, call, f64
+from test_gpu_rope import inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +50,72 @@ def test_weights_in_two_parts(jb, D, H, Hkv, new, kv, out):
         far = np.abs(o[at:at + t] - eo)
         assert (far <= tol).all(), (b, (far / tol).max())
         at += t
+
+
+# ------------------------------------------------- values that are not finite
+
+BAD = [float("inf"), -float("inf"), float("nan")]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("rot", [0, 32])
+@pytest.mark.parametrize("bad", BAD)
+def test_unrotated_values_pass_through(jb, dtype, pairs, rot, bad):
+    """The rotation does not reach past the first rot values: without the norm the rest leave as they
+    came, whatever they are, and none of them is felt elsewhere; with the norm as the oracle has it."""
+    n, H, Hkv, D = 5, 3, 1, 64
+    d, g = inputs(n, H, Hkv, D, rot, dtype, seed=rot + 1)
+    run = lambda x, **a: dict(zip("qk", jb.qk_norm_rope(x["q"], x["k"], x["pos"], x["inv_freq"], interleaved=pairs, **a)))
+    clean = run(g, normalize=False)
+    where = [(0, 0, rot), (1, 0, D - 1), (2, 0, 45), (4, 0, 50)]
+    for x in "qk":
+        for at in where:
+            d[x][at] = bad
+        g[x] = d[x].cuda()
+    y = run(g, normalize=False)
+    for x in "qk":
+        for at in where:
+            want = torch.tensor(bad).to(y[x].dtype)
+            assert torch.equal(torch.nan_to_num(y[x][at].cpu(), 7, 8, 9), torch.nan_to_num(want, 7, 8, 9)), (x, at)
+            y[x][at], clean[x][at] = 0, 0
+        assert torch.equal(y[x], clean[x])
+    y = run(g, wq=g["wq"], wk=g["wk"])
+    for x in "qk":
+        with np.errstate(invalid="ignore"):
+            want = ref.norm_rope(f64(d[x]), d["pos"].numpy(), d["inv_freq"].numpy(), f64(d["w" + x]), interleaved=pairs)
+        got = same_kind(y[x], want)
+        fine = np.isfinite(want)
+        assert (np.abs(got - want)[fine] <= 2.0 ** -7 * np.abs(want[fine]) + 1e-5).all()
+
+
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("rot", [0, 32])
+@pytest.mark.parametrize("bad", BAD)
+def test_unrotated_gradients_pass_through(jb, pairs, rot, bad):
+    """The same of the gradient: an incoming value that is not finite and not rotated."""
+    n, H, Hkv, D = 4, 2, 1, 64
+    d, g = inputs(n, H, Hkv, D, rot, F32, seed=rot + 2)
+    gen = torch.Generator().manual_seed(rot)
+    dy = {x: torch.randn(d[x].shape, generator=gen) for x in "qk"}
+    run = lambda **a: jb.qk_norm_rope_backward(g["q"], g["k"], g["pos"], g["inv_freq"], dy["q"].cuda(), dy["k"].cuda(),
+                                               interleaved=pairs, **a)
+    clean, clean_norm = run(normalize=False), run(wq=g["wq"], wk=g["wk"])
+    where = [(0, 0, rot), (2, 0, 51)]
+    for x in "qk":
+        for at in where:
+            dy[x][at] = bad
+    r, rn = run(normalize=False), run(wq=g["wq"], wk=g["wk"])
+    for x in "qk":
+        for at in where:
+            assert torch.equal(torch.nan_to_num(r["d" + x][at].cpu(), 7, 8, 9), torch.nan_to_num(torch.tensor(bad), 7, 8, 9))
+            r["d" + x][at] = clean["d" + x][at] = 0
+        assert torch.equal(r["d" + x], clean["d" + x])
+        with np.errstate(invalid="ignore"):
+            dx, dw = ref.norm_rope_backward(f64(d[x]), d["pos"].numpy(), d["inv_freq"].numpy(), f64(dy[x]), f64(d["w" + x]),
+                                            interleaved=pairs)
+        same_kind(rn["d" + x], dx)
+        same_kind(rn["dw" + x], dw)
+        keep = torch.ones(D, dtype=torch.bool)
+        keep[[at[2] for at in where]] = False
+        assert torch.equal(rn["dw" + x].cpu()[keep], clean_norm["dw" + x].cpu()[keep])
