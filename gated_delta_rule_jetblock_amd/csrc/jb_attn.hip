@@ -104,23 +104,25 @@ __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirs
 // the token of row r of a sequence's T G
 __device__ __forceinline__ int token_of(const Args& a, int64_t r) { return (int)(((double)r + 0.5) * a.inv_g); }
 
-// first token and length of sequence b, and its cache rows; all clamped to the
-// tensors (they come from device memory)
+// first token and length of sequence b (the a.T first tokens of a longer one), and
+// its cache rows up to the last of them; all clamped to the tensors (they come from
+// device memory).  kv - T is -2^30 at least, so a window behind it fits 32 bits.
 struct Seq {
   int64_t tok0;
   int T, kv;
 };
 __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
   Seq s;
+  int all = a.T;
   if (a.cu) {
     const_int_p cu = (const_int_p)a.cu;
-    clamp_span(cu[b], cu[b + 1], a.T, a.total, s.tok0, s.T);
+    clamp_span(cu[b], cu[b + 1], 0x7fffffff, a.total, s.tok0, all);
   } else {
     s.tok0 = (int64_t)b * a.T;
-    s.T = a.T;
   }
+  s.T = min(all, a.T);
   const int cap = (int)min((int64_t)a.max_pages << a.pshift, (int64_t)0x7fffffff);
-  s.kv = min(max(((const_int_p)a.kv_lens)[b], 0), cap);
+  s.kv = max(min(max(((const_int_p)a.kv_lens)[b], 0), cap) - (all - s.T), s.T - (1 << 30));
   return s;
 }
 
@@ -698,7 +700,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
 __device__ __forceinline__ int steps_of(const Args& a, const Seq& s, int rows_a_step) {
   const int64_t nr = (int64_t)s.T * a.G;
   if (nr == 0 || nr > 32) return 0;  // none, or attn_tile_kernel's
-  const int hi = s.kv, lo = a.window ? min(max(s.kv - s.T - a.window + 1, 0), hi) : 0;
+  const int hi = max(s.kv, 0), lo = a.window ? min(max(s.kv - s.T - a.window + 1, 0), hi) : 0;
   // (a sequence without rows has its output to write)
   return max((hi + rows_a_step - 1) / rows_a_step - lo / rows_a_step, 1);
 }

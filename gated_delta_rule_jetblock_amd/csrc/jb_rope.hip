@@ -228,7 +228,7 @@ __global__ __launch_bounds__(256) void rope_kernel(Args a) {
   if constexpr (PAGED) {
     int b;
     int64_t i;
-    int T;
+    int T = c.T;  // the sequence's tokens (those behind the first c.T are not taken)
     if (c.packed) {
       // the sequence of the workgroup's first token, then on from there
       const int64_t t0 = (int64_t)blockIdx.x * GROUPS / a.parts;
@@ -242,13 +242,12 @@ __global__ __launch_bounds__(256) void rope_kernel(Args a) {
       b = max(n - 1, 0);
       while (b + 1 < c.B && c.cu_seqlens[b + 1] <= t) ++b;
       int64_t tok0;
-      clamp_span(c.cu_seqlens[b], c.cu_seqlens[b + 1], c.T, c.total, tok0, T);
+      clamp_span(c.cu_seqlens[b], c.cu_seqlens[b + 1], 0x7fffffff, c.total, tok0, T);
       i = t - tok0;
-      live = live && i >= 0 && i < T;
+      live = live && i >= 0 && i < min(T, c.T);
     } else {
       b = (int)((uint32_t)t / (uint32_t)c.T);
       i = t - (int64_t)b * c.T;
-      T = c.T;
     }
     const int pshift = __builtin_ctz((unsigned)c.page);
     const int cap = (int)min((int64_t)c.max_pages << pshift, (int64_t)0x7fffffff);

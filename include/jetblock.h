@@ -396,8 +396,10 @@ jb_status jb_backward(const jb_shape* shape, const void* x, const void* q, const
  *                  last of them
  *   lse            [tokens][H] float32
  * Tokens are B x T (cu_seqlens NULL), or packed: sequence b is rows
- * cu_seqlens[b] .. cu_seqlens[b+1] - 1 of total_tokens, at most its first
- * shape.T of them; rows that no sequence owns are left as they are.
+ * cu_seqlens[b] .. cu_seqlens[b+1] - 1 of total_tokens.  Of a sequence of more
+ * than shape.T tokens the first shape.T are computed, at the cache rows they have
+ * in it; the others, and rows that no sequence owns, are left as they are (not
+ * appended, their outputs not written).
  * q, k and v may have any distance between tokens (the strides below, for
  * slices of one projection's output); the caches any distance between pages.
  * Device-side values cannot be checked on the host, and none makes a call

@@ -1,5 +1,6 @@
 """GPU tests of the attention-layer operators at their edges: what the softmax weights' rounding
-leaves of an fp32 output and of a decode step, values that are not finite next to the rotation."""
+leaves of an fp32 output and of a decode step, values that are not finite next to the rotation,
+packed sequences longer than the planned length."""
 import numpy as np
 import pytest
 import torch
@@ -7,7 +8,7 @@ import torch
 from layer_checks import numbers, same_kind
 from oracle import attention as ref
 from test_gpu_attn import BF, F32, batch, call, f64
-from test_gpu_rope import inputs
+from test_gpu_rope import append, append_inputs, inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +120,42 @@ def test_unrotated_gradients_pass_through(jb, pairs, rot, bad):
         keep = torch.ones(D, dtype=torch.bool)
         keep[[at[2] for at in where]] = False
         assert torch.equal(rn["dw" + x].cpu()[keep], clean_norm["dw" + x].cpu()[keep])
+
+
+# ------------------------------------- sequences longer than the planned length
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("new,kv,most,window", [
+    ([90, 20, 70], [200, 64, 50], 60, 0), ([90, 20], [200, 64], 60, 40), ([9, 1, 2], [300, 9, 1], 4, 0),
+    ([9, 1, 2], [300, 9, 70], 4, 33),
+])
+def test_tokens_of_a_cut_sequence_keep_their_rows(jb, dtype, new, kv, most, window):
+    """Of a sequence longer than max_seqlen the first tokens are computed: as tokens of that sequence,
+    at the rows they have in it (the last one is row kv - 1), in attention and in the append."""
+    H, Hkv, D, page = 6, 2, 64, 16
+    d = append_inputs(new, kv, H, Hkv, D, page, dtype, seed=40 + most)
+    whole, cut = append(jb, d), append(jb, d, max_seqlen=most)
+    attended = {k: d[k] for k in ("q", "k_cache", "v_cache", "table", "kv", "cu")}
+    o, part = call(jb, attended, window=window), call(jb, attended, window=window, max_seqlen=most)
+    at = 0
+    for b, (t, l) in enumerate(zip(new, kv)):
+        here = slice(at, at + min(t, most))
+        assert torch.equal(cut["q"][here], whole["q"][here]), b
+        seen = f64(o["lse"][here])
+        # perhaps by another kernel, its sums in another order.  lse: either is off by some 66 2^-24 sum |q k| / 8
+        # and 2^-17; o: by half a step of a weight and of o itself (fp32: twice lse's error), relative to |v|
+        far = np.abs(f64(part["lse"][here]) - seen)
+        assert (np.isneginf(seen) == np.isneginf(f64(part["lse"][here]))).all()
+        assert (far[np.isfinite(seen)] <= 2.0 ** -13 * (1 + np.abs(seen[np.isfinite(seen)]))).all(), b
+        v = np.abs(ref.gather(f64(d["v_cache"]), d["table"][b].tolist(), l)).max() if l else 0.0
+        assert (np.abs(f64(part["o"][here]) - f64(o["o"][here])) <= (1.1 * 2.0 ** -6 if dtype == BF else 2.0 ** -14) * v).all(), b
+        for i in range(t):
+            row = l - t + i
+            if row < 0:
+                continue
+            p, x = int(d["table"][b, row // page]), row % page
+            src = whole if i < most else d
+            for c in ("k_cache", "v_cache"):
+                assert torch.equal(cut[c][p, :, x].cpu(), src[c][p, :, x].cpu()), (b, i)
+        at += t
