@@ -854,7 +854,8 @@ __global__ __launch_bounds__(NW * 64, 1) void attn_row_kernel(Args a) {
       ml[NW * 32 + wave * 32 + c] = l;
     }
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    const bool whole = s0 == 0 && s1 == steps;
+    // (a unit that is a run has no place for a part, whatever the lengths in memory do meanwhile)
+    const bool whole = a.direct || (s0 == 0 && s1 == steps);
     if (s0 == 0 && !whole) {  // (in the grid whatever the lengths in memory do meanwhile)
       const int last = (int)min(quotient(at + steps - 1, 1.0 / run_steps), (int64_t)gridDim.x - 1);
       shared = {b, kvh, last - (int)blockIdx.x, seg};
