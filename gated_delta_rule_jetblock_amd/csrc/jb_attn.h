@@ -26,7 +26,7 @@ struct AttnCall {
   void* workspace;
 };
 // pieces and workgroups depend on the sizes only, not on device memory
-int64_t attn_workgroups(const AttnCall& c);
+int64_t attn_workgroups(const AttnCall& c);  // of the largest launch, at most 256 threads each
 size_t attn_workspace_bytes(const AttnCall& c);
 hipError_t launch_attn(const AttnCall& c, hipStream_t stream);
 

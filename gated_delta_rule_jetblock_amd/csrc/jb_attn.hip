@@ -1322,7 +1322,7 @@ hipError_t launch(const AttnCall& c, const Plan& p, const Args& a, hipStream_t s
 int64_t attn_workgroups(const AttnCall& c) {
   const Plan p = plan(c);
   const int64_t tiles = p.tiles ? tile_workgroups(c, p) : 0, join = p.tail * c.Hkv * p.pitch;
-  return std::max(std::max(tiles, join), p.rows ? p.runs * 32 : 0);
+  return std::max(std::max(tiles, join), !p.rows ? 0 : p.direct ? p.runs : p.runs * p.rows_a_unit);
 }
 
 size_t attn_workspace_bytes(const AttnCall& c) { return layout(c, plan(c)).bytes; }

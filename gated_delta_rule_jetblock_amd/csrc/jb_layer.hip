@@ -29,6 +29,8 @@ jb_status hip_status(const char* fn, hipError_t e) {
   } while (0)
 
 constexpr int64_t MOST = (int64_t)1 << 40;
+// workgroups of 256 threads that a launch can have: its work-items are a 32-bit count
+constexpr int64_t MOST_GROUPS = 0xffffffffLL / 256;
 
 // Heads, dtypes, tokens and token strides; total: rows of the token-major tensors.
 jb_status check_shape(const char* fn, const jb_attn_shape* s, int64_t total, bool packed) {
@@ -122,7 +124,7 @@ jb_status check_attn(const char* fn, const jb_attn_shape* s, int64_t total, bool
   if (!st) st = check_cache(fn, s);
   if (st) return st;
   if (s->flags) return fail(JB_ERR_INVALID_ARG, "%s: flags must be 0", fn);
-  if (total && jb::attn_workgroups(attn_call(s, total, packed)) > 0x7fffffffLL)
+  if (total && jb::attn_workgroups(attn_call(s, total, packed)) > MOST_GROUPS)
     return fail(JB_ERR_UNSUPPORTED, "%s: more workgroups than a launch can have", fn);
   return JB_OK;
 }
@@ -147,7 +149,7 @@ jb_status jb_qk_norm_rope(const jb_attn_shape* s, const void* q, const void* k, 
   if (!c.norm && (wq || wk)) return fail(JB_ERR_INVALID_ARG, "%s: wq and wk must be NULL with JB_ROPE_NO_NORM", fn);
   c.q = q, c.k = k, c.wq = wq, c.wk = wk, c.inv_freq = inv_freq, c.positions = positions, c.eps = eps;
   c.q_out = q_out, c.k_out = k_out;
-  if (jb::rope_workgroups(c) > 0x7fffffffLL)
+  if (jb::rope_workgroups(c) > MOST_GROUPS)
     return fail(JB_ERR_UNSUPPORTED, "%s: more workgroups than a launch can have", fn);
   return hip_status(fn, jb::launch_rope(c, static_cast<hipStream_t>(stream)));
 }
@@ -223,7 +225,7 @@ jb_status jb_qk_norm_rope_paged(const jb_attn_shape* s, int64_t total_tokens, co
   c.cu_seqlens = cu_seqlens, c.kv_lens = kv_lens, c.page_table = page_table;
   c.q = q, c.k = k, c.v = v, c.wq = wq, c.wk = wk, c.inv_freq = inv_freq, c.positions = positions, c.eps = eps;
   c.q_out = q_out, c.k_out = k_cache, c.v_out = v_cache;
-  if (jb::rope_workgroups(c) > 0x7fffffffLL)
+  if (jb::rope_workgroups(c) > MOST_GROUPS)
     return fail(JB_ERR_UNSUPPORTED, "%s: more workgroups than a launch can have", fn);
   return hip_status(fn, jb::launch_rope(c, static_cast<hipStream_t>(stream)));
 }

@@ -412,8 +412,10 @@ jb_status jb_backward(const jb_shape* shape, const void* x, const void* q, const
  *
  * Supported: D in {64, 128, 256}; H <= 256, a multiple of Hkv; page a power of
  * two in [16, 4096]; max_pages * page <= 2^30; both dtypes; 1 <= B <= 65535;
- * 0 <= T <= 2^30; total_tokens < 2^31; fewer than 2^40 elements in any tensor.
- * Pointers 16-byte aligned (cu_seqlens, kv_lens, page_table, positions,
+ * 0 <= T <= 2^30; total_tokens < 2^31; fewer than 2^40 elements in any tensor;
+ * fewer than 2^24 workgroups in a launch (at most about 2^35 / D tokens in
+ * jb_qk_norm_rope and _paged; in jb_attn_paged about B Hkv + total_tokens H / 128 of
+ * them, fp32 total_tokens H / 16).  Pointers 16-byte aligned (cu_seqlens, kv_lens, page_table, positions,
  * inv_freq and lse: 4-byte).
  * ------------------------------------------------------------------------- */
 

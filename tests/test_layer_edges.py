@@ -1,5 +1,7 @@
 """CPU tests around the attention-layer operators: the comparisons of their GPU tests and the
 binding's and the library's handling of calls at their limits."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -38,3 +40,34 @@ def test_comparisons_refuse_nan():
     for bad in (torch.full((2, 3, 4), float("nan")), torch.tensor([1.0] * 23 + [float("nan")]).view(2, 3, 4)):
         with pytest.raises(AssertionError):
             near(bad, want, want)
+
+
+@pytest.fixture(scope="module")
+def jb():
+    from gated_delta_rule_jetblock_amd import jetblock
+    return jetblock
+
+
+def test_calls_of_more_work_items_than_a_launch_has(jb):
+    """A launch has fewer than 2^32 work-items, 2^24 workgroups of 256: what needs more is refused
+    by the library, with its own message, before anything is launched."""
+    def size(f32, total, packed, **kw):
+        s = jb.AttnShape(65535, 1, 256, 256, 64, 0, 16, 8, 20, 0, 0, f32, f32, 0, 0, 0, 0, 0)
+        for k, v in kw.items():
+            setattr(s, k, v)
+        n = ctypes.c_size_t(0)
+        return jb.library().jb_attn_paged_workspace_size(ctypes.byref(s), total, packed, ctypes.byref(n))
+    # fp32: a tile of 16 query rows for each sequence, and one for 16 tokens in a packed batch, times 256 heads
+    assert size(jb.JB_F32, 15, 1) == 0                       # 65535 x 256 = 2^24 - 256
+    assert size(jb.JB_F32, 16, 1) == 2                       # 2^24
+    assert "more workgroups than a launch" in jb.last_error()
+    assert size(jb.JB_F32, 131070, 1, T=2) == 2
+    assert size(jb.JB_F32, 65535, 0) == 0
+    assert size(jb.JB_BF16, 65535, 0) == 0                   # decode, a workgroup for each sequence and head
+    assert size(jb.JB_BF16, 65535 * 40, 0, T=40) == 0
+    assert size(jb.JB_BF16, 65535 * 140, 0, T=140) == 2      # two tiles each
+    good = ctypes.c_void_p(0x10000)
+    s = jb.AttnShape(1, (1 << 27) - 7, 1, 1, 256, 64, 0, 0, 0, 0, 0, jb.JB_BF16, jb.JB_BF16, 0, 0, 0, 0, 0)
+    rope = jb.library().jb_qk_norm_rope
+    assert rope(ctypes.byref(s), good, good, good, good, good, good, 1e-6, good, good, None) == 2   # 8 tokens a workgroup
+    assert "more workgroups than a launch" in jb.last_error()
