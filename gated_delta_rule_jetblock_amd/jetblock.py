@@ -551,7 +551,7 @@ def _rows(t, name: str):
             raise ValueError(f"{name}: tokens must lie at one distance")
     else:
         raise ValueError(f"{name}: expected [tokens, heads, D] or [B, T, heads, D], got {tuple(shape)}")
-    if st[-1] != 1 or st[-2] != d:
+    if st[-1] != 1 or (heads > 1 and st[-2] != d):
         raise ValueError(f"{name}: a token's heads must be contiguous")
     if n <= 1:
         return t.data_ptr(), n, 0
@@ -709,7 +709,9 @@ def _batch(q, cu_seqlens, max_seqlen):
 def _pages(k_cache, v_cache, page_table, kv_lens, B, D):
     """num_pages, Hkv, page, page stride and max_pages of a cache."""
     shape, st = k_cache.shape, k_cache.stride()
-    if len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != st:
+    vst = v_cache.stride()
+    if len(shape) != 4 or v_cache.shape != shape or \
+            vst != st and any(n > 1 and a != b for n, a, b in zip(shape, st, vst)):
         raise ValueError("k_cache and v_cache are [pages, Hkv, page, D] alike")
     P, Hkv, page, d = shape
     if d != D or st[3] != 1 or st[2] != D or (Hkv > 1 and st[1] != page * D):

@@ -71,3 +71,25 @@ def test_calls_of_more_work_items_than_a_launch_has(jb):
     rope = jb.library().jb_qk_norm_rope
     assert rope(ctypes.byref(s), good, good, good, good, good, good, 1e-6, good, good, None) == 2   # 8 tokens a workgroup
     assert "more workgroups than a launch" in jb.last_error()
+
+
+def test_a_stride_of_one_head_or_page_says_nothing(jb):
+    """Tensors whose strides differ from the usual ones only where a dimension has one entry."""
+    bf = torch.bfloat16
+    x = torch.zeros(1, 6, 64, dtype=bf).transpose(0, 1)                 # [6, 1, 64], heads 384 apart
+    assert x.stride(1) != 64 and x.is_contiguous() and jb._rows(x, "k")[1:] == (6, 64)
+    wide = torch.zeros(6, 256, dtype=bf)[:, None, 64:128]               # a slice of one projection's output
+    assert wide.stride(1) != 64 and jb._rows(wide, "k")[1:] == (6, 256)
+    assert jb._rows(wide.unsqueeze(0), "k")[1:] == (6, 256)
+    assert jb._rows(torch.zeros(3, 2, 256, dtype=bf)[:, :, None, :64], "k")[1:] == (6, 256)
+    with pytest.raises(ValueError):
+        jb._rows(torch.zeros(6, 2, 128, dtype=bf)[..., :64], "k")      # two heads that are not next to each other
+    table, kv = torch.zeros(3, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    k = torch.zeros(1, 2, 16, 64, dtype=bf)
+    v = torch.zeros(1, 4, 16, 64, dtype=bf)[:, :2]                      # one page: the distance to the next is nobody's
+    assert k.stride() != v.stride() and jb._pages(k, v, table, kv, 3, 64) == (1, 2, 16, 0, 4)
+    k = torch.zeros(5, 1, 16, 64, dtype=bf)
+    v = torch.zeros(1, 5, 16, 64, dtype=bf).transpose(0, 1)
+    assert k.stride() != v.stride() and jb._pages(k, v, table, kv, 3, 64) == (5, 1, 16, 1024, 4)
+    with pytest.raises(ValueError):
+        jb._pages(k, torch.zeros(5, 2, 16, 64, dtype=bf)[:, :1], table, kv, 3, 64)
