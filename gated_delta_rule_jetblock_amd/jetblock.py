@@ -610,9 +610,11 @@ def _on_stream(fn, args):
     """fn(**args) on the stream args names (a torch stream or a handle): the call, and what it
     allocates, belong to that stream, so nothing it still uses is handed out on another."""
     args = dict(args)
-    stream = args.pop("stream")
+    stream, di = args.pop("stream"), _device(args["q"])
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=args["q"].device)
+    elif stream.device.index != di:
+        raise ValueError(f"stream is of {stream.device}, q on cuda:{di}")
     with torch.cuda.stream(stream):
         return fn(**args)
 

@@ -93,3 +93,29 @@ def test_a_stride_of_one_head_or_page_says_nothing(jb):
     assert k.stride() != v.stride() and jb._pages(k, v, table, kv, 3, 64) == (5, 1, 16, 1024, 4)
     with pytest.raises(ValueError):
         jb._pages(k, torch.zeros(5, 2, 16, 64, dtype=bf)[:, :1], table, kv, 3, 64)
+
+
+class _Stream:
+    """What the binding looks at of a torch stream, and the context torch would enter for it."""
+
+    def __init__(self, device):
+        self.device, self.cuda_stream = torch.device(device), 7
+
+
+def test_stream_of_another_device_is_refused(jb, monkeypatch):
+    """A call runs on q's device: a stream of another one cannot order it, and is not passed over."""
+    import contextlib
+    entered = []
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: entered.append(s) or contextlib.nullcontext())
+
+    class Q:
+        is_cuda, device = True, torch.device("cuda:1")
+        get_device = staticmethod(lambda: 1)
+    ran = lambda **kw: kw
+    mine = _Stream("cuda:1")
+    assert jb._on_stream(ran, dict(q=Q, stream=mine, k=3)) == dict(q=Q, k=3) and entered == [mine]
+    with pytest.raises(ValueError, match="stream"):
+        jb._on_stream(ran, dict(q=Q, stream=_Stream("cuda:0")))
+    assert entered == [mine]
+    with pytest.raises(ValueError, match="device tensors"):
+        jb._on_stream(ran, dict(q=torch.zeros(1), stream=_Stream("cuda:0")))
