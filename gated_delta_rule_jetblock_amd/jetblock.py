@@ -700,11 +700,15 @@ def qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, wq=None, wk
 
 
 def _batch(q, cu_seqlens, max_seqlen):
-    """B and T of q: packed [tokens,H,D] with cu_seqlens, [B,T,H,D], or [B,H,D] (one token each)."""
+    """B and T of q: packed [tokens,H,D] with cu_seqlens, [B,T,H,D], or [B,H,D] (one token each).
+    Packed rows that no sequence owns may be more than B max_seqlen has room for: T covers them."""
     if cu_seqlens is not None:
         if q.dim() != 3 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("packed: q is [tokens, H, D] and cu_seqlens [B + 1]")
-        return cu_seqlens.numel() - 1, q.shape[0] if max_seqlen is None else min(int(max_seqlen), q.shape[0])
+        B, n = cu_seqlens.numel() - 1, q.shape[0]
+        if max_seqlen is not None and max_seqlen < 0:
+            raise ValueError(f"max_seqlen = {max_seqlen} must be >= 0")
+        return B, n if max_seqlen is None else min(max(int(max_seqlen), -(-n // B)), n)
     return (q.shape[0], q.shape[1]) if q.dim() == 4 else (q.shape[0], 1)
 
 

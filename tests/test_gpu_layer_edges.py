@@ -159,3 +159,29 @@ def test_tokens_of_a_cut_sequence_keep_their_rows(jb, dtype, new, kv, most, wind
             for c in ("k_cache", "v_cache"):
                 assert torch.equal(cut[c][p, :, x].cpu(), src[c][p, :, x].cpu()), (b, i)
         at += t
+
+
+# --------------------------------------------------------------- padded batches
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("behind", [1, 60])
+def test_padded_decode_batch(jb, dtype, behind):
+    """Single tokens, packed, with rows behind them that nobody owns (a batch padded to a size of its
+    own): their outputs stay, the others are as without them."""
+    new, kv = [1, 1, 0, 1], [90, 300, 5, 17]
+    d = append_inputs(new, kv, 4, 2, 64, 16, dtype, seed=50, behind=behind)
+    bare = dict(d, **{x: d[x][:3] for x in "qkv"})
+    qo = torch.full(d["q"].shape, 5.0, dtype=dtype, device="cuda")
+    r, e = append(jb, d, max_seqlen=1, q_out=qo), append(jb, bare, max_seqlen=1)
+    assert torch.equal(r["q"][:3], e["q"]) and (qo[3:] == 5).all()
+    for c in ("k_cache", "v_cache"):
+        assert torch.equal(r[c], e[c])
+    attended = {k: d[k] for k in ("q", "k_cache", "v_cache", "table", "kv", "cu")}
+    o = torch.full(d["q"].shape, 5.0, dtype=dtype, device="cuda")
+    r, e = call(jb, attended, max_seqlen=1, o=o), call(jb, dict(attended, q=bare["q"]), max_seqlen=1)
+    numbers(r["o"])
+    assert (o[3:] == 5).all()
+    # (perhaps by another kernel: half a step of a weight and of o, each side; fp32 as above)
+    far = (r["o"][:3].float() - e["o"].float()).abs().max()
+    assert far <= (1.1 * 2.0 ** -6 if dtype == BF else 2.0 ** -14) * d["v_cache"].float().abs().max()

@@ -119,3 +119,20 @@ def test_stream_of_another_device_is_refused(jb, monkeypatch):
     assert entered == [mine]
     with pytest.raises(ValueError, match="device tensors"):
         jb._on_stream(ran, dict(q=torch.zeros(1), stream=_Stream("cuda:0")))
+
+
+def test_packed_rows_behind_the_last_sequence_need_no_longer_hint(jb):
+    """A packed batch may have rows that no sequence owns, more of them than B max_seqlen leaves room
+    for: the planned length grows, so that the library takes the call."""
+    def plan(n, B, most):
+        return jb._batch(torch.zeros(n, 2, 64), torch.zeros(B + 1, dtype=torch.int32), most)
+    assert plan(100, 4, 60) == (4, 60) and plan(100, 4, None) == (4, 100) and plan(100, 4, 1000) == (4, 100)
+    assert plan(8, 4, 2) == (4, 2)
+    for n, B, most in ((9, 4, 2), (8, 3, 1), (64, 4, 1), (5, 4, 0)):
+        b, t = plan(n, B, most)
+        assert b == B and t == -(-n // B)
+        s = jb.AttnShape(B, t, 2, 2, 64, 0, 16, 8, 20, 0, 0, jb.JB_BF16, jb.JB_BF16, 0, 0, 0, 0, 0)
+        jb.attn_paged_workspace_size(s, n, True)   # (raises for a total that the shape cannot hold)
+    assert plan(0, 4, 7) == (4, 0)
+    with pytest.raises(ValueError, match="max_seqlen"):
+        plan(8, 4, -1)
