@@ -738,7 +738,9 @@ def qk_norm_rope_paged(q, k, v, k_cache, v_cache, page_table, kv_lens, inv_freq,
     """jb_qk_norm_rope_paged: rotated queries out, rotated keys and values into the caches
     [pages,Hkv,page,D] (in place).  q [B,T,H,D], [B,H,D] (one token each) or packed [tokens,H,D]
     with cu_seqlens int32 [B+1]; page_table int32 [B,max_pages], kv_lens int32 [B] (the new tokens
-    among the rows).  Returns dict(q, k_cache, v_cache)."""
+    among the rows).  max_seqlen (packed) is a limit: of a longer sequence the tokens behind its
+    first max_seqlen may be left out, neither appended nor written to q's output (default: none
+    are).  Returns dict(q, k_cache, v_cache)."""
     if stream is not None:
         return _on_stream(qk_norm_rope_paged, locals())
     di, io = _device(q), q.dtype
@@ -781,8 +783,11 @@ def attn_paged(q, k_cache, v_cache, page_table, kv_lens, *, cu_seqlens=None, max
     them already).  q [B,T,H,D], [B,H,D] (decode) or packed [tokens,H,D] with cu_seqlens int32
     [B+1]; caches, page_table and kv_lens as for qk_norm_rope_paged.  max_seqlen and max_kv, host
     integers, are the longest sequence's new tokens (packed; default: all) and cache rows (default:
-    the table's capacity); they plan the launch, nothing is read back from the device.  Returns
-    dict(o, lse): o of q's shape and out_dtype (default: q's), lse f32 [..., H] or None."""
+    the table's capacity); the launch is planned by them, nothing is read back from the device.
+    max_kv is a hint, longer caches are right too; max_seqlen is a limit: of a longer sequence the
+    tokens behind its first max_seqlen may be left out, their rows of o and lse not written.  scale
+    None (or 0) is 1 / sqrt(D).  Returns dict(o, lse): o of q's shape and out_dtype (default: q's;
+    float32 also takes the softmax weights more exactly), lse f32 [..., H] or None."""
     if stream is not None:
         return _on_stream(attn_paged, locals())
     di, io = _device(q), q.dtype
