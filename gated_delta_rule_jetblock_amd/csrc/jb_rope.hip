@@ -106,7 +106,8 @@ template <int D> __device__ __forceinline__ int partner(const RopeCall& c, int s
 
 // sin and cos of 2 pi t for |t| <= 1/2 (turns): the nearest quarter turn comes
 // off (exactly), the rest, at most an eighth, goes through the Taylor series of
-// both, cut where a term falls below 2^-31 (x^9, x^10 at pi / 4).
+// both up to x^9 and x^10; the first terms left out are at most 2^-29 and 2^-33 (at
+// pi / 4).  Off by at most 9e-8, with t's own rounding to 24 bits by 1.5e-7.
 __device__ __forceinline__ void sincos_turn(float t, float& sn, float& cs) {
   const float n = rintf(4.f * t), x = fmaf(-0.25f, n, t), y = x * x;
   const float s = x * fmaf(y, fmaf(y, fmaf(y, fmaf(y, 42.0586939f, -76.7058598f), 81.6052493f), -41.3417022f), 6.28318531f);
