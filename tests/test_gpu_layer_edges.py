@@ -1,6 +1,6 @@
 """GPU tests of the attention-layer operators at their edges: what the softmax weights' rounding
 leaves of an fp32 output and of a decode step, values that are not finite next to the rotation,
-packed sequences longer than the planned length."""
+packed sequences longer than the planned length, padded batches, long sums of weight gradients."""
 import numpy as np
 import pytest
 import torch
@@ -8,7 +8,7 @@ import torch
 from layer_checks import numbers, same_kind
 from oracle import attention as ref
 from test_gpu_attn import BF, F32, batch, call, f64
-from test_gpu_rope import append, append_inputs, inputs
+from test_gpu_rope import append, append_inputs, inputs, swap
 
 pytestmark = pytest.mark.gpu
 
@@ -185,3 +185,25 @@ def test_padded_decode_batch(jb, dtype, behind):
     # (perhaps by another kernel: half a step of a weight and of o, each side; fp32 as above)
     far = (r["o"][:3].float() - e["o"].float()).abs().max()
     assert far <= (1.1 * 2.0 ** -6 if dtype == BF else 2.0 ** -14) * d["v_cache"].float().abs().max()
+
+
+# ---------------------------------------------------------- weight gradients
+
+
+@pytest.mark.parametrize("n,H,Hkv,adds", [(1, 1, 1, 1), (2, 3, 1, 6), (65536, 2, 1, 94)])
+def test_sums_of_the_weights_gradients(jb, n, H, Hkv, adds):
+    """dwq, dwk relative to the sum of |n| (|y| + |y'|).  A term, in units of 2^-24: cosine and sine off
+    by 5 (the fraction of a turn rounded, 1.6; the series and its roundings), two roundings of
+    y c + y' s; of n = x r 11 (8 + 5 of the sum of squares, halved by the root, eps, the root 2, the
+    quotient, the product): 18.  And one for each sum on the longest way: all terms at most; for
+    many tokens a lane's 3 x 2, 32 groups of a workgroup, 24 workgroups of a thread and 32 threads."""
+    D = 64
+    d, g = inputs(n, H, Hkv, D, D, F32, seed=n)
+    gen = torch.Generator().manual_seed(n + 1)
+    dy = {x: torch.randn(d[x].shape, generator=gen) for x in "qk"}
+    r = jb.qk_norm_rope_backward(g["q"], g["k"], g["pos"], g["inv_freq"], dy["q"].cuda(), dy["k"].cuda(), g["wq"], g["wk"])
+    for x in "qk":
+        v = f64(d[x])
+        _, dw = ref.norm_rope_backward(v, d["pos"].numpy(), d["inv_freq"].numpy(), f64(dy[x]), f64(d["w" + x]))
+        size = (swap(f64(dy[x]), D, False) * np.abs(v) / np.sqrt((v * v).mean(-1, keepdims=True) + 1e-6)).sum((0, 1))
+        assert (np.abs(f64(r["dw" + x]) - dw) <= (18 + adds) * 2.0 ** -24 * size).all(), x
