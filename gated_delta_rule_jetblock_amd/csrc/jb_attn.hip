@@ -403,8 +403,8 @@ template <int D> struct Wave {
   // A tile that every query sees whole.  The maximum and the first weights, which
   // nothing of this wave overlaps, go before the other wave's work, and the
   // products with V, mixed with the other weights, before its products with K
-  // (at equal priority 2K tokens on 64K rows took 782 us and an 8K prompt 289; so
-  // 735 and 253).
+  // (at equal priority 2K tokens on 64K rows take 787 us and an 8K prompt 289; so
+  // 755 and 261 on the same card).
   template <int NB, bool TWO> __device__ void full(const Args& a, const lds_char* lk, const lds_char* lv) {
     f16_t s[NB];
     scores<NB>(lk, s);
@@ -597,12 +597,12 @@ __device__ __forceinline__ int64_t out_row(const Args& a, const Seq& s, int kvh,
 // Bound by the matrix cores and by what feeds them in turn: a wave's tile is 1024
 // cycles of products (D = 128) and about 900 of vector work (32 exponentials at a
 // quarter of the rate, the maximum, the sums), so two waves of two workgroups
-// share a SIMD; 128 rows a workgroup keep two on a CU (64 KB of LDS, 208
+// share a SIMD; 128 rows a workgroup keep two on a CU (64 KB of LDS, 198
 // registers) and read every K and V value once for 128 queries.  2K tokens on 64K
-// rows, 12 heads on 2: 722 us, 1125 TFLOP/s (the library's product of 8192^3
-// reaches 1226 on this card), matrix cores busy 62% of the cycles at the 1.7 GHz
-// the card then holds, no bank conflicts.  Head size 64, as much vector work for
-// half the products: 790 TFLOP/s; 256, one wave a SIMD: 970.
+// rows, 12 heads on 2: 751-766 us over the cards, 1060-1080 TFLOP/s (the library's
+// product of 8192^3 reaches 1226), matrix cores busy 62% of the cycles at the 1.7
+// GHz the card then holds, no bank conflicts.  Head size 64, as much vector work for
+// half the products: 452 us, 900 TFLOP/s; 256, one wave a SIMD: 1574 us, 1030.
 template <int D, typename OUT>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a) {
   constexpr int NW = 4, R = 64, IMG = R * D * 2;
@@ -694,9 +694,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
 // The lengths live in device memory: every workgroup adds them up itself, and
 // says which shared unit begins in its run.
 // Bound by HBM: each wave keeps a 16 KB tile on its way (64 KB a CU) while it uses
-// another, without a barrier.  64 sequences of 64K rows, 2 key heads of 128: 677
-// us, 6.3 TB/s; of 1K to 64K rows: 355 us, 6.1 TB/s (cut into 16 even pieces each,
-// without regard to the others: 377); 256 of 1K rows: 47 us, 5.8 TB/s.
+// another, without a barrier.  64 sequences of 64K rows, 2 key heads of 128: 707
+// us, 6.1 TB/s (a plain kernel that only reads reaches 7.2); of 1K to 64K rows: 365
+// us, 5.9 TB/s (in an earlier form 361, and 377 cut into 16 even pieces each, without
+// regard to the others); 256 of 1K rows: 48 us, 5.6 TB/s.
 __device__ __forceinline__ int steps_of(const Args& a, const Seq& s, int rows_a_step) {
   const int64_t nr = (int64_t)s.T * a.G;
   if (nr == 0 || nr > 32) return 0;  // none, or attn_tile_kernel's
@@ -987,8 +988,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(Args a, int rshift) {
 // Everything stays fp32.  4 waves x 16 query rows share 32-row tiles; for at
 // most 16 query rows (decode, SHARE) every wave has the same queries and takes
 // 16 of a tile's 64 cache rows, joined in LDS at the end.  16 sequences of 8K
-// rows, 2 key heads of 128: 66 us, 4.1 TB/s; 1K tokens on 4K rows, 8 heads: 191
-// us, 79 TFLOP/s (the library's fp32 product reaches 154).
+// rows, 2 key heads of 128: 68 us, 4.0 TB/s; 1K tokens on 4K rows, 8 heads: 201
+// us, 75 TFLOP/s (the library's fp32 product reaches 154).
 template <int D, bool SHARE, typename OUT>
 __global__ __launch_bounds__(256, 1) void attn_f32_kernel(Args a) {
   constexpr int R = SHARE ? 64 : 32, LD = D + 4, NW = 4, QR = SHARE ? 16 : NW * 16;
@@ -1209,10 +1210,14 @@ Plan plan(const AttnCall& c) {
   const int R = 1 << p.rshift;
   p.pitch = (int)std::min<int64_t>(R, (per + 15) & ~(int64_t)15);
   // bf16 sequences of at most 32 rows go to attn_row_kernel.  A packed batch may
-  // hold both kinds, and gets both kernels unless the cache range is so short
-  // that a workgroup of the tile kernel walks it while others still work (16
-  // sequences of 1 to 1024 tokens under a window of 1152: 104 us with both
-  // kernels, 93 with one).
+  // hold both kinds, and gets both kernels unless no cache range is longer than a
+  // workgroup of the tile kernel walks while others still work.  12 heads on 2 of
+  // 128, the tile kernel alone and both kernels.  Ranges up to 2048: 16 sequences of 1
+  // to 1024 tokens under a window of 1152 95 and 106 us, 60 single tokens and 4 chunks
+  // of 512 46 and 64, 252 and 4 90 and 102.  Longer ones that are alike lose too (60 and
+  // 4 on 4K rows: 109 and 140; on 16K and more either), but unlike ones need the
+  // equal runs: one of 64K rows among 255 of 1K 538 and 463, and single tokens
+  // packed without a planned length 291 and 151.
   const int64_t reach = c.window ? std::min(c.max_kv, c.window) : c.max_kv;
   p.tiles = f32 || per > 32;
   p.rows = !f32 && (per <= 32 || (c.packed && c.total < (int64_t)c.B * c.T && reach > 2048));
@@ -1228,9 +1233,12 @@ Plan plan(const AttnCall& c) {
   p.runs = p.direct ? units : std::min<int64_t>(c.D == 64 ? 512 : 256, units * cdiv(range, step));
   if (!p.tiles) return p;
   if (f32) {
-    // about the workgroups that the chip holds, by the LDS and registers of the
-    // head size (16 x 8K rows of decode at head size 256: 256 workgroups take
-    // 138 us, 1024 172; at 64 the other way round, 56 and 44)
+    // pieces for about so many workgroups, by measurement; registers hold fewer at
+    // once in some (chunks: 1024, 768 and 256 by the head size; decode: 768, 512, 256).
+    // For 256, 512, 768 and 1024 workgroups: 1K tokens on 4K rows, 8 heads on 8, head
+    // size 64 168, 117, 108 and 102 us, 128 284, 203, 188 and 203, 256 522, 477, 493 and
+    // 502; decode of 16 x 8K rows, 2 key heads, 64 59, 49, 49 and 52, 128 84, 69, 87 and
+    // 74, 256 142, 154, 178 and 179.
     const int64_t hold = std::min((p.share ? 65536 : 131072) / c.D, 1024);
     const int64_t want = cdiv(hold, p.slots * c.Hkv), most = cdiv(reach, 64);
     p.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 128));
@@ -1243,9 +1251,9 @@ Plan plan(const AttnCall& c) {
   // traffic.  A workgroup alone on its CU walks a tile in 1.7 us (D = 128), 2.0
   // with a second one there, so a last round of at most 256 costs less than a
   // whole one.  2K tokens, 16 heads on 2 (256 units) under a window of 1152: 1
-  // piece 33 us, 2 40; 2K tokens on 64K rows (192 units): 6 pieces 1119 us, 8
-  // (three whole rounds) 975, 16 1108; an 8K prompt (1024 units): 1 piece 290
-  // us, 2 331 (the last two with an earlier form of the kernel).
+  // piece 33 us, 2 41; 2K tokens on 64K rows (192 units): 6 pieces 892 us, 8
+  // (three whole rounds) 753, 16 783; an 8K prompt (1024 units): 1 piece 261
+  // us, 2 301.
   const int cu = c.D == 64 ? 3 : c.D == 128 ? 2 : 1;  // workgroups a CU holds
   // (a packed batch has more slots than tiles; half a tile of each sequence is a guess)
   const int64_t work = (c.packed ? cdiv(c.total * G, R) + c.B / 2 : p.slots) * c.Hkv;
@@ -1263,7 +1271,7 @@ Plan plan(const AttnCall& c) {
   p.tail = p.nsplit > 1 ? p.slots : 0;
   // Whole ranges in more than one round: those of the last, partial round (the
   // shortest) may be in pieces (12 heads on 2 of 128: 528 units under a window of
-  // 1152 take 64 us so, 76 whole; 600 under one of 2304 108, 126).
+  // 1152 take 62 us so, 75 whole; 600 under one of 2304 116, 132).
   const int64_t rest = work % (256 * cu);
   if (p.nsplit == 1 && work > 256 * cu && rest) {
     const double shortest = tiles(std::max<int64_t>(c.max_kv - c.T, 1));

@@ -19,10 +19,11 @@
 // x' the other member of the pair, fetched from its lane as raw bits.
 // dw is summed in fp32 in a fixed order: lanes over their tokens, the
 // workgroup through LDS, then one kernel over the workgroups' sums (5 us).
-// 64K tokens of 12 + 2 heads of 128, bf16: 88 us, 5.4 TB/s (the library's copy
-// reaches 5.0 on this card); backward 130 us, 5.4 TB/s, 3 workgroups a CU; the
-// append of 13K tokens in 32 chunks, 16 + 2 heads: 35 us, 3.8 TB/s, a quarter of
-// it the chain of loads that finds a token's place.
+// 64K tokens of 12 + 2 heads of 128, bf16: 87-92 us over the cards, 5.1-5.4 TB/s (a plain
+// copy kernel reaches 6.3, the library's copy 5.0); backward 130-137 us, 5.2-5.4
+// TB/s, 3 workgroups a CU; fp32 199 and 297 us, 4.7 TB/s; the append of 13K tokens in
+// 32 chunks, 16 + 2 heads: 35 us, 3.8 TB/s, a quarter of it the chain of loads that
+// finds a token's place (fp32 76 us, 3.4 TB/s).
 #include "jb_attn.h"
 #include "jb_device.h"
 
@@ -49,9 +50,10 @@ template <> struct Raw<float> {
   __device__ float get(int i) const { return __uint_as_float(u[i]); }
 };
 typedef uint32_t u4_t __attribute__((ext_vector_type(4)));
-// NT: a stream that no cache need keep: training's loads and stores and the
-// append's q_out.  64K tokens took 93 us forward and 143 backward without, 88
-// and 130 with; the append's own loads gain nothing.
+// NT: past the caches: training's loads and stores, and the append's q_out although
+// the attention reads that next.  64K tokens take 95.7 us forward and 143 backward
+// without, 88.9 and 132.5 with; an append of 13K tokens 36.7 and 35.0 (its loads gain
+// nothing).
 template <bool NT = false, typename T> __device__ __forceinline__ Raw<T> load8(const T* p) {
   Raw<T> r;
 #pragma unroll
@@ -192,8 +194,8 @@ template <typename T> __device__ __forceinline__ void weights(const void* w, int
 template <int D, typename IO, typename OUT, bool PAGED>
 __global__ __launch_bounds__(256) void rope_kernel(Args a) {
   constexpr int L = D / 8, GROUPS = 256 / L;
-  // rows in use, and as many on their way (64K tokens: 4 took 91 us, 2 93, and 96
-  // with none on their way; an append of 13K tokens: 2 take 35 us, 4 38)
+  // rows in use, and as many on their way (64K tokens: 4 take 88.9 us, 2 90.9; an
+  // append of 13K tokens 34.5 and 35.0, where 2 need fewer registers)
   constexpr int U = PAGED || sizeof(IO) == 4 ? 2 : 4;
   const RopeCall& c = a.c;
   const int lane = lane_id(), s = lane % L, group = threadIdx.x / L;
