@@ -22,8 +22,9 @@
 // itself loses (together 2.0-2.4e-3 of o's norm, o's rounding alone 1.65e-3).
 // Where the caller wants o in fp32, and in decode, P is two parts, hi + lo
 // (within 2^-15), and their products with V are two: nothing in decode (64
-// sequences of 64K rows 365 us either way), but a third more with many queries (2K
-// tokens on 64K rows 766 us, in two parts 1030; an 8K prompt 258 and 346).
+// sequences of 1K to 64K rows 365 us either way), but a third more with many queries
+// (2K tokens on 64K rows 766 us, in two parts 1030; an 8K prompt 258 and 346; with
+// fp32 o, which also leaves so, 988 and 344).
 //   attn_tile_kernel  many queries: 4 waves x 32 rows of one key head walk the
 //                     same 64-row cache tiles through two LDS buffers.
 //   attn_row_kernel   at most 32 rows (decode): every wave takes its own 32-row
