@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libjetblock.so")
 SOURCES = ["jb_api.hip", "jb_gen.hip", "jb_prefill.hip", "jb_fwd.hip", "jb_decode.hip", "jb_proj.hip",
-           "jb_backward.hip", "jb_layer.hip", "jb_attn.hip", "jb_rope.hip"]
+           "jb_backward.hip", "jb_layer.hip", "jb_attn.hip", "jb_rope.hip", "jb_layer8.hip", "jb_attn8.hip", "jb_blocks.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -28,7 +28,7 @@ FLAGS = [
 
 # matrix-core accumulators in the vector registers: the attention kernels that
 # run one wave a SIMD otherwise move them to and fro, and spill at head size 256
-EXTRA = {"jb_attn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+EXTRA = dict.fromkeys(["jb_attn.hip", "jb_attn8.hip"], ["-mllvm", "-amdgpu-mfma-vgpr-form=1"])
 
 
 def _compile(src: str) -> str:

@@ -1,0 +1,487 @@
+// jb_blocks.hip -- attention over selected pages of the cache: the pages' mean keys and
+// their scores for each new token, the selection by score, and the lists that the
+// attention kernels (jb_attn_core.h) walk.
+//
+// Token i of a sequence sits at cache row p and sees pages 0 .. p / page.  With mean_j the
+// mean of the rows that page j holds of a key head (fp32),
+//     score_j = max over the key head's query heads of q . mean_j,
+// and of the pages it sees the token reads its first and last ones and the best others.
+#include <type_traits>
+
+#include "jb_attn.h"
+#include "jb_device.h"
+#include "jb_e4m3.h"
+
+namespace jb {
+
+namespace {
+
+typedef unsigned int u4_t __attribute__((ext_vector_type(4)));
+
+struct Args {
+  BlockCall c;
+  int G, pshift;
+  int64_t slots;  // places for a sequence's pages (means) or token tiles (scores)
+};
+
+// a sequence's tokens (the first c.T of them) and the cache row of the first one, all
+// clamped to the tensors (they come from device memory)
+struct Seq {
+  int64_t tok0;
+  int T, row0;
+};
+__device__ __forceinline__ Seq seq_of(const Args& a, int b) {
+  const BlockCall& c = a.c;
+  Seq s;
+  int all = c.T;
+  s.tok0 = (int64_t)b * c.T;
+  if (c.cu_seqlens) clamp_span(c.cu_seqlens[b], c.cu_seqlens[b + 1], 0x7fffffff, c.total, s.tok0, all);
+  s.T = min(all, c.T);
+  const int cap = (int)min((int64_t)c.max_pages << a.pshift, (int64_t)0x7fffffff);
+  s.row0 = min(max(c.kv_lens[b], 0), cap) - all;
+  return s;
+}
+
+// Place `slot` among the sequences': sequence b's start at per b, or packed at
+// (cu[b] >> shift) + more b, which leaves room for all of them and never decreases.
+// All threads of the workgroup call this together.
+__device__ __forceinline__ int seq_at(const Args& a, int64_t slot, int shift, int more, int64_t per, int64_t& nth) {
+  const BlockCall& c = a.c;
+  if (!c.cu_seqlens) {
+    const int b = (int)(slot / per);
+    nth = slot - b * per;
+    return b;
+  }
+  auto base = [&](int j) {
+    return (min(max((int64_t)c.cu_seqlens[j], (int64_t)0), c.total) >> shift) + more * (int64_t)j;
+  };
+  int n = 0;
+  for (int k = 0; k < c.B; k += blockDim.x) {
+    const int j = k + threadIdx.x;
+    const int m = __syncthreads_count(j < c.B && base(j) <= slot);
+    n += m;
+    if (m < (int)blockDim.x) break;
+  }
+  const int b = max(n - 1, 0);
+  nth = slot - base(b);
+  return b;
+}
+
+// Sequence of token t and its place in it; false: no sequence owns it (or it is one of
+// those behind the first c.T).  t0: the workgroup's first token, the same for all threads.
+__device__ __forceinline__ bool token_at(const Args& a, int64_t t0, int64_t t, int& b, Seq& s, int& i) {
+  const BlockCall& c = a.c;
+  int64_t nth;
+  b = seq_at(a, t0, 0, 0, max(c.T, 1), nth);
+  if (c.cu_seqlens) {
+    while (b + 1 < c.B && c.cu_seqlens[b + 1] <= t) ++b;
+  } else {
+    b = (int)(t / max(c.T, 1));
+  }
+  s = seq_of(a, b);
+  const int64_t at = t - s.tok0;
+  i = (int)at;
+  return at >= 0 && at < s.T;
+}
+
+// 8 values of a cache row as floats
+template <typename KV> __device__ __forceinline__ void row8(const void* p, uint32_t e, float (&x)[8]) {
+  if constexpr (sizeof(KV) == 1) {
+    const uint2 u = *static_cast<const uint2*>(p);
+    const float4 lo = floats_of_e4m3(u.x, e), hi = floats_of_e4m3(u.y, e);
+    x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+  } else if constexpr (sizeof(KV) == 2) {
+    const u4_t u = *static_cast<const u4_t*>(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(i & 1 ? u[i >> 1] & 0xffff0000u : u[i >> 1] << 16);
+  } else {
+    const float4 lo = static_cast<const float4*>(p)[0], hi = static_cast<const float4*>(p)[1];
+    x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w, x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+  }
+}
+
+// Mean key of every page that holds new tokens, over the rows that it holds by now: a
+// workgroup a page and key head, D / 8 lanes a row, summed in a fixed order (a lane group's
+// rows in order, then the groups).
+template <int D, typename KV>
+__global__ __launch_bounds__(256) void block_means_kernel(Args a) {
+  constexpr int L = D / 8, GROUPS = 256 / L;
+  const BlockCall& c = a.c;
+  const uint32_t slot = blockIdx.x / (uint32_t)c.Hkv;
+  const int head = blockIdx.x - slot * (uint32_t)c.Hkv, page = 1 << a.pshift;
+  int64_t nth;
+  const int b = seq_at(a, slot, a.pshift, 2, ((int64_t)c.T + page - 2) / page + 1, nth);
+  const Seq s = seq_of(a, b);
+  const int end = s.row0 + s.T;
+  const int64_t j = (max(s.row0, 0) >> a.pshift) + nth;  // the page's place in the sequence
+  if (nth < 0 || s.T == 0 || j << a.pshift >= end) return;
+  const int pid = c.page_table[(int64_t)b * c.max_pages + j];
+  if (pid < 0 || pid >= c.num_pages) return;
+  const int held = (int)min((int64_t)end - (j << a.pshift), (int64_t)page);
+  const int lane = threadIdx.x % L, group = threadIdx.x / L;
+  const int64_t row0 = (int64_t)head << a.pshift;
+  const char* k = (const char*)c.k_cache + (pid * c.page_stride + row0 * D + 8 * lane) * (int64_t)sizeof(KV);
+  const uint8_t* e = sizeof(KV) == 1 ? c.k_scales + pid * c.scale_stride + (row0 >> 4) : nullptr;
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int r = group; r < held; r += GROUPS) {
+    float x[8];
+    row8<KV>(k + (int64_t)r * D * sizeof(KV), sizeof(KV) == 1 ? e[r >> 4] : 0u, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] += x[i];
+  }
+  __shared__ float part[GROUPS][D + 1];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) part[group][8 * lane + i] = sum[i];
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float total = 0.f;
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) total += part[g][threadIdx.x];
+    c.means[((int64_t)pid * c.Hkv + head) * D + threadIdx.x] = total / (float)held;
+  }
+}
+
+// the larger of two scores; NaN stays
+__device__ __forceinline__ float larger(float m, float x) { return x > m || x != x ? x : m; }
+
+// Scores of 16 tokens and 16 pages at a time on matrix cores: rows are tokens, columns
+// pages, one product for each query head, their maximum taken in the accumulators.  bf16
+// queries meet a mean as three bf16 parts (hi + mid + lo are its 24 bits, so every product
+// is exact and the sums are fp32's); fp32 ones take fp32 products.
+// A wave takes TM x 16 tokens and 2 x 16 pages, a workgroup 4 times as many pages.
+constexpr int TM = 2, NB = 2, TOKENS = 16 * TM, PAGES = 4 * 16 * NB;
+
+template <int D, typename IO> struct Means;  // of 16 pages: lane (page lane % 16, group g) has d = 8 g + e of every 32
+template <int D> struct Means<D, bf16_t> {
+  bf16x8_t part[D / 32][3];
+  __device__ void take(const float* p, bool ok) {
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+      const float4 lo = ok ? *reinterpret_cast<const float4*>(p + 32 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 hi = ok ? *reinterpret_cast<const float4*>(p + 32 * k + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const __bf16 a = (__bf16)x[e];
+        const float r = x[e] - (float)a;
+        const __bf16 b = (__bf16)r;
+        part[k][0][e] = a, part[k][1][e] = b, part[k][2][e] = (__bf16)(r - (float)b);
+      }
+    }
+  }
+};
+template <int D> struct Means<D, float> {
+  f4_t lo[D / 32], hi[D / 32];
+  __device__ void take(const float* p, bool ok) {
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+      lo[k] = ok ? *reinterpret_cast<const f4_t*>(p + 32 * k) : zero4();
+      hi[k] = ok ? *reinterpret_cast<const f4_t*>(p + 32 * k + 4) : zero4();
+    }
+  }
+};
+
+template <int D, typename IO>
+__global__ __launch_bounds__(256) void block_scores_kernel(Args a, uint32_t groups) {
+  const BlockCall& c = a.c;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n16 = lane & 15, g = lane >> 4;
+  const uint32_t per = (uint32_t)c.Hkv * groups, slot = blockIdx.x / per, rest = blockIdx.x - slot * per;
+  const int head = rest / groups, j0 = (int)(rest - head * groups) * PAGES + wave * 16 * NB;
+  int64_t nth;
+  const int b = seq_at(a, slot, 5, 1, ((int64_t)c.T + TOKENS - 1) / TOKENS, nth);
+  static_assert(TOKENS == 32, "2^5 tokens a slot");
+  const Seq s = seq_of(a, b);
+  if (nth < 0 || nth * TOKENS >= s.T || j0 >= c.max_pages) return;
+  const int i0 = (int)nth * TOKENS, live = min(s.T - i0, TOKENS);
+  const int seen = ((s.row0 + i0 + live - 1) >> a.pshift) + 1;  // pages that some token sees (negative rows: none)
+  const int* table = c.page_table + (int64_t)b * c.max_pages;
+  f4_t best[TM][NB];
+#pragma unroll
+  for (int t = 0; t < TM; ++t)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) best[t][n] = f4_t{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  if (j0 < seen) {
+    Means<D, IO> m[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const int j = j0 + 16 * n + n16;
+      const int pid = j < min(seen, c.max_pages) ? table[j] : -1;
+      const bool ok = pid >= 0 && pid < c.num_pages;
+      m[n].take(c.means + ((int64_t)(ok ? pid : 0) * c.Hkv + head) * D + 8 * g, ok);
+    }
+    for (int h = 0; h < a.G; ++h) {
+#pragma unroll
+      for (int t = 0; t < TM; ++t) {
+        if (t && 16 * t >= live) break;
+        const int i = i0 + min(16 * t + n16, live - 1);
+        const IO* q = (const IO*)c.q + (s.tok0 + i) * c.q_stride + (int64_t)(head * a.G + h) * D + 8 * g;
+        f4_t x[NB];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) x[n] = zero4();
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          if constexpr (sizeof(IO) == 2) {
+            const bf16x8_t qk = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u4_t*>(q + 32 * k));
+#pragma unroll
+            for (int part = 0; part < 3; ++part)
+#pragma unroll
+              for (int n = 0; n < NB; ++n)
+                x[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qk, m[n].part[k][part], x[n], 0, 0, 0);
+          } else {
+            const f4_t lo = *reinterpret_cast<const f4_t*>(q + 32 * k), hi = *reinterpret_cast<const f4_t*>(q + 32 * k + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int n = 0; n < NB; ++n) {
+                x[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(lo[e], m[n].lo[k][e], x[n], 0, 0, 0);
+                x[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(hi[e], m[n].hi[k][e], x[n], 0, 0, 0);
+              }
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) best[t][n][e] = h ? larger(best[t][n][e], x[n][e]) : x[n][e];
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TM; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 16 * t + 4 * g + e;
+      if (i >= live) continue;
+      const int own = (s.row0 + i0 + i) >> a.pshift;
+      float* out = c.scores + ((s.tok0 + i0 + i) * c.Hkv + head) * c.max_pages;
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const int j = j0 + 16 * n + n16;
+        if (j < c.max_pages) out[j] = j <= own ? best[t][n][e] : -INFINITY;
+      }
+    }
+}
+
+// Selection by a search for the count-th largest score, bit by bit from the top: a row's
+// scores stay in registers as whole numbers in the scores' order, V a lane, and a step
+// counts those that reach a candidate (a compare, a scalar bit count).  W waves a row; with
+// one the row needs no barrier.  Places are ascending: lane l of wave w has pages
+// (w V + v) 64 + l.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t u = __float_as_uint(x != x ? -INFINITY : x + 0.f);  // (-0 as 0)
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+template <int W, int V>
+__global__ __launch_bounds__(W == 1 ? 256 : W * 64) void block_select_kernel(Args a) {
+  constexpr int ROWS = W == 1 ? 4 : 1;  // rows a workgroup
+  const BlockCall& c = a.c;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, w = W == 1 ? 0 : wave;
+  const int64_t rows = c.total * c.Hkv, row0 = (int64_t)blockIdx.x * ROWS, row = row0 + (W == 1 ? wave : 0);
+  const int64_t t = min(row, rows - 1) / c.Hkv;
+  int b, i;
+  Seq s;
+  const bool live = token_at(a, row0 / c.Hkv, t, b, s, i) && row < rows;
+  if (!live) return;  // (with W > 1 the workgroup's only row)
+  const int own = (s.row0 + i) >> a.pshift;  // (of a negative row negative: it sees no page)
+  const int nv = min(own + 1, c.max_pages), count = c.count;
+  int* const out = c.blocks + row * count;
+  const int at = w * V * 64 + lane;
+  if (nv <= count) {  // all of them
+    for (int j = W == 1 ? lane : (int)threadIdx.x; j < count; j += W * 64) out[j] = j < nv ? j : -1;
+    return;
+  }
+  const float* x = c.scores_in + row * c.max_pages;
+  uint32_t key[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int j = at + 64 * v;
+    key[v] = 0;
+    if (j < nv) key[v] = j < c.first || j > own - c.recent ? 0xffffffffu : order_of(x[j]);
+  }
+  __shared__ int counts[2][W];
+  auto over_waves = [&](int n, int turn) {  // the sum of the waves' n (a scalar of each)
+    if constexpr (W == 1) return n;
+    if (lane == 0) counts[turn & 1][w] = n;
+    __syncthreads();
+    int sum = 0;
+#pragma unroll
+    for (int u = 0; u < W; ++u) sum += counts[turn & 1][u];
+    return sum;
+  };
+  uint32_t low = 0;  // at least `count` scores reach it
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t t = low | 1u << bit;
+    int n = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) n += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[v] >= t));
+    n = over_waves(n, bit);
+    if (n >= count) low = t;
+    if (n == count) break;
+  }
+  // those above `low`, and of those equal to it the first ones
+  int above = 0, equal = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    above += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[v] > low));
+    equal += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[v] == low));
+  }
+  int need, taken = 0, equals = 0;  // equal ones to take; taken and equal ones before this wave's
+  if constexpr (W == 1) {
+    need = count - above;
+  } else {
+    __shared__ int2 both[W];
+    __syncthreads();
+    if (lane == 0) both[w] = make_int2(above, equal);
+    __syncthreads();
+    int sum = 0, before = 0;
+#pragma unroll
+    for (int u = 0; u < W; ++u) {
+      sum += both[u].x;
+      if (u < w) before += both[u].x, equals += both[u].y;
+    }
+    need = count - sum;
+    taken = before + min(equals, need);
+  }
+  const uint64_t below = (1ull << lane) - 1;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const uint64_t eq = __builtin_amdgcn_ballot_w64(key[v] == low);
+    const bool take = key[v] > low || (key[v] == low && equals + __builtin_popcountll(eq & below) < need);
+    const uint64_t all = __builtin_amdgcn_ballot_w64(take);
+    if (take) out[taken + __builtin_popcountll(all & below)] = at + 64 * v;
+    taken += __builtin_popcountll(all);
+    equals += __builtin_popcountll(eq);
+  }
+}
+
+// The pages of every (token, key head), one wave each, as a cache of their own: page
+// indices in order and the rows seen.  An entry counts if it is a page that the token sees
+// and larger than every one before it; -1 rows: no sequence owns the token.
+__global__ __launch_bounds__(256) void block_list_kernel(Args a, int* table, int* kv) {
+  const BlockCall& c = a.c;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int64_t units = c.total * c.Hkv, unit0 = (int64_t)blockIdx.x * 4, unit = unit0 + wave;
+  const int64_t t = min(unit, units - 1) / c.Hkv;
+  int b, i;
+  Seq s;
+  const bool live = token_at(a, unit0 / c.Hkv, t, b, s, i);
+  if (unit >= units) return;
+  if (!live) {
+    if (lane == 0) kv[unit] = -1;
+    return;
+  }
+  const int p = s.row0 + i, own = p >> a.pshift;
+  const int* list = c.blocks + unit * c.count;
+  const int* pages = c.page_table + (int64_t)b * c.max_pages;
+  int* out = table + unit * c.count;
+  int last = -1, n = 0;  // the largest so far, and how many
+  for (int k = 0; k < c.count; k += 64) {
+    const int x = k + lane < c.count ? list[k + lane] : -1;
+    const int mine = x >= 0 && x <= own ? x : -1;
+    int most = mine;  // of this lane and those before it
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(most, o, WAVE);
+      if (lane >= o) most = max(most, u);
+    }
+    int before = __shfl_up(most, 1, WAVE);
+    before = max(lane ? before : -1, last);
+    const bool take = mine > before;
+    const uint64_t all = __builtin_amdgcn_ballot_w64(take);
+    if (take) out[n + __builtin_popcountll(all & ((1ull << lane) - 1))] = pages[mine];
+    n += __builtin_popcountll(all);
+    last = max(last, __builtin_amdgcn_readlane(most, 63));
+  }
+  if (lane == 0) kv[unit] = n && last == own ? ((n - 1) << a.pshift) + (p & ((1 << a.pshift) - 1)) + 1 : n << a.pshift;
+}
+
+int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
+size_t a256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+Args args_of(const BlockCall& c) {
+  Args a;
+  a.c = c;
+  a.G = c.H / c.Hkv, a.pshift = __builtin_ctz((unsigned)c.page);
+  a.slots = 0;
+  return a;
+}
+
+int64_t mean_slots(const BlockCall& c) {
+  return c.packed ? (c.total / c.page) + 2 * (int64_t)c.B : (int64_t)c.B * (((int64_t)c.T + c.page - 2) / c.page + 1);
+}
+int64_t score_slots(const BlockCall& c) { return c.packed ? c.total / TOKENS + c.B : (int64_t)c.B * cdiv(c.T, TOKENS); }
+
+template <int D, typename IO> hipError_t scores(const BlockCall& c, hipStream_t stream) {
+  const Args a = args_of(c);
+  const dim3 grid((unsigned)(mean_slots(c) * c.Hkv));
+  if (c.bits8) block_means_kernel<D, uint8_t><<<grid, dim3(256), 0, stream>>>(a);
+  else block_means_kernel<D, IO><<<grid, dim3(256), 0, stream>>>(a);
+  if (c.scores) {
+    const int64_t groups = cdiv(c.max_pages, PAGES);
+    block_scores_kernel<D, IO><<<dim3((unsigned)(score_slots(c) * c.Hkv * groups)), dim3(256), 0, stream>>>(a, (uint32_t)groups);
+  }
+  return hipGetLastError();
+}
+
+// attention over the listed pages: every (token, key head) is a sequence of one token
+AttnCall listed(const BlockCall& c, const AttnCall& attn) {
+  AttnCall x = attn;
+  x.units = c.Hkv;
+  x.B = (int)(c.total * c.Hkv), x.T = 1, x.H = c.H / c.Hkv, x.Hkv = 1, x.total = x.B;
+  x.max_pages = c.count, x.max_kv = (int)std::min<int64_t>((int64_t)c.count << __builtin_ctz((unsigned)c.page), x.max_kv);
+  x.packed = false, x.cu_seqlens = nullptr, x.window = 0;
+  return x;
+}
+size_t list_bytes(const BlockCall& c) { return a256((size_t)c.total * c.Hkv * c.count * 4) + a256((size_t)c.total * c.Hkv * 4); }
+
+}  // namespace
+
+int64_t block_scores_workgroups(const BlockCall& c) {
+  return std::max(mean_slots(c) * c.Hkv, c.scores ? score_slots(c) * c.Hkv * cdiv(c.max_pages, PAGES) : 0);
+}
+
+hipError_t launch_block_scores(const BlockCall& c, hipStream_t stream) {
+  const bool f = c.io == IO_F32;
+  switch (c.D) {
+    case 64: return f ? scores<64, float>(c, stream) : scores<64, bf16_t>(c, stream);
+    case 128: return f ? scores<128, float>(c, stream) : scores<128, bf16_t>(c, stream);
+    case 256: return f ? scores<256, float>(c, stream) : scores<256, bf16_t>(c, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+int64_t block_select_workgroups(const BlockCall& c) { return c.total * c.Hkv * (c.max_pages <= 4096 ? 1 : 4); }
+
+hipError_t launch_block_select(const BlockCall& c, hipStream_t stream) {
+  const Args a = args_of(c);
+  const dim3 grid((unsigned)cdiv(c.total * c.Hkv, c.max_pages <= 1024 ? 4 : 1));
+  if (c.max_pages <= 256) block_select_kernel<1, 4><<<grid, dim3(256), 0, stream>>>(a);
+  else if (c.max_pages <= 1024) block_select_kernel<1, 16><<<grid, dim3(256), 0, stream>>>(a);
+  else if (c.max_pages <= 4096) block_select_kernel<4, 16><<<grid, dim3(256), 0, stream>>>(a);
+  else if (c.max_pages <= 16384) block_select_kernel<16, 16><<<grid, dim3(1024), 0, stream>>>(a);
+  else block_select_kernel<16, 64><<<grid, dim3(1024), 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+int64_t attn_blocks_workgroups(const BlockCall& c, const AttnCall& attn) {
+  return std::max(attn_workgroups(listed(c, attn)), cdiv(c.total * c.Hkv, 4));
+}
+
+size_t attn_blocks_workspace_bytes(const BlockCall& c, const AttnCall& attn) {
+  return list_bytes(c) + attn_workspace_bytes(listed(c, attn));
+}
+
+hipError_t launch_attn_blocks(const BlockCall& c, const AttnCall& attn, hipStream_t stream) {
+  AttnCall x = listed(c, attn);
+  char* const ws = static_cast<char*>(attn.workspace);
+  int* const table = reinterpret_cast<int*>(ws);
+  int* const kv = reinterpret_cast<int*>(ws + a256((size_t)c.total * c.Hkv * c.count * 4));
+  block_list_kernel<<<dim3((unsigned)cdiv(c.total * c.Hkv, 4)), dim3(256), 0, stream>>>(args_of(c), table, kv);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  x.page_table = table, x.kv_lens = kv, x.workspace = ws + list_bytes(c);
+  return x.bits8 ? launch_attn8(x, stream) : launch_attn(x, stream);
+}
+
+}  // namespace jb

@@ -26,6 +26,7 @@
 // finds a token's place (fp32 76 us, 3.4 TB/s).
 #include "jb_attn.h"
 #include "jb_device.h"
+#include "jb_e4m3.h"
 
 namespace jb {
 
@@ -36,6 +37,8 @@ struct Args {
   int parts, heads;   // head parts a token is cut into, heads a part
   int64_t units;      // tokens x parts
   float* sums;        // backward: [workgroups][2][D]
+  int64_t cells;      // append in 8 bits: places for 16 cache rows with new ones
+  int kv_heads;       // and its key heads (c.Hkv is 0: the heads by token are the queries)
 };
 
 template <typename T> struct Raw;
@@ -191,15 +194,16 @@ template <typename T> __device__ __forceinline__ void weights(const void* w, int
   }
 }
 
+// workgroup `block` of the heads of all tokens
 template <int D, typename IO, typename OUT, bool PAGED>
-__global__ __launch_bounds__(256) void rope_kernel(Args a) {
+__device__ __forceinline__ void rope_rows(const Args& a, uint32_t block) {
   constexpr int L = D / 8, GROUPS = 256 / L;
   // rows in use, and as many on their way (64K tokens: 4 take 88.9 us, 2 90.9; an
   // append of 13K tokens 34.5 and 35.0, where 2 need fewer registers)
   constexpr int U = PAGED || sizeof(IO) == 4 ? 2 : 4;
   const RopeCall& c = a.c;
   const int lane = lane_id(), s = lane % L, group = threadIdx.x / L;
-  const int64_t unit = (int64_t)blockIdx.x * GROUPS + group;
+  const int64_t unit = (int64_t)block * GROUPS + group;
   bool live = unit < a.units;
   // (fewer than 2^31 units where a token has several)
   int64_t t = !live ? 0 : a.parts == 1 ? unit : (uint32_t)unit / (uint32_t)a.parts;
@@ -234,7 +238,7 @@ __global__ __launch_bounds__(256) void rope_kernel(Args a) {
     int T = c.T;  // the sequence's tokens (those behind the first c.T are not taken)
     if (c.packed) {
       // the sequence of the workgroup's first token, then on from there
-      const int64_t t0 = (int64_t)blockIdx.x * GROUPS / a.parts;
+      const int64_t t0 = (int64_t)block * GROUPS / a.parts;
       int n = 0;
       for (int k = 0; k < c.B; k += 256) {
         const int j = k + threadIdx.x;
@@ -255,7 +259,7 @@ __global__ __launch_bounds__(256) void rope_kernel(Args a) {
     const int pshift = __builtin_ctz((unsigned)c.page);
     const int cap = (int)min((int64_t)c.max_pages << pshift, (int64_t)0x7fffffff);
     row = min(max(c.kv_lens[b], 0), cap) - T + (int)i;
-    if (live && row >= 0) {
+    if (live && row >= 0 && c.Hkv) {
       const int pid = c.page_table[(int64_t)b * c.max_pages + (row >> pshift)];
       if (pid >= 0 && pid < c.num_pages) slot = pid * c.page_stride + (int64_t)(row & (c.page - 1)) * D;
     }
@@ -300,6 +304,163 @@ __global__ __launch_bounds__(256) void rope_kernel(Args a) {
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) x[u] = next[u];
+  }
+}
+
+template <int D, typename IO, typename OUT, bool PAGED>
+__global__ __launch_bounds__(256) void rope_kernel(Args a) {
+  rope_rows<D, IO, OUT, PAGED>(a, blockIdx.x);
+}
+
+// Exponent e of the smallest scale 2^(e - 127) with most <= 448 times it, 1 at least:
+// 448 = 1.75 * 2^8, so it is most's exponent less 8, or less 7 where its fraction is over 1.75.
+__device__ __forceinline__ int exponent_for(float most) {
+  const uint32_t u = __float_as_uint(most);
+  return max((int)(u >> 23) - ((u & 0x7fffffu) > 0x600000u ? 7 : 8), 1);
+}
+// 2^(127 - e), what values are divided by their scale with
+__device__ __forceinline__ float inverse_scale(int e) { return __uint_as_float(e >= 254 ? 1u << 22 : (uint32_t)(254 - e) << 23); }
+
+// 8 values to the nearest codes, ties to even (|x| <= 448; infinities and NaN become NaN)
+__device__ __forceinline__ uint2 e4m3_of(const float (&x)[8]) {
+  int lo = 0, hi = 0;
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], lo, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[4], x[5], hi, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(x[6], x[7], hi, true);
+  return make_uint2(lo, hi);
+}
+
+// The append to a cache in 8 bits.  The first a.cells * Hkv workgroups take 16 cache rows
+// of one key head each, K and V: its lane groups form the new rows' values, the largest
+// finite one sets the scale, and if rows of earlier calls share it the larger of the two
+// scales holds: their codes are divided by 2^k (exactly, but for those that fall below the
+// smallest normal code, which are rounded again).  Rows behind the new ones keep their codes.
+// The other workgroups rotate the queries.
+template <int D, typename IO>
+__global__ __launch_bounds__(256) void rope_append8_kernel(Args a) {
+  constexpr int L = D / 8, GROUPS = 256 / L, N = 32 / GROUPS;  // rows at once; times for 16 of K and 16 of V
+  const RopeCall& c = a.c;
+  const uint32_t cells = (uint32_t)a.cells * (uint32_t)a.kv_heads;
+  if (blockIdx.x >= cells) {
+    rope_rows<D, IO, IO, true>(a, blockIdx.x - cells);
+    return;
+  }
+  const uint32_t cell = blockIdx.x / (uint32_t)a.kv_heads;
+  const int head = blockIdx.x - cell * (uint32_t)a.kv_heads;
+  const int lane = lane_id(), s = lane % L, group = threadIdx.x / L;
+  // the cell's sequence and its place among those that hold the sequence's new rows
+  int b, T = c.T, all = c.T;
+  int64_t nth, tok0;
+  if (c.packed) {
+    // sequence j's cells start at cu[j] / 16 + 2 j, which leaves room for all of them
+    auto base = [&](int j) { return (min(max((int64_t)c.cu_seqlens[j], (int64_t)0), c.total) >> 4) + 2 * (int64_t)j; };
+    int n = 0;
+    for (int k = 0; k < c.B; k += 256) {
+      const int j = k + threadIdx.x;
+      const int m = __syncthreads_count(j < c.B && base(j) <= cell);
+      n += m;
+      if (m < 256) break;
+    }
+    b = max(n - 1, 0);
+    nth = (int64_t)cell - base(b);
+    clamp_span(c.cu_seqlens[b], c.cu_seqlens[b + 1], 0x7fffffff, c.total, tok0, all);
+    T = min(all, c.T);
+  } else {
+    const uint32_t per = (uint32_t)(c.T + 14) / 16 + 1;
+    b = (int)(cell / per);
+    nth = cell - (uint32_t)b * per;
+    tok0 = (int64_t)b * c.T;
+  }
+  const int pshift = __builtin_ctz((unsigned)c.page), cap = (int)min((int64_t)c.max_pages << pshift, (int64_t)0x7fffffff);
+  const int row0 = min(max(c.kv_lens[b], 0), cap) - all;  // of the first new token
+  const int end = row0 + T;
+  const int64_t first = ((int64_t)(max(row0, 0) >> 4) + nth) << 4;
+  if (nth < 0 || T == 0 || first >= end) return;
+  const int pid = c.page_table[(int64_t)b * c.max_pages + (first >> pshift)];
+  if (pid < 0 || pid >= c.num_pages) return;
+  const int64_t at = pid * c.page_stride + (((int64_t)head << pshift) + (first & (c.page - 1))) * D + 8 * s;
+  const int64_t scale = pid * c.scale_stride + ((((int64_t)head << pshift) + (first & (c.page - 1))) >> 4);
+  const bool shared = row0 > first;  // rows of earlier calls
+  const int es = partner<D>(c, s) * 8, from = (lane & ~(L - 1)) + es / 8;
+  Raw<IO> x[N];
+  uint2 was[N];
+  bool fresh[N], kept[N];
+  int position[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int r = n * GROUPS + group, row = (int)first + (r & 15);
+    fresh[n] = row >= row0 && row < end;
+    kept[n] = row < row0;
+    const int64_t t = tok0 + (fresh[n] ? row - row0 : 0);
+#pragma unroll
+    for (int i = 0; i < Raw<IO>::N; ++i) x[n].u[i] = 0u;
+    was[n] = make_uint2(0u, 0u);
+    position[n] = row;
+    if (fresh[n]) {
+      x[n] = load8(r < 16 ? (const IO*)c.k + t * c.k_stride + (int64_t)head * D + 8 * s
+                          : (const IO*)c.v + t * c.v_stride + (int64_t)head * D + 8 * s);
+      if (c.positions && r < 16) position[n] = c.positions[t];
+    } else if (kept[n]) {
+      was[n] = *reinterpret_cast<const uint2*>((const char*)(r < 16 ? c.k_out : c.v_out) + at + (int64_t)(r & 15) * D);
+    }
+  }
+  int e_was[2] = {0, 0};
+  if (shared) e_was[0] = c.k_scales[scale], e_was[1] = c.v_scales[scale];
+  float f[8], wk[8], wkp[8];
+  frequencies(c, s, f);
+  weights<IO>(c.wk, 8 * s, wk);
+  weights<IO>(c.wk, es, wkp);
+  __shared__ float largest[32];
+  float y[N][8];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int r = n * GROUPS + group;
+    const bool key = r < 16;  // (the same for a wave: 16 rows are a whole number of its lane groups)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[n][e] = x[n].get(e);
+    if (key) {
+      float q = 1.f;
+      if (c.norm) {
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fmaf(y[n][e], y[n][e], sum);
+        q = 1.f / sqrtf(row_sum<L>(sum) * (1.f / D) + c.eps);
+      }
+      const Turn turn = turn_of<D>(c, s, f, position[n]);
+      const Raw<IO> xp = others(x[n], c.interleaved, from, 8 * s < c.rot);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        y[n][e] = q * fmaf(y[n][e], wk[e] * turn.cos[e], xp.get(e) * ((c.interleaved ? wkp[e ^ 1] : wkp[e]) * turn.sin[e]));
+    }
+    float most = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) most = fmaxf(most, isfinite(y[n][e]) ? fabsf(y[n][e]) : 0.f);
+#pragma unroll
+    for (int o = L / 2; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, WAVE));
+    if (s == 0) largest[r] = fresh[n] ? most : 0.f;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int r = n * GROUPS + group, kv = r >> 4;
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) most = fmaxf(most, largest[kv * 16 + i]);
+    const int e = shared ? max(exponent_for(most), e_was[kv]) : exponent_for(most);
+    char* const cache = (char*)(kv ? c.v_out : c.k_out);
+    if (fresh[n]) {
+      const float inv = inverse_scale(e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[n][i] *= inv;
+      *reinterpret_cast<uint2*>(cache + at + (int64_t)(r & 15) * D) = e4m3_of(y[n]);
+    } else if (kept[n] && e != e_was[kv]) {
+      const float4 lo = floats_of_e4m3(was[n].x, e_was[kv]), hi = floats_of_e4m3(was[n].y, e_was[kv]);
+      const float inv = inverse_scale(e);
+      const float z[8] = {lo.x * inv, lo.y * inv, lo.z * inv, lo.w * inv, hi.x * inv, hi.y * inv, hi.z * inv, hi.w * inv};
+      *reinterpret_cast<uint2*>(cache + at + (int64_t)(r & 15) * D) = e4m3_of(z);
+    }
+    if ((r & 15) == 0 && s == 0) (kv ? c.v_scales : c.k_scales)[scale] = (uint8_t)e;
   }
 }
 
@@ -412,10 +573,26 @@ Args args_of(const RopeCall& c) {
   a.parts = (int)cdiv(nh, a.heads);
   a.units = c.total * a.parts;
   a.sums = nullptr;
+  a.cells = 0, a.kv_heads = 0;
   return a;
 }
 
+Args append8_args(const RopeCall& c) {
+  RopeCall q = c;
+  q.Hkv = 0;
+  Args a = args_of(q);
+  a.kv_heads = c.Hkv;
+  a.cells = c.packed ? (c.total >> 4) + 2 * (int64_t)c.B : (int64_t)c.B * (((int64_t)c.T + 14) / 16 + 1);
+  return a;
+}
+int64_t append8_workgroups(const Args& a) { return a.cells * a.kv_heads + cdiv(a.units, 256 / (a.c.D / 8)); }
+
 template <int D, typename IO, typename OUT> hipError_t forward(const RopeCall& c, hipStream_t stream) {
+  if (c.bits8) {
+    const Args a = append8_args(c);
+    rope_append8_kernel<D, IO><<<dim3((unsigned)append8_workgroups(a)), dim3(256), 0, stream>>>(a);
+    return hipGetLastError();
+  }
   const Args a = args_of(c);
   const dim3 grid((unsigned)cdiv(a.units, 256 / (D / 8)));
   if (c.paged) rope_kernel<D, IO, OUT, true><<<grid, dim3(256), 0, stream>>>(a);
@@ -461,6 +638,7 @@ template <int D, typename IO, typename OUT> struct Backward {
 }  // namespace
 
 int64_t rope_workgroups(const RopeCall& c) {
+  if (c.bits8) return append8_workgroups(append8_args(c));
   return cdiv(args_of(c).units, 256 / (c.D / 8));
 }
 

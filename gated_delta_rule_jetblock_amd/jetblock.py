@@ -43,7 +43,7 @@ class AttnShape(ctypes.Structure):
                [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "page_stride")]
 
 
-ROPE_INTERLEAVED, ROPE_NO_NORM = 1, 2
+ROPE_INTERLEAVED, ROPE_NO_NORM, CACHE_E4M3 = 1, 2, 4
 
 
 def flag_segment(n: int) -> int:
@@ -95,7 +95,15 @@ _lib.jb_qk_norm_rope_backward.argtypes = [_A] + [_P] * 6 + [_F] + [_P] * 7 + [_S
 _lib.jb_qk_norm_rope_paged.argtypes = [_A, _L] + [_P] * 10 + [_F] + [_P] * 4
 _lib.jb_attn_paged_workspace_size.argtypes = [_A, _L, ctypes.c_int32, ctypes.POINTER(_SZ)]
 _lib.jb_attn_paged.argtypes = [_A, _L] + [_P] * 6 + [_F] + [_P] * 3 + [_SZ, _P]
-for _f in ("jb_qk_norm_rope", "jb_qk_norm_rope_backward_workspace_size", "jb_qk_norm_rope_backward",
+_lib.jb_qk_norm_rope_paged8.argtypes = [_A, _L] + [_P] * 10 + [_F] + [_P] * 5 + [_L, _P]
+_lib.jb_attn_paged8_workspace_size.argtypes = [_A, _L, ctypes.c_int32, ctypes.POINTER(_SZ)]
+_lib.jb_attn_paged8.argtypes = [_A, _L] + [_P] * 8 + [_L, _F] + [_P] * 3 + [_SZ, _P]
+_lib.jb_block_scores.argtypes = [_A, _L] + [_P] * 6 + [_L] + [_P] * 3
+_lib.jb_block_select.argtypes = [_A, _L] + [_P] * 3 + [ctypes.c_int32] * 3 + [_P] * 2
+_lib.jb_attn_blocks_workspace_size.argtypes = [_A, _L, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(_SZ)]
+_lib.jb_attn_blocks.argtypes = [_A, _L] + [_P] * 8 + [_L, _P, ctypes.c_int32, _F] + [_P] * 3 + [_SZ, _P]
+for _f in ("jb_qk_norm_rope_paged8", "jb_attn_paged8_workspace_size", "jb_attn_paged8", "jb_block_scores",
+           "jb_block_select", "jb_attn_blocks_workspace_size", "jb_attn_blocks", "jb_qk_norm_rope", "jb_qk_norm_rope_backward_workspace_size", "jb_qk_norm_rope_backward",
            "jb_qk_norm_rope_paged", "jb_attn_paged_workspace_size", "jb_attn_paged",
            "jb_prefill_workspace_size", "jb_decode_workspace_size", "jb_prefill", "jb_prefill_noalloc",
            "jb_decode_step",
@@ -560,7 +568,7 @@ def _rows(t, name: str):
     return t.data_ptr(), n, stride
 
 
-def _same(di, *groups):
+def _same(di, *groups, first="q"):
     """Every tensor of each (dtype, names, tensors) group of that dtype and on device di."""
     for dtype, names, tensors in groups:
         for t in tensors:
@@ -568,7 +576,7 @@ def _same(di, *groups):
                 name = names.split()[[x is t for x in tensors].index(True)]
                 if t.dtype is not dtype:
                     raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-                raise ValueError(f"{name} is on {t.device}, q on cuda:{di}")
+                raise ValueError(f"{name} is on {t.device}, {first} on cuda:{di}")
 
 
 def _flat(t, name: str, *shape):
@@ -606,15 +614,15 @@ def _launch(di: int, fn, *args):
             _check(fn(*args, _raw_stream(di)))
 
 
-def _on_stream(fn, args):
+def _on_stream(fn, args, first="q"):
     """fn(**args) on the stream args names (a torch stream or a handle): the call, and what it
     allocates, belong to that stream, so nothing it still uses is handed out on another."""
     args = dict(args)
-    stream, di = args.pop("stream"), _device(args["q"])
+    stream, di = args.pop("stream"), _device(args[first])
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=args["q"].device)
+        stream = torch.cuda.ExternalStream(int(stream), device=args[first].device)
     elif stream.device.index != di:
-        raise ValueError(f"stream is of {stream.device}, q on cuda:{di}")
+        raise ValueError(f"stream is of {stream.device}, {first} on cuda:{di}")
     with torch.cuda.stream(stream):
         return fn(**args)
 
@@ -818,4 +826,213 @@ def attn_paged(q, k_cache, v_cache, page_table, kv_lens, *, cu_seqlens=None, max
             v_cache.data_ptr(), 0.0 if scale is None else float(scale), _flat(o, "o", *q.shape),
             _flat(lse, "lse", *q.shape[:-1]), None if ws is None else ws.data_ptr(),
             0 if ws is None else ws.numel())
+    return {"o": o, "lse": lse}
+
+
+# ---------------------------------------------------------------- caches in 8 bits, selected pages
+
+E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _scales(scales, other, name: str, P, Hkv, page):
+    """Distance between the pages of a cache's scales [pages, Hkv, page / 16] (0: contiguous)."""
+    shape, st = (P, Hkv, page // 16), scales.stride()
+    for t in (scales, other):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name}: expected {shape}, got {tuple(t.shape)}")
+    if other is not None and any(n > 1 and a != b for n, a, b in zip(shape, st, other.stride())):
+        raise ValueError(f"{name}: expected the strides alike, got {st} and {other.stride()}")
+    if (page > 16 and st[2] != 1) or (Hkv > 1 and st[1] != page // 16):
+        raise ValueError(f"{name}: a page's scales must be contiguous")
+    if P > 1 and st[0] < Hkv * page // 16:
+        raise ValueError(f"{name}: pages overlap (page stride {st[0]})")
+    return st[0] if P > 1 else 0
+
+
+def qk_norm_rope_paged8(q, k, v, k_cache, v_cache, k_scales, v_scales, page_table, kv_lens, inv_freq, wq=None, wk=None, *,
+                        cu_seqlens=None, max_seqlen: int | None = None, positions=None, eps=1e-6, interleaved=False,
+                        normalize=True, q_out=None, stream=None):
+    """jb_qk_norm_rope_paged8: qk_norm_rope_paged into a cache in 8 bits, float8_e4m3fn caches
+    [pages,Hkv,page,D] with float8_e8m0fnu scales [pages,Hkv,page/16] (both in place).  Returns
+    dict(q, k_cache, v_cache, k_scales, v_scales)."""
+    if stream is not None:
+        return _on_stream(qk_norm_rope_paged8, locals())
+    di, io = _device(q), q.dtype
+    _same(di, (io, "k v wq wk q_out", (k, v, wq, wk, q_out)), (E4M3, "k_cache v_cache", (k_cache, v_cache)),
+          (E8M0, "k_scales v_scales", (k_scales, v_scales)),
+          (torch.int32, "page_table kv_lens cu_seqlens positions", (page_table, kv_lens, cu_seqlens, positions)),
+          (torch.float32, "inv_freq", (inv_freq,)))
+    H, D = q.shape[-2:]
+    pairs = inv_freq.numel()
+    qp, n, qs = _rows(q, "q")
+    kp, nk, ks = _rows(k, "k")
+    vp, nv, vs = _rows(v, "v")
+    B, T = _batch(q, cu_seqlens, max_seqlen)
+    P, Hkv, page, ps, max_pages = _pages(k_cache, v_cache, page_table, kv_lens, B, D)
+    if nk != n or nv != n or k.shape[-2:] != (Hkv, D) or v.shape[-2:] != (Hkv, D):
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} do not go with q {tuple(q.shape)} and the caches")
+    ss = _scales(k_scales, v_scales, "k_scales and v_scales", P, Hkv, page)
+    if q_out is None:
+        q_out = _empty(q, io)
+    code = _io_code(q)
+    shape = AttnShape(B, T, H, Hkv, D, 2 * pairs, page, max_pages, P, 0, 0, code, code,
+                      _rope_flags(interleaved, normalize), qs, ks, vs, ps)
+    _launch(di, _lib.jb_qk_norm_rope_paged8, shape, n,
+            None if cu_seqlens is None else _flat(cu_seqlens, "cu_seqlens", B + 1), _flat(kv_lens, "kv_lens", B),
+            _flat(page_table, "page_table", B, max_pages), qp, kp, vp, _flat(wq, "wq", D), _flat(wk, "wk", D),
+            _flat(inv_freq, "inv_freq", pairs),
+            None if positions is None else _positions(positions, n), eps,
+            _flat(q_out, "q_out", *q.shape), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
+            v_scales.data_ptr(), ss)
+    return {"q": q_out, "k_cache": k_cache, "v_cache": v_cache, "k_scales": k_scales, "v_scales": v_scales}
+
+
+def attn_paged8_workspace_size(shape: AttnShape, total_tokens: int, packed: bool) -> int:
+    n = _SZ(0)
+    _check(_lib.jb_attn_paged8_workspace_size(shape, int(total_tokens), int(packed), n))
+    return n.value
+
+
+def attn_paged8(q, k_cache, v_cache, k_scales, v_scales, page_table, kv_lens, *, cu_seqlens=None,
+                max_seqlen: int | None = None, max_kv: int | None = None, window: int = 0, scale: float | None = None,
+                out_dtype=None, o=None, want_lse=False, lse=None, ws=None, stream=None):
+    """jb_attn_paged8: attn_paged over a cache in 8 bits (as for qk_norm_rope_paged8); its other
+    arguments and its result are attn_paged's."""
+    if stream is not None:
+        return _on_stream(attn_paged8, locals())
+    di, io = _device(q), q.dtype
+    out_dtype = out_dtype or (o.dtype if o is not None else io)
+    _same(di, (E4M3, "k_cache v_cache", (k_cache, v_cache)), (E8M0, "k_scales v_scales", (k_scales, v_scales)),
+          (torch.int32, "page_table kv_lens cu_seqlens", (page_table, kv_lens, cu_seqlens)),
+          (out_dtype, "o", (o,)), (torch.float32, "lse", (lse,)), (torch.uint8, "ws", (ws,)))
+    H, D = q.shape[-2:]
+    qp, n, qs = _rows(q, "q")
+    B, T = _batch(q, cu_seqlens, max_seqlen)
+    P, Hkv, page, ps, max_pages = _pages(k_cache, v_cache, page_table, kv_lens, B, D)
+    ss = _scales(k_scales, v_scales, "k_scales and v_scales", P, Hkv, page)
+    if not 0 <= window <= 1 << 30:
+        raise ValueError(f"window = {window} not in [0, 2^30]")
+    max_kv = 0 if max_kv is None else max(1, min(int(max_kv), max_pages * page))
+    if o is None:
+        o = _empty(q, out_dtype)
+    if lse is None and want_lse:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    packed = cu_seqlens is not None
+    shape = AttnShape(B, T, H, Hkv, D, 0, page, max_pages, P, max_kv, int(window),
+                      _io_code(q), _code(out_dtype), 0, qs, 0, 0, ps)
+    if ws is None:
+        need = attn_paged8_workspace_size(shape, n, packed)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _launch(di, _lib.jb_attn_paged8, shape, n, _flat(cu_seqlens, "cu_seqlens", B + 1),
+            _flat(kv_lens, "kv_lens", B), _flat(page_table, "page_table", B, max_pages), qp, k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), ss, 0.0 if scale is None else float(scale),
+            _flat(o, "o", *q.shape), _flat(lse, "lse", *q.shape[:-1]), None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel())
+    return {"o": o, "lse": lse}
+
+
+def _cache_of(io, k_cache, k_scales, *v):
+    """The dtype groups of a cache in 8 bits (with scales) or of q's type."""
+    names = "k_cache v_cache" if v else "k_cache"
+    caches = (k_cache, v[0]) if v else (k_cache,)
+    if k_scales is None and not (v and v[1] is not None):
+        return [(io, names, caches)]
+    if v and (k_scales is None) != (v[1] is None):
+        raise ValueError("k_scales and v_scales go together")
+    return [(E4M3, names, caches), (E8M0, "k_scales v_scales" if v else "k_scales", (k_scales, v[1]) if v else (k_scales,))]
+
+
+def block_scores(q, k_cache, means, page_table, kv_lens, *, k_scales=None, cu_seqlens=None, max_seqlen: int | None = None,
+                 want_scores=True, scores=None, stream=None):
+    """jb_block_scores: the pages' scores for each new token (q and the batch as for attn_paged).
+    means f32 [pages,Hkv,D], in place: those of the pages that hold the new tokens are formed anew;
+    a cache in 8 bits comes with its k_scales.  want_scores=False: the means only.  Returns
+    dict(scores, means): scores f32 [..., Hkv, max_pages] or None."""
+    if stream is not None:
+        return _on_stream(block_scores, locals())
+    di, io = _device(q), q.dtype
+    _same(di, *_cache_of(io, k_cache, k_scales),
+          (torch.int32, "page_table kv_lens cu_seqlens", (page_table, kv_lens, cu_seqlens)),
+          (torch.float32, "means scores", (means, scores)))
+    H, D = q.shape[-2:]
+    qp, n, qs = _rows(q, "q")
+    B, T = _batch(q, cu_seqlens, max_seqlen)
+    P, Hkv, page, ps, max_pages = _pages(k_cache, k_cache, page_table, kv_lens, B, D)
+    ss = 0 if k_scales is None else _scales(k_scales, None, "k_scales", P, Hkv, page)
+    if scores is None and want_scores:
+        scores = torch.empty(*q.shape[:-2], Hkv, max_pages, dtype=torch.float32, device=q.device)
+    shape = AttnShape(B, T, H, Hkv, D, 0, page, max_pages, P, 0, 0, _io_code(q), JB_F32,
+                      0 if k_scales is None else CACHE_E4M3, qs, 0, 0, ps)
+    _launch(di, _lib.jb_block_scores, shape, n, _flat(cu_seqlens, "cu_seqlens", B + 1), _flat(kv_lens, "kv_lens", B),
+            _flat(page_table, "page_table", B, max_pages), qp, k_cache.data_ptr(),
+            None if k_scales is None else k_scales.data_ptr(), ss, _flat(means, "means", P, Hkv, D),
+            _flat(scores, "scores", *q.shape[:-2], Hkv, max_pages))
+    return {"scores": scores, "means": means}
+
+
+def block_select(scores, kv_lens, count: int, page: int, *, cu_seqlens=None, max_seqlen: int | None = None,
+                 first: int = 1, recent: int = 1, blocks=None, stream=None):
+    """jb_block_select: of scores f32 [B,T,Hkv,max_pages], [B,Hkv,max_pages] (one token each) or
+    packed [tokens,Hkv,max_pages] with cu_seqlens, as block_scores returns them, the pages (of
+    `page` rows) that each token reads: its `first` first, its `recent` last, and the best others,
+    `count` in all.  Returns int32 [..., Hkv, count], ascending, -1 behind the last."""
+    if stream is not None:
+        return _on_stream(block_select, locals(), "scores")
+    di = _device(scores)
+    _same(di, (torch.float32, "scores", (scores,)), (torch.int32, "kv_lens cu_seqlens blocks", (kv_lens, cu_seqlens, blocks)),
+          first="scores")
+    if scores.dim() < 3:
+        raise ValueError(f"scores: expected [tokens, Hkv, max_pages] or [B, T, Hkv, max_pages], got {tuple(scores.shape)}")
+    lead, (Hkv, max_pages) = scores.shape[:-2], scores.shape[-2:]
+    B, T = _batch(scores, cu_seqlens, max_seqlen)
+    n = lead.numel()
+    if blocks is None:
+        blocks = torch.empty(*lead, Hkv, count, dtype=torch.int32, device=scores.device)
+    shape = AttnShape(B, T, Hkv, Hkv, 64, 0, page, max_pages, 1, 0, 0, JB_F32, JB_F32, 0, 0, 0, 0, 0)
+    _launch(di, _lib.jb_block_select, shape, n, _flat(cu_seqlens, "cu_seqlens", B + 1), _flat(kv_lens, "kv_lens", B),
+            _flat(scores, "scores", *scores.shape), count, first, recent,
+            _flat(blocks, "blocks", *lead, Hkv, count))
+    return blocks
+
+
+def attn_blocks_workspace_size(shape: AttnShape, total_tokens: int, packed: bool, count: int) -> int:
+    n = _SZ(0)
+    _check(_lib.jb_attn_blocks_workspace_size(shape, int(total_tokens), int(packed), int(count), n))
+    return n.value
+
+
+def attn_blocks(q, k_cache, v_cache, page_table, kv_lens, blocks, *, k_scales=None, v_scales=None, cu_seqlens=None,
+                max_seqlen: int | None = None, scale: float | None = None, out_dtype=None, o=None, want_lse=False, lse=None,
+                ws=None, stream=None):
+    """jb_attn_blocks: attention of each new token over the pages that blocks int32 [..., Hkv, count]
+    lists for it and its key head (as block_select returns them); q, caches and the batch as for
+    attn_paged, or a cache in 8 bits with its scales.  Returns dict(o, lse) as attn_paged does."""
+    if stream is not None:
+        return _on_stream(attn_blocks, locals())
+    di, io = _device(q), q.dtype
+    out_dtype = out_dtype or (o.dtype if o is not None else io)
+    _same(di, *_cache_of(io, k_cache, k_scales, v_cache, v_scales),
+          (torch.int32, "page_table kv_lens blocks cu_seqlens", (page_table, kv_lens, blocks, cu_seqlens)),
+          (out_dtype, "o", (o,)), (torch.float32, "lse", (lse,)), (torch.uint8, "ws", (ws,)))
+    H, D = q.shape[-2:]
+    qp, n, qs = _rows(q, "q")
+    B, T = _batch(q, cu_seqlens, max_seqlen)
+    P, Hkv, page, ps, max_pages = _pages(k_cache, v_cache, page_table, kv_lens, B, D)
+    ss = 0 if k_scales is None else _scales(k_scales, v_scales, "k_scales and v_scales", P, Hkv, page)
+    count = blocks.shape[-1]
+    if o is None:
+        o = _empty(q, out_dtype)
+    if lse is None and want_lse:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    packed = cu_seqlens is not None
+    shape = AttnShape(B, T, H, Hkv, D, 0, page, max_pages, P, 0, 0, _io_code(q), _code(out_dtype),
+                      0 if k_scales is None else CACHE_E4M3, qs, 0, 0, ps)
+    if ws is None:
+        ws = torch.empty(attn_blocks_workspace_size(shape, n, packed, count), dtype=torch.uint8, device=q.device)
+    _launch(di, _lib.jb_attn_blocks, shape, n, _flat(cu_seqlens, "cu_seqlens", B + 1), _flat(kv_lens, "kv_lens", B),
+            _flat(page_table, "page_table", B, max_pages), qp, k_cache.data_ptr(), v_cache.data_ptr(),
+            None if k_scales is None else k_scales.data_ptr(), None if v_scales is None else v_scales.data_ptr(), ss,
+            _flat(blocks, "blocks", *q.shape[:-2], Hkv, count), count, 0.0 if scale is None else float(scale),
+            _flat(o, "o", *q.shape), _flat(lse, "lse", *q.shape[:-1]), ws.data_ptr(), ws.numel())
     return {"o": o, "lse": lse}

@@ -508,6 +508,106 @@ jb_status jb_attn_paged(const jb_attn_shape* shape, int64_t total_tokens, const 
                         void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The same layers at long contexts (the pages serve 64K and 256K rows, where
+ * reading the cache bounds a decode step: csdn translation, section 2.5, finding
+ * 4): a cache in 8 bits, and attention over selected pages.
+ *
+ * A cache in 8 bits holds e4m3 codes (4 exponent and 3 fraction bits, largest 448,
+ * 0x7f and 0xff NaN) in k_cache's and v_cache's layout, and for every 16 rows of
+ * a key head a power of two, held as its exponent:
+ *   k_scales, v_scales [num_pages][Hkv][page / 16] uint8: e stands for 2^(e - 127),
+ *                      255 for NaN;  a value is its code times its rows' scale
+ * (a value below the smallest bf16 number may be rounded to one).  scale_stride: elements
+ * between pages of the scales, 0: contiguous.  page_stride counts codes (bytes), a
+ * multiple of 16.  A page index outside [0, num_pages) reads as rows of zeros and is
+ * not written to, as above; layouts, limits and conventions are those above but for
+ * what follows.  The calls over pages take total_tokens Hkv < 2^24 and count page <= 2^30.
+ * ------------------------------------------------------------------------- */
+
+/* jb_block_scores, jb_attn_blocks: the cache is in 8 bits (else of io_dtype). */
+#define JB_CACHE_E4M3 ((int32_t)4)
+
+/*
+ * jb_qk_norm_rope_paged8 -- jb_qk_norm_rope_paged into a cache in 8 bits.  The new
+ * rows' keys (from the fp32 rotation) and values are divided by their 16 rows' scale and
+ * rounded once, to the nearest code, ties to even; infinities and NaN become NaN.  The
+ * scale is the smallest 2^k, k >= -126, with 448 * 2^k at least the largest finite magnitude
+ * among the call's rows of the 16 - or, where rows before them share the 16, the
+ * one in the cache if that is larger; where the scale grows, the codes of those rows are
+ * divided by the quotient (and rounded again where they fall below the smallest normal
+ * code).  Codes of rows behind the new ones stay as they are, under the new scale.
+ */
+jb_status jb_qk_norm_rope_paged8(const jb_attn_shape* shape, int64_t total_tokens, const int32_t* cu_seqlens,
+                                 const int32_t* kv_lens, const int32_t* page_table, const void* q,
+                                 const void* k, const void* v, const void* wq, const void* wk,
+                                 const float* inv_freq, const int32_t* positions, float eps, void* q_out,
+                                 void* k_cache, void* v_cache, uint8_t* k_scales, uint8_t* v_scales,
+                                 int64_t scale_stride, void* stream);
+
+/* Workspace bytes of jb_attn_paged8 (packed: whether cu_seqlens will be given). */
+jb_status jb_attn_paged8_workspace_size(const jb_attn_shape* shape, int64_t total_tokens, int32_t packed,
+                                        size_t* bytes);
+
+/*
+ * jb_attn_paged8 -- jb_attn_paged over a cache in 8 bits.  bf16 q: the cache's values
+ * are bf16 values, and the arithmetic is jb_attn_paged's; fp32 q: fp32 throughout.
+ */
+jb_status jb_attn_paged8(const jb_attn_shape* shape, int64_t total_tokens, const int32_t* cu_seqlens,
+                         const int32_t* kv_lens, const int32_t* page_table, const void* q,
+                         const void* k_cache, const void* v_cache, const uint8_t* k_scales,
+                         const uint8_t* v_scales, int64_t scale_stride, float scale, void* o, float* lse,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * jb_block_scores -- a cheap score of every page for every new token.  A token at cache
+ * row p sees pages j = 0 .. p / page.
+ *   means  [num_pages][Hkv][D] float32, kept by the caller beside the cache: the mean key of the rows
+ *          that a page holds.  The call forms anew those of the pages that hold its new tokens
+ *          (which are in the cache by now, and are counted up to the last of them)
+ *   scores [tokens][Hkv][max_pages] float32, nullable (the means only, q may be NULL):
+ *          the largest q . mean_j over the key head's query heads, -inf for pages that the
+ *          token does not see; NaN where a product is NaN
+ * Sums are fp32 (bf16 q: of exact products).  shape.window must be 0.  k_scales and
+ * scale_stride: with JB_CACHE_E4M3, else NULL.
+ */
+jb_status jb_block_scores(const jb_attn_shape* shape, int64_t total_tokens, const int32_t* cu_seqlens,
+                          const int32_t* kv_lens, const int32_t* page_table, const void* q,
+                          const void* k_cache, const uint8_t* k_scales, int64_t scale_stride, float* means,
+                          float* scores, void* stream);
+
+/*
+ * jb_block_select -- the pages each token and key head reads: of those that the token sees
+ * the `first` first and the `recent` last ones (its own among them: recent >= 1), then those
+ * of the highest scores, until there are `count`; of equal scores the lowest page, NaN
+ * counting as -inf.
+ *   scores [tokens][Hkv][max_pages] float32 (only those of pages that are seen are read)
+ *   blocks [tokens][Hkv][count] int32, ascending, -1 behind the last where fewer are seen
+ * first + recent <= count; max_pages <= 65536; shape.window and flags must be 0.
+ */
+jb_status jb_block_select(const jb_attn_shape* shape, int64_t total_tokens, const int32_t* cu_seqlens,
+                          const int32_t* kv_lens, const float* scores, int32_t count, int32_t first,
+                          int32_t recent, int32_t* blocks, void* stream);
+
+/* Workspace bytes of jb_attn_blocks (packed: whether cu_seqlens will be given). */
+jb_status jb_attn_blocks_workspace_size(const jb_attn_shape* shape, int64_t total_tokens, int32_t packed,
+                                        int32_t count, size_t* bytes);
+
+/*
+ * jb_attn_blocks -- attention of each new token over listed pages: jb_attn_paged (or
+ * jb_attn_paged8, with JB_CACHE_E4M3) where the token and its key head's queries see the
+ * rows j <= p of the pages in blocks [tokens][Hkv][count] and no others.  An entry counts if
+ * it is a page that the token sees and larger than every such entry before it; others (-1,
+ * one that comes twice) are passed over, and a token with none gets o = 0 and lse = -inf.
+ * The softmax weights are taken as in decode.  shape.window must be 0; max_kv is not used.
+ */
+jb_status jb_attn_blocks(const jb_attn_shape* shape, int64_t total_tokens, const int32_t* cu_seqlens,
+                         const int32_t* kv_lens, const int32_t* page_table, const void* q,
+                         const void* k_cache, const void* v_cache, const uint8_t* k_scales,
+                         const uint8_t* v_scales, int64_t scale_stride, const int32_t* blocks, int32_t count,
+                         float scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* ---------------------------------------------------------------------------
  * Single-stage entry points.  Each runs one stage of the path by itself so
  * that it can be checked on its own; the two calls above fuse these stages.
  * ------------------------------------------------------------------------- */
