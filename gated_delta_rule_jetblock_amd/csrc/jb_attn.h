@@ -83,6 +83,11 @@ hipError_t launch_block_scores(const BlockCall& c, hipStream_t stream);
 int64_t block_select_workgroups(const BlockCall& c);  // at most, of 256 threads
 hipError_t launch_block_select(const BlockCall& c, hipStream_t stream);
 int64_t attn_blocks_workgroups(const BlockCall& c, const AttnCall& attn);
+// the lists that the decode kernel takes itself (otherwise they become tables in memory)
+bool attn_lists_fit(const BlockCall& c);
+size_t attn_lists_bytes(const BlockCall& c);
+hipError_t launch_attn_lists(const AttnCall& attn, const BlockCall& c, hipStream_t stream);
+hipError_t launch_attn8_lists(const AttnCall& attn, const BlockCall& c, hipStream_t stream);
 size_t attn_blocks_workspace_bytes(const BlockCall& c, const AttnCall& attn);
 hipError_t launch_attn_blocks(const BlockCall& c, const AttnCall& attn, hipStream_t stream);
 

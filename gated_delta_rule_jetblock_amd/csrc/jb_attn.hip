@@ -7,6 +7,14 @@ int64_t attn_workgroups(const AttnCall& c) { return workgroups(c); }
 
 size_t attn_workspace_bytes(const AttnCall& c) { return layout(c, plan(c)).bytes; }
 
+bool attn_lists_fit(const BlockCall& c) { return list_rows(c); }
+
+size_t attn_lists_bytes(const BlockCall& c) { return list_rows_bytes(c); }
+
+hipError_t launch_attn_lists(const AttnCall& attn, const BlockCall& c, hipStream_t stream) {
+  return run_lists<false>(attn, c, stream);
+}
+
 hipError_t launch_attn(const AttnCall& c, hipStream_t stream) { return run<false>(c, stream); }
 
 }  // namespace jb

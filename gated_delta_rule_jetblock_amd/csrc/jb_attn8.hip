@@ -3,6 +3,10 @@
 
 namespace jb {
 
+hipError_t launch_attn8_lists(const AttnCall& attn, const BlockCall& c, hipStream_t stream) {
+  return run_lists<true>(attn, c, stream);
+}
+
 hipError_t launch_attn8(const AttnCall& c, hipStream_t stream) { return run<true>(c, stream); }
 
 }  // namespace jb

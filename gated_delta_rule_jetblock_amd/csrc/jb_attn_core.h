@@ -65,6 +65,9 @@ typedef __attribute__((address_space(3))) u4_t lds_u4;
 typedef __attribute__((address_space(3))) uint32_t lds_u32;
 typedef __attribute__((address_space(3))) uint16_t lds_u16;
 typedef __attribute__((address_space(3))) float lds_float;
+typedef __attribute__((address_space(3))) int lds_int;
+typedef int i2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) i2_t lds_i2;
 typedef float f16_t __attribute__((ext_vector_type(16)));
 typedef const __attribute__((address_space(4))) int* const_int_p;
 
@@ -99,6 +102,10 @@ struct Args {
   const uint8_t *ks, *vs;  // a cache in 8 bits: exponents of its scales
   int64_t scale_stride;
   int units;       // attention over listed pages: a token's key heads, each a sequence of its own; else 0
+  // attn_row_kernel over the lists themselves: the batch they are for, and the pieces of a list
+  int seqs, seq_T, seq_pages, count, pieces;
+  const int *seq_cu, *seq_kv, *seq_table, *lists;
+  int64_t tokens;
 
   // key head of the cache that sequence b's head kvh reads
   __device__ __forceinline__ int head(int b, int kvh) const { return units ? (int)((uint32_t)b % (uint32_t)units) : kvh; }
@@ -225,18 +232,21 @@ __device__ __forceinline__ void dma2(v4i_t desc, int v0, int v1, uint32_t lds) {
       : "memory");
 }
 
-// The pages of one sequence.
+// The pages of one sequence, in memory or (a list's) in LDS.
 struct Pages {
   const int* table;
+  const lds_int* list;
   int e0, ents;  // table entries e0 + lane
-  __device__ Pages(const Args& a, int b) : table(a.table + (int64_t)b * a.max_pages), e0(-64) {}
+  __device__ Pages(const Args& a, int b, const lds_int* list)
+      : table(a.table + (int64_t)b * a.max_pages), list(list), e0(-64) {}
+  __device__ __forceinline__ int entry(const Args& a, int e) const { return list ? list[e] : table[min(e, a.max_pages - 1)]; }
   // Page index of row0 < hi <= max_pages * page.  64 entries of the table wait
   // in a register, so that hardly any tile waits for one.
   __device__ int page(const Args& a, int row0) {
     const int e = row0 >> a.pshift;
     if ((unsigned)(e - e0) >= 64u) {
       e0 = e;
-      ents = table[min(e + lane_id(), a.max_pages - 1)];
+      ents = entry(a, e + lane_id());
       asm volatile("" : "+v"(ents));  // waited for here
     }
     return __builtin_amdgcn_readlane(ents, e - e0);
@@ -249,7 +259,7 @@ template <int D> struct Loader : Pages {
   static constexpr int N = I::PR / 4;  // 1 KB transfers for 16 rows
   int vk[N], vv;                       // byte in the rows, less i KB, of transfer i (the same for V's)
   const bf16_t *k, *v;
-  __device__ Loader(const Args& a, int b, int kvh) : Pages(a, b) {
+  __device__ Loader(const Args& a, int b, int kvh, const lds_int* list = nullptr) : Pages(a, b, list) {
     const int lane = lane_id();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -284,67 +294,120 @@ template <int D> struct Loader : Pages {
   static constexpr int fv_flip(int i) { return D == 256 && i ? (2 << 2) * 16 : 0; }
 };
 
-// The same from a cache in 8 bits, ROWS (16 or 32) at a time, by way of registers: the
-// codes of later tiles are on their way into a Tile while this one is used, and become
-// bf16 as they go into the images (exactly: an e4m3 code has 4 significant bits, and the
-// scale is a power of two).  So every value is converted once for all queries of the
-// workgroup, and what follows is as for a bf16 cache.
-template <int D, int ROWS> struct Loader8 : Pages {
+// The same from a cache in 8 bits, by way of registers: the codes of 16 rows of the next
+// tile are on their way while this one is used, and become bf16 as they go into the images
+// (exactly: an e4m3 code has 4 significant bits, and the scale is a power of two).  So every
+// value is converted once for all queries of the workgroup, and what follows is as for a
+// bf16 cache.
+template <int D> struct Loader8 : Pages {
   using I = Img<D>;
-  static constexpr int LPR = D / 16, RPL = 64 / LPR, H = ROWS / 16, N = 16 / RPL;  // lanes a row, rows a load; loads of 16 rows
-  struct Tile {
-    u4_t k[H * N], v[H * N];
-    uint32_t e;    // lane 2 h: exponent of K's scale of 16 rows h, lane 2 h + 1: V's
-    bool ok[H];
-  };
+  static constexpr int LPR = D / 16, RPL = 64 / LPR, N = 16 / RPL;  // lanes a row, rows a load; loads of 16 rows
+  u4_t ck[N], cv[N];
+  uint32_t e;  // lane 0: exponent of K's scale, lane 1: V's
+  bool ok;
   const char *k, *v;
   const uint8_t* scales;  // this lane's: K's or V's
-  __device__ Loader8(const Args& a, int b, int kvh) : Pages(a, b) {
+  __device__ Loader8(const Args& a, int b, int kvh) : Pages(a, b, nullptr) {
     const int64_t head = (int64_t)a.head(b, kvh) << a.pshift;
     k = (const char*)a.k + head * D;
     v = (const char*)a.v + head * D;
     scales = (lane_id() & 1 ? a.vs : a.ks) + (head >> 4);
   }
-  // rows row0 .. row0 + ROWS - 1 (row0 a multiple of 16); zeros from row hi on
-  __device__ __forceinline__ void fetch(const Args& a, int row0, int hi, Tile& t) {
-    const int lane = lane_id(), inside = (1 << a.pshift) - 1;
-    int64_t scale = 0;
+  // rows row .. row + 15 (row a multiple of 16); zeros from row hi on
+  __device__ __forceinline__ void fetch(const Args& a, int row, int hi) {
+    const int lane = lane_id(), inside = (1 << a.pshift) - 1, pid = row < hi ? page(a, row) : -1;
+    ok = (unsigned)pid < (unsigned)a.num_pages;
+    const int at = ok ? pid : 0, n = ok ? min(hi - row, 16) : 0;
+    const int64_t from = at * a.page_stride + (int64_t)(row & inside) * D;
+    const auto rk = __builtin_amdgcn_make_buffer_rsrc((void*)(k + from), 0, n * D, 0x00020000);
+    const auto rv = __builtin_amdgcn_make_buffer_rsrc((void*)(v + from), 0, n * D, 0x00020000);
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const int row = row0 + 16 * h, pid = row < hi ? page(a, row) : -1;
-      t.ok[h] = (unsigned)pid < (unsigned)a.num_pages;
-      const int at = t.ok[h] ? pid : 0, n = t.ok[h] ? min(hi - row, 16) : 0;
-      const int64_t from = at * a.page_stride + (int64_t)(row & inside) * D;
-      const auto rk = __builtin_amdgcn_make_buffer_rsrc((void*)(k + from), 0, n * D, 0x00020000);
-      const auto rv = __builtin_amdgcn_make_buffer_rsrc((void*)(v + from), 0, n * D, 0x00020000);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        t.k[h * N + i] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rk, lane * 16 + i * 1024, 0, 0));
-        t.v[h * N + i] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rv, lane * 16 + i * 1024, 0, 0));
-      }
-      const int64_t mine = at * a.scale_stride + ((row & inside) >> 4);
-      scale = h == 0 || (lane & 2 * h) ? mine : scale;
+    for (int i = 0; i < N; ++i) {
+      ck[i] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rk, lane * 16 + i * 1024, 0, 0));
+      cv[i] = __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(rv, lane * 16 + i * 1024, 0, 0));
     }
-    t.e = scales[scale];
+    e = scales[at * a.scale_stride + ((row & inside) >> 4)];
   }
-  // the tile's images, of its rows 0 .. ROWS - 1
-  __device__ __forceinline__ void put(const Tile& t, lds_char* ik, lds_char* iv) const {
+  // the images of these 16 rows
+  __device__ __forceinline__ void put(lds_char* ik, lds_char* iv) const {
     const int lane = lane_id(), pc = 2 * (lane % LPR);
+    const float sk = scale_of(ok ? __builtin_amdgcn_readlane(e, 0) : 127u);
+    const float sv = scale_of(ok ? __builtin_amdgcn_readlane(e, 1) : 127u);
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-      const float sk = scale_of(t.ok[h] ? __builtin_amdgcn_readlane(t.e, 2 * h) : 127u);
-      const float sv = scale_of(t.ok[h] ? __builtin_amdgcn_readlane(t.e, 2 * h + 1) : 127u);
+    for (int i = 0; i < N; ++i) {
+      const int r = i * RPL + lane / LPR;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int r = 16 * h + i * RPL + lane / LPR;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const u4_t wk = t.k[h * N + i], wv = t.v[h * N + i];
-          *(lds_u4*)(ik + r * I::ROWB + (((pc + j) ^ I::fk(r)) << 4)) = bf16_of_e4m3(wk[2 * j], wk[2 * j + 1], sk);
-          *(lds_u4*)(iv + r * I::ROWB + (((pc + j) ^ I::fv(r)) << 4)) = bf16_of_e4m3(wv[2 * j], wv[2 * j + 1], sv);
-        }
+      for (int j = 0; j < 2; ++j) {
+        *(lds_u4*)(ik + r * I::ROWB + (((pc + j) ^ I::fk(r)) << 4)) = bf16_of_e4m3(ck[i][2 * j], ck[i][2 * j + 1], sk);
+        *(lds_u4*)(iv + r * I::ROWB + (((pc + j) ^ I::fv(r)) << 4)) = bf16_of_e4m3(cv[i][2 * j], cv[i][2 * j + 1], sv);
       }
     }
+  }
+};
+
+// LDS tile of 32 rows of D codes of K, then of V, as they are: 16-byte pieces permuted by
+// row so that 16 rows' reads of one piece, and 16 rows' of two neighbouring ones down
+// their columns, meet distinct banks (256 / D rows fill the banks once).
+template <int D> struct Raw8 {
+  static constexpr int PR = D / 16, TILE = 32 * D;
+  __device__ static int f(int r) { return (r / (256 / D)) & (PR - 1); }
+};
+
+// Tiles of a wave that takes every NW-th one, straight into LDS.  Of 64 tiles at a time the
+// lanes hold the page indices and the scales' exponents: a wait for them once in 64
+// tiles.
+template <int D, int NW> struct LoaderRaw8 : Pages {
+  using W = Raw8<D>;
+  static constexpr int N = W::PR / 4;  // 1 KB transfers for 16 rows
+  int vo[N], i, pid0, pid1;
+  uint32_t e;  // exponents: K's of the first 16 rows, V's, K's of the other 16, V's
+  const char *k, *v;
+  const uint8_t *ks, *vs;
+  __device__ LoaderRaw8(const Args& a, int b, int kvh, const lds_int* list) : Pages(a, b, list), i(64) {
+    const int64_t head = (int64_t)a.head(b, kvh) << a.pshift;
+    k = (const char*)a.k + head * D, v = (const char*)a.v + head * D;
+    ks = a.ks + (head >> 4), vs = a.vs + (head >> 4);
+    const int lane = lane_id(), r = lane / W::PR;
+#pragma unroll
+    for (int t = 0; t < N; ++t) vo[t] = r * D + ((lane % W::PR) ^ W::f(t * 64 / W::PR + r)) * 16;
+  }
+  template <typename O> __device__ __forceinline__ void fill(const Args& a, const O& ord, int n, int nt, int hi) {
+    const int m = n + lane_id() * NW, row = m < nt ? ord.tile(m) * 32 : hi, inside = (1 << a.pshift) - 1;
+    pid0 = row < hi ? entry(a, row >> a.pshift) : -1;
+    pid1 = row + 16 < hi ? entry(a, (row + 16) >> a.pshift) : -1;
+    if ((unsigned)pid0 >= (unsigned)a.num_pages) pid0 = -1;
+    if ((unsigned)pid1 >= (unsigned)a.num_pages) pid1 = -1;
+    uint32_t e0 = 127, e1 = 127, e2 = 127, e3 = 127;
+    if (pid0 >= 0) {
+      const int64_t at = pid0 * a.scale_stride + ((row & inside) >> 4);
+      e0 = ks[at], e1 = vs[at];
+    }
+    if (pid1 >= 0) {
+      const int64_t at = pid1 * a.scale_stride + (((row + 16) & inside) >> 4);
+      e2 = ks[at], e3 = vs[at];
+    }
+    e = e0 | e1 << 8 | e2 << 16 | e3 << 24;
+    i = 0;
+  }
+  // tile n (of this wave, in order) into LDS at `to`; returns its exponents
+  template <typename O>
+  __device__ __forceinline__ uint32_t load(const Args& a, const O& ord, int n, int nt, int hi, uint32_t to) {
+    if (i == 64) fill(a, ord, n, nt, hi);
+    const int row0 = ord.tile(n) * 32, inside = (1 << a.pshift) - 1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = row0 + 16 * h, pid = __builtin_amdgcn_readlane(h ? pid1 : pid0, i);
+      const int rows = pid >= 0 ? min(max(hi - row, 0), 16) : 0;
+      const int64_t at = max(pid, 0) * a.page_stride + (row & inside) * D;
+      rows16(buf_desc(k + at, rows * D), to + h * 16 * D);
+      rows16(buf_desc(v + at, rows * D), to + W::TILE + h * 16 * D);
+    }
+    return (uint32_t)__builtin_amdgcn_readlane((int)e, i++);
+  }
+  __device__ __forceinline__ void rows16(v4i_t desc, uint32_t to) const {
+    if constexpr (N == 1) dma16(desc, vo[0], 0, to);
+    else if constexpr (N == 2) dma2(desc, vo[0], vo[1], to);
+    else dma4(desc, vo[0], vo[1], vo[2], vo[3], to);
   }
 };
 
@@ -381,9 +444,50 @@ __device__ __attribute__((noinline)) void add_odd_values(float* o, const float* 
   }
 }
 
+// The same for a tile of V's codes (e: the tile's exponents): whether one is NaN, NaN to the
+// queries that see its row, and those codes (and scales) as zeros.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+template <int D> __device__ __forceinline__ bool odd_codes(const lds_char* v, uint32_t e) {
+  bool odd = ((e >> 8) & 255u) == 255u || e >> 24 == 255u;
+#pragma unroll
+  for (int i = lane_id() * 16; i < 32 * D; i += 1024) {
+    const u4_t w = *(const lds_u4*)(v + i);
+    odd |= (nan_codes(w[0]) | nan_codes(w[1]) | nan_codes(w[2]) | nan_codes(w[3])) != 0;
+  }
+  return __any(odd);
+}
+template <int D>
+__device__ __attribute__((noinline)) void add_odd_codes(float* o, const lds_char* v, uint32_t e, int j0, int p, int lw) {
+  using W = Raw8<D>;
+  const int g = lane_id() >> 5;
+  for (int r = 0; r < 32; ++r) {
+    if (j0 + r > p || j0 + r <= lw) continue;
+    const bool all = (r < 16 ? (e >> 8) & 255u : e >> 24) == 255u;
+    for (int i = 0; i < D / 2; ++i) {
+      const int d = 32 * (i >> 4) + 8 * ((i >> 2) & 3) + 4 * g + (i & 3);
+      const int code = v[r * D + (((d >> 4) ^ W::f(r & 15)) << 4) + (d & 15)];
+      if (all || (code & 127) == 127) o[i] = NAN;
+    }
+  }
+}
+template <int D> __device__ __forceinline__ uint32_t clean_codes(lds_char* v, uint32_t e) {
+  const bool a = ((e >> 8) & 255u) == 255u, b = e >> 24 == 255u;
+  for (int i = lane_id() * 4; i < 32 * D; i += 256) {
+    uint32_t w = *(const lds_u32*)(v + i);
+    w &= ~((nan_codes(w) >> 7) * 255u);
+    *(lds_u32*)(v + i) = (i < 16 * D ? a : b) ? 0u : w;
+  }
+  if (a) e = (e & 0xffff00ffu) | 127u << 8;
+  if (b) e = (e & 0x00ffffffu) | 127u << 24;
+  return e;
+}
+
 // One wave's 32 queries and what they have gathered so far.
-template <int D> struct Wave {
+template <int D, bool Q8 = false> struct Wave {
   using I = Img<D>;
+  using W8 = Raw8<D>;
+  // a lane's d of step k: 8 in order from q0 g + qk k (of 8 bits, so that a lane's codes lie together)
+  static constexpr int q0 = Q8 ? D / 2 : 8, qk = Q8 ? 8 : 16;
   bf16x8_t q[D / 16];
   f16_t o[D / 32];  // O^T: o[db][i] is d = 32 db + 8 (i / 4) + 4 g + i % 4
   float m, l;       // m as the exponent base 2 subtracts it; l of this lane's half of the rows
@@ -404,11 +508,11 @@ template <int D> struct Wave {
       phi = uniform(base + token_of(a, last));
       if (a.window) lwlo = uniform(base + token_of(a, r0)) - a.window;
     }
-    const bf16_t* src = (const bf16_t*)a.q + a.query(s.tok0 + i, kvh, D) + (int64_t)g * D + 8 * (lane >> 5);
+    const bf16_t* src = (const bf16_t*)a.q + a.query(s.tok0 + i, kvh, D) + (int64_t)g * D + q0 * (lane >> 5);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (real) w = *reinterpret_cast<const uint4*>(src + 16 * k);
+      if (real) w = *reinterpret_cast<const uint4*>(src + qk * k);
       q[k] = __builtin_bit_cast(bf16x8_t, w);
     }
 #pragma unroll
@@ -568,6 +672,110 @@ template <int D> struct Wave {
     }
   }
 
+  // The same from a tile of codes (e: its exponents).  A lane's codes of a row are D / 2 in
+  // order, converted as their products need them: K's scale is the row's, V's the step's.
+  __device__ void scores8(const lds_char* lk, uint32_t e, f16_t (&s)[1]) const {
+    const int lane = lane_id(), c = lane & 31, g = lane >> 5;
+    const float scale = scale_of(c < 16 ? e & 255u : (e >> 16) & 255u);
+    constexpr int STEPS = D / 32, AHEAD = 2;
+    const int kb = c * D + (((STEPS * g) ^ W8::f(c & 15)) << 4);
+    u4_t w[STEPS];
+    f16_t z;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) z[i] = 0.f;
+    auto read = [&](int k) { w[k] = *(const lds_u4*)(lk + (kb ^ (k << 4))); };
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) read(k);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+      if (k + AHEAD < STEPS) read(k + AHEAD);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u4_t f = bf16_of_e4m3(w[k][2 * h], w[k][2 * h + 1], scale);
+        s[0] = mfma32(__builtin_bit_cast(bf16x8_t, f), q[2 * k + h], k || h ? s[0] : z);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  // ds_read_b64_tr_b8: of each 16 lanes, lane 8 a + b gets byte b of the 8-byte pieces that
+  // lanes 2 j + a address (j = 0 .. 7): 8 rows of a column.
+  template <bool EXP> __device__ void values8(const Args& a, const lds_char* lv, uint32_t e, f16_t (&s)[1], float ms) {
+    const int lane = lane_id(), g = lane >> 5, n16 = lane & 15, j = n16 >> 1, row = 4 * g + (j & 3) + 8 * (j >> 2);
+    const int vb = row * D + ((((lane >> 4) & 1) ^ W8::f(row)) << 4) + (n16 & 1) * 8;
+    constexpr int DB = D / 32, STEPS = 2, PART = 8 / DB, AHEAD = 2;
+    i2_t v[STEPS * DB];
+    auto read = [&](int i) {
+      v[i] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i2*)(lv + (vb ^ ((i % DB) << 5)) + (i / DB) * 16 * D));
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) read(i);
+    if constexpr (EXP) {
+      weights<1>(a, s, ms, 0);
+      __builtin_amdgcn_s_setprio(1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+      const float scale = scale_of((e >> (16 * k + 8)) & 255u);
+      bf16x8_t w, lo;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x = s[0][8 * k + i];
+        const uint32_t hi = __float_as_uint(x) & 0xffff0000u;
+        w[i] = __builtin_bit_cast(__bf16, (uint16_t)(hi >> 16));
+        lo[i] = (__bf16)(x - __uint_as_float(hi));
+      }
+#pragma unroll
+      for (int db = 0; db < DB; ++db) {
+        const int i = k * DB + db;
+        if (i + AHEAD < STEPS * DB) read(i + AHEAD);
+        const bf16x8_t f = __builtin_bit_cast(bf16x8_t, bf16_of_e4m3(v[i][0], v[i][1], scale));
+        o[db] = mfma32(f, w, o[db]);
+        o[db] = mfma32(f, lo, o[db]);
+        if constexpr (EXP)
+          if (k + 1 < STEPS) weights<1>(a, s, ms, k + 1, db * PART, PART);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  // a tile that every query sees whole, and one that some see in part
+  __device__ void full8(const Args& a, const lds_char* lk, uint32_t e) {
+    f16_t s[1];
+    scores8(lk, e, s);
+    __builtin_amdgcn_s_setprio(2);
+    const float ms = take_max<1>(a, s);
+    values8<true>(a, lk + W8::TILE, e, s, ms);
+    __builtin_amdgcn_s_setprio(0);
+  }
+  __device__ void part8(const Args& a, lds_char* lk, uint32_t e, int j0) {
+    const int g = lane_id() >> 5;
+    if (j0 > phi || j0 + 31 <= lwlo) return;
+    f16_t s[1];
+    scores8(lk, e, s);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int j = j0 + 8 * (i >> 2) + 4 * g + (i & 3);
+      if (j > p || j <= lw) s[0][i] = -INFINITY;
+    }
+    const float ms = take_max<1>(a, s);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) weights<1>(a, s, ms, k);
+    lds_char* const v = lk + W8::TILE;
+    if (odd_codes<D>(v, e)) {
+      float so[D / 2];
+#pragma unroll
+      for (int i = 0; i < D / 2; ++i) so[i] = o[i >> 4][i & 15];
+      add_odd_codes<D>(so, v, e, j0, p, lw);
+#pragma unroll
+      for (int i = 0; i < D / 2; ++i) o[i >> 4][i & 15] = so[i];
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      e = clean_codes<D>(v, e);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+    values8<false>(a, v, e, s, 0.f);
+  }
+
   // o += weight times value for the values that are not finite, of rows that are seen
   template <int NB> __device__ void odd_values(const f16_t (&s)[NB], const lds_char* lv, int j0) {
     float so[D / 2], ss[NB * 16];
@@ -708,18 +916,17 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
   const Span x = span_of(a, s, r0, r1, R, at.split, at.n);
   Wave<D> w;
   w.init(a, s, kvh, r0 + wave * 32);
-  std::conditional_t<Q8, Loader8<D, 16>, Loader<D>> ld(a, b, kvh);
+  std::conditional_t<Q8, Loader8<D>, Loader<D>> ld(a, b, kvh);
   lds_char* const base = (lds_char*)ring;
   const Order ord(a, s, x, r0, r1, R);
   const int nf = ord.nf, nt = ord.nt;
   auto tile = [&](int n) { return ord.tile(n); };
-  typename Loader8<D, 16>::Tile codes;
   auto issue = [&](int n) {
     const int row0 = tile(n) * R + wave * 16;
     lds_char* const to = base + (n & 1) * 2 * IMG + wave * 16 * D * 2;
     if constexpr (Q8) {  // tile n's codes are here; the next tile's leave
-      ld.put(codes, to, to + IMG);
-      if (n + 1 < nt) ld.fetch(a, tile(n + 1) * R + wave * 16, x.hi, codes);
+      ld.put(to, to + IMG);
+      if (n + 1 < nt) ld.fetch(a, tile(n + 1) * R + wave * 16, x.hi);
     } else {
       ld.load(a, row0, x.hi, (uint32_t)(uintptr_t)to, (uint32_t)(uintptr_t)(to + IMG));
     }
@@ -728,7 +935,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
   if (nt > 0) ld.page(a, min(tile(0) * R + wave * 16, x.hi - 1));
   w.arrived();
   if constexpr (Q8)
-    if (nt > 0) ld.fetch(a, tile(0) * R + wave * 16, x.hi, codes);
+    if (nt > 0) ld.fetch(a, tile(0) * R + wave * 16, x.hi);
   if (nt > 0) issue(0);
   auto next = [&](int n) {
     // every wave's rows of tile n have landed, and every wave has left tile n - 1
@@ -801,18 +1008,95 @@ __device__ __forceinline__ int steps_of(const Args& a, const Seq& s, int rows_a_
   return max((hi + rows_a_step - 1) / rows_a_step - lo / rows_a_step, 1);
 }
 
-template <int D, int NW, typename OUT, bool Q8>
-__global__ __launch_bounds__(NW * 64, Q8 && D < 256 ? 2 : 1) void attn_row_kernel(Args a) {
+// A list's unit: the first wave takes the entries that count to LDS (pages), as page indices
+// in order; returns the rows that the unit's queries see, -1 where no sequence owns the
+// token.  An entry counts if it is a page that the token sees and larger than every such
+// one before it.
+constexpr int MOST_LISTED = 2048;
+__device__ __forceinline__ int take_list(const Args& a, int unit, lds_int* pages, lds_int* found) {
+  const int lane = lane_id(), t = (uint32_t)unit / (uint32_t)a.units;
+  const int* list = a.lists + (int64_t)unit * a.count;
+  const bool first = threadIdx.x < 64;
+  int x = first && lane < a.count ? list[lane] : -1;  // on its way while the sequence is found
+  int b, all = a.seq_T;
+  int64_t tok0;
+  if (a.seq_cu) {
+    int n = 0;
+    for (int i = 0; i < a.seqs; i += blockDim.x) {
+      const int c = __syncthreads_count(i + (int)threadIdx.x < a.seqs && a.seq_cu[i + threadIdx.x] <= t);
+      n += c;
+      if (c < (int)blockDim.x) break;
+    }
+    b = uniform(max(n - 1, 0));
+    clamp_span(((const_int_p)a.seq_cu)[b], ((const_int_p)a.seq_cu)[b + 1], 0x7fffffff, a.tokens, tok0, all);
+  } else {
+    b = (uint32_t)t / (uint32_t)a.seq_T;
+    tok0 = (int64_t)b * a.seq_T;
+  }
+  const int cap = (int)min((int64_t)a.seq_pages << a.pshift, (int64_t)0x7fffffff);
+  const int64_t i = t - tok0;
+  if (i < 0 || i >= min(all, a.seq_T)) return -1;  // (the same for all threads)
+  const int p = min(max(((const_int_p)a.seq_kv)[b], 0), cap) - all + (int)i, own = p >> a.pshift;
+  if (first) {
+    const int* table = a.seq_table + (int64_t)b * a.seq_pages;
+    int last = -1, n = 0;  // the largest so far, and how many
+    for (int k = 0; k < a.count; k += 64) {
+      if (k) x = k + lane < a.count ? list[k + lane] : -1;
+      const int mine = x >= 0 && x <= own ? x : -1;
+      int most = mine;  // of this lane and those before it
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(most, o, WAVE);
+        if (lane >= o) most = max(most, u);
+      }
+      const int u = __shfl_up(most, 1, WAVE);
+      const bool take = mine > max(lane ? u : -1, last);
+      const uint64_t taken = __builtin_amdgcn_ballot_w64(take);
+      if (take) pages[n + __builtin_popcountll(taken & ((1ull << lane) - 1))] = table[mine];
+      n += __builtin_popcountll(taken);
+      last = max(last, __builtin_amdgcn_readlane(most, 63));
+    }
+    if (lane == 0) *found = n && last == own ? ((n - 1) << a.pshift) + (p & ((1 << a.pshift) - 1)) + 1 : n << a.pshift;
+  }
+  __syncthreads();
+  return uniform(*found);
+}
+
+// LIST: a workgroup takes a piece of the pages listed for one (token, key head), which are a
+// sequence of one token to it.
+template <int D, int NW, typename OUT, bool Q8, bool LIST>
+__global__ __launch_bounds__(NW * 64, Q8 ? 2 : 1) void attn_row_kernel(Args a) {
   constexpr int R = 32, IMG = R * D * 2, STEP = R * NW, NTHR = NW * 64;
-  constexpr int RING = NW * 4 * IMG / (Q8 ? 2 : 1) + (Q8 ? NW * 32 * 8 : 0);  // a tile of 8 bits waits in registers
+  constexpr int TILE = Q8 ? Raw8<D>::TILE * 2 : 2 * IMG;  // K and V of a tile
+  constexpr int RING = NW * 2 * TILE + (Q8 ? NW * 32 * 8 : 0);  // (and the waves' sums, at the end)
   __shared__ __attribute__((aligned(1024))) char ring[RING];
   __shared__ int64_t found[2];
   __shared__ int sums[NW];
+  __shared__ int listed[LIST ? MOST_LISTED + 64 : 1];  // (64 entries are read at a time)
+  const lds_int* const list = LIST ? (const lds_int*)listed : nullptr;
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   int b;
   int64_t at, end, start;  // this run's steps, and the first sequence's first one
   int64_t run_steps = 0;
-  if (a.direct) {         // many units: each is a run
+  int rows = 0, piece = 0;  // LIST: of the unit
+  if constexpr (LIST) {
+    // Neighbouring tokens list much the same pages: each of the 8 dies, which take
+    // workgroups in turn, has consecutive units.
+    const uint32_t each = gridDim.x / 8, more = gridDim.x % 8, die = blockIdx.x % 8;
+    const uint32_t at_die = die * each + min(die, more) + blockIdx.x / 8;
+    b = (int)(at_die / (uint32_t)a.pieces);
+    piece = at_die - b * (uint32_t)a.pieces;
+    rows = take_list(a, b, (lds_int*)listed, (lds_int*)sums);
+    if (rows < 0) {
+      if (a.pieces > 1 && (int)threadIdx.x < a.G)
+        a.run_ml[((int64_t)piece * a.B + b) * a.G + threadIdx.x] = make_float2(-INFINITY, -1.f);
+      return;
+    }
+    const int n_steps = max((rows + STEP - 1) / STEP, 1);
+    start = 0;
+    at = (int64_t)n_steps * piece / a.pieces;
+    end = (int64_t)n_steps * (piece + 1) / a.pieces;
+  } else if (a.direct) {  // many units: each is a run
     b = blockIdx.x / (unsigned)a.Hkv;
     const int n = steps_of(a, seq_of(a, b), STEP);
     start = 0;
@@ -866,16 +1150,16 @@ __global__ __launch_bounds__(NW * 64, Q8 && D < 256 ? 2 : 1) void attn_row_kerne
   }
   Shared shared = {0, 0, 0, 0};
 
-  constexpr int NT = 4 * Loader<D>::N;  // transfers a tile
-  lds_char* const base = (lds_char*)ring + wave * (Q8 ? 2 : 4) * IMG;
-  for (int seg = 0; at < end && b < a.B; seg = 1) {
-    const Seq s = seq_of(a, b);
-    const int steps = steps_of(a, s, STEP);
+  constexpr int NT = 4 * (Q8 ? LoaderRaw8<D, NW>::N : Loader<D>::N);  // transfers a tile
+  lds_char* const base = (lds_char*)ring + wave * 2 * TILE;
+  for (int seg = 0; (LIST || at < end) && b < a.B; seg = 1) {
+    const Seq s = LIST ? Seq{b, 1, rows} : seq_of(a, b);
+    const int steps = LIST ? max((rows + STEP - 1) / STEP, 1) : steps_of(a, s, STEP);
     if (steps == 0) {  // (only behind a sequence that has some)
       ++b;
       continue;
     }
-    const int kvh = uniform((int)quotient(at - start, 1.0 / steps)), s0 = uniform((int)(at - start - (int64_t)kvh * steps));
+    const int kvh = LIST ? 0 : uniform((int)quotient(at - start, 1.0 / steps)), s0 = uniform((int)(at - start - (int64_t)kvh * steps));
     const int s1 = uniform((int)min((int64_t)steps, s0 + end - at));
     if (kvh >= a.Hkv) break;  // (lengths that changed meanwhile)
     const int nr = (int)(s.T * a.G);
@@ -885,54 +1169,44 @@ __global__ __launch_bounds__(NW * 64, Q8 && D < 256 ? 2 : 1) void attn_row_kerne
     const int n0 = x.lo / STEP * NW;
     x.t0 = max(n0 + s0 * NW, x.lo / R);
     x.t1 = min(n0 + s1 * NW, (x.hi + R - 1) / R);
-    Wave<D> w;
+    Wave<D, Q8> w;
     w.init(a, s, kvh, 0);
     const Order ord(a, s, x, 0, nr - 1, R);
     const int nf = ord.nf, nt = ord.nt;
-    auto in_part = [&](lds_char* k, int n) {
-      lds_char* const v = k + IMG;
-      f16_t s1[1];
-      if (w.template part<1>(a, k, ord.tile(n) * R, s1)) {
-        if (odd_part(v, IMG)) {
-          w.template odd_values<1>(s1, v, ord.tile(n) * R);
-          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-          clean_part(v, IMG);
-          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        }
-        w.template values<1, false, true>(a, v, s1, 0.f);
-      }
-    };
+    // tile n has landed, and the wave's next one is on its way into the other buffer
+    int par = 0;
     if constexpr (Q8) {
-      // the next tile's codes are on their way while this one is used
-      Loader8<D, R> ld(a, b, kvh);
-      typename Loader8<D, R>::Tile codes;
-      w.arrived();
-      if (wave < nt) ld.fetch(a, ord.tile(wave) * R, x.hi, codes);
-      auto next = [&](int n) {
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's reads of the images are done
-        ld.put(codes, base, base + IMG);
-        if (n + NW < nt) ld.fetch(a, ord.tile(n + NW) * R, x.hi, codes);
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      LoaderRaw8<D, NW> ld(a, b, kvh, list);
+      uint32_t e = 0, after = 0;
+      auto issue = [&](int n, int par) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's reads of the buffer are done
+        after = ld.load(a, ord, n, nt, x.hi, (uint32_t)(uintptr_t)(base + par * TILE));
       };
+      auto next = [&](int n) {
+        e = after;
+        if (n + NW < nt) {
+          issue(n + NW, par ^ 1);
+          asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NT) : "memory");
+        } else {
+          asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+        lds_char* const k = base + par * TILE;
+        par ^= 1;
+        return k;
+      };
+      w.arrived();
+      if (wave < nt) issue(wave, 0);
       int n = wave;
-      for (; n < nf; n += NW) {
-        next(n);
-        w.template full<1, true>(a, base, base + IMG);
-      }
-      for (; n < nt; n += NW) {
-        next(n);
-        in_part(base, n);
-      }
+      for (; n < nf; n += NW) w.full8(a, next(n), e);
+      for (; n < nt; n += NW) w.part8(a, next(n), e, ord.tile(n) * R);
     } else {
-      Loader<D> ld(a, b, kvh);
+      Loader<D> ld(a, b, kvh, list);
       auto issue = [&](int t, int par) {
         const uint32_t to = (uint32_t)(uintptr_t)(base + par * 2 * IMG);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this wave's reads of the buffer are done
         ld.load(a, t * R, x.hi, to, to + IMG);
         ld.load(a, t * R + 16, x.hi, to + 16 * D * 2, to + IMG + 16 * D * 2);
       };
-      int par = 0;
-      // tile n has landed, and the wave's next one is on its way into the other buffer
       auto next = [&](int n) {
         if (n + NW < nt) {
           issue(ord.tile(n + NW), par ^ 1);
@@ -953,7 +1227,18 @@ __global__ __launch_bounds__(NW * 64, Q8 && D < 256 ? 2 : 1) void attn_row_kerne
         w.template full<1, true>(a, k, k + IMG);
       }
       for (; n < nt; n += NW) {
-        in_part(next(n), n);
+        lds_char* const k = next(n);
+        lds_char* const v = k + IMG;
+        f16_t s1[1];
+        if (w.template part<1>(a, k, ord.tile(n) * R, s1)) {
+          if (odd_part(v, IMG)) {
+            w.template odd_values<1>(s1, v, ord.tile(n) * R);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            clean_part(v, IMG);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          }
+          w.template values<1, false, true>(a, v, s1, 0.f);
+        }
       }
     }
     // join the waves: O and (m, l) of each in LDS
@@ -977,12 +1262,12 @@ __global__ __launch_bounds__(NW * 64, Q8 && D < 256 ? 2 : 1) void attn_row_kerne
     }
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     // (a unit that is a run has no place for a part, whatever the lengths in memory do meanwhile)
-    const bool whole = a.direct || (s0 == 0 && s1 == steps);
-    if (s0 == 0 && !whole) {  // (in the grid whatever the lengths in memory do meanwhile)
+    const bool whole = LIST ? a.pieces == 1 : a.direct || (s0 == 0 && s1 == steps);
+    if (!LIST && s0 == 0 && !whole) {  // (in the grid whatever the lengths in memory do meanwhile)
       const int last = (int)min(quotient(at + steps - 1, 1.0 / run_steps), (int64_t)gridDim.x - 1);
       shared = {b, kvh, last - (int)blockIdx.x, seg};
     }
-    const int64_t slot = 2 * (int64_t)blockIdx.x + seg;
+    const int64_t part = LIST ? ((int64_t)piece * a.B + b) * a.G : (2 * (int64_t)blockIdx.x + seg) * 32;
     constexpr int LPR = D / 4;
     for (int i = threadIdx.x / LPR; i < nr; i += NTHR / LPR) {
       const int d = (threadIdx.x % LPR) * 4;
@@ -1001,8 +1286,8 @@ __global__ __launch_bounds__(NW * 64, Q8 && D < 256 ? 2 : 1) void attn_row_kerne
         sum += v * f;
       }
       if (!whole) {
-        if (d == 0) a.run_ml[slot * 32 + i] = make_float2(m, lt);
-        *reinterpret_cast<f4_t*>(a.run_o + (slot * 32 + i) * D + d) = sum;
+        if (d == 0) a.run_ml[part + i] = make_float2(m, lt);
+        *reinterpret_cast<f4_t*>(a.run_o + (part + i) * D + d) = sum;
       } else {
         const int64_t to = out_row(a, s, kvh, i);
         const float f = lt == 0.f ? 0.f : 1.f / lt;
@@ -1010,12 +1295,13 @@ __global__ __launch_bounds__(NW * 64, Q8 && D < 256 ? 2 : 1) void attn_row_kerne
         store4((OUT*)a.o + to * D + d, sum * f);
       }
     }
+    if constexpr (LIST) break;
     at += s1 - s0;
     if (at >= end) break;
     if (kvh == a.Hkv - 1) start += (int64_t)steps * a.Hkv, ++b;
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the staging is read
   }
-  if (!a.direct && threadIdx.x == 0) a.shared[blockIdx.x] = shared;
+  if (!LIST && !a.direct && threadIdx.x == 0) a.shared[blockIdx.x] = shared;
 }
 
 // Adds up (m, l, o) pieces in the order they come.
@@ -1068,6 +1354,23 @@ __global__ __launch_bounds__(256) void attn_row_join_kernel(Args a, int rows) {
   __shared__ float2 sml[SG][LPR];
   x.template over<SG, LPR>(sg, 0, d4, so, sml);
   if (sg == 0) x.template store<OUT, D>(a, out_row(a, s, u.kvh, r), d4 * 4);
+}
+
+// Adds up the pieces of every (token, key head)'s list, D / 4 lanes a row.
+template <int D, typename OUT>
+__global__ __launch_bounds__(256) void attn_list_join_kernel(Args a) {
+  constexpr int LPR = D / 4, RPB = 256 / LPR;
+  const int64_t rows = (int64_t)a.B * a.G, row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
+  const int d = threadIdx.x % LPR * 4;
+  if (row >= rows) return;
+  Sum x;
+#pragma unroll 4
+  for (int n = 0; n < a.pieces; ++n) {
+    const float2 ml = a.run_ml[n * rows + row];
+    if (ml.y < 0.f) return;  // nobody's token
+    x.add(ml.x, ml.y, *reinterpret_cast<const f4_t*>(a.run_o + (n * rows + row) * D + d));
+  }
+  x.template store<OUT, D>(a, row, d);
 }
 
 // Adds up the pieces of every row of the tiles (of 2^rshift rows) that are in
@@ -1453,7 +1756,7 @@ hipError_t launch(const AttnCall& c, const Plan& p, const Args& a, hipStream_t s
     constexpr int NW = row_waves(D);
     if (p.tiles) attn_tile_kernel<D, OUT, Q8><<<tiles, dim3(256), 0, stream>>>(a);
     if (p.rows) {
-      attn_row_kernel<D, NW, OUT, Q8><<<dim3((unsigned)p.runs), dim3(NW * 64), 0, stream>>>(a);
+      attn_row_kernel<D, NW, OUT, Q8, false><<<dim3((unsigned)p.runs), dim3(NW * 64), 0, stream>>>(a);
       if (!p.direct)
         attn_row_join_kernel<D, OUT><<<dim3((unsigned)(p.runs * p.rows_a_unit)), dim3(256), 0, stream>>>(a, p.rows_a_unit);
     }
@@ -1483,6 +1786,8 @@ template <bool Q8> hipError_t run(const AttnCall& c, hipStream_t stream) {
   a.kv_lens = c.kv_lens, a.table = c.page_table;
   a.q = c.q, a.k = c.k_cache, a.v = c.v_cache, a.o = c.o, a.lse = c.lse;
   a.ks = c.k_scales, a.vs = c.v_scales, a.scale_stride = c.scale_stride, a.units = c.units;
+  a.seqs = a.seq_T = a.seq_pages = a.count = a.pieces = 0;
+  a.seq_cu = a.seq_kv = a.seq_table = a.lists = nullptr, a.tokens = 0;
   const Layout w = layout(c, p);
   char* ws = static_cast<char*>(c.workspace);
   a.part_o = reinterpret_cast<float*>(ws + w.part_o);
@@ -1499,6 +1804,60 @@ template <bool Q8> hipError_t run(const AttnCall& c, hipStream_t stream) {
     case 64: return bf ? launch<64, bf16_t, Q8>(c, p, a, stream) : launch<64, float, Q8>(c, p, a, stream);
     case 128: return bf ? launch<128, bf16_t, Q8>(c, p, a, stream) : launch<128, float, Q8>(c, p, a, stream);
     case 256: return bf ? launch<256, bf16_t, Q8>(c, p, a, stream) : launch<256, float, Q8>(c, p, a, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+// Attention over lists by attn_row_kernel itself: at most 32 queries to a key head, lists that
+// fit LDS.  (Others go through tables in memory and the kernels above.)
+bool list_rows(const BlockCall& b) { return b.io == IO_BF16 && b.H / b.Hkv <= 32 && b.count <= MOST_LISTED; }
+
+// Pieces of a list: the rounds of workgroups take the steps of the longest list and some 3
+// steps' worth of start and end each; a join is worth 8.
+int list_pieces(const BlockCall& b) {
+  const int64_t units = b.total * b.Hkv, hold = b.D == 64 || b.bits8 ? 512 : 256, step = 32 * row_waves(b.D);
+  const int64_t steps = cdiv((int64_t)std::min(b.count, b.max_pages) * b.page, step);
+  int64_t best = 0;
+  int pieces = 1;
+  for (int n = 1; n <= 32 && n <= steps; ++n) {
+    const int64_t t = cdiv(units * n, hold) * (cdiv(steps, n) + 3) + (n > 1 ? 8 : 0);
+    if (n == 1 || t < best) best = t, pieces = n;
+  }
+  return pieces;
+}
+size_t list_rows_bytes(const BlockCall& b) {
+  const size_t rows = (size_t)b.total * b.H * list_pieces(b);
+  return list_pieces(b) == 1 ? 0 : a256(rows * b.D * sizeof(float)) + a256(rows * sizeof(float2));
+}
+
+template <int D, typename OUT, bool Q8> hipError_t launch_lists(const Args& a, hipStream_t stream) {
+  constexpr int NW = row_waves(D), RPB = 256 / (D / 4);
+  attn_row_kernel<D, NW, OUT, Q8, true><<<dim3((unsigned)a.B * a.pieces), dim3(NW * 64), 0, stream>>>(a);
+  if (a.pieces > 1)
+    attn_list_join_kernel<D, OUT><<<dim3((unsigned)cdiv((int64_t)a.B * a.G, RPB)), dim3(256), 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <bool Q8> hipError_t run_lists(const AttnCall& c, const BlockCall& b, hipStream_t stream) {
+  Args a = {};
+  a.units = b.Hkv, a.G = b.H / b.Hkv;
+  a.B = (int)(b.total * b.Hkv), a.T = 1, a.H = a.G, a.Hkv = 1, a.total = a.B, a.direct = true;
+  a.pshift = __builtin_ctz((unsigned)b.page), a.num_pages = b.num_pages;
+  a.q_stride = b.q_stride, a.page_stride = b.page_stride, a.scale_stride = c.scale_stride;
+  a.q = c.q, a.k = c.k_cache, a.v = c.v_cache, a.o = c.o, a.lse = c.lse, a.ks = c.k_scales, a.vs = c.v_scales;
+  a.scale = c.scale * 1.4426950408889634f;
+  a.inv_g = 1.0 / a.G;
+  a.seqs = b.B, a.seq_T = b.T, a.seq_pages = b.max_pages, a.count = b.count, a.pieces = list_pieces(b);
+  a.seq_cu = b.packed ? b.cu_seqlens : nullptr, a.seq_kv = b.kv_lens, a.seq_table = b.page_table, a.lists = b.blocks;
+  a.tokens = b.total;
+  const size_t rows = (size_t)b.total * b.H * a.pieces;
+  a.run_o = static_cast<float*>(c.workspace);
+  a.run_ml = reinterpret_cast<float2*>(static_cast<char*>(c.workspace) + a256(rows * b.D * sizeof(float)));
+  const bool bf = c.out == IO_BF16;
+  switch (b.D) {
+    case 64: return bf ? launch_lists<64, bf16_t, Q8>(a, stream) : launch_lists<64, float, Q8>(a, stream);
+    case 128: return bf ? launch_lists<128, bf16_t, Q8>(a, stream) : launch_lists<128, float, Q8>(a, stream);
+    case 256: return bf ? launch_lists<256, bf16_t, Q8>(a, stream) : launch_lists<256, float, Q8>(a, stream);
   }
   return hipErrorInvalidValue;
 }

@@ -465,14 +465,16 @@ hipError_t launch_block_select(const BlockCall& c, hipStream_t stream) {
 }
 
 int64_t attn_blocks_workgroups(const BlockCall& c, const AttnCall& attn) {
+  if (attn_lists_fit(c)) return c.total * c.Hkv * 32;  // at most 32 pieces, or rows in the join
   return std::max(attn_workgroups(listed(c, attn)), cdiv(c.total * c.Hkv, 4));
 }
 
 size_t attn_blocks_workspace_bytes(const BlockCall& c, const AttnCall& attn) {
-  return list_bytes(c) + attn_workspace_bytes(listed(c, attn));
+  return attn_lists_fit(c) ? attn_lists_bytes(c) : list_bytes(c) + attn_workspace_bytes(listed(c, attn));
 }
 
 hipError_t launch_attn_blocks(const BlockCall& c, const AttnCall& attn, hipStream_t stream) {
+  if (attn_lists_fit(c)) return c.bits8 ? launch_attn8_lists(attn, c, stream) : launch_attn_lists(attn, c, stream);
   AttnCall x = listed(c, attn);
   char* const ws = static_cast<char*>(attn.workspace);
   int* const table = reinterpret_cast<int*>(ws);

@@ -358,7 +358,10 @@ def test_every_scale(jb):
         for q in (F32, BF):
             d8["q"] = d["q"].to(q)
             got = f64(call(jb, d8, window=1, out_dtype=F32)["o"])[0, 0]
-            assert np.array_equal(got, want), (row, q)  # weight 1, exact products
+            # One weight w, e^0 but for the rounding of the maximum that its exponent subtracts, and l = w:
+            # o = fl(fl(w v) fl(1 / l)), three roundings of 2^-24; the weight's second bf16 part holds what
+            # the first leaves of it (a few units of 2^-24) exactly.
+            assert (np.abs(got - want) <= 2.0 ** -22 * np.abs(want)).all(), (row, q)
 
 
 def test_rows_behind_the_last_sequence_stay(jb):
