@@ -39,6 +39,7 @@ struct Args {
   float* sums;        // backward: [workgroups][2][D]
   int64_t cells;      // append in 8 bits: places for 16 cache rows with new ones
   int kv_heads;       // and its key heads (c.Hkv is 0: the heads by token are the queries)
+  double share;       // of the workgroups that take a cell and key head: i share of the first i do
 };
 
 template <typename T> struct Raw;
@@ -126,16 +127,16 @@ __device__ __forceinline__ void sincos_turn(float t, float& sn, float& cs) {
 typedef float f4u_t __attribute__((ext_vector_type(4), aligned(4)));  // four floats anywhere
 
 // the frequencies of this lane's pairs (8, or 4 interleaved); 0 where nothing turns
+// (loads without a branch, from the first row of q where there is nothing to load: several
+// then wait together)
 __device__ __forceinline__ void frequencies(const RopeCall& c, int s, float (&f)[8]) {
+  const bool turns = 8 * s < c.rot;
+  const float* p = c.inv_freq + (c.interleaved ? 4 * s : 8 * s < c.rot / 2 ? 8 * s : 8 * s - c.rot / 2);
+  if (!turns) p = static_cast<const float*>(c.q);
+  const f4u_t u = *reinterpret_cast<const f4u_t*>(p);
+  const f4u_t v = *reinterpret_cast<const f4u_t*>(p + (c.interleaved ? 0 : 4));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = 0.f;
-  if (8 * s < c.rot) {
-    const float* p = c.inv_freq + (c.interleaved ? 4 * s : 8 * s < c.rot / 2 ? 8 * s : 8 * s - c.rot / 2);
-    const f4u_t u = *reinterpret_cast<const f4u_t*>(p);
-    const f4u_t v = c.interleaved ? u : *reinterpret_cast<const f4u_t*>(p + 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = u[i], f[4 + i] = v[i];
-  }
+  for (int i = 0; i < 4; ++i) f[i] = turns ? u[i] : 0.f, f[4 + i] = turns ? v[i] : 0.f;
 }
 
 template <int D> __device__ __forceinline__ Turn turn_of(const RopeCall& c, int s, const float (&f)[8], int position) {
@@ -184,20 +185,17 @@ __device__ __forceinline__ Raw<T> others(const Raw<T>& x, bool interleaved, int 
   return y;
 }
 
-template <typename T> __device__ __forceinline__ void weights(const void* w, int e0, float (&out)[8]) {
+template <typename T> __device__ __forceinline__ void weights(const RopeCall& c, const void* w, int e0, float (&out)[8]) {
+  const Raw<T> r = load8((const T*)(w ? w : c.q) + e0);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) out[i] = 1.f;
-  if (w) {
-    const Raw<T> r = load8((const T*)w + e0);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = r.get(i);
-  }
+  for (int i = 0; i < 8; ++i) out[i] = w ? r.get(i) : 1.f;
 }
 
-// workgroup `block` of the heads of all tokens
-template <int D, typename IO, typename OUT, bool PAGED>
+// workgroup `block` of the heads of all tokens; KV: keys (and values) too, else the queries
+template <int D, typename IO, typename OUT, bool PAGED, bool KV>
 __device__ __forceinline__ void rope_rows(const Args& a, uint32_t block) {
   constexpr int L = D / 8, GROUPS = 256 / L;
+  block = __builtin_amdgcn_readfirstlane(block);
   // rows in use, and as many on their way (64K tokens: 4 take 88.9 us, 2 90.9; an
   // append of 13K tokens 34.5 and 35.0, where 2 need fewer registers)
   constexpr int U = PAGED || sizeof(IO) == 4 ? 2 : 4;
@@ -209,7 +207,7 @@ __device__ __forceinline__ void rope_rows(const Args& a, uint32_t block) {
   int64_t t = !live ? 0 : a.parts == 1 ? unit : (uint32_t)unit / (uint32_t)a.parts;
   const int h0 = a.parts == 1 || !live ? 0 : (int)((uint32_t)unit % (uint32_t)a.parts) * a.heads;
   // what does not depend on the token's place is on its way while that is found
-  const int nh = c.H + (PAGED ? 2 : 1) * c.Hkv, h1 = min(h0 + a.heads, nh);
+  const int nh = c.H + (!KV ? 0 : PAGED ? 2 : 1) * c.Hkv, h1 = min(h0 + a.heads, nh);
   const IO* q = (const IO*)c.q + t * c.q_stride + 8 * s;
   const IO* k = (const IO*)c.k + t * c.k_stride + 8 * s;
   const IO* v = (const IO*)c.v + (PAGED ? t * c.v_stride + 8 * s : 0);
@@ -226,10 +224,10 @@ __device__ __forceinline__ void rope_rows(const Args& a, uint32_t block) {
   const int es = partner<D>(c, s) * 8, from = (lane & ~(L - 1)) + es / 8;
   float f[8], wq[8], wqp[8], wk[8], wkp[8];
   frequencies(c, s, f);
-  weights<IO>(c.wq, 8 * s, wq);
-  weights<IO>(c.wq, es, wqp);
-  weights<IO>(c.wk, 8 * s, wk);
-  weights<IO>(c.wk, es, wkp);
+  weights<IO>(c, c.wq, 8 * s, wq);
+  weights<IO>(c, c.wq, es, wqp);
+  weights<IO>(c, c.wk, 8 * s, wk);
+  weights<IO>(c, c.wk, es, wkp);
   int row = 0;          // the token's row in its sequence's cache
   int64_t slot = -1;    // and in the pool (element offset of key head 0), or -1
   if constexpr (PAGED) {
@@ -259,7 +257,7 @@ __device__ __forceinline__ void rope_rows(const Args& a, uint32_t block) {
     const int pshift = __builtin_ctz((unsigned)c.page);
     const int cap = (int)min((int64_t)c.max_pages << pshift, (int64_t)0x7fffffff);
     row = min(max(c.kv_lens[b], 0), cap) - T + (int)i;
-    if (live && row >= 0 && c.Hkv) {
+    if (KV && live && row >= 0) {
       const int pid = c.page_table[(int64_t)b * c.max_pages + (row >> pshift)];
       if (pid >= 0 && pid < c.num_pages) slot = pid * c.page_stride + (int64_t)(row & (c.page - 1)) * D;
     }
@@ -309,7 +307,7 @@ __device__ __forceinline__ void rope_rows(const Args& a, uint32_t block) {
 
 template <int D, typename IO, typename OUT, bool PAGED>
 __global__ __launch_bounds__(256) void rope_kernel(Args a) {
-  rope_rows<D, IO, OUT, PAGED>(a, blockIdx.x);
+  rope_rows<D, IO, OUT, PAGED, true>(a, blockIdx.x);
 }
 
 // Exponent e of the smallest scale 2^(e - 127) with most <= 448 times it, 1 at least:
@@ -331,7 +329,7 @@ __device__ __forceinline__ uint2 e4m3_of(const float (&x)[8]) {
   return make_uint2(lo, hi);
 }
 
-// The append to a cache in 8 bits.  The first a.cells * Hkv workgroups take 16 cache rows
+// The append to a cache in 8 bits.  a.cells * Hkv workgroups take 16 cache rows
 // of one key head each, K and V: its lane groups form the new rows' values, the largest
 // finite one sets the scale, and if rows of earlier calls share it the larger of the two
 // scales holds: their codes are divided by 2^k (exactly, but for those that fall below the
@@ -342,12 +340,15 @@ __global__ __launch_bounds__(256) void rope_append8_kernel(Args a) {
   constexpr int L = D / 8, GROUPS = 256 / L, N = 32 / GROUPS;  // rows at once; times for 16 of K and 16 of V
   const RopeCall& c = a.c;
   const uint32_t cells = (uint32_t)a.cells * (uint32_t)a.kv_heads;
-  if (blockIdx.x >= cells) {
-    rope_rows<D, IO, IO, true>(a, blockIdx.x - cells);
+  // both kinds of workgroup in turn: those of the keys wait for what they look up, while
+  // the queries' keep the memory busy (first the ones and then the others: LATER us)
+  const uint32_t before = min((uint32_t)(blockIdx.x * a.share), cells);  // of the first kind
+  if (min((uint32_t)((blockIdx.x + 1) * a.share), cells) == before) {
+    rope_rows<D, IO, IO, true, false>(a, blockIdx.x - before);
     return;
   }
-  const uint32_t cell = blockIdx.x / (uint32_t)a.kv_heads;
-  const int head = blockIdx.x - cell * (uint32_t)a.kv_heads;
+  const uint32_t cell = before / (uint32_t)a.kv_heads;
+  const int head = before - cell * (uint32_t)a.kv_heads;
   const int lane = lane_id(), s = lane % L, group = threadIdx.x / L;
   // the cell's sequence and its place among those that hold the sequence's new rows
   int b, T = c.T, all = c.T;
@@ -409,8 +410,8 @@ __global__ __launch_bounds__(256) void rope_append8_kernel(Args a) {
   if (shared) e_was[0] = c.k_scales[scale], e_was[1] = c.v_scales[scale];
   float f[8], wk[8], wkp[8];
   frequencies(c, s, f);
-  weights<IO>(c.wk, 8 * s, wk);
-  weights<IO>(c.wk, es, wkp);
+  weights<IO>(c, c.wk, 8 * s, wk);
+  weights<IO>(c, c.wk, es, wkp);
   __shared__ float largest[32];
   float y[N][8];
 #pragma unroll
@@ -471,8 +472,8 @@ __global__ __launch_bounds__(256, 3) void rope_backward_kernel(Args a) {
   const int lane = lane_id(), s = lane % L, group = threadIdx.x / L;
   const int from = (lane & ~(L - 1)) + partner<D>(c, s);
   float wq[8], wk[8], dwq[8], dwk[8];
-  weights<IO>(c.wq, 8 * s, wq);
-  weights<IO>(c.wk, 8 * s, wk);
+  weights<IO>(c, c.wq, 8 * s, wq);
+  weights<IO>(c, c.wk, 8 * s, wk);
   float f[8];
   frequencies(c, s, f);
 #pragma unroll
@@ -573,7 +574,7 @@ Args args_of(const RopeCall& c) {
   a.parts = (int)cdiv(nh, a.heads);
   a.units = c.total * a.parts;
   a.sums = nullptr;
-  a.cells = 0, a.kv_heads = 0;
+  a.cells = 0, a.kv_heads = 0, a.share = 0;
   return a;
 }
 
@@ -589,7 +590,9 @@ int64_t append8_workgroups(const Args& a) { return a.cells * a.kv_heads + cdiv(a
 
 template <int D, typename IO, typename OUT> hipError_t forward(const RopeCall& c, hipStream_t stream) {
   if (c.bits8) {
-    const Args a = append8_args(c);
+    Args a = append8_args(c);
+    // (a hair more, so that the last workgroup's share is all of them; fewer than 2^24 of each)
+    a.share = (double)(a.cells * a.kv_heads) / append8_workgroups(a) * (1 + 1e-15);
     rope_append8_kernel<D, IO><<<dim3((unsigned)append8_workgroups(a)), dim3(256), 0, stream>>>(a);
     return hipGetLastError();
   }
