@@ -191,6 +191,24 @@ template <typename T> __device__ __forceinline__ void weights(const RopeCall& c,
   for (int i = 0; i < 8; ++i) out[i] = w ? r.get(i) : 1.f;
 }
 
+// The sequence of a packed batch that holds `target`, where sequence j's share begins at
+// start(its offset, j), which never decreases: its index, offsets and cache length in one
+// step, found by the thread that looks at it.  (Offsets that decrease: any one.)
+struct Found {
+  int b, from, to, kv;
+};
+template <typename F> __device__ __forceinline__ Found find_sequence(const RopeCall& c, int64_t target, F start) {
+  __shared__ __attribute__((aligned(16))) int at[4];
+  for (int j = threadIdx.x; j < c.B; j += 256) {
+    const int from = c.cu_seqlens[j], to = c.cu_seqlens[j + 1], kv = c.kv_lens[j];
+    if ((j == 0 || start(from, j) <= target) && (j + 1 == c.B || start(to, j + 1) > target))
+      *reinterpret_cast<int4*>(at) = make_int4(j, from, to, kv);
+  }
+  __syncthreads();
+  return {min(max(__builtin_amdgcn_readfirstlane(at[0]), 0), c.B - 1), __builtin_amdgcn_readfirstlane(at[1]),
+          __builtin_amdgcn_readfirstlane(at[2]), __builtin_amdgcn_readfirstlane(at[3])};
+}
+
 // workgroup `block` of the heads of all tokens; KV: keys (and values) too, else the queries
 template <int D, typename IO, typename OUT, bool PAGED, bool KV>
 __device__ __forceinline__ void rope_rows(const Args& a, uint32_t block) {
@@ -234,29 +252,28 @@ __device__ __forceinline__ void rope_rows(const Args& a, uint32_t block) {
     int b;
     int64_t i;
     int T = c.T;  // the sequence's tokens (those behind the first c.T are not taken)
+    int kv;
     if (c.packed) {
       // the sequence of the workgroup's first token, then on from there
       const int64_t t0 = (int64_t)block * GROUPS / a.parts;
-      int n = 0;
-      for (int k = 0; k < c.B; k += 256) {
-        const int j = k + threadIdx.x;
-        const int m = __syncthreads_count(j < c.B && c.cu_seqlens[j] <= t0);
-        n += m;
-        if (m < 256) break;
+      Found f = find_sequence(c, t0, [](int from, int) { return (int64_t)from; });
+      while (f.b + 1 < c.B && f.to <= t) {
+        ++f.b;
+        f.from = f.to, f.to = c.cu_seqlens[f.b + 1], f.kv = c.kv_lens[f.b];
       }
-      b = max(n - 1, 0);
-      while (b + 1 < c.B && c.cu_seqlens[b + 1] <= t) ++b;
+      b = f.b, kv = f.kv;
       int64_t tok0;
-      clamp_span(c.cu_seqlens[b], c.cu_seqlens[b + 1], 0x7fffffff, c.total, tok0, T);
+      clamp_span(f.from, f.to, 0x7fffffff, c.total, tok0, T);
       i = t - tok0;
       live = live && i >= 0 && i < min(T, c.T);
     } else {
       b = (int)((uint32_t)t / (uint32_t)c.T);
       i = t - (int64_t)b * c.T;
+      kv = c.kv_lens[b];
     }
     const int pshift = __builtin_ctz((unsigned)c.page);
     const int cap = (int)min((int64_t)c.max_pages << pshift, (int64_t)0x7fffffff);
-    row = min(max(c.kv_lens[b], 0), cap) - T + (int)i;
+    row = min(max(kv, 0), cap) - T + (int)i;
     if (KV && live && row >= 0) {
       const int pid = c.page_table[(int64_t)b * c.max_pages + (row >> pshift)];
       if (pid >= 0 && pid < c.num_pages) slot = pid * c.page_stride + (int64_t)(row & (c.page - 1)) * D;
@@ -351,37 +368,30 @@ __global__ __launch_bounds__(256) void rope_append8_kernel(Args a) {
   const int head = before - cell * (uint32_t)a.kv_heads;
   const int lane = lane_id(), s = lane % L, group = threadIdx.x / L;
   // the cell's sequence and its place among those that hold the sequence's new rows
-  int b, T = c.T, all = c.T;
+  int b, kv, T = c.T, all = c.T;
   int64_t nth, tok0;
   if (c.packed) {
     // sequence j's cells start at cu[j] / 16 + 2 j, which leaves room for all of them
-    auto base = [&](int j) { return (min(max((int64_t)c.cu_seqlens[j], (int64_t)0), c.total) >> 4) + 2 * (int64_t)j; };
-    int n = 0;
-    for (int k = 0; k < c.B; k += 256) {
-      const int j = k + threadIdx.x;
-      const int m = __syncthreads_count(j < c.B && base(j) <= cell);
-      n += m;
-      if (m < 256) break;
-    }
-    b = max(n - 1, 0);
-    nth = (int64_t)cell - base(b);
-    clamp_span(c.cu_seqlens[b], c.cu_seqlens[b + 1], 0x7fffffff, c.total, tok0, all);
+    auto start = [&](int from, int j) { return (min(max((int64_t)from, (int64_t)0), c.total) >> 4) + 2 * (int64_t)j; };
+    const Found f = find_sequence(c, cell, start);
+    b = f.b, kv = f.kv;
+    nth = (int64_t)cell - start(f.from, b);
+    clamp_span(f.from, f.to, 0x7fffffff, c.total, tok0, all);
     T = min(all, c.T);
   } else {
     const uint32_t per = (uint32_t)(c.T + 14) / 16 + 1;
     b = (int)(cell / per);
     nth = cell - (uint32_t)b * per;
     tok0 = (int64_t)b * c.T;
+    kv = c.kv_lens[b];
   }
   const int pshift = __builtin_ctz((unsigned)c.page), cap = (int)min((int64_t)c.max_pages << pshift, (int64_t)0x7fffffff);
-  const int row0 = min(max(c.kv_lens[b], 0), cap) - all;  // of the first new token
+  const int row0 = min(max(kv, 0), cap) - all;  // of the first new token
   const int end = row0 + T;
   const int64_t first = ((int64_t)(max(row0, 0) >> 4) + nth) << 4;
   if (nth < 0 || T == 0 || first >= end) return;
+  // the new rows and the page index arrive together, then what the page holds
   const int pid = c.page_table[(int64_t)b * c.max_pages + (first >> pshift)];
-  if (pid < 0 || pid >= c.num_pages) return;
-  const int64_t at = pid * c.page_stride + (((int64_t)head << pshift) + (first & (c.page - 1))) * D + 8 * s;
-  const int64_t scale = pid * c.scale_stride + ((((int64_t)head << pshift) + (first & (c.page - 1))) >> 4);
   const bool shared = row0 > first;  // rows of earlier calls
   const int es = partner<D>(c, s) * 8, from = (lane & ~(L - 1)) + es / 8;
   Raw<IO> x[N];
@@ -394,20 +404,25 @@ __global__ __launch_bounds__(256) void rope_append8_kernel(Args a) {
     fresh[n] = row >= row0 && row < end;
     kept[n] = row < row0;
     const int64_t t = tok0 + (fresh[n] ? row - row0 : 0);
-#pragma unroll
-    for (int i = 0; i < Raw<IO>::N; ++i) x[n].u[i] = 0u;
-    was[n] = make_uint2(0u, 0u);
+    x[n] = load8(r < 16 ? (const IO*)c.k + t * c.k_stride + (int64_t)head * D + 8 * s
+                        : (const IO*)c.v + t * c.v_stride + (int64_t)head * D + 8 * s);
     position[n] = row;
-    if (fresh[n]) {
-      x[n] = load8(r < 16 ? (const IO*)c.k + t * c.k_stride + (int64_t)head * D + 8 * s
-                          : (const IO*)c.v + t * c.v_stride + (int64_t)head * D + 8 * s);
-      if (c.positions && r < 16) position[n] = c.positions[t];
-    } else if (kept[n]) {
-      was[n] = *reinterpret_cast<const uint2*>((const char*)(r < 16 ? c.k_out : c.v_out) + at + (int64_t)(r & 15) * D);
+    if (c.positions && r < 16) position[n] = c.positions[t];
+  }
+  if (pid < 0 || pid >= c.num_pages) return;
+  const int64_t at = pid * c.page_stride + (((int64_t)head << pshift) + (first & (c.page - 1))) * D + 8 * s;
+  const int64_t scale = pid * c.scale_stride + ((((int64_t)head << pshift) + (first & (c.page - 1))) >> 4);
+  int e_was[2] = {0, 0};
+#pragma unroll
+  for (int n = 0; n < N; ++n) was[n] = make_uint2(0u, 0u);
+  if (shared) {
+    e_was[0] = c.k_scales[scale], e_was[1] = c.v_scales[scale];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int r = n * GROUPS + group;
+      if (kept[n]) was[n] = *reinterpret_cast<const uint2*>((const char*)(r < 16 ? c.k_out : c.v_out) + at + (int64_t)(r & 15) * D);
     }
   }
-  int e_was[2] = {0, 0};
-  if (shared) e_was[0] = c.k_scales[scale], e_was[1] = c.v_scales[scale];
   float f[8], wk[8], wkp[8];
   frequencies(c, s, f);
   weights<IO>(c, c.wk, 8 * s, wk);
@@ -439,7 +454,7 @@ __global__ __launch_bounds__(256) void rope_append8_kernel(Args a) {
     for (int e = 0; e < 8; ++e) most = fmaxf(most, isfinite(y[n][e]) ? fabsf(y[n][e]) : 0.f);
 #pragma unroll
     for (int o = L / 2; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor(most, o, WAVE));
-    if (s == 0) largest[r] = fresh[n] ? most : 0.f;
+    if (s == 0) largest[r] = fresh[n] ? most : 0.f;  // (the others hold the first new token's row)
   }
   __syncthreads();
 #pragma unroll
