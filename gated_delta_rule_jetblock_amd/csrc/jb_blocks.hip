@@ -100,24 +100,11 @@ template <typename KV> __device__ __forceinline__ void row8(const void* p, uint3
   }
 }
 
-// Mean key of every page that holds new tokens, over the rows that it holds by now: a
-// workgroup a page and key head, D / 8 lanes a row, summed in a fixed order (a lane group's
-// rows in order, then the groups).
-template <int D, typename KV>
-__global__ __launch_bounds__(256) void block_means_kernel(Args a) {
+// Mean key of the first `held` rows of page pid: a workgroup's D / 8 lanes a row, summed in a
+// fixed order (a lane group's rows in order, then the groups); threads 0 .. D - 1 have it.
+template <int D, typename KV> __device__ __forceinline__ float mean_key(const Args& a, int pid, int head, int held) {
   constexpr int L = D / 8, GROUPS = 256 / L;
   const BlockCall& c = a.c;
-  const uint32_t slot = blockIdx.x / (uint32_t)c.Hkv;
-  const int head = blockIdx.x - slot * (uint32_t)c.Hkv, page = 1 << a.pshift;
-  int64_t nth;
-  const int b = seq_at(a, slot, a.pshift, 2, ((int64_t)c.T + page - 2) / page + 1, nth);
-  const Seq s = seq_of(a, b);
-  const int end = s.row0 + s.T;
-  const int64_t j = (max(s.row0, 0) >> a.pshift) + nth;  // the page's place in the sequence
-  if (nth < 0 || s.T == 0 || j << a.pshift >= end) return;
-  const int pid = c.page_table[(int64_t)b * c.max_pages + j];
-  if (pid < 0 || pid >= c.num_pages) return;
-  const int held = (int)min((int64_t)end - (j << a.pshift), (int64_t)page);
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
   const int64_t row0 = (int64_t)head << a.pshift;
   const char* k = (const char*)c.k_cache + (pid * c.page_stride + row0 * D + 8 * lane) * (int64_t)sizeof(KV);
@@ -134,56 +121,223 @@ __global__ __launch_bounds__(256) void block_means_kernel(Args a) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) part[group][8 * lane + i] = sum[i];
   __syncthreads();
+  float total = 0.f;
   if (threadIdx.x < D) {
-    float total = 0.f;
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) total += part[g][threadIdx.x];
-    c.means[((int64_t)pid * c.Hkv + head) * D + threadIdx.x] = total / (float)held;
   }
+  return total / (float)held;
+}
+
+// Mean key of every page that holds new tokens, over the rows that it holds by now: a
+// workgroup a page and key head.
+template <int D, typename KV>
+__global__ __launch_bounds__(256) void block_means_kernel(Args a) {
+  const BlockCall& c = a.c;
+  const uint32_t slot = blockIdx.x / (uint32_t)c.Hkv;
+  const int head = blockIdx.x - slot * (uint32_t)c.Hkv, page = 1 << a.pshift;
+  int64_t nth;
+  const int b = seq_at(a, slot, a.pshift, 2, ((int64_t)c.T + page - 2) / page + 1, nth);
+  const Seq s = seq_of(a, b);
+  const int end = s.row0 + s.T;
+  const int64_t j = (max(s.row0, 0) >> a.pshift) + nth;  // the page's place in the sequence
+  if (nth < 0 || s.T == 0 || j << a.pshift >= end) return;
+  const int pid = c.page_table[(int64_t)b * c.max_pages + j];
+  if (pid < 0 || pid >= c.num_pages) return;
+  const int held = (int)min((int64_t)end - (j << a.pshift), (int64_t)page);
+  const float mean = mean_key<D, KV>(a, pid, head, held);
+  if (threadIdx.x < D) c.means[((int64_t)pid * c.Hkv + head) * D + threadIdx.x] = mean;
 }
 
 // the larger of two scores; NaN stays
 __device__ __forceinline__ float larger(float m, float x) { return x > m || x != x ? x : m; }
 
-// Scores of 16 tokens and 16 pages at a time on matrix cores: rows are tokens, columns
-// pages, one product for each query head, their maximum taken in the accumulators.  bf16
-// queries meet a mean as three bf16 parts (hi + mid + lo are its 24 bits, so every product
-// is exact and the sums are fp32's); fp32 ones take fp32 products.
-// A wave takes TM x 16 tokens and 2 x 16 pages, a workgroup 4 times as many pages.
-constexpr int TM = 2, NB = 2, TOKENS = 16 * TM, PAGES = 4 * 16 * NB;
+// A mean's 8 values as three bf16 parts: hi + mid + lo are its 24 bits, so products with bf16
+// queries are exact and their sums fp32's.
+struct Parts {
+  bf16x8_t part[3];
+  __device__ __forceinline__ void take(const float* p, bool ok) {
+    const float4 lo = ok ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 hi = ok ? *reinterpret_cast<const float4*>(p + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const __bf16 a = (__bf16)x[e];
+      const float r = x[e] - (float)a;
+      const __bf16 b = (__bf16)r;
+      part[0][e] = a, part[1][e] = b, part[2][e] = (__bf16)(r - (float)b);
+    }
+  }
+};
 
-template <int D, typename IO> struct Means;  // of 16 pages: lane (page lane % 16, group g) has d = 8 g + e of every 32
-template <int D> struct Means<D, bf16_t> {
-  bf16x8_t part[D / 32][3];
-  __device__ void take(const float* p, bool ok) {
+typedef float f16_t __attribute__((ext_vector_type(16)));
+
+// Scores of tokens of longer chunks, bf16: 32 tokens by 32 pages on matrix cores, one
+// product for each query head, their maximum taken in the accumulators (rows are tokens,
+// columns pages).  A wave keeps its pages' means in registers, split once, and walks
+// `tiles` tiles of tokens, the next head's queries on their way while these are used; a
+// workgroup takes 4 times as many pages.  Bound by the matrix cores (three products where
+// one would do for bf16 means): FIGS.
+constexpr int PAGES = 128;  // of a workgroup
+
+template <int D>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void block_scores_kernel(Args a, uint32_t groups, int tiles) {
+  constexpr int STEPS = D / 16;
+  const BlockCall& c = a.c;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n32 = lane & 31, g = lane >> 5;
+  const uint32_t per = (uint32_t)c.Hkv * groups, place = blockIdx.x / per, rest = blockIdx.x - place * per;
+  const int head = rest / groups, j0 = (int)(rest - head * groups) * PAGES + wave * 32, j = j0 + n32;
+  Parts m[STEPS];
+  int held = -1;  // the sequence whose means these are
+  for (int k = 0; k < tiles; ++k) {
+    const int64_t slot = (int64_t)place * tiles + k;
+    if (slot >= a.slots) break;
+    int64_t nth;
+    const int b = seq_at(a, slot, 5, 1, ((int64_t)c.T + 31) / 32, nth);
+    const Seq s = seq_of(a, b);
+    if (nth < 0 || nth * 32 >= s.T || j0 >= c.max_pages) continue;
+    const int i0 = (int)nth * 32, live = min(s.T - i0, 32);
+    const int seen = min(((s.row0 + i0 + live - 1) >> a.pshift) + 1, c.max_pages);  // pages that some token sees (or fewer than 1)
+    f16_t best;
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) {
-      const float4 lo = ok ? *reinterpret_cast<const float4*>(p + 32 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float4 hi = ok ? *reinterpret_cast<const float4*>(p + 32 * k + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    for (int e = 0; e < 16; ++e) best[e] = -INFINITY;
+    if (j0 < seen) {
+      const bf16_t* q = (const bf16_t*)c.q + (s.tok0 + i0 + min(n32, live - 1)) * c.q_stride + (int64_t)head * a.G * D + 8 * g;
+      u4_t now[STEPS], next[STEPS];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const __bf16 a = (__bf16)x[e];
-        const float r = x[e] - (float)a;
-        const __bf16 b = (__bf16)r;
-        part[k][0][e] = a, part[k][1][e] = b, part[k][2][e] = (__bf16)(r - (float)b);
+      for (int i = 0; i < STEPS; ++i) next[i] = *reinterpret_cast<const u4_t*>(q + 16 * i);
+      // (later tiles of the sequence see more pages: all that may ever be seen are taken)
+      if (held != b) {
+        const int cap = min(max(s.row0 + s.T, 0), 0x7fffffff);
+        const int pid = j < min((int)(((int64_t)cap + (1 << a.pshift) - 1) >> a.pshift), c.max_pages) ? c.page_table[(int64_t)b * c.max_pages + j] : -1;
+        const bool ok = pid >= 0 && pid < c.num_pages;
+        const float* mean = c.means + ((int64_t)(ok ? pid : 0) * c.Hkv + head) * D + 8 * g;
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) m[i].take(mean + 16 * i, ok);
+        held = b;
+      }
+      for (int h = 0; h < a.G; ++h) {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) now[i] = next[i];
+        if (h + 1 < a.G)
+#pragma unroll
+          for (int i = 0; i < STEPS; ++i) next[i] = *reinterpret_cast<const u4_t*>(q + (int64_t)(h + 1) * D + 16 * i);
+        f16_t x, y;  // two sums: their products do not wait for each other
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = y[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          const bf16x8_t f = __builtin_bit_cast(bf16x8_t, now[i]);
+          x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, m[i].part[0], x, 0, 0, 0);
+          y = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, m[i].part[1], y, 0, 0, 0);
+          y = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, m[i].part[2], y, 0, 0, 0);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) best[e] = h ? larger(best[e], x[e] + y[e]) : x[e] + y[e];
+      }
+    }
+    if (j < c.max_pages)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int i = 8 * (e >> 2) + 4 * g + (e & 3);
+        if (i < live)
+          c.scores[((s.tok0 + i0 + i) * c.Hkv + head) * c.max_pages + j] =
+              j <= (s.row0 + i0 + i) >> a.pshift ? best[e] : -INFINITY;
+      }
+  }
+}
+
+// Decode (T = 1), bf16: rows are 16 query heads of the one token, columns 16 pages; the
+// maximum over the rows is taken across the lanes.  The one page that holds the token is
+// averaged by the workgroup that scores it, so the step is one launch.  Bound by what it
+// waits for (the length and the page indices, then the means): FIGS.
+template <int D, typename KV>
+__global__ __launch_bounds__(256) void block_scores_one_kernel(Args a, uint32_t groups) {
+  constexpr int STEPS = D / 32, NB = 2;
+  const BlockCall& c = a.c;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n16 = lane & 15, g = lane >> 4;
+  const uint32_t per = (uint32_t)c.Hkv * groups, t = blockIdx.x / per, rest = blockIdx.x - t * per;
+  const int head = rest / groups, group = (int)(rest - head * groups), j0 = group * PAGES + wave * 32;
+  int b = t, i = 0;
+  Seq s;
+  if (c.cu_seqlens) {
+    if (!token_at(a, t, t, b, s, i)) return;  // (the same for all threads)
+  } else {
+    s = seq_of(a, b);
+  }
+  const int* table = c.page_table + (int64_t)b * c.max_pages;
+  int pid[NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) pid[n] = j0 + 16 * n + n16 < c.max_pages ? table[j0 + 16 * n + n16] : -1;
+  const bf16_t* q = (const bf16_t*)c.q + t * c.q_stride + (int64_t)head * a.G * D + 8 * g;
+  u4_t f[STEPS];
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) f[k] = *reinterpret_cast<const u4_t*>(q + (int64_t)min(n16, a.G - 1) * D + 32 * k);
+  const int p = s.row0 + i, own = p >> a.pshift;  // (negative: no page)
+  __shared__ float fresh[D];
+  bool formed = false;
+  if (own >= 0 && own / PAGES == group) {
+    const int mine = table[own];
+    if (mine >= 0 && mine < c.num_pages) {
+      const float mean = mean_key<D, KV>(a, mine, head, (p & ((1 << a.pshift) - 1)) + 1);
+      if (threadIdx.x < D) {
+        c.means[((int64_t)mine * c.Hkv + head) * D + threadIdx.x] = mean;
+        fresh[threadIdx.x] = mean;
+      }
+      __syncthreads();
+      formed = true;
+    }
+  }
+  float best[NB];
+#pragma unroll
+  for (int n = 0; n < NB; ++n) best[n] = -INFINITY;
+  if (j0 <= own) {
+    Parts m[NB][STEPS];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const int j = j0 + 16 * n + n16;
+      const bool ok = j < own && pid[n] >= 0 && pid[n] < c.num_pages;
+      const float* mean = c.means + ((int64_t)(ok ? pid[n] : 0) * c.Hkv + head) * D;
+#pragma unroll
+      for (int k = 0; k < STEPS; ++k) m[n][k].take(mean + 8 * g + 32 * k, ok);
+      if (formed && j == own)
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) m[n][k].take(fresh + 8 * g + 32 * k, true);
+    }
+    for (int h = 0; h < a.G; h += 16) {
+      if (h)
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) f[k] = *reinterpret_cast<const u4_t*>(q + (int64_t)min(h + n16, a.G - 1) * D + 32 * k);
+      f4_t x[NB];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) x[n] = zero4();
+#pragma unroll
+      for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+        for (int part = 0; part < 3; ++part)
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+            x[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f[k]), m[n][k].part[part], x[n], 0, 0, 0);
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        float v = larger(larger(x[n][0], x[n][1]), larger(x[n][2], x[n][3]));  // (rows past the heads repeat the last)
+        v = larger(v, __shfl_xor(v, 16, WAVE));
+        v = larger(v, __shfl_xor(v, 32, WAVE));
+        best[n] = h ? larger(best[n], v) : v;
       }
     }
   }
-};
-template <int D> struct Means<D, float> {
-  f4_t lo[D / 32], hi[D / 32];
-  __device__ void take(const float* p, bool ok) {
-#pragma unroll
-    for (int k = 0; k < D / 32; ++k) {
-      lo[k] = ok ? *reinterpret_cast<const f4_t*>(p + 32 * k) : zero4();
-      hi[k] = ok ? *reinterpret_cast<const f4_t*>(p + 32 * k + 4) : zero4();
-    }
-  }
-};
+  // lanes 0 .. 31 write the wave's 32 pages
+  const int j = j0 + lane;
+  if (lane < 32 && j < c.max_pages)
+    c.scores[((int64_t)t * c.Hkv + head) * c.max_pages + j] = j <= own ? (lane < 16 ? best[0] : best[1]) : -INFINITY;
+}
 
-template <int D, typename IO>
-__global__ __launch_bounds__(256) void block_scores_kernel(Args a, uint32_t groups) {
+// The same in fp32: 16 tokens and 16 pages at a time with fp32 products, TM x 16 tokens and
+// 2 x 16 pages a wave.
+template <int D>
+__global__ __launch_bounds__(256) void block_scores_f32_kernel(Args a, uint32_t groups) {
+  constexpr int TM = 2, NB = 2, TOKENS = 16 * TM;
   const BlockCall& c = a.c;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n16 = lane & 15, g = lane >> 4;
   const uint32_t per = (uint32_t)c.Hkv * groups, slot = blockIdx.x / per, rest = blockIdx.x - slot * per;
@@ -202,42 +356,32 @@ __global__ __launch_bounds__(256) void block_scores_kernel(Args a, uint32_t grou
 #pragma unroll
     for (int n = 0; n < NB; ++n) best[t][n] = f4_t{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
   if (j0 < seen) {
-    Means<D, IO> m[NB];
+    f4_t m[NB][D / 16];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       const int j = j0 + 16 * n + n16;
       const int pid = j < min(seen, c.max_pages) ? table[j] : -1;
       const bool ok = pid >= 0 && pid < c.num_pages;
-      m[n].take(c.means + ((int64_t)(ok ? pid : 0) * c.Hkv + head) * D + 8 * g, ok);
+      const float* mean = c.means + ((int64_t)(ok ? pid : 0) * c.Hkv + head) * D + 4 * g;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) m[n][k] = ok ? *reinterpret_cast<const f4_t*>(mean + 16 * k) : zero4();
     }
     for (int h = 0; h < a.G; ++h) {
 #pragma unroll
       for (int t = 0; t < TM; ++t) {
         if (t && 16 * t >= live) break;
         const int i = i0 + min(16 * t + n16, live - 1);
-        const IO* q = (const IO*)c.q + (s.tok0 + i) * c.q_stride + (int64_t)(head * a.G + h) * D + 8 * g;
+        const float* q = (const float*)c.q + (s.tok0 + i) * c.q_stride + (int64_t)(head * a.G + h) * D + 4 * g;
         f4_t x[NB];
 #pragma unroll
         for (int n = 0; n < NB; ++n) x[n] = zero4();
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          if constexpr (sizeof(IO) == 2) {
-            const bf16x8_t qk = __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u4_t*>(q + 32 * k));
+        for (int k = 0; k < D / 16; ++k) {
+          const f4_t f = *reinterpret_cast<const f4_t*>(q + 16 * k);
 #pragma unroll
-            for (int part = 0; part < 3; ++part)
+          for (int e = 0; e < 4; ++e)
 #pragma unroll
-              for (int n = 0; n < NB; ++n)
-                x[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qk, m[n].part[k][part], x[n], 0, 0, 0);
-          } else {
-            const f4_t lo = *reinterpret_cast<const f4_t*>(q + 32 * k), hi = *reinterpret_cast<const f4_t*>(q + 32 * k + 4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-              for (int n = 0; n < NB; ++n) {
-                x[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(lo[e], m[n].lo[k][e], x[n], 0, 0, 0);
-                x[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(hi[e], m[n].hi[k][e], x[n], 0, 0, 0);
-              }
-          }
+            for (int n = 0; n < NB; ++n) x[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(f[e], m[n][k][e], x[n], 0, 0, 0);
         }
 #pragma unroll
         for (int n = 0; n < NB; ++n)
@@ -410,16 +554,33 @@ Args args_of(const BlockCall& c) {
 int64_t mean_slots(const BlockCall& c) {
   return c.packed ? (c.total / c.page) + 2 * (int64_t)c.B : (int64_t)c.B * (((int64_t)c.T + c.page - 2) / c.page + 1);
 }
-int64_t score_slots(const BlockCall& c) { return c.packed ? c.total / TOKENS + c.B : (int64_t)c.B * cdiv(c.T, TOKENS); }
+int64_t score_slots(const BlockCall& c) { return c.packed ? c.total / 32 + c.B : (int64_t)c.B * cdiv(c.T, 32); }
 
-template <int D, typename IO> hipError_t scores(const BlockCall& c, hipStream_t stream) {
-  const Args a = args_of(c);
-  const dim3 grid((unsigned)(mean_slots(c) * c.Hkv));
-  if (c.bits8) block_means_kernel<D, uint8_t><<<grid, dim3(256), 0, stream>>>(a);
-  else block_means_kernel<D, IO><<<grid, dim3(256), 0, stream>>>(a);
-  if (c.scores) {
-    const int64_t groups = cdiv(c.max_pages, PAGES);
-    block_scores_kernel<D, IO><<<dim3((unsigned)(score_slots(c) * c.Hkv * groups)), dim3(256), 0, stream>>>(a, (uint32_t)groups);
+template <int D, typename KV> hipError_t means(const Args& a, hipStream_t stream) {
+  block_means_kernel<D, KV><<<dim3((unsigned)(mean_slots(a.c) * a.c.Hkv)), dim3(256), 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+template <int D> hipError_t scores(const BlockCall& c, hipStream_t stream) {
+  Args a = args_of(c);
+  const bool f32 = c.io == IO_F32;
+  const int64_t groups = cdiv(c.max_pages, PAGES);
+  if (c.scores && c.T == 1 && !f32) {
+    const dim3 grid((unsigned)(c.total * c.Hkv * groups));
+    if (c.bits8) block_scores_one_kernel<D, uint8_t><<<grid, dim3(256), 0, stream>>>(a, (uint32_t)groups);
+    else block_scores_one_kernel<D, bf16_t><<<grid, dim3(256), 0, stream>>>(a, (uint32_t)groups);
+    return hipGetLastError();
+  }
+  const hipError_t e = c.bits8 ? means<D, uint8_t>(a, stream) : f32 ? means<D, float>(a, stream) : means<D, bf16_t>(a, stream);
+  if (e != hipSuccess || !c.scores) return e;
+  a.slots = score_slots(c);
+  if (f32) {
+    block_scores_f32_kernel<D><<<dim3((unsigned)(a.slots * c.Hkv * groups)), dim3(256), 0, stream>>>(a, (uint32_t)groups);
+  } else {
+    // tiles a workgroup: as many workgroups as the chip holds, where there are more tiles
+    const int64_t all = a.slots * c.Hkv * groups, tiles = std::min<int64_t>(std::max<int64_t>(all / (D == 256 ? 256 : 512), 1), 16);
+    block_scores_kernel<D><<<dim3((unsigned)(cdiv(a.slots, tiles) * c.Hkv * groups)), dim3(256), 0, stream>>>(
+        a, (uint32_t)groups, (int)tiles);
   }
   return hipGetLastError();
 }
@@ -438,15 +599,15 @@ size_t list_bytes(const BlockCall& c) { return a256((size_t)c.total * c.Hkv * c.
 }  // namespace
 
 int64_t block_scores_workgroups(const BlockCall& c) {
-  return std::max(mean_slots(c) * c.Hkv, c.scores ? score_slots(c) * c.Hkv * cdiv(c.max_pages, PAGES) : 0);
+  const int64_t groups = cdiv(c.max_pages, PAGES);
+  return std::max(mean_slots(c) * c.Hkv, c.scores ? (c.T == 1 ? c.total : score_slots(c)) * c.Hkv * groups : 0);
 }
 
 hipError_t launch_block_scores(const BlockCall& c, hipStream_t stream) {
-  const bool f = c.io == IO_F32;
   switch (c.D) {
-    case 64: return f ? scores<64, float>(c, stream) : scores<64, bf16_t>(c, stream);
-    case 128: return f ? scores<128, float>(c, stream) : scores<128, bf16_t>(c, stream);
-    case 256: return f ? scores<256, float>(c, stream) : scores<256, bf16_t>(c, stream);
+    case 64: return scores<64>(c, stream);
+    case 128: return scores<128>(c, stream);
+    case 256: return scores<256>(c, stream);
   }
   return hipErrorInvalidValue;
 }
