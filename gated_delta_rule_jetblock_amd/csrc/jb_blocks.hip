@@ -102,8 +102,12 @@ template <typename KV> __device__ __forceinline__ void row8(const void* p, uint3
 
 // Mean key of the first `held` rows of page pid: a workgroup's D / 8 lanes a row, summed in a
 // fixed order (a lane group's rows in order, then the groups); threads 0 .. D - 1 have it.
-template <int D, typename KV> __device__ __forceinline__ float mean_key(const Args& a, int pid, int head, int held) {
+// part: GROUPS x (D + 1) floats of LDS.
+template <int D> constexpr int mean_floats = 256 / (D / 8) * (D + 1);
+template <int D, typename KV>
+__device__ __forceinline__ float mean_key(const Args& a, int pid, int head, int held, float* lds) {
   constexpr int L = D / 8, GROUPS = 256 / L;
+  float(*const part)[D + 1] = reinterpret_cast<float(*)[D + 1]>(lds);
   const BlockCall& c = a.c;
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
   const int64_t row0 = (int64_t)head << a.pshift;
@@ -117,7 +121,6 @@ template <int D, typename KV> __device__ __forceinline__ float mean_key(const Ar
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum[i] += x[i];
   }
-  __shared__ float part[GROUPS][D + 1];
 #pragma unroll
   for (int i = 0; i < 8; ++i) part[group][8 * lane + i] = sum[i];
   __syncthreads();
@@ -145,49 +148,94 @@ __global__ __launch_bounds__(256) void block_means_kernel(Args a) {
   const int pid = c.page_table[(int64_t)b * c.max_pages + j];
   if (pid < 0 || pid >= c.num_pages) return;
   const int held = (int)min((int64_t)end - (j << a.pshift), (int64_t)page);
-  const float mean = mean_key<D, KV>(a, pid, head, held);
+  __shared__ float lds[mean_floats<D>];
+  const float mean = mean_key<D, KV>(a, pid, head, held, lds);
   if (threadIdx.x < D) c.means[((int64_t)pid * c.Hkv + head) * D + threadIdx.x] = mean;
 }
 
 // the larger of two scores; NaN stays
 __device__ __forceinline__ float larger(float m, float x) { return x > m || x != x ? x : m; }
 
-// A mean's 8 values as three bf16 parts: hi + mid + lo are its 24 bits, so products with bf16
-// queries are exact and their sums fp32's.
-struct Parts {
-  bf16x8_t part[3];
-  __device__ __forceinline__ void take(const float* p, bool ok) {
-    const float4 lo = ok ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4 hi = ok ? *reinterpret_cast<const float4*>(p + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+// The means of NB x 16 pages as operands: lane (page lane % 16, group g) has d = 8 g + e of
+// every 32, each value as three bf16 parts: hi + mid + lo are its 24 bits, so products with
+// bf16 queries are exact and their sums fp32's.
+// They come by way of LDS (a region of 16 D floats for each wave): lanes that lie next to each
+// other read one row, where an operand's neighbouring lanes are of different rows and cost
+// the vector memory unit a cycle each (a chunk of 2K tokens on 64K rows with the queries
+// read so too: 33 us, of which 24 were that).
+typedef __attribute__((address_space(3))) float4 lds_float4;
+typedef __attribute__((address_space(3))) u4_t lds_u4;
+typedef __attribute__((address_space(3))) char lds_char;
+
+template <int D, int NB> struct Means {
+  static constexpr int STEPS = D / 32, LPR = D / 4, RPI = 64 / LPR, LOADS = 16 / RPI;  // lanes a row, rows a load
+  float4 x[NB][LOADS];
+  bf16x8_t part[NB][STEPS][3];
+  // pid[n]: lane n16's page of 16 n + n16, -1 for zeros
+  __device__ __forceinline__ void fetch(const Args& a, int head, const int (&pid)[NB]) {
+    const int lane = lane_id();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const __bf16 a = (__bf16)x[e];
-      const float r = x[e] - (float)a;
-      const __bf16 b = (__bf16)r;
-      part[0][e] = a, part[1][e] = b, part[2][e] = (__bf16)(r - (float)b);
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const int from = __shfl(pid[n], i * RPI + lane / LPR, WAVE);
+        const float4 v = reinterpret_cast<const float4*>(a.c.means + ((int64_t)max(from, 0) * a.c.Hkv + head) * D)[lane % LPR];
+        x[n][i] = from >= 0 ? v : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+  }
+  // row `row` of the 16 n is `fresh` instead (none: -1)
+  __device__ __forceinline__ void split(lds_char* at, const float* fresh, int row) {
+    const int lane = lane_id(), n16 = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // what was there is read
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const int r = i * RPI + lane / LPR, piece = lane % LPR;
+        *(lds_u4*)(at + r * D * 4 + ((piece ^ r) << 4)) = __builtin_bit_cast(u4_t, x[n][i]);
+      }
+      if (fresh && row >> 4 == n && lane < LPR) {
+        const int r = row & 15;
+        *(lds_u4*)(at + r * D * 4 + ((lane ^ r) << 4)) = __builtin_bit_cast(u4_t, reinterpret_cast<const float4*>(fresh)[lane]);
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+      for (int k = 0; k < STEPS; ++k) {
+        const float4 lo = __builtin_bit_cast(float4, *(const lds_u4*)(at + n16 * D * 4 + (((2 * g + 8 * k) ^ n16) << 4)));
+        const float4 hi = __builtin_bit_cast(float4, *(const lds_u4*)(at + n16 * D * 4 + (((2 * g + 8 * k + 1) ^ n16) << 4)));
+        const float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const __bf16 a = (__bf16)y[e];
+          const float r = y[e] - (float)a;
+          const __bf16 b = (__bf16)r;
+          part[n][k][0][e] = a, part[n][k][1][e] = b, part[n][k][2][e] = (__bf16)(r - (float)b);
+        }
+      }
     }
   }
 };
 
-typedef float f16_t __attribute__((ext_vector_type(16)));
-
-// Scores of tokens of longer chunks, bf16: 32 tokens by 32 pages on matrix cores, one
-// product for each query head, their maximum taken in the accumulators (rows are tokens,
-// columns pages).  A wave keeps its pages' means in registers, split once, and walks
-// `tiles` tiles of tokens, the next head's queries on their way while these are used; a
-// workgroup takes 4 times as many pages.  Bound by the matrix cores (three products where
-// one would do for bf16 means): FIGS.
+// Scores of tokens of longer chunks, bf16: 16 tokens by 16 pages at a time on matrix cores
+// (rows are tokens, columns pages), one product for each query head, their maximum taken in
+// the accumulators.  A wave keeps the means of 2 x 16 pages in registers, split once, and
+// walks `tiles` tiles of 2 x 16 tokens, the next head's queries on their way while these are
+// used; a workgroup takes 4 times as many pages.  FIGS.
 constexpr int PAGES = 128;  // of a workgroup
 
 template <int D>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void block_scores_kernel(Args a, uint32_t groups, int tiles) {
-  constexpr int STEPS = D / 16;
+  constexpr int STEPS = D / 32, TM = 2, NB = 2;
   const BlockCall& c = a.c;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n32 = lane & 31, g = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n16 = lane & 15, g = lane >> 4;
   const uint32_t per = (uint32_t)c.Hkv * groups, place = blockIdx.x / per, rest = blockIdx.x - place * per;
-  const int head = rest / groups, j0 = (int)(rest - head * groups) * PAGES + wave * 32, j = j0 + n32;
-  Parts m[STEPS];
+  const int head = rest / groups, j0 = (int)(rest - head * groups) * PAGES + wave * 16 * NB;
+  constexpr int PR = D / 8, PER = 32 * PR / 256;  // 16-byte pieces of a row; of 32 rows a thread
+  __shared__ __attribute__((aligned(16))) char qs[2][32 * D * 2];  // a head's queries, and the next one's
+  __shared__ __attribute__((aligned(16))) char ms[4][16 * D * 4];
+  lds_char* const lq = (lds_char*)qs[0];
+  auto place_of = [](int r, int piece) { return r * D * 2 + ((piece ^ (PR < 16 ? (r >> 1) & 7 : r & 15)) << 4); };
+  Means<D, NB> m;
   int held = -1;  // the sequence whose means these are
   for (int k = 0; k < tiles; ++k) {
     const int64_t slot = (int64_t)place * tiles + k;
@@ -195,54 +243,91 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void block_scores_kernel(Arg
     int64_t nth;
     const int b = seq_at(a, slot, 5, 1, ((int64_t)c.T + 31) / 32, nth);
     const Seq s = seq_of(a, b);
-    if (nth < 0 || nth * 32 >= s.T || j0 >= c.max_pages) continue;
+    if (nth < 0 || nth * 32 >= s.T) continue;  // (the same for all waves)
     const int i0 = (int)nth * 32, live = min(s.T - i0, 32);
     const int seen = min(((s.row0 + i0 + live - 1) >> a.pshift) + 1, c.max_pages);  // pages that some token sees (or fewer than 1)
-    f16_t best;
+    f4_t best[TM][NB];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) best[e] = -INFINITY;
-    if (j0 < seen) {
-      const bf16_t* q = (const bf16_t*)c.q + (s.tok0 + i0 + min(n32, live - 1)) * c.q_stride + (int64_t)head * a.G * D + 8 * g;
-      u4_t now[STEPS], next[STEPS];
+    for (int t = 0; t < TM; ++t)
 #pragma unroll
-      for (int i = 0; i < STEPS; ++i) next[i] = *reinterpret_cast<const u4_t*>(q + 16 * i);
-      // (later tiles of the sequence see more pages: all that may ever be seen are taken)
+      for (int n = 0; n < NB; ++n) best[t][n] = f4_t{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    if (j0 - wave * 16 * NB < seen) {  // some wave's pages are seen
+      const bf16_t* q[PER];
+      u4_t next[PER];
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        const int e = u * 256 + threadIdx.x;
+        q[u] = (const bf16_t*)c.q + (s.tok0 + i0 + min(e / PR, live - 1)) * c.q_stride + (int64_t)head * a.G * D + e % PR * 8;
+        next[u] = *reinterpret_cast<const u4_t*>(q[u]);
+      }
+      auto put = [&](int h) {
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+          const int e = u * 256 + threadIdx.x;
+          *(lds_u4*)(lq + (h & 1) * 32 * D * 2 + place_of(e / PR, e % PR)) = next[u];
+          next[u] = *reinterpret_cast<const u4_t*>(q[u] + (int64_t)min(h + 1, a.G - 1) * D);
+        }
+      };
       if (held != b) {
-        const int cap = min(max(s.row0 + s.T, 0), 0x7fffffff);
-        const int pid = j < min((int)(((int64_t)cap + (1 << a.pshift) - 1) >> a.pshift), c.max_pages) ? c.page_table[(int64_t)b * c.max_pages + j] : -1;
-        const bool ok = pid >= 0 && pid < c.num_pages;
-        const float* mean = c.means + ((int64_t)(ok ? pid : 0) * c.Hkv + head) * D + 8 * g;
+        // (later tiles of the sequence see more pages: all that may ever be seen are taken)
+        const int last = min((max(s.row0 + s.T, 1) - 1) >> a.pshift, c.max_pages - 1);
+        int pid[NB];
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) m[i].take(mean + 16 * i, ok);
+        for (int n = 0; n < NB; ++n) {
+          const int j = j0 + 16 * n + n16;
+          pid[n] = j <= last ? c.page_table[(int64_t)b * c.max_pages + j] : -1;
+          if (pid[n] >= c.num_pages) pid[n] = -1;
+        }
+        m.fetch(a, head, pid);
+        m.split((lds_char*)ms[wave], nullptr, -1);
         held = b;
       }
+      __syncthreads();  // (the last tile's queries are read)
+      put(0);
       for (int h = 0; h < a.G; ++h) {
+        __syncthreads();
+        if (h + 1 < a.G) put(h + 1);
+        const lds_char* const at = lq + (h & 1) * 32 * D * 2;
+        f4_t x[TM][NB];
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) now[i] = next[i];
-        if (h + 1 < a.G)
+        for (int t = 0; t < TM; ++t)
 #pragma unroll
-          for (int i = 0; i < STEPS; ++i) next[i] = *reinterpret_cast<const u4_t*>(q + (int64_t)(h + 1) * D + 16 * i);
-        f16_t x, y;  // two sums: their products do not wait for each other
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = y[e] = 0.f;
+          for (int n = 0; n < NB; ++n) x[t][n] = zero4();
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
-          const bf16x8_t f = __builtin_bit_cast(bf16x8_t, now[i]);
-          x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, m[i].part[0], x, 0, 0, 0);
-          y = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, m[i].part[1], y, 0, 0, 0);
-          y = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, m[i].part[2], y, 0, 0, 0);
+          bf16x8_t f[TM];
+#pragma unroll
+          for (int t = 0; t < TM; ++t)
+            f[t] = __builtin_bit_cast(bf16x8_t, *(const lds_u4*)(at + place_of(16 * t + n16, 4 * i + g)));
+#pragma unroll
+          for (int part = 0; part < 3; ++part)
+#pragma unroll
+            for (int t = 0; t < TM; ++t)
+#pragma unroll
+              for (int n = 0; n < NB; ++n)
+                x[t][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[t], m.part[n][i][part], x[t][n], 0, 0, 0);
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) best[e] = h ? larger(best[e], x[e] + y[e]) : x[e] + y[e];
+        for (int t = 0; t < TM; ++t)
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) best[t][n][e] = h ? larger(best[t][n][e], x[t][n][e]) : x[t][n][e];
       }
     }
-    if (j < c.max_pages)
+    if (j0 >= c.max_pages) continue;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int i = 8 * (e >> 2) + 4 * g + (e & 3);
+    for (int t = 0; t < TM; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 16 * t + 4 * g + e, own = (s.row0 + i0 + i) >> a.pshift;
+        float* out = c.scores + ((s.tok0 + i0 + i) * c.Hkv + head) * c.max_pages;
         if (i < live)
-          c.scores[((s.tok0 + i0 + i) * c.Hkv + head) * c.max_pages + j] =
-              j <= (s.row0 + i0 + i) >> a.pshift ? best[e] : -INFINITY;
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+            const int j = j0 + 16 * n + n16;
+            if (j < c.max_pages) out[j] = j <= own ? best[t][n][e] : -INFINITY;
+          }
       }
   }
 }
@@ -252,7 +337,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void block_scores_kernel(Arg
 // averaged by the workgroup that scores it, so the step is one launch.  Bound by what it
 // waits for (the length and the page indices, then the means): FIGS.
 template <int D, typename KV>
-__global__ __launch_bounds__(256) void block_scores_one_kernel(Args a, uint32_t groups) {
+__global__ __launch_bounds__(256, D == 64 ? 5 : D == 128 ? 3 : 2) void block_scores_one_kernel(Args a, uint32_t groups) {
   constexpr int STEPS = D / 32, NB = 2;
   const BlockCall& c = a.c;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n16 = lane & 15, g = lane >> 4;
@@ -274,12 +359,19 @@ __global__ __launch_bounds__(256) void block_scores_one_kernel(Args a, uint32_t 
 #pragma unroll
   for (int k = 0; k < STEPS; ++k) f[k] = *reinterpret_cast<const u4_t*>(q + (int64_t)min(n16, a.G - 1) * D + 32 * k);
   const int p = s.row0 + i, own = p >> a.pshift;  // (negative: no page)
-  __shared__ float fresh[D];
+  Means<D, NB> m;
+#pragma unroll
+  for (int n = 0; n < NB; ++n)
+    if (j0 + 16 * n + n16 >= own || pid[n] >= c.num_pages) pid[n] = -1;  // (the own page's is formed here)
+  if (j0 <= own) m.fetch(a, head, pid);
+  __shared__ __attribute__((aligned(16))) float fresh[D];
+  __shared__ __attribute__((aligned(16))) char ms[4][16 * D * 4];
+  static_assert(mean_floats<D> * 4 <= sizeof(ms), "the mean's sums fit");
   bool formed = false;
   if (own >= 0 && own / PAGES == group) {
     const int mine = table[own];
     if (mine >= 0 && mine < c.num_pages) {
-      const float mean = mean_key<D, KV>(a, mine, head, (p & ((1 << a.pshift) - 1)) + 1);
+      const float mean = mean_key<D, KV>(a, mine, head, (p & ((1 << a.pshift) - 1)) + 1, (float*)ms);
       if (threadIdx.x < D) {
         c.means[((int64_t)mine * c.Hkv + head) * D + threadIdx.x] = mean;
         fresh[threadIdx.x] = mean;
@@ -292,18 +384,7 @@ __global__ __launch_bounds__(256) void block_scores_one_kernel(Args a, uint32_t 
 #pragma unroll
   for (int n = 0; n < NB; ++n) best[n] = -INFINITY;
   if (j0 <= own) {
-    Parts m[NB][STEPS];
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      const int j = j0 + 16 * n + n16;
-      const bool ok = j < own && pid[n] >= 0 && pid[n] < c.num_pages;
-      const float* mean = c.means + ((int64_t)(ok ? pid[n] : 0) * c.Hkv + head) * D;
-#pragma unroll
-      for (int k = 0; k < STEPS; ++k) m[n][k].take(mean + 8 * g + 32 * k, ok);
-      if (formed && j == own)
-#pragma unroll
-        for (int k = 0; k < STEPS; ++k) m[n][k].take(fresh + 8 * g + 32 * k, true);
-    }
+    m.split((lds_char*)ms[wave], formed ? fresh : nullptr, own - j0);
     for (int h = 0; h < a.G; h += 16) {
       if (h)
 #pragma unroll
@@ -317,7 +398,7 @@ __global__ __launch_bounds__(256) void block_scores_one_kernel(Args a, uint32_t 
         for (int part = 0; part < 3; ++part)
 #pragma unroll
           for (int n = 0; n < NB; ++n)
-            x[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f[k]), m[n][k].part[part], x[n], 0, 0, 0);
+            x[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f[k]), m.part[n][k][part], x[n], 0, 0, 0);
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
         float v = larger(larger(x[n][0], x[n][1]), larger(x[n][2], x[n][3]));  // (rows past the heads repeat the last)
@@ -364,7 +445,11 @@ __global__ __launch_bounds__(256) void block_scores_f32_kernel(Args a, uint32_t 
       const bool ok = pid >= 0 && pid < c.num_pages;
       const float* mean = c.means + ((int64_t)(ok ? pid : 0) * c.Hkv + head) * D + 4 * g;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) m[n][k] = ok ? *reinterpret_cast<const f4_t*>(mean + 16 * k) : zero4();
+      for (int k = 0; k < D / 16; ++k) {
+        const f4_t v = *reinterpret_cast<const f4_t*>(mean + 16 * k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m[n][k][e] = ok ? v[e] : 0.f;
+      }
     }
     for (int h = 0; h < a.G; ++h) {
 #pragma unroll
