@@ -48,7 +48,7 @@ __device__ __forceinline__ Seq seq_of(const Args& a, int b) {
 __device__ __forceinline__ int seq_at(const Args& a, int64_t slot, int shift, int more, int64_t per, int64_t& nth) {
   const BlockCall& c = a.c;
   if (!c.cu_seqlens) {
-    const int b = (int)(slot / per);
+    const int b = (int)((uint32_t)slot / (uint32_t)per);  // (both below 2^31)
     nth = slot - b * per;
     return b;
   }
@@ -76,7 +76,7 @@ __device__ __forceinline__ bool token_at(const Args& a, int64_t t0, int64_t t, i
   if (c.cu_seqlens) {
     while (b + 1 < c.B && c.cu_seqlens[b + 1] <= t) ++b;
   } else {
-    b = (int)(t / max(c.T, 1));
+    b = (int)((uint32_t)t / (uint32_t)max(c.T, 1));
   }
   s = seq_of(a, b);
   const int64_t at = t - s.tok0;
@@ -493,9 +493,10 @@ __global__ __launch_bounds__(256) void block_scores_f32_kernel(Args a, uint32_t 
 
 // Selection by a search for the count-th largest score, bit by bit from the top: a row's
 // scores stay in registers as whole numbers in the scores' order, V a lane, and a step
-// counts those that reach a candidate (a compare, a scalar bit count).  W waves a row; with
-// one the row needs no barrier.  Places are ascending: lane l of wave w has pages
-// (w V + v) 64 + l.
+// counts those that reach a candidate (a compare, a scalar bit count).  Once at most 64 are
+// undecided they are gathered, one a lane, and the other steps cost one compare each.  W waves
+// a row; with one the row needs no barrier.  Places are ascending: lane l of wave w has pages
+// (w V + v) 64 + l.  Bound by its chain of steps: FIGS.
 __device__ __forceinline__ uint32_t order_of(float x) {
   const uint32_t u = __float_as_uint(x != x ? -INFINITY : x + 0.f);  // (-0 as 0)
   return u & 0x80000000u ? ~u : u | 0x80000000u;
@@ -506,81 +507,169 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void block_select_kernel(Arg
   constexpr int ROWS = W == 1 ? 4 : 1;  // rows a workgroup
   const BlockCall& c = a.c;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, w = W == 1 ? 0 : wave;
-  const int64_t rows = c.total * c.Hkv, row0 = (int64_t)blockIdx.x * ROWS, row = row0 + (W == 1 ? wave : 0);
-  const int64_t t = min(row, rows - 1) / c.Hkv;
+  // (fewer than 2^24 rows)
+  const uint32_t rows = (uint32_t)(c.total * c.Hkv), row0 = blockIdx.x * ROWS, row = row0 + (W == 1 ? wave : 0);
+  const uint32_t t = min(row, rows - 1) / (uint32_t)c.Hkv;
+  const int at = w * V * 64 + lane;
+  // the scores are on their way while the token's place is found
+  const float* x = c.scores_in + (int64_t)min(row, rows - 1) * c.max_pages;
+  float score[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) score[v] = x[min(at + 64 * v, c.max_pages - 1)];
   int b, i;
   Seq s;
-  const bool live = token_at(a, row0 / c.Hkv, t, b, s, i) && row < rows;
+  const bool live = token_at(a, row0 / (uint32_t)c.Hkv, t, b, s, i) && row < rows;
   if (!live) return;  // (with W > 1 the workgroup's only row)
-  const int own = (s.row0 + i) >> a.pshift;  // (of a negative row negative: it sees no page)
+  const int own = __builtin_amdgcn_readfirstlane((s.row0 + i) >> a.pshift);  // (of a negative row negative: it sees no page)
   const int nv = min(own + 1, c.max_pages), count = c.count;
-  int* const out = c.blocks + row * count;
-  const int at = w * V * 64 + lane;
+  int* const out = c.blocks + (int64_t)row * count;
   if (nv <= count) {  // all of them
     for (int j = W == 1 ? lane : (int)threadIdx.x; j < count; j += W * 64) out[j] = j < nv ? j : -1;
     return;
   }
-  const float* x = c.scores_in + row * c.max_pages;
   uint32_t key[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int j = at + 64 * v;
-    key[v] = 0;
-    if (j < nv) key[v] = j < c.first || j > own - c.recent ? 0xffffffffu : order_of(x[j]);
+    key[v] = order_of(score[v]);
+    const int j0 = at - lane + 64 * v;  // (the same for the wave: most of its rows of 64 hold no exception)
+    if (j0 < c.first || j0 + 63 > own - c.recent)
+      key[v] = j >= nv ? 0u : j < c.first || j > own - c.recent ? 0xffffffffu : key[v];
   }
-  __shared__ int counts[2][W];
-  auto over_waves = [&](int n, int turn) {  // the sum of the waves' n (a scalar of each)
-    if constexpr (W == 1) return n;
-    if (lane == 0) counts[turn & 1][w] = n;
+  __shared__ int2 counts[2][W];
+  __shared__ uint32_t few[ROWS][64];
+  // the sums of the waves' x and y (scalars of each), and of those before this one
+  int turn = 0;
+  auto over_waves = [&](int x, int y, int2& before) {
+    before = make_int2(0, 0);
+    if constexpr (W == 1) return make_int2(x, y);
+    if (lane == 0) counts[turn & 1][w] = make_int2(x, y);
     __syncthreads();
-    int sum = 0;
+    int2 sum = make_int2(0, 0);
 #pragma unroll
-    for (int u = 0; u < W; ++u) sum += counts[turn & 1][u];
+    for (int u = 0; u < W; ++u) {
+      const int2 n = counts[turn & 1][u];
+      sum.x += n.x, sum.y += n.y;
+      if (u < w) before.x += n.x, before.y += n.y;
+    }
+    ++turn;
     return sum;
   };
-  uint32_t low = 0;  // at least `count` scores reach it
-  for (int bit = 31; bit >= 0; --bit) {
+  const uint64_t below = (1ull << lane) - 1;
+  if (W == 1 && count <= 64) {
+    // The count-th largest of the lanes' largest is reached by at least `count` scores, and
+    // by few more: where those are at most 64, the rest is one score a lane.
+    uint32_t most = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) most = max(most, key[v]);
+    auto nth = [&](uint32_t x, int& n) {  // the largest t that `count` of x reach, and how many do (n: at t = 0)
+      uint32_t t = 0;
+      for (int bit = 31; bit >= 0 && n != count; --bit) {
+        const int m = __builtin_popcountll(__builtin_amdgcn_ballot_w64(x >= (t | 1u << bit)));
+        if (m >= count) t |= 1u << bit, n = m;
+      }
+      return t;
+    };
+    int n = 64;
+    const uint32_t low = max(nth(most, n), 1u);
+    n = 0;
+    uint64_t all[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      all[v] = __builtin_amdgcn_ballot_w64(key[v] >= low);
+      n += __builtin_popcountll(all[v]);
+    }
+    if (n <= 64) {
+      __shared__ uint2 list[ROWS][64];
+      int place = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (all[v]) {
+          if (key[v] >= low) list[wave][place + __builtin_popcountll(all[v] & below)] = make_uint2(key[v], at + 64 * v);
+          place += __builtin_popcountll(all[v]);
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      const uint2 one = lane < n ? list[wave][lane] : make_uint2(0u, 0u);
+      const uint32_t t = nth(one.x, n);
+      const uint64_t eq = __builtin_amdgcn_ballot_w64(one.x == t);
+      const int more = __builtin_popcountll(__builtin_amdgcn_ballot_w64(one.x > t));
+      const bool take = one.x > t || (one.x == t && more + __builtin_popcountll(eq & below) < count);
+      const uint64_t taken = __builtin_amdgcn_ballot_w64(take);
+      if (take) out[__builtin_popcountll(taken & below)] = one.y;
+      return;
+    }
+  }
+  int2 before;
+  // `reach` scores reach `low`, at least `count`; `above` reach what it may still grow to, fewer
+  uint32_t low = 0;
+  int reach = nv, above = 0, bit = 31;
+  for (; bit >= 0 && reach != count && reach - above > 64; --bit) {
     const uint32_t t = low | 1u << bit;
     int n = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) n += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[v] >= t));
-    n = over_waves(n, bit);
-    if (n >= count) low = t;
-    if (n == count) break;
+    n = over_waves(n, 0, before).x;
+    if (n >= count) low = t, reach = n;
+    else above = n;
+  }
+  if (bit >= 0 && reach != count) {
+    // the undecided ones share the bits above `bit`, and only those
+    const uint32_t top = bit == 31 ? 0u : low >> (bit + 1);
+    int n = 0, mine = 0;
+    auto undecided = [&](int v) { return key[v] && (bit == 31 || key[v] >> (bit + 1) == top); };
+    if constexpr (W > 1) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) mine += __builtin_popcountll(__builtin_amdgcn_ballot_w64(undecided(v)));
+      over_waves(mine, 0, before);
+      n = before.x;
+    }
+    uint32_t* const list = few[W == 1 ? wave : 0];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const bool is = undecided(v);
+      const uint64_t all = __builtin_amdgcn_ballot_w64(is);
+      if (all) {
+        if (is) list[n + __builtin_popcountll(all & below)] = key[v];
+        n += __builtin_popcountll(all);
+      }
+    }
+    if constexpr (W > 1) __syncthreads();
+    else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const uint32_t one = lane < reach - above ? list[lane] : 0u;
+    const int sure = above;
+    for (; bit >= 0 && reach != count; --bit) {
+      const uint32_t t = low | 1u << bit;
+      const int n = sure + __builtin_popcountll(__builtin_amdgcn_ballot_w64(one >= t));
+      if (n >= count) low = t, reach = n;
+      else above = n;
+    }
   }
   // those above `low`, and of those equal to it the first ones
-  int above = 0, equal = 0;
+  int need = 0x7fffffff, taken = 0, equals = 0;  // equal ones to take; taken and equal ones before this wave's
+  if (reach != count) need = count - above;
+  if constexpr (W > 1) {
+    int more = 0, same = 0;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    above += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[v] > low));
-    equal += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[v] == low));
-  }
-  int need, taken = 0, equals = 0;  // equal ones to take; taken and equal ones before this wave's
-  if constexpr (W == 1) {
-    need = count - above;
-  } else {
-    __shared__ int2 both[W];
-    __syncthreads();
-    if (lane == 0) both[w] = make_int2(above, equal);
-    __syncthreads();
-    int sum = 0, before = 0;
-#pragma unroll
-    for (int u = 0; u < W; ++u) {
-      sum += both[u].x;
-      if (u < w) before += both[u].x, equals += both[u].y;
+    for (int v = 0; v < V; ++v) {
+      more += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[v] > low));
+      same += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[v] == low));
     }
-    need = count - sum;
-    taken = before + min(equals, need);
+    over_waves(more, same, before);
+    equals = before.y;
+    taken = before.x + min(equals, need);
   }
-  const uint64_t below = (1ull << lane) - 1;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const uint64_t eq = __builtin_amdgcn_ballot_w64(key[v] == low);
-    const bool take = key[v] > low || (key[v] == low && equals + __builtin_popcountll(eq & below) < need);
-    const uint64_t all = __builtin_amdgcn_ballot_w64(take);
-    if (take) out[taken + __builtin_popcountll(all & below)] = at + 64 * v;
-    taken += __builtin_popcountll(all);
-    equals += __builtin_popcountll(eq);
+    uint64_t all = __builtin_amdgcn_ballot_w64(key[v] >= low);
+    if (all) {
+      const uint64_t eq = __builtin_amdgcn_ballot_w64(key[v] == low);
+      const bool take = key[v] > low || (key[v] == low && equals + __builtin_popcountll(eq & below) < need);
+      all = __builtin_amdgcn_ballot_w64(take);
+      if (take) out[taken + __builtin_popcountll(all & below)] = at + 64 * v;
+      taken += __builtin_popcountll(all);
+      equals += __builtin_popcountll(eq);
+    }
   }
 }
 
