@@ -456,15 +456,16 @@ template <int D> __device__ __forceinline__ bool odd_codes(const lds_char* v, ui
   }
   return __any(odd);
 }
-template <int D>
+// (COLS queries a wave: o are D COLS / 64 accumulators, in 32 or 16 columns' order)
+template <int D, int COLS>
 __device__ __attribute__((noinline)) void add_odd_codes(float* o, const lds_char* v, uint32_t e, int j0, int p, int lw) {
   using W = Raw8<D>;
-  const int g = lane_id() >> 5;
+  const int g = lane_id() / COLS;
   for (int r = 0; r < 32; ++r) {
     if (j0 + r > p || j0 + r <= lw) continue;
     const bool all = (r < 16 ? (e >> 8) & 255u : e >> 24) == 255u;
-    for (int i = 0; i < D / 2; ++i) {
-      const int d = 32 * (i >> 4) + 8 * ((i >> 2) & 3) + 4 * g + (i & 3);
+    for (int i = 0; i < D * COLS / 64; ++i) {
+      const int d = COLS == 32 ? 32 * (i >> 4) + 8 * ((i >> 2) & 3) + 4 * g + (i & 3) : 16 * (i >> 2) + 4 * g + (i & 3);
       const int code = v[r * D + (((d >> 4) ^ W::f(r & 15)) << 4) + (d & 15)];
       if (all || (code & 127) == 127) o[i] = NAN;
     }
@@ -480,6 +481,12 @@ template <int D> __device__ __forceinline__ uint32_t clean_codes(lds_char* v, ui
   if (a) e = (e & 0xffff00ffu) | 127u << 8;
   if (b) e = (e & 0x00ffffffu) | 127u << 24;
   return e;
+}
+
+// element (row r, d .. d + 3) of a wave's staged 32 x D fp32 rows: 16-byte
+// pieces permuted by row
+template <int D> __device__ __forceinline__ lds_f4* stage_at(lds_char* st, int r, int d) {
+  return (lds_f4*)(st + r * D * 4 + (((d >> 2) ^ (r & 15)) << 4));
 }
 
 // One wave's 32 queries and what they have gathered so far.
@@ -521,6 +528,17 @@ template <int D, bool Q8 = false> struct Wave {
       for (int e = 0; e < 16; ++e) o[db][e] = 0.f;
     m = -INFINITY;
     l = 0.f;
+  }
+
+  __device__ __forceinline__ float sum() const { return l + other_half(l); }
+  // the rows of O to LDS
+  __device__ __forceinline__ void stage(lds_char* st) const {
+    const int c = lane_id() & 31, g = lane_id() >> 5;
+#pragma unroll
+    for (int db = 0; db < D / 32; ++db)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *stage_at<D>(st, c, 32 * db + 8 * e + 4 * g) = f4_t{o[db][4 * e], o[db][4 * e + 1], o[db][4 * e + 2], o[db][4 * e + 3]};
   }
 
   // The queries are here: not in the loop, where a wait for them would be one
@@ -766,7 +784,7 @@ template <int D, bool Q8 = false> struct Wave {
       float so[D / 2];
 #pragma unroll
       for (int i = 0; i < D / 2; ++i) so[i] = o[i >> 4][i & 15];
-      add_odd_codes<D>(so, v, e, j0, p, lw);
+      add_odd_codes<D, 32>(so, v, e, j0, p, lw);
 #pragma unroll
       for (int i = 0; i < D / 2; ++i) o[i >> 4][i & 15] = so[i];
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -786,6 +804,173 @@ template <int D, bool Q8 = false> struct Wave {
     add_odd_values<D, NB>(so, ss, lv, j0, p, lw);
 #pragma unroll
     for (int e = 0; e < D / 2; ++e) o[e >> 4][e & 15] = so[e];
+  }
+};
+
+// One wave's at most 16 queries over a cache in 8 bits (decode), on 16x16x32 products: half
+// the products and exponentials of 32 columns.  Lane: query n = lane % 16, rows 4 g + i of
+// every 16 (g = lane / 16), so the accumulators of two times 16 rows are the operand of the
+// product with V as they stand.  QR = 8: at most 8 queries, and the weights' second bf16 part
+// takes the columns that are left: columns 8 .. 15 form the same scores again and hold
+// what the first part leaves of their weights.
+template <int D, int QR> struct Wave16 {
+  using W8 = Raw8<D>;
+  bf16x8_t q[D / 32];  // d = D / 4 g + 8 k + e, so that a lane's codes of a row lie together
+  f4_t o[D / 16];      // O^T: o[db][i] is d = 16 db + 4 g + i
+  float m, l;
+  int p, lw, phi, lwlo;
+
+  __device__ void init(const Args& a, const Seq& s, int kvh, int64_t) {
+    const int lane = lane_id(), r = lane & (QR - 1), nr = s.T * a.G, base = s.kv - s.T;
+    const bool real = r < nr;
+    const int i = real ? token_of(a, r) : 0, g = real ? r - i * a.G : 0;
+    p = real ? base + i : -1;
+    lw = a.window ? p - a.window : -1;
+    phi = lwlo = -1;
+    if (nr > 0) {
+      phi = uniform(base + token_of(a, min(QR, nr) - 1));
+      if (a.window) lwlo = uniform(base) - a.window;
+    }
+    const bf16_t* src = (const bf16_t*)a.q + a.query(s.tok0 + i, kvh, D) + (int64_t)g * D + D / 4 * (lane >> 4);
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (real) w = *reinterpret_cast<const uint4*>(src + 8 * k);
+      q[k] = __builtin_bit_cast(bf16x8_t, w);
+    }
+#pragma unroll
+    for (int db = 0; db < D / 16; ++db) o[db] = zero4();
+    m = -INFINITY;
+    l = 0.f;
+  }
+  __device__ void arrived() {
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) asm volatile("" : "+v"(q[k]));
+  }
+  // the largest (the sum) over the lanes of a query
+  __device__ __forceinline__ static float quarter_max(float x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+  }
+  __device__ __forceinline__ float sum() const {
+    const float x = l + __shfl_xor(l, 16, WAVE);
+    return x + __shfl_xor(x, 32, WAVE);
+  }
+
+  // rows 0 .. 31 of the tile at lk, exponents e
+  __device__ __forceinline__ void scores(const lds_char* lk, uint32_t e, f4_t (&s)[2]) const {
+    const int lane = lane_id(), n = lane & 15, g = lane >> 4;
+    constexpr int READS = D / 64;
+    const int kb = n * D + (((READS * g) ^ W8::f(n)) << 4);
+    u4_t w[2][READS];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int r = 0; r < READS; ++r) w[h][r] = *(const lds_u4*)(lk + (kb ^ (r << 4)) + h * 16 * D);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float scale = scale_of((e >> (16 * h)) & 255u);
+        const u4_t f = bf16_of_e4m3(w[h][k >> 1][2 * (k & 1)], w[h][k >> 1][2 * (k & 1) + 1], scale);
+        s[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, f), q[k], k ? s[h] : zero4(), 0, 0, 0);
+      }
+  }
+  // takes the scores into the maximum (as Wave does: it may lag 2^8 behind) and forms the weights
+  __device__ __forceinline__ void weigh(const Args& a, f4_t (&s)[2]) {
+    float mx = s[0][0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[i >> 2][i & 3]);
+    mx = quarter_max(mx) * a.scale;
+    if (__any(mx > m + 8.f)) {
+      const float mn = fmaxf(m, mx);
+      const float f = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
+#pragma unroll
+      for (int db = 0; db < D / 16; ++db) o[db] *= f;
+      l *= f;
+      m = mn;
+    }
+    const float ms = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = fast_exp2(fmaf(s[i >> 2][i & 3], a.scale, -ms));
+      s[i >> 2][i & 3] = x;
+      l += x;
+    }
+  }
+  // O^T += V^T P^T: lane 16 g + n reads 8 rows (4 g .. and 16 + 4 g ..) of column 16 db + n
+  __device__ __forceinline__ void values(const lds_char* lv, uint32_t e, const f4_t (&s)[2]) {
+    const int lane = lane_id(), n = lane & 15, g = lane >> 4, j = n >> 1, row = 4 * g + (j & 3);
+    // (rows 16 apart have the same order of pieces)
+    const int vb = (row + 16 * (j >> 2)) * D + (W8::f(row) << 4) + (n & 1) * 8;
+    i2_t v[D / 16];
+#pragma unroll
+    for (int db = 0; db < D / 16; ++db) v[db] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i2*)(lv + (vb ^ (db << 4))));
+    bf16x8_t w, lo;
+    const bool second = QR == 8 && (lane & 8);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = s[i >> 2][i & 3];
+      const float hi = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+      if constexpr (QR == 8) {
+        w[i] = (__bf16)(second ? x - hi : hi);
+      } else {
+        w[i] = (__bf16)hi;
+        lo[i] = (__bf16)(x - hi);
+      }
+    }
+    const float s0 = scale_of((e >> 8) & 255u), s1 = scale_of(e >> 24);
+#pragma unroll
+    for (int db = 0; db < D / 16; ++db) {
+      const u4_t f0 = bf16_of_e4m3(v[db][0], v[db][0], s0), f1 = bf16_of_e4m3(v[db][1], v[db][1], s1);
+      const bf16x8_t f = __builtin_bit_cast(bf16x8_t, u4_t{f0[0], f0[1], f1[0], f1[1]});
+      o[db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, w, o[db], 0, 0, 0);
+      if constexpr (QR == 16) o[db] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, lo, o[db], 0, 0, 0);
+    }
+  }
+  __device__ void full8(const Args& a, const lds_char* lk, uint32_t e) {
+    f4_t s[2];
+    scores(lk, e, s);
+    weigh(a, s);
+    values(lk + W8::TILE, e, s);
+  }
+  __device__ void part8(const Args& a, lds_char* lk, uint32_t e, int j0) {
+    const int g = lane_id() >> 4;
+    if (j0 > phi || j0 + 31 <= lwlo) return;
+    f4_t s[2];
+    scores(lk, e, s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int j = j0 + 16 * (i >> 2) + 4 * g + (i & 3);
+      if (j > p || j <= lw) s[i >> 2][i & 3] = -INFINITY;
+    }
+    weigh(a, s);
+    lds_char* const v = lk + W8::TILE;
+    if (odd_codes<D>(v, e)) {
+      float so[D / 4];
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) so[i] = o[i >> 2][i & 3];
+      add_odd_codes<D, 16>(so, v, e, j0, p, lw);
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) o[i >> 2][i & 3] = so[i];
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      e = clean_codes<D>(v, e);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+    values(v, e, s);
+  }
+  // the rows of O to LDS
+  __device__ __forceinline__ void stage(lds_char* st) const {
+    const int lane = lane_id();
+#pragma unroll
+    for (int db = 0; db < D / 16; ++db) {
+      f4_t v = o[db];
+      if constexpr (QR == 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], 8, WAVE);
+      *stage_at<D>(st, lane & 15, 16 * db + 4 * (lane >> 4)) = v;
+    }
   }
 };
 
@@ -843,12 +1028,6 @@ struct Order {
   }
   __device__ int tile(int n) const { return n < nf ? f0 + n : n - nf < f0 - t0 ? t0 + n - nf : t0 + n; }
 };
-
-// element (row r, d .. d + 3) of a wave's staged 32 x D fp32 rows: 16-byte
-// pieces permuted by row
-template <int D> __device__ __forceinline__ lds_f4* stage_at(lds_char* st, int r, int d) {
-  return (lds_f4*)(st + r * D * 4 + (((d >> 2) ^ (r & 15)) << 4));
-}
 
 template <typename OUT> __device__ __forceinline__ void store4(OUT* p, f4_t v);
 template <> __device__ __forceinline__ void store4<float>(float* p, f4_t v) { *reinterpret_cast<f4_t*>(p) = v; }
@@ -1064,8 +1243,9 @@ __device__ __forceinline__ int take_list(const Args& a, int unit, lds_int* pages
 
 // LIST: a workgroup takes a piece of the pages listed for one (token, key head), which are a
 // sequence of one token to it.
-template <int D, int NW, typename OUT, bool Q8, bool LIST>
+template <int D, int NW, typename OUT, bool Q8, bool LIST, int QR>
 __global__ __launch_bounds__(NW * 64, Q8 ? 2 : 1) void attn_row_kernel(Args a) {
+  static_assert(Q8 || QR == 32, "queries of a unit, at most");
   constexpr int R = 32, IMG = R * D * 2, STEP = R * NW, NTHR = NW * 64;
   constexpr int TILE = Q8 ? Raw8<D>::TILE * 2 : 2 * IMG;  // K and V of a tile
   constexpr int RING = NW * 2 * TILE + (Q8 ? NW * 32 * 8 : 0);  // (and the waves' sums, at the end)
@@ -1169,7 +1349,7 @@ __global__ __launch_bounds__(NW * 64, Q8 ? 2 : 1) void attn_row_kernel(Args a) {
     const int n0 = x.lo / STEP * NW;
     x.t0 = max(n0 + s0 * NW, x.lo / R);
     x.t1 = min(n0 + s1 * NW, (x.hi + R - 1) / R);
-    Wave<D, Q8> w;
+    std::conditional_t<QR == 32, Wave<D, Q8>, Wave16<D, QR>> w;
     w.init(a, s, kvh, 0);
     const Order ord(a, s, x, 0, nr - 1, R);
     const int nf = ord.nf, nt = ord.nt;
@@ -1242,19 +1422,14 @@ __global__ __launch_bounds__(NW * 64, Q8 ? 2 : 1) void attn_row_kernel(Args a) {
       }
     }
     // join the waves: O and (m, l) of each in LDS
-    const int c = lane & 31, g = lane >> 5;
-    const float l = w.l + other_half(w.l);
+    constexpr int COLS = QR == 32 ? 32 : 16;
+    const int c = lane & (COLS - 1), g = lane / COLS;
+    const float l = w.sum();
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     lds_char* const all = (lds_char*)ring;
-    constexpr int ST = 32 * D * 4;
+    constexpr int ST = COLS * D * 4;
     static_assert(NW * ST + NW * 32 * 8 <= RING, "staging fits");
-    lds_char* st = all + wave * ST;
-#pragma unroll
-    for (int db = 0; db < D / 32; ++db)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        *stage_at<D>(st, c, 32 * db + 8 * e + 4 * g) =
-            f4_t{w.o[db][4 * e], w.o[db][4 * e + 1], w.o[db][4 * e + 2], w.o[db][4 * e + 3]};
+    w.stage(all + wave * ST);
     lds_float* ml = (lds_float*)(all + NW * ST);  // [2][NW][32]
     if (g == 0) {
       ml[wave * 32 + c] = w.m;
@@ -1756,7 +1931,10 @@ hipError_t launch(const AttnCall& c, const Plan& p, const Args& a, hipStream_t s
     constexpr int NW = row_waves(D);
     if (p.tiles) attn_tile_kernel<D, OUT, Q8><<<tiles, dim3(256), 0, stream>>>(a);
     if (p.rows) {
-      attn_row_kernel<D, NW, OUT, Q8, false><<<dim3((unsigned)p.runs), dim3(NW * 64), 0, stream>>>(a);
+      const dim3 runs((unsigned)p.runs), threads(NW * 64);
+      if (Q8 && p.rows_a_unit <= 8) attn_row_kernel<D, NW, OUT, Q8, false, Q8 ? 8 : 32><<<runs, threads, 0, stream>>>(a);
+      else if (Q8 && p.rows_a_unit <= 16) attn_row_kernel<D, NW, OUT, Q8, false, Q8 ? 16 : 32><<<runs, threads, 0, stream>>>(a);
+      else attn_row_kernel<D, NW, OUT, Q8, false, 32><<<runs, threads, 0, stream>>>(a);
       if (!p.direct)
         attn_row_join_kernel<D, OUT><<<dim3((unsigned)(p.runs * p.rows_a_unit)), dim3(256), 0, stream>>>(a, p.rows_a_unit);
     }
@@ -1832,7 +2010,10 @@ size_t list_rows_bytes(const BlockCall& b) {
 
 template <int D, typename OUT, bool Q8> hipError_t launch_lists(const Args& a, hipStream_t stream) {
   constexpr int NW = row_waves(D), RPB = 256 / (D / 4);
-  attn_row_kernel<D, NW, OUT, Q8, true><<<dim3((unsigned)a.B * a.pieces), dim3(NW * 64), 0, stream>>>(a);
+  const dim3 units((unsigned)a.B * a.pieces), threads(NW * 64);
+  if (Q8 && a.G <= 8) attn_row_kernel<D, NW, OUT, Q8, true, Q8 ? 8 : 32><<<units, threads, 0, stream>>>(a);
+  else if (Q8 && a.G <= 16) attn_row_kernel<D, NW, OUT, Q8, true, Q8 ? 16 : 32><<<units, threads, 0, stream>>>(a);
+  else attn_row_kernel<D, NW, OUT, Q8, true, 32><<<units, threads, 0, stream>>>(a);
   if (a.pieces > 1)
     attn_list_join_kernel<D, OUT><<<dim3((unsigned)cdiv((int64_t)a.B * a.G, RPB)), dim3(256), 0, stream>>>(a);
   return hipGetLastError();
