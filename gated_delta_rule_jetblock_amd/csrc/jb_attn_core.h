@@ -102,10 +102,9 @@ struct Args {
   const uint8_t *ks, *vs;  // a cache in 8 bits: exponents of its scales
   int64_t scale_stride;
   int units;       // attention over listed pages: a token's key heads, each a sequence of its own; else 0
-  // attn_row_kernel over the lists themselves: the batch they are for, and the pieces of a list
-  int seqs, seq_T, seq_pages, count, pieces;
-  const int *seq_cu, *seq_kv, *seq_table, *lists;
-  int64_t tokens;
+  // attn_row_kernel over the lists themselves: tokens a unit (2^gshift), and the pieces of a unit
+  int count, gshift, pieces;
+  const int* lists;
 
   // key head of the cache that sequence b's head kvh reads
   __device__ __forceinline__ int head(int b, int kvh) const { return units ? (int)((uint32_t)b % (uint32_t)units) : kvh; }
@@ -428,19 +427,42 @@ __device__ __forceinline__ float half_max(float x) {
 // its own, on memory: it is rare, and inline it took the registers of the loops.
 template <int D, int NB>
 __device__ __attribute__((noinline)) void add_odd_values(float* o, const float* s, const lds_char* lv, int j0, int p,
-                                                         int lw) {
+                                                         int p1, int lw) {
   using I = Img<D>;
   const int g = lane_id() >> 5;
   for (int r = 0; r < NB * 32; ++r) {
     const float mine = s[(r >> 5) * 16 + ((r & 31) >> 3) * 4 + (r & 3)], other = __shfl_xor(mine, 32, WAVE);
     const float w = ((r >> 2) & 1) == g ? mine : other;
-    if (j0 + r > p || j0 + r <= lw) continue;
+    if (j0 + r > (NB == 1 && r >= 16 ? p1 : p) || j0 + r <= lw) continue;
     for (int e = 0; e < D / 2; ++e) {
       const int d = 32 * (e >> 4) + 8 * ((e >> 2) & 3) + 4 * g + (e & 3);
       const uint32_t u = *(const lds_u16*)(lv + r * I::ROWB + (((d >> 3) ^ I::fv(r)) << 4) + (d & 7) * 2);
       const float v = __uint_as_float(u << 16);
       if (!isfinite(v)) o[e] = fmaf(w, v, o[e]);
     }
+  }
+}
+
+// whether a 16-byte aligned part of a V image holds a value that is not finite
+// (exponent all ones); clean_part sets those to 0
+__device__ __forceinline__ bool odd_bits(uint32_t u) {
+  return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ bool odd_part(const lds_char* v, int bytes) {
+  bool odd = false;
+#pragma unroll 4
+  for (int i = lane_id() * 16; i < bytes; i += 1024) {
+    const u4_t w = *(const lds_u4*)(v + i);
+    odd |= odd_bits(w[0]) || odd_bits(w[1]) || odd_bits(w[2]) || odd_bits(w[3]);
+  }
+  return __any(odd);
+}
+__device__ __forceinline__ void clean_part(lds_char* v, int bytes) {
+  for (int i = lane_id() * 4; i < bytes; i += 256) {
+    uint32_t u = *(const lds_u32*)(v + i);
+    if ((u & 0x7f80u) == 0x7f80u) u &= 0xffff0000u;
+    if ((u & 0x7f800000u) == 0x7f800000u) u &= 0xffffu;
+    *(lds_u32*)(v + i) = u;
   }
 }
 
@@ -458,11 +480,11 @@ template <int D> __device__ __forceinline__ bool odd_codes(const lds_char* v, ui
 }
 // (COLS queries a wave: o are D COLS / 64 accumulators, in 32 or 16 columns' order)
 template <int D, int COLS>
-__device__ __attribute__((noinline)) void add_odd_codes(float* o, const lds_char* v, uint32_t e, int j0, int p, int lw) {
+__device__ __attribute__((noinline)) void add_odd_codes(float* o, const lds_char* v, uint32_t e, int j0, int p, int p1, int lw) {
   using W = Raw8<D>;
   const int g = lane_id() / COLS;
   for (int r = 0; r < 32; ++r) {
-    if (j0 + r > p || j0 + r <= lw) continue;
+    if (j0 + r > (r >= 16 ? p1 : p) || j0 + r <= lw) continue;
     const bool all = (r < 16 ? (e >> 8) & 255u : e >> 24) == 255u;
     for (int i = 0; i < D * COLS / 64; ++i) {
       const int d = COLS == 32 ? 32 * (i >> 4) + 8 * ((i >> 2) & 3) + 4 * g + (i & 3) : 16 * (i >> 2) + 4 * g + (i & 3);
@@ -499,6 +521,7 @@ template <int D, bool Q8 = false> struct Wave {
   f16_t o[D / 32];  // O^T: o[db][i] is d = 32 db + 8 (i / 4) + 4 g + i % 4
   float m, l;       // m as the exponent base 2 subtracts it; l of this lane's half of the rows
   int p, lw;        // sees rows lw < j <= p
+  int p1;           // the same for rows 16 .. of a tile of 32 (p, but in lists of 16-row pages)
   int phi, lwlo;    // of the wave's real rows: the last row seen, and the least lw
 
   __device__ void init(const Args& a, const Seq& s, int kvh, int64_t r0) {
@@ -507,7 +530,7 @@ template <int D, bool Q8 = false> struct Wave {
     const int base = s.kv - s.T;
     const bool real = r < nr;
     const int i = real ? token_of(a, r) : 0, g = real ? (int)(r - (int64_t)i * a.G) : 0;
-    p = real ? base + i : -1;
+    p = p1 = real ? base + i : -1;
     lw = a.window ? p - a.window : -1;
     const int64_t last = min(r0 + 32, nr) - 1;
     phi = lwlo = -1;
@@ -633,7 +656,7 @@ template <int D, bool Q8 = false> struct Wave {
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const int j = j0 + 32 * n + 8 * (e >> 2) + 4 * g + (e & 3);
-        if (j > p || j <= lw) s[n][e] = -INFINITY;
+        if (j > (NB == 1 && e >= 8 ? p1 : p) || j <= lw) s[n][e] = -INFINITY;
       }
     const float ms = take_max<NB>(a, s);
 #pragma unroll
@@ -757,6 +780,58 @@ template <int D, bool Q8 = false> struct Wave {
       }
     }
   }
+  // A tile of listed pages, as codes or as bf16 (lk: K, then V; whole: every query sees all of
+  // it).  Masked weights are 0, but 0 times a NaN is not: `careful` looks for what is not
+  // finite first.
+  __device__ __forceinline__ void listed(const Args& a, lds_char* lk, uint32_t e, int j0, bool whole, bool careful) {
+    const int g = lane_id() >> 5;
+    lds_char* const lv = lk + (Q8 ? W8::TILE : 32 * D * 2);
+    f16_t s[1];
+    if constexpr (Q8) scores8(lk, e, s);
+    else scores<1>(lk, s);
+    if (!whole)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (j0 + 8 * (i >> 2) + 4 * g + (i & 3) > (i >= 8 ? p1 : p)) s[0][i] = -INFINITY;
+    __builtin_amdgcn_s_setprio(2);
+    const float ms = take_max<1>(a, s);
+    if (careful) {
+      if constexpr (Q8) {
+        e = without_odd(lv, e, j0);
+      } else if (odd_part(lv, 32 * D * 2)) {
+        f16_t x[1];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[0][i] = fast_exp2(fmaf(s[0][i], a.scale, -ms));
+        odd_values<1>(x, lv, j0);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        clean_part(lv, 32 * D * 2);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      }
+    }
+    if constexpr (Q8) values8<true>(a, lv, e, s, ms);
+    else values<1, true, true>(a, lv, s, ms);
+    __builtin_amdgcn_s_setprio(0);
+  }
+  __device__ __forceinline__ bool finite() const {
+    bool fine = isfinite(l);
+#pragma unroll
+    for (int i = 0; i < D / 2; ++i) fine &= isfinite(o[i >> 4][i & 15]);
+    return fine;
+  }
+  // NaN codes of V to the queries that see them, and out of the tile
+  __device__ __forceinline__ uint32_t without_odd(lds_char* v, uint32_t e, int j0) {
+    if (!odd_codes<D>(v, e)) return e;
+    float so[D / 2];
+#pragma unroll
+    for (int i = 0; i < D / 2; ++i) so[i] = o[i >> 4][i & 15];
+    add_odd_codes<D, 32>(so, v, e, j0, p, p1, lw);
+#pragma unroll
+    for (int i = 0; i < D / 2; ++i) o[i >> 4][i & 15] = so[i];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    e = clean_codes<D>(v, e);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    return e;
+  }
   // a tile that every query sees whole, and one that some see in part
   __device__ void full8(const Args& a, const lds_char* lk, uint32_t e) {
     f16_t s[1];
@@ -774,23 +849,13 @@ template <int D, bool Q8 = false> struct Wave {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int j = j0 + 8 * (i >> 2) + 4 * g + (i & 3);
-      if (j > p || j <= lw) s[0][i] = -INFINITY;
+      if (j > (i >= 8 ? p1 : p) || j <= lw) s[0][i] = -INFINITY;
     }
     const float ms = take_max<1>(a, s);
 #pragma unroll
     for (int k = 0; k < 2; ++k) weights<1>(a, s, ms, k);
     lds_char* const v = lk + W8::TILE;
-    if (odd_codes<D>(v, e)) {
-      float so[D / 2];
-#pragma unroll
-      for (int i = 0; i < D / 2; ++i) so[i] = o[i >> 4][i & 15];
-      add_odd_codes<D, 32>(so, v, e, j0, p, lw);
-#pragma unroll
-      for (int i = 0; i < D / 2; ++i) o[i >> 4][i & 15] = so[i];
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      e = clean_codes<D>(v, e);
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    }
+    e = without_odd(v, e, j0);
     values8<false>(a, v, e, s, 0.f);
   }
 
@@ -801,7 +866,7 @@ template <int D, bool Q8 = false> struct Wave {
     for (int e = 0; e < D / 2; ++e) so[e] = o[e >> 4][e & 15];
 #pragma unroll
     for (int e = 0; e < NB * 16; ++e) ss[e] = s[e >> 4][e & 15];
-    add_odd_values<D, NB>(so, ss, lv, j0, p, lw);
+    add_odd_values<D, NB>(so, ss, lv, j0, p, p1, lw);
 #pragma unroll
     for (int e = 0; e < D / 2; ++e) o[e >> 4][e & 15] = so[e];
   }
@@ -818,13 +883,13 @@ template <int D, int QR> struct Wave16 {
   bf16x8_t q[D / 32];  // d = D / 4 g + 8 k + e, so that a lane's codes of a row lie together
   f4_t o[D / 16];      // O^T: o[db][i] is d = 16 db + 4 g + i
   float m, l;
-  int p, lw, phi, lwlo;
+  int p, p1, lw, phi, lwlo;  // (as Wave's)
 
   __device__ void init(const Args& a, const Seq& s, int kvh, int64_t) {
     const int lane = lane_id(), r = lane & (QR - 1), nr = s.T * a.G, base = s.kv - s.T;
     const bool real = r < nr;
     const int i = real ? token_of(a, r) : 0, g = real ? r - i * a.G : 0;
-    p = real ? base + i : -1;
+    p = p1 = real ? base + i : -1;
     lw = a.window ? p - a.window : -1;
     phi = lwlo = -1;
     if (nr > 0) {
@@ -943,22 +1008,47 @@ template <int D, int QR> struct Wave16 {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int j = j0 + 16 * (i >> 2) + 4 * g + (i & 3);
-      if (j > p || j <= lw) s[i >> 2][i & 3] = -INFINITY;
+      if (j > (i >= 4 ? p1 : p) || j <= lw) s[i >> 2][i & 3] = -INFINITY;
     }
     weigh(a, s);
     lds_char* const v = lk + W8::TILE;
-    if (odd_codes<D>(v, e)) {
-      float so[D / 4];
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) so[i] = o[i >> 2][i & 3];
-      add_odd_codes<D, 16>(so, v, e, j0, p, lw);
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) o[i >> 2][i & 3] = so[i];
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      e = clean_codes<D>(v, e);
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    }
+    e = without_odd(v, e, j0);
     values(v, e, s);
+  }
+  // A tile of listed pages (whole: every query sees all of it).  Masked weights are 0, but 0
+  // times a NaN is not: `careful` looks for them first.
+  __device__ __forceinline__ void listed(const Args& a, lds_char* lk, uint32_t e, int j0, bool whole, bool careful) {
+    const int g = lane_id() >> 4;
+    f4_t s[2];
+    scores(lk, e, s);
+    if (!whole)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (j0 + 16 * (i >> 2) + 4 * g + (i & 3) > (i >= 4 ? p1 : p)) s[i >> 2][i & 3] = -INFINITY;
+    weigh(a, s);
+    lds_char* const v = lk + W8::TILE;
+    if (careful) e = without_odd(v, e, j0);
+    values(v, e, s);
+  }
+  __device__ __forceinline__ bool finite() const {
+    bool fine = isfinite(l);
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) fine &= isfinite(o[i >> 2][i & 3]);
+    return fine;
+  }
+  // NaN codes of V to the queries that see them, and out of the tile
+  __device__ __forceinline__ uint32_t without_odd(lds_char* v, uint32_t e, int j0) {
+    if (!odd_codes<D>(v, e)) return e;
+    float so[D / 4];
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) so[i] = o[i >> 2][i & 3];
+    add_odd_codes<D, 16>(so, v, e, j0, p, p1, lw);
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) o[i >> 2][i & 3] = so[i];
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    e = clean_codes<D>(v, e);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    return e;
   }
   // the rows of O to LDS
   __device__ __forceinline__ void stage(lds_char* st) const {
@@ -973,29 +1063,6 @@ template <int D, int QR> struct Wave16 {
     }
   }
 };
-
-// whether a 16-byte aligned part of a V image holds a value that is not finite
-// (exponent all ones); clean_part sets those to 0
-__device__ __forceinline__ bool odd_bits(uint32_t u) {
-  return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
-}
-__device__ __forceinline__ bool odd_part(const lds_char* v, int bytes) {
-  bool odd = false;
-#pragma unroll 4
-  for (int i = lane_id() * 16; i < bytes; i += 1024) {
-    const u4_t w = *(const lds_u4*)(v + i);
-    odd |= odd_bits(w[0]) || odd_bits(w[1]) || odd_bits(w[2]) || odd_bits(w[3]);
-  }
-  return __any(odd);
-}
-__device__ __forceinline__ void clean_part(lds_char* v, int bytes) {
-  for (int i = lane_id() * 4; i < bytes; i += 256) {
-    uint32_t u = *(const lds_u32*)(v + i);
-    if ((u & 0x7f80u) == 0x7f80u) u &= 0xffff0000u;
-    if ((u & 0x7f800000u) == 0x7f800000u) u &= 0xffffu;
-    *(lds_u32*)(v + i) = u;
-  }
-}
 
 // the cache rows [lo, hi) that queries r0 .. r1 (of one sequence) see, and the
 // part of their R-row tiles that piece `split` of `n` takes
@@ -1187,58 +1254,130 @@ __device__ __forceinline__ int steps_of(const Args& a, const Seq& s, int rows_a_
   return max((hi + rows_a_step - 1) / rows_a_step - lo / rows_a_step, 1);
 }
 
-// A list's unit: the first wave takes the entries that count to LDS (pages), as page indices
-// in order; returns the rows that the unit's queries see, -1 where no sequence owns the
-// token.  An entry counts if it is a page that the token sees and larger than every such
-// one before it.
-constexpr int MOST_LISTED = 2048;
-__device__ __forceinline__ int take_list(const Args& a, int unit, lds_int* pages, lds_int* found) {
-  const int lane = lane_id(), t = (uint32_t)unit / (uint32_t)a.units;
-  const int* list = a.lists + (int64_t)unit * a.count;
-  const bool first = threadIdx.x < 64;
-  int x = first && lane < a.count ? list[lane] : -1;  // on its way while the sequence is found
-  int b, all = a.seq_T;
-  int64_t tok0;
-  if (a.seq_cu) {
+// What a unit of listed pages reads.  A unit is one key head of 2^gshift tokens next to each
+// other (as many as 32 rows of queries hold): the pages that any of them lists are walked
+// once, in order, as rows of a sequence of their own, and each token sees those of its own
+// list.  An entry of a list counts if it is a page that the token sees and larger than every
+// such one before it.
+constexpr int MOST_LISTED = 2048;  // entries of a unit's lists together
+constexpr int MOST_MERGED = 4096;  // pages of a sequence where several tokens' lists are merged
+struct Listed {
+  int64_t tok0;  // first token, and how many
+  int T;
+  int p0;        // its row in the sequence's cache (negative: it sees none)
+  int n, whole;  // pages, and those before the first token's own: every token that lists one sees it whole
+  int tail;      // place in the sequence of the page behind those (the next one's is one more, if there is one)
+  int hi;        // rows
+};
+
+// one wave: the entries that count of a list, each to take(entry, its number)
+template <typename F> __device__ __forceinline__ int walk_list(const Args& a, const int* list, int own, F take) {
+  const int lane = lane_id();
+  int last = -1, n = 0;  // the largest so far, and how many
+  for (int k = 0; k < a.count; k += 64) {
+    const int x = k + lane < a.count ? list[k + lane] : -1;
+    const int mine = x >= 0 && x <= own ? x : -1;
+    int most = mine;  // of this lane and those before it
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(most, o, WAVE);
+      if (lane >= o) most = max(most, u);
+    }
+    const int u = __shfl_up(most, 1, WAVE);
+    const bool counts = mine > max(lane ? u : -1, last);
+    const uint64_t all = __builtin_amdgcn_ballot_w64(counts);
+    if (counts) take(mine, n + __builtin_popcountll(all & ((1ull << lane) - 1)));
+    n += __builtin_popcountll(all);
+    last = max(last, __builtin_amdgcn_readlane(most, 63));
+  }
+  return n;
+}
+
+// Unit `slot`'s tokens (T = 0: nobody's), and its pages and their tokens (bits) to LDS.
+// bitmap: MOST_MERGED words of LDS, free afterwards.
+__device__ __forceinline__ Listed take_lists(const Args& a, uint32_t slot, int kvh, lds_int* pages, lds_u16* masks,
+                                             lds_u32* bitmap, lds_int* found) {
+  const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  Listed u = {};
+  int b, all = a.T;
+  int64_t nth;
+  if (a.cu) {
+    // sequence j's units start at cu[j] >> gshift + j, which leaves room for all of them
+    auto start = [&](int64_t from, int j) { return (min(max(from, (int64_t)0), a.total) >> a.gshift) + j; };
     int n = 0;
-    for (int i = 0; i < a.seqs; i += blockDim.x) {
-      const int c = __syncthreads_count(i + (int)threadIdx.x < a.seqs && a.seq_cu[i + threadIdx.x] <= t);
+    for (int i = 0; i < a.B; i += blockDim.x) {
+      const int j = i + threadIdx.x, c = __syncthreads_count(j < a.B && start(a.cu[j], j) <= slot);
       n += c;
       if (c < (int)blockDim.x) break;
     }
     b = uniform(max(n - 1, 0));
-    clamp_span(((const_int_p)a.seq_cu)[b], ((const_int_p)a.seq_cu)[b + 1], 0x7fffffff, a.tokens, tok0, all);
+    nth = slot - start(((const_int_p)a.cu)[b], b);
+    clamp_span(((const_int_p)a.cu)[b], ((const_int_p)a.cu)[b + 1], 0x7fffffff, a.total, u.tok0, all);
   } else {
-    b = (uint32_t)t / (uint32_t)a.seq_T;
-    tok0 = (int64_t)b * a.seq_T;
+    const uint32_t per = ((uint32_t)a.T + (1u << a.gshift) - 1) >> a.gshift;
+    b = slot / per;
+    nth = slot - b * per;
+    u.tok0 = (int64_t)b * a.T;
   }
-  const int cap = (int)min((int64_t)a.seq_pages << a.pshift, (int64_t)0x7fffffff);
-  const int64_t i = t - tok0;
-  if (i < 0 || i >= min(all, a.seq_T)) return -1;  // (the same for all threads)
-  const int p = min(max(((const_int_p)a.seq_kv)[b], 0), cap) - all + (int)i, own = p >> a.pshift;
-  if (first) {
-    const int* table = a.seq_table + (int64_t)b * a.seq_pages;
-    int last = -1, n = 0;  // the largest so far, and how many
-    for (int k = 0; k < a.count; k += 64) {
-      if (k) x = k + lane < a.count ? list[k + lane] : -1;
-      const int mine = x >= 0 && x <= own ? x : -1;
-      int most = mine;  // of this lane and those before it
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(most, o, WAVE);
-        if (lane >= o) most = max(most, u);
-      }
-      const int u = __shfl_up(most, 1, WAVE);
-      const bool take = mine > max(lane ? u : -1, last);
-      const uint64_t taken = __builtin_amdgcn_ballot_w64(take);
-      if (take) pages[n + __builtin_popcountll(taken & ((1ull << lane) - 1))] = table[mine];
-      n += __builtin_popcountll(taken);
-      last = max(last, __builtin_amdgcn_readlane(most, 63));
+  const int i0 = (int)(nth << a.gshift);
+  if (nth < 0 || i0 < 0 || i0 >= min(all, a.T)) return u;  // (the same for all threads)
+  u.T = min(min(all, a.T) - i0, 1 << a.gshift);
+  u.tok0 += i0;
+  const int cap = (int)min((int64_t)a.max_pages << a.pshift, (int64_t)0x7fffffff);
+  u.p0 = min(max(((const_int_p)a.kv_lens)[b], 0), cap) - all + i0;
+  const int own = u.p0 >> a.pshift, last = (u.p0 + u.T - 1) >> a.pshift;
+  const int* table = a.table + (int64_t)b * a.max_pages;
+  const int* list = a.lists + (u.tok0 * a.Hkv + kvh) * a.count;
+  const int64_t step = (int64_t)a.Hkv * a.count;  // to the next token's
+  // rows up to the last that a token sees
+  auto rows_of = [&](const Listed& u) {
+    if (u.n == u.whole) return u.n << a.pshift;
+    const int page = u.tail + u.n - u.whole - 1;  // the last one's place
+    return ((u.n - 1) << a.pshift) + min(u.p0 + u.T - (page << a.pshift), 1 << a.pshift);
+  };
+  if (a.gshift == 0) {
+    if (wave == 0) {
+      if (lane == 0) found[1] = 0;
+      const int n = walk_list(a, list, own, [&](int page, int i) {
+        pages[i] = table[page], masks[i] = 1;
+        if (page == own) found[1] = 1;  // (the last)
+      });
+      if (lane == 0) found[0] = n;
     }
-    if (lane == 0) *found = n && last == own ? ((n - 1) << a.pshift) + (p & ((1 << a.pshift) - 1)) + 1 : n << a.pshift;
+    __syncthreads();
+    u.n = uniform(found[0]), u.whole = u.n - uniform(found[1]), u.tail = own;
+    u.hi = rows_of(u);
+    return u;
   }
+  const int seen = last + 1;  // pages
+  for (int i = threadIdx.x; i < seen; i += blockDim.x) bitmap[i] = 0u;
   __syncthreads();
-  return uniform(*found);
+  for (int t = wave; t < u.T; t += blockDim.x / 64)
+    walk_list(a, list + t * step, (u.p0 + t) >> a.pshift, [&](int page, int) {
+      __hip_atomic_fetch_or(bitmap + page, 1u << t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    });
+  __syncthreads();
+  int n = 0, whole = 0;
+  for (int i = 0; i < seen; i += blockDim.x) {
+    const int page = i + threadIdx.x;
+    const uint32_t m = page < seen ? bitmap[page] : 0u;
+    const uint64_t some = __builtin_amdgcn_ballot_w64(m != 0);
+    if (lane == 0) found[wave] = __builtin_popcountll(some);
+    const int before_own = __syncthreads_count(m != 0 && page < own);
+    int at = n + __builtin_popcountll(some & ((1ull << lane) - 1));
+    for (int w = 0; w < (int)blockDim.x / 64; ++w) {
+      if (w < wave) at += found[w];
+      n += found[w];
+    }
+    whole += before_own;
+    if (m) pages[at] = table[page], masks[at] = (uint16_t)m;
+    __syncthreads();
+  }
+  u.n = uniform(n), u.whole = uniform(whole);
+  u.tail = uniform(own >= 0 && bitmap[max(own, 0)] ? own : own + 1);
+  u.hi = rows_of(u);
+  __syncthreads();  // (the bitmap is read)
+  return u;
 }
 
 // LIST: a workgroup takes a piece of the pages listed for one (token, key head), which are a
@@ -1253,29 +1392,30 @@ __global__ __launch_bounds__(NW * 64, Q8 ? 2 : 1) void attn_row_kernel(Args a) {
   __shared__ int64_t found[2];
   __shared__ int sums[NW];
   __shared__ int listed[LIST ? MOST_LISTED + 64 : 1];  // (64 entries are read at a time)
+  __shared__ uint16_t listing[LIST ? MOST_LISTED : 1];  // and the tokens that list them
+  static_assert(!LIST || RING >= MOST_MERGED * 4, "the lists are merged there");
   const lds_int* const list = LIST ? (const lds_int*)listed : nullptr;
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
   int b;
   int64_t at, end, start;  // this run's steps, and the first sequence's first one
   int64_t run_steps = 0;
-  int rows = 0, piece = 0;  // LIST: of the unit
+  Listed unit = {};
+  int piece = 0, unit_head = 0;
   if constexpr (LIST) {
     // Neighbouring tokens list much the same pages: each of the 8 dies, which take
     // workgroups in turn, has consecutive units.
     const uint32_t each = gridDim.x / 8, more = gridDim.x % 8, die = blockIdx.x % 8;
-    const uint32_t at_die = die * each + min(die, more) + blockIdx.x / 8;
-    b = (int)(at_die / (uint32_t)a.pieces);
-    piece = at_die - b * (uint32_t)a.pieces;
-    rows = take_list(a, b, (lds_int*)listed, (lds_int*)sums);
-    if (rows < 0) {
-      if (a.pieces > 1 && (int)threadIdx.x < a.G)
-        a.run_ml[((int64_t)piece * a.B + b) * a.G + threadIdx.x] = make_float2(-INFINITY, -1.f);
-      return;
-    }
-    const int n_steps = max((rows + STEP - 1) / STEP, 1);
+    const uint32_t i = die * each + min(die, more) + blockIdx.x / 8, at_unit = i / (uint32_t)a.pieces;
+    const uint32_t slot = at_unit / (uint32_t)a.Hkv;
+    piece = i - at_unit * (uint32_t)a.pieces;
+    unit_head = at_unit - slot * (uint32_t)a.Hkv;
+    unit = take_lists(a, slot, unit_head, (lds_int*)listed, (lds_u16*)listing, (lds_u32*)ring, (lds_int*)sums);
+    if (unit.T == 0) return;
+    const int steps = max((unit.hi + STEP - 1) / STEP, 1);
+    b = 0;
     start = 0;
-    at = (int64_t)n_steps * piece / a.pieces;
-    end = (int64_t)n_steps * (piece + 1) / a.pieces;
+    at = (int64_t)steps * piece / a.pieces;
+    end = (int64_t)steps * (piece + 1) / a.pieces;
   } else if (a.direct) {  // many units: each is a run
     b = blockIdx.x / (unsigned)a.Hkv;
     const int n = steps_of(a, seq_of(a, b), STEP);
@@ -1333,13 +1473,13 @@ __global__ __launch_bounds__(NW * 64, Q8 ? 2 : 1) void attn_row_kernel(Args a) {
   constexpr int NT = 4 * (Q8 ? LoaderRaw8<D, NW>::N : Loader<D>::N);  // transfers a tile
   lds_char* const base = (lds_char*)ring + wave * 2 * TILE;
   for (int seg = 0; (LIST || at < end) && b < a.B; seg = 1) {
-    const Seq s = LIST ? Seq{b, 1, rows} : seq_of(a, b);
-    const int steps = LIST ? max((rows + STEP - 1) / STEP, 1) : steps_of(a, s, STEP);
+    const Seq s = LIST ? Seq{unit.tok0, unit.T, unit.hi} : seq_of(a, b);
+    const int steps = LIST ? max((unit.hi + STEP - 1) / STEP, 1) : steps_of(a, s, STEP);
     if (steps == 0) {  // (only behind a sequence that has some)
       ++b;
       continue;
     }
-    const int kvh = LIST ? 0 : uniform((int)quotient(at - start, 1.0 / steps)), s0 = uniform((int)(at - start - (int64_t)kvh * steps));
+    const int kvh = LIST ? unit_head : uniform((int)quotient(at - start, 1.0 / steps)), s0 = LIST ? (int)at : uniform((int)(at - start - (int64_t)kvh * steps));
     const int s1 = uniform((int)min((int64_t)steps, s0 + end - at));
     if (kvh >= a.Hkv) break;  // (lengths that changed meanwhile)
     const int nr = (int)(s.T * a.G);
@@ -1349,10 +1489,35 @@ __global__ __launch_bounds__(NW * 64, Q8 ? 2 : 1) void attn_row_kernel(Args a) {
     const int n0 = x.lo / STEP * NW;
     x.t0 = max(n0 + s0 * NW, x.lo / R);
     x.t1 = min(n0 + s1 * NW, (x.hi + R - 1) / R);
+    // LIST: a second time, carefully, where the first leaves something that is not finite
+    bool careful = false;
+  again:
     std::conditional_t<QR == 32, Wave<D, Q8>, Wave16<D, QR>> w;
     w.init(a, s, kvh, 0);
-    const Order ord(a, s, x, 0, nr - 1, R);
+    Order ord(a, s, x, 0, nr - 1, R);
+    if constexpr (LIST) ord.f0 = ord.t0, ord.nf = 0;  // (in order)
     const int nf = ord.nf, nt = ord.nt;
+    // LIST: what this lane's query sees of tile t goes into w.p and w.p1; whether all see all of it
+    int token = 0;
+    if constexpr (LIST) {
+      const int r = lane & (QR - 1);
+      token = r < nr ? token_of(a, r) : -1;
+      w.phi = 0x7fffffff;
+    }
+    auto whole_tile = [&](int t) {
+      const int j0 = t * R, i0 = j0 >> a.pshift, i1 = (j0 + 16) >> a.pshift;
+      const int m0 = uniform(listing[i0]), m1 = i1 < unit.n ? uniform(listing[i1]) : 0;
+      if (i1 < unit.whole && (m0 & m1) == (1 << unit.T) - 1) {
+        w.p = w.p1 = 0x3fffffff;
+        return true;
+      }
+      auto last = [&](int i, int m) {  // the last row of page i that the query sees, as a row of all
+        if (token < 0 || !(m >> token & 1)) return -1;
+        return i < unit.whole ? 0x3fffffff : unit.p0 + token - ((unit.tail + i - unit.whole - i) << a.pshift);
+      };
+      w.p = last(i0, m0), w.p1 = last(i1, m1);
+      return false;
+    };
     // tile n has landed, and the wave's next one is on its way into the other buffer
     int par = 0;
     if constexpr (Q8) {
@@ -1377,6 +1542,13 @@ __global__ __launch_bounds__(NW * 64, Q8 ? 2 : 1) void attn_row_kernel(Args a) {
       w.arrived();
       if (wave < nt) issue(wave, 0);
       int n = wave;
+      if constexpr (LIST) {
+        for (; n < nt; n += NW) {
+          const bool whole = whole_tile(ord.tile(n));
+          lds_char* const k = next(n);
+          w.listed(a, k, e, ord.tile(n) * R, whole, careful);
+        }
+      }
       for (; n < nf; n += NW) w.full8(a, next(n), e);
       for (; n < nt; n += NW) w.part8(a, next(n), e, ord.tile(n) * R);
     } else {
@@ -1407,6 +1579,11 @@ __global__ __launch_bounds__(NW * 64, Q8 ? 2 : 1) void attn_row_kernel(Args a) {
         w.template full<1, true>(a, k, k + IMG);
       }
       for (; n < nt; n += NW) {
+        if constexpr (LIST) {
+          const bool whole = whole_tile(ord.tile(n));
+          w.listed(a, next(n), 0, ord.tile(n) * R, whole, careful);
+          continue;
+        }
         lds_char* const k = next(n);
         lds_char* const v = k + IMG;
         f16_t s1[1];
@@ -1422,6 +1599,11 @@ __global__ __launch_bounds__(NW * 64, Q8 ? 2 : 1) void attn_row_kernel(Args a) {
       }
     }
     // join the waves: O and (m, l) of each in LDS
+    if constexpr (LIST)
+      if (!careful && __syncthreads_or(!w.finite())) {
+        careful = true;
+        goto again;
+      }
     constexpr int COLS = QR == 32 ? 32 : 16;
     const int c = lane & (COLS - 1), g = lane / COLS;
     const float l = w.sum();
@@ -1442,7 +1624,7 @@ __global__ __launch_bounds__(NW * 64, Q8 ? 2 : 1) void attn_row_kernel(Args a) {
       const int last = (int)min(quotient(at + steps - 1, 1.0 / run_steps), (int64_t)gridDim.x - 1);
       shared = {b, kvh, last - (int)blockIdx.x, seg};
     }
-    const int64_t part = LIST ? ((int64_t)piece * a.B + b) * a.G : (2 * (int64_t)blockIdx.x + seg) * 32;
+    const int64_t part = (2 * (int64_t)blockIdx.x + seg) * 32;
     constexpr int LPR = D / 4;
     for (int i = threadIdx.x / LPR; i < nr; i += NTHR / LPR) {
       const int d = (threadIdx.x % LPR) * 4;
@@ -1461,8 +1643,9 @@ __global__ __launch_bounds__(NW * 64, Q8 ? 2 : 1) void attn_row_kernel(Args a) {
         sum += v * f;
       }
       if (!whole) {
-        if (d == 0) a.run_ml[part + i] = make_float2(m, lt);
-        *reinterpret_cast<f4_t*>(a.run_o + (part + i) * D + d) = sum;
+        const int64_t to = LIST ? piece * a.total * a.H + out_row(a, s, kvh, i) : part + i;
+        if (d == 0) a.run_ml[to] = make_float2(m, lt);
+        *reinterpret_cast<f4_t*>(a.run_o + to * D + d) = sum;
       } else {
         const int64_t to = out_row(a, s, kvh, i);
         const float f = lt == 0.f ? 0.f : 1.f / lt;
@@ -1531,18 +1714,31 @@ __global__ __launch_bounds__(256) void attn_row_join_kernel(Args a, int rows) {
   if (sg == 0) x.template store<OUT, D>(a, out_row(a, s, u.kvh, r), d4 * 4);
 }
 
-// Adds up the pieces of every (token, key head)'s list, D / 4 lanes a row.
+// Adds up the pieces of every row of o that is of a sequence's token, D / 4 lanes a row.
 template <int D, typename OUT>
 __global__ __launch_bounds__(256) void attn_list_join_kernel(Args a) {
   constexpr int LPR = D / 4, RPB = 256 / LPR;
-  const int64_t rows = (int64_t)a.B * a.G, row = (int64_t)blockIdx.x * RPB + threadIdx.x / LPR;
+  const int64_t rows = a.total * a.H, row0 = (int64_t)blockIdx.x * RPB, row = row0 + threadIdx.x / LPR;
   const int d = threadIdx.x % LPR * 4;
+  if (a.cu) {
+    const int64_t t0 = row0 / a.H, t = row / a.H;
+    int n = 0;
+    for (int i = 0; i < a.B; i += 256) {
+      const int c = __syncthreads_count(i + (int)threadIdx.x < a.B && a.cu[i + threadIdx.x] <= t0);
+      n += c;
+      if (c < 256) break;
+    }
+    int b = max(n - 1, 0), all;
+    while (b + 1 < a.B && a.cu[b + 1] <= t) ++b;
+    int64_t tok0;
+    clamp_span(a.cu[b], a.cu[b + 1], 0x7fffffff, a.total, tok0, all);
+    if (t < tok0 || t - tok0 >= min(all, a.T)) return;
+  }
   if (row >= rows) return;
   Sum x;
 #pragma unroll 4
   for (int n = 0; n < a.pieces; ++n) {
     const float2 ml = a.run_ml[n * rows + row];
-    if (ml.y < 0.f) return;  // nobody's token
     x.add(ml.x, ml.y, *reinterpret_cast<const f4_t*>(a.run_o + (n * rows + row) * D + d));
   }
   x.template store<OUT, D>(a, row, d);
@@ -1964,8 +2160,7 @@ template <bool Q8> hipError_t run(const AttnCall& c, hipStream_t stream) {
   a.kv_lens = c.kv_lens, a.table = c.page_table;
   a.q = c.q, a.k = c.k_cache, a.v = c.v_cache, a.o = c.o, a.lse = c.lse;
   a.ks = c.k_scales, a.vs = c.v_scales, a.scale_stride = c.scale_stride, a.units = c.units;
-  a.seqs = a.seq_T = a.seq_pages = a.count = a.pieces = 0;
-  a.seq_cu = a.seq_kv = a.seq_table = a.lists = nullptr, a.tokens = 0;
+  a.count = a.gshift = a.pieces = 0, a.lists = nullptr;
   const Layout w = layout(c, p);
   char* ws = static_cast<char*>(c.workspace);
   a.part_o = reinterpret_cast<float*>(ws + w.part_o);
@@ -1990,10 +2185,24 @@ template <bool Q8> hipError_t run(const AttnCall& c, hipStream_t stream) {
 // fit LDS.  (Others go through tables in memory and the kernels above.)
 bool list_rows(const BlockCall& b) { return b.io == IO_BF16 && b.H / b.Hkv <= 32 && b.count <= MOST_LISTED; }
 
-// Pieces of a list: the rounds of workgroups take the steps of the longest list and some 3
-// steps' worth of start and end each; a join is worth 8.
+// Tokens of a unit (log2): as many as fill 32 rows, where lists and sequences fit.
+int list_gshift(const BlockCall& b) {
+  const int G = b.H / b.Hkv;
+  int g = 0;
+  while (b.max_pages <= MOST_MERGED && g < 4 && G << (g + 1) <= 32 && (int64_t)b.count << (g + 1) <= MOST_LISTED &&
+         1 << g < b.T)
+    ++g;
+  return g;
+}
+int64_t list_units(const BlockCall& b) {
+  const int g = list_gshift(b);
+  return (b.packed ? (b.total >> g) + b.B : (int64_t)b.B * cdiv(b.T, 1 << g)) * b.Hkv;
+}
+
+// Pieces of a unit's pages: the rounds of workgroups take the steps of the longest list and
+// some 3 steps' worth of start and end each; a join is worth 8.
 int list_pieces(const BlockCall& b) {
-  const int64_t units = b.total * b.Hkv, hold = b.D == 64 || b.bits8 ? 512 : 256, step = 32 * row_waves(b.D);
+  const int64_t units = list_units(b), hold = b.D == 64 || b.bits8 ? 512 : 256, step = 32 * row_waves(b.D);
   const int64_t steps = cdiv((int64_t)std::min(b.count, b.max_pages) * b.page, step);
   int64_t best = 0;
   int pieces = 1;
@@ -2008,37 +2217,37 @@ size_t list_rows_bytes(const BlockCall& b) {
   return list_pieces(b) == 1 ? 0 : a256(rows * b.D * sizeof(float)) + a256(rows * sizeof(float2));
 }
 
-template <int D, typename OUT, bool Q8> hipError_t launch_lists(const Args& a, hipStream_t stream) {
+template <int D, typename OUT, bool Q8> hipError_t launch_lists(const Args& a, int64_t units, hipStream_t stream) {
   constexpr int NW = row_waves(D), RPB = 256 / (D / 4);
-  const dim3 units((unsigned)a.B * a.pieces), threads(NW * 64);
-  if (Q8 && a.G <= 8) attn_row_kernel<D, NW, OUT, Q8, true, Q8 ? 8 : 32><<<units, threads, 0, stream>>>(a);
-  else if (Q8 && a.G <= 16) attn_row_kernel<D, NW, OUT, Q8, true, Q8 ? 16 : 32><<<units, threads, 0, stream>>>(a);
-  else attn_row_kernel<D, NW, OUT, Q8, true, 32><<<units, threads, 0, stream>>>(a);
+  const dim3 grid((unsigned)(units * a.pieces)), threads(NW * 64);
+  const int rows = a.G << a.gshift;
+  if (Q8 && rows <= 8) attn_row_kernel<D, NW, OUT, Q8, true, Q8 ? 8 : 32><<<grid, threads, 0, stream>>>(a);
+  else if (Q8 && rows <= 16) attn_row_kernel<D, NW, OUT, Q8, true, Q8 ? 16 : 32><<<grid, threads, 0, stream>>>(a);
+  else attn_row_kernel<D, NW, OUT, Q8, true, 32><<<grid, threads, 0, stream>>>(a);
   if (a.pieces > 1)
-    attn_list_join_kernel<D, OUT><<<dim3((unsigned)cdiv((int64_t)a.B * a.G, RPB)), dim3(256), 0, stream>>>(a);
+    attn_list_join_kernel<D, OUT><<<dim3((unsigned)cdiv(a.total * a.H, RPB)), dim3(256), 0, stream>>>(a);
   return hipGetLastError();
 }
 
 template <bool Q8> hipError_t run_lists(const AttnCall& c, const BlockCall& b, hipStream_t stream) {
   Args a = {};
-  a.units = b.Hkv, a.G = b.H / b.Hkv;
-  a.B = (int)(b.total * b.Hkv), a.T = 1, a.H = a.G, a.Hkv = 1, a.total = a.B, a.direct = true;
-  a.pshift = __builtin_ctz((unsigned)b.page), a.num_pages = b.num_pages;
+  a.B = b.B, a.T = b.T, a.H = b.H, a.Hkv = b.Hkv, a.G = b.H / b.Hkv, a.total = b.total, a.direct = true;
+  a.pshift = __builtin_ctz((unsigned)b.page), a.max_pages = b.max_pages, a.num_pages = b.num_pages;
   a.q_stride = b.q_stride, a.page_stride = b.page_stride, a.scale_stride = c.scale_stride;
+  a.cu = b.packed ? b.cu_seqlens : nullptr, a.kv_lens = b.kv_lens, a.table = b.page_table;
   a.q = c.q, a.k = c.k_cache, a.v = c.v_cache, a.o = c.o, a.lse = c.lse, a.ks = c.k_scales, a.vs = c.v_scales;
   a.scale = c.scale * 1.4426950408889634f;
   a.inv_g = 1.0 / a.G;
-  a.seqs = b.B, a.seq_T = b.T, a.seq_pages = b.max_pages, a.count = b.count, a.pieces = list_pieces(b);
-  a.seq_cu = b.packed ? b.cu_seqlens : nullptr, a.seq_kv = b.kv_lens, a.seq_table = b.page_table, a.lists = b.blocks;
-  a.tokens = b.total;
+  a.count = b.count, a.gshift = list_gshift(b), a.pieces = list_pieces(b), a.lists = b.blocks;
   const size_t rows = (size_t)b.total * b.H * a.pieces;
   a.run_o = static_cast<float*>(c.workspace);
   a.run_ml = reinterpret_cast<float2*>(static_cast<char*>(c.workspace) + a256(rows * b.D * sizeof(float)));
   const bool bf = c.out == IO_BF16;
+  const int64_t units = list_units(b);
   switch (b.D) {
-    case 64: return bf ? launch_lists<64, bf16_t, Q8>(a, stream) : launch_lists<64, float, Q8>(a, stream);
-    case 128: return bf ? launch_lists<128, bf16_t, Q8>(a, stream) : launch_lists<128, float, Q8>(a, stream);
-    case 256: return bf ? launch_lists<256, bf16_t, Q8>(a, stream) : launch_lists<256, float, Q8>(a, stream);
+    case 64: return bf ? launch_lists<64, bf16_t, Q8>(a, units, stream) : launch_lists<64, float, Q8>(a, units, stream);
+    case 128: return bf ? launch_lists<128, bf16_t, Q8>(a, units, stream) : launch_lists<128, float, Q8>(a, units, stream);
+    case 256: return bf ? launch_lists<256, bf16_t, Q8>(a, units, stream) : launch_lists<256, float, Q8>(a, units, stream);
   }
   return hipErrorInvalidValue;
 }

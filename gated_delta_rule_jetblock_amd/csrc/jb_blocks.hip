@@ -800,7 +800,7 @@ hipError_t launch_block_select(const BlockCall& c, hipStream_t stream) {
 }
 
 int64_t attn_blocks_workgroups(const BlockCall& c, const AttnCall& attn) {
-  if (attn_lists_fit(c)) return c.total * c.Hkv * 32;  // at most 32 pieces, or rows in the join
+  if (attn_lists_fit(c)) return attn_lists_workgroups(c);
   return std::max(attn_workgroups(listed(c, attn)), cdiv(c.total * c.Hkv, 4));
 }
 
