@@ -636,9 +636,12 @@ template <int D, bool Q8 = false> struct Wave {
   // products with V, mixed with the other weights, before its products with K
   // (at equal priority 2K tokens on 64K rows take 787 us and an 8K prompt 289; so
   // 755 and 261 on the same card).
-  template <int NB, bool TWO> __device__ void full(const Args& a, const lds_char* lk, const lds_char* lv) {
+  // between: work to be done behind the products with K
+  template <int NB, bool TWO, typename F>
+  __device__ __forceinline__ void full(const Args& a, const lds_char* lk, const lds_char* lv, F between) {
     f16_t s[NB];
     scores<NB>(lk, s);
+    between();
     __builtin_amdgcn_s_setprio(2);
     const float ms = take_max<NB>(a, s);
     values<NB, true, TWO>(a, lv, s, ms);
@@ -1183,16 +1186,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
   if constexpr (Q8)
     if (nt > 0) ld.fetch(a, tile(0) * R + wave * 16, x.hi);
   if (nt > 0) issue(0);
-  auto next = [&](int n) {
+  auto next = [&](int n, bool more = true) {
     // every wave's rows of tile n have landed, and every wave has left tile n - 1
     if constexpr (Q8) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (n + 1 < nt) issue(n + 1);
+    if (more && n + 1 < nt) issue(n + 1);
     return base + (n & 1) * 2 * IMG;
   };
   for (int n = 0; n < nf; ++n) {
-    const lds_char* k = next(n);
-    w.template full<2, TWO>(a, k, k + IMG);
+    const lds_char* k = next(n, !Q8);
+    w.template full<2, TWO>(a, k, k + IMG, [&] {
+      if (Q8 && n + 1 < nt) issue(n + 1);
+    });
   }
   for (int n = nf; n < nt; ++n) {
     lds_char* const k = next(n);
@@ -1576,7 +1581,7 @@ __global__ __launch_bounds__(NW * 64, Q8 ? 2 : 1) void attn_row_kernel(Args a) {
       int n = wave;
       for (; n < nf; n += NW) {
         const lds_char* k = next(n);
-        w.template full<1, true>(a, k, k + IMG);
+        w.template full<1, true>(a, k, k + IMG, [] {});
       }
       for (; n < nt; n += NW) {
         if constexpr (LIST) {
@@ -2200,14 +2205,16 @@ int64_t list_units(const BlockCall& b) {
 }
 
 // Pieces of a unit's pages: the rounds of workgroups take the steps of the longest list and
-// some 3 steps' worth of start and end each; a join is worth 8.
+// some 3 steps' worth of start and end each; a join is worth 3.5 and 2 more for each piece.
+// 64 decode steps over 32 pages of 64 rows (128 units): 1 piece 22.0 us, 2 19.6, 4 20.9, 8
+// 25.8; one over 16 pages 14.8, 17.2, 18.1, 17.2.
 int list_pieces(const BlockCall& b) {
   const int64_t units = list_units(b), hold = b.D == 64 || b.bits8 ? 512 : 256, step = 32 * row_waves(b.D);
   const int64_t steps = cdiv((int64_t)std::min(b.count, b.max_pages) * b.page, step);
   int64_t best = 0;
   int pieces = 1;
   for (int n = 1; n <= 32 && n <= steps; ++n) {
-    const int64_t t = cdiv(units * n, hold) * (cdiv(steps, n) + 3) + (n > 1 ? 8 : 0);
+    const int64_t t = 2 * cdiv(units * n, hold) * (cdiv(steps, n) + 3) + (n > 1 ? 7 + 4 * n : 0);
     if (n == 1 || t < best) best = t, pieces = n;
   }
   return pieces;
