@@ -443,3 +443,51 @@ def test_streams_and_graphs(jb):
         assert torch.equal(out["o"], want["o"]) and torch.equal(out["lse"], want["lse"])
         for a, b in zip(own, theirs):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_cache_past_32_bit_offsets(jb):
+    """Pages and scales more than 2^32 bytes apart from the pool's start: append, then attention."""
+    new, kv, H, Hkv, D, page = [3, 1], [40, 600], 4, 2, 64, 16
+    x = append_inputs(new, kv, H, Hkv, D, page, BF, seed=40)
+    P, far = len(x["k_cache"]), 1 << 27
+    pools = [torch.empty(P * far, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    caches = [p.as_strided((P, Hkv, page, D), (far, page * D, D, 1)) for p in pools]
+    scales = [p.as_strided((P, Hkv, page // 16), (far, page // 16, 1), 1 << 26) for p in pools]
+    assert P * far > 1 << 32
+    for t, name in zip(caches + scales, ("k_cache", "v_cache", "k_scales", "v_scales")):
+        t.copy_(x[name].view(torch.uint8))
+    g = on_gpu({n: x[n] for n in ("q", "k", "v", "wq", "wk", "table", "kv", "cu")})
+    f = frequencies(D)
+    views = (caches[0].view(E4M3), caches[1].view(E4M3), scales[0].view(E8M0), scales[1].view(E8M0))
+    r = jb.qk_norm_rope_paged8(g["q"], g["k"], g["v"], *views, g["table"], g["kv"], f.cuda(), g["wq"], g["wk"],
+                               cu_seqlens=g["cu"])
+    torch.cuda.synchronize()
+    check_append(x, {n: t if n == "q" else t.view(torch.uint8).contiguous().view(t.dtype) for n, t in r.items()}, new, kv, f)
+    o = jb.attn_paged8(r["q"], *views, g["table"], g["kv"], cu_seqlens=g["cu"], want_lse=True)
+    torch.cuda.synchronize()
+    held = dict(x, q=r["q"].cpu(), k_cache=torch.from_numpy(ref8.dequantise(*(codes_of(t.contiguous()) for t in (caches[0], scales[0])))),
+                v_cache=torch.from_numpy(ref8.dequantise(*(codes_of(t.contiguous()) for t in (caches[1], scales[1])))))
+    strict(held, o, new, kv)
+
+
+@pytest.mark.parametrize("G", [1, 3, 8, 9, 16, 17, 32])
+def test_every_width_of_the_decode_kernels(jb, G):
+    """Queries to a key head on both sides of 8, 16 and 32 columns, windows and single rows too."""
+    kv = [1, 40, 333, 2000]
+    for T, window in ((1, 0), (1, 50), (2, 0)):
+        d, d8 = batch8([T] * 4, kv, 2 * G, 2, 128, 16, BF, seed=G + T, packed=False)
+        for out in (BF, F32):
+            strict(d, call(jb, d8, window=window, out_dtype=out), [T] * 4, kv, window)
+
+
+def test_a_second_stream_and_workspaces_of_their_own(jb):
+    """Two calls that run at the same time, each on a stream of its own."""
+    d, d8 = batch8([1] * 4, [3000, 5, 800, 64], 12, 2, 128, 64, BF, seed=50, packed=False)
+    g = on_gpu(d8)
+    args = (g["q"][:, 0], g["k_cache"], g["v_cache"], g["k_scales"], g["v_scales"], g["table"], g["kv"])
+    want = jb.attn_paged8(*args)["o"]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [jb.attn_paged8(*args, stream=s if i else s.cuda_stream)["o"] for i, s in enumerate(streams) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(want, o) for o in got)

@@ -415,3 +415,109 @@ def test_another_stream(jb):
     o2 = jb.attn_blocks(g["q"], g["k_cache"], g["v_cache"], g["table"], g["kv"], l2, stream=side.cuda_stream)["o"]
     side.synchronize()
     assert torch.equal(s, s2) and torch.equal(lists, l2) and torch.equal(want, o2)
+
+
+# --------------------------------------------------------- what breaks easily
+
+
+@pytest.mark.parametrize("dtype,bits", CACHES)
+@pytest.mark.parametrize("H,Hkv,page", [(8, 1, 16), (6, 3, 32)])
+def test_not_finite_in_a_page_of_some(jb, dtype, bits, H, Hkv, page):
+    """Tokens next to each other are computed together: a value that is not finite in a page that
+    some of them list reaches those and no others, and a row behind a token's own none before it."""
+    new, kv, D = [7], [150], 64
+    d, g = inputs(new, kv, H, Hkv, D, page, dtype, bits, seed=20)
+    own = [(kv[0] - 7 + i) // page for i in range(7)]
+    lists = torch.tensor([[[0, 2 if t % 2 else 1, own[t], -1]] * Hkv for t in range(7)], dtype=torch.int32)
+    clean = attend(jb, g, lists)
+    check_blocks(d, clean, lists, new, kv)
+    vc = g["v_cache"].view(torch.uint8) if bits == 8 else g["v_cache"]
+    vc[int(d["table"][0, 2]), 0, 3, 40] = 0x7f if bits == 8 else float("inf")      # page 2: the odd tokens'
+    last = 149
+    vc[int(d["table"][0, last // page]), Hkv - 1, last % page, 9] = 0xff if bits == 8 else float("nan")  # the last token's row
+    dirty = attend(jb, g, lists)
+    G = H // Hkv
+    want = torch.zeros(7, H, D, dtype=torch.bool)
+    want[1::2, :G, 40] = True
+    want[6, H - G:, 9] = True
+    got = ~torch.isfinite(dirty["o"].float()).cpu()
+    assert torch.equal(got, want)
+    # (the second, careful pass takes the same steps)
+    assert torch.equal(dirty["o"].cpu()[~want], clean["o"].cpu()[~want]) and torch.equal(dirty["lse"], clean["lse"])
+
+
+@pytest.mark.parametrize("dtype,bits", CACHES)
+def test_lists_that_go_through_memory(jb, dtype, bits):
+    """Lists longer than LDS holds, and tables too wide to merge tokens' lists."""
+    for T, kv, count, width in ((1, 300, 2100, 40), (5, 300, 3, 5000), (5, 300, 2100, 5000)):
+        d, g = inputs([T], [kv], 4, 2, 64, 16, dtype, bits, seed=count, packed=False)
+        d["table"] = torch.cat([d["table"], torch.full((1, width - d["table"].shape[1]), -3, dtype=torch.int32)], 1)
+        g["table"] = d["table"].cuda()
+        lists = torch.full((T, 2, count), -1, dtype=torch.int32)
+        lists[:, :, :3] = some_lists([T], [kv], 2, 16, 3, 4)
+        lists[0, 0, :19] = torch.arange(19)[:count] if count >= 19 else lists[0, 0, :19]
+        shaped = lists.view(1, T, 2, count)
+        check_blocks(d, attend(jb, g, shaped), lists, [T], [kv])
+
+
+@pytest.mark.parametrize("dtype,bits", CACHES)
+@pytest.mark.parametrize("T", [2, 3, 17])
+def test_dense_batches_of_several_tokens(jb, dtype, bits, T):
+    kv = [40, T - 1, 333, 64]
+    d, g = inputs([T] * 4, kv, 8, 2, 128, 32, dtype, bits, seed=T, packed=False)
+    lists = some_lists([T] * 4, kv, 2, 32, 5, T)
+    check_blocks(d, attend(jb, g, lists.view(4, T, 2, 5)), lists, [T] * 4, kv)
+
+
+def test_packed_decode(jb):
+    """One token a sequence, packed, with an empty sequence and rows behind the last one: scores,
+    selection and attention are those of the dense batch."""
+    new, kv = [1, 0, 1, 1], [100, 50, 17, 640]
+    d, g = inputs(new, kv, 6, 2, 128, 16, BF, 8, seed=30, behind=1)
+    keep = [0, 2, 3]
+    means = [torch.from_numpy(f64(d["k_cache"]).mean(2)).float().cuda() for _ in range(2)]
+    s = torch.full((4, 2, d["table"].shape[1]), 7.0, device="cuda")
+    jb.block_scores(g["q"], g["k_cache"], means[0], g["table"], g["kv"], k_scales=g["k_scales"], cu_seqlens=g["cu"],
+                    max_seqlen=1, scores=s)
+    args = (g["table"][keep].contiguous(), g["kv"][keep].contiguous())
+    want = jb.block_scores(g["q"][:3], g["k_cache"], means[1], *args, k_scales=g["k_scales"])["scores"]
+    assert torch.equal(s[:3], want) and (s[3] == 7).all() and torch.equal(means[0], means[1])
+    lists = torch.full((4, 2, 4), 9, dtype=torch.int32, device="cuda")
+    jb.block_select(s, g["kv"], 4, 16, cu_seqlens=g["cu"], max_seqlen=1, blocks=lists)
+    want = jb.block_select(want, args[1], 4, 16)
+    assert torch.equal(lists[:3], want) and (lists[3] == 9).all()
+    o = torch.full_like(g["q"], 3.0)
+    jb.attn_blocks(g["q"], g["k_cache"], g["v_cache"], g["table"], g["kv"], lists, k_scales=g["k_scales"],
+                   v_scales=g["v_scales"], cu_seqlens=g["cu"], max_seqlen=1, o=o)
+    want = jb.attn_blocks(g["q"][:3], g["k_cache"], g["v_cache"], *args, want, k_scales=g["k_scales"],
+                          v_scales=g["v_scales"])["o"]
+    assert torch.equal(o[:3], want) and (o[3] == 3).all()
+
+
+@pytest.mark.parametrize("H,Hkv,D", [(40, 2, 64), (17, 1, 256), (64, 1, 128)])
+def test_scores_of_many_heads(jb, H, Hkv, D):
+    """More query heads to a key head than a product has rows."""
+    for T in (1, 5):
+        d, g = inputs([T], [500], H, Hkv, D, 16, BF, 16, seed=H + T, packed=False)
+        means = torch.from_numpy(f64(d["k_cache"]).mean(2)).float().cuda()
+        got = f64(jb.block_scores(g["q"], g["k_cache"], means, g["table"], g["kv"])["scores"]).reshape(T, Hkv, -1)
+        q, m, G = f64(d["q"]).reshape(T, H, D), f64(means), H // Hkv
+        for i in range(T):
+            own = (500 - T + i) // 16
+            for h in range(Hkv):
+                ms, qs = m[d["table"][0, :own + 1].numpy(), h], q[i, h * G:(h + 1) * G]
+                slack = (3 * D + 2) * 2.0 ** -24 * (np.abs(qs) @ np.abs(ms).T).max(0)
+                assert (np.abs(got[i, h, :own + 1] - (qs @ ms.T).max(0)) <= slack).all()
+                assert (got[i, h, own + 1:] == -np.inf).all()
+
+
+def test_select_at_the_widest(jb):
+    """65536 pages, the most there may be; all scores equal; descending ones."""
+    page, width, count = 16, 65536, 40
+    kv = torch.tensor([page * width, page * 40000 + 3], dtype=torch.int32)
+    for x in (torch.zeros(2, 1, width), -torch.arange(width, dtype=torch.float32).expand(2, 1, width).contiguous(),
+              torch.randn(2, 1, width, generator=torch.Generator().manual_seed(1))):
+        got = jb.block_select(x.cuda(), kv.cuda(), count, page, first=2, recent=3).cpu()
+        for i in range(2):
+            own = (int(kv[i]) - 1) // page
+            assert got[i, 0].tolist() == ref8.select(x[i, 0].tolist(), own, count, 2, 3)
