@@ -86,7 +86,7 @@ int64_t attn_blocks_workgroups(const BlockCall& c, const AttnCall& attn);
 // the lists that the decode kernel takes itself (otherwise they become tables in memory)
 bool attn_lists_fit(const BlockCall& c);
 size_t attn_lists_bytes(const BlockCall& c);
-int64_t attn_lists_workgroups(const BlockCall& c);
+int64_t attn_lists_workgroups(const BlockCall& c);  // at most, of 256 threads
 hipError_t launch_attn_lists(const AttnCall& attn, const BlockCall& c, hipStream_t stream);
 hipError_t launch_attn8_lists(const AttnCall& attn, const BlockCall& c, hipStream_t stream);
 size_t attn_blocks_workspace_bytes(const BlockCall& c, const AttnCall& attn);

@@ -12,7 +12,7 @@ bool attn_lists_fit(const BlockCall& c) { return list_rows(c); }
 size_t attn_lists_bytes(const BlockCall& c) { return list_rows_bytes(c); }
 
 int64_t attn_lists_workgroups(const BlockCall& c) {
-  return std::max(list_units(c) * list_pieces(c), cdiv(c.total * c.H, 1024 / c.D));
+  return std::max(list_units(c) * list_pieces(c) * cdiv(list_waves(c.D, c.bits8), 4), cdiv(c.total * c.H, 1024 / c.D));
 }
 
 hipError_t launch_attn_lists(const AttnCall& attn, const BlockCall& c, hipStream_t stream) {

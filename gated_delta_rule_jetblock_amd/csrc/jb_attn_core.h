@@ -270,24 +270,37 @@ template <int D> struct Loader : Pages {
     k = (const bf16_t*)a.k + head * D;
     v = (const bf16_t*)a.v + head * D;
   }
-  // rows row0 .. row0 + 15 (row0 a multiple of 16) of K and V; zeros from row hi on
-  __device__ void load(const Args& a, int row0, int hi, uint32_t ldsk, uint32_t ldsv) {
+  // where rows row0 .. row0 + 15 (row0 a multiple of 16) lie, and the bytes of those before hi
+  struct Rows {
+    int64_t at;
+    int bytes;
+  };
+  __device__ __forceinline__ Rows find(const Args& a, int row0, int hi) {
     const int pid = row0 < hi ? page(a, row0) : -1;
     const bool ok = (unsigned)pid < (unsigned)a.num_pages;
     const int n = ok ? min(max(hi - row0, 0), 16) : 0;
-    const int64_t at = (ok ? pid : 0) * a.page_stride + (row0 & ((1 << a.pshift) - 1)) * D;
-    const int bytes = n * I::ROWB;
-    if constexpr (N == 2) {
-      dma2(buf_desc(k + at, bytes), vk[0], vk[1], ldsk);
-      dma2(buf_desc(v + at, bytes), vv, vv, ldsv);
-    } else {
+    return {(ok ? pid : 0) * a.page_stride + (row0 & ((1 << a.pshift) - 1)) * D, n * I::ROWB};
+  }
+  // (a descriptor for 4 KB: its range check sees every offset)
+  __device__ __forceinline__ void get_k(Rows x, uint32_t lds) const {
+    if constexpr (N == 2) dma2(buf_desc(k + x.at, x.bytes), vk[0], vk[1], lds);
+    else
 #pragma unroll
-      for (int i = 0; i < N; i += 4) {  // (a descriptor for 4 KB: its range check sees every offset)
-        const int left = max(bytes - i * 1024, 0);
-        dma4(buf_desc(k + at + i * 512, left), vk[i], vk[i + 1], vk[i + 2], vk[i + 3], ldsk + i * 1024);
-        dma4(buf_desc(v + at + i * 512, left), vv, vv ^ fv_flip(1), vv, vv ^ fv_flip(1), ldsv + i * 1024);
-      }
-    }
+      for (int i = 0; i < N; i += 4)
+        dma4(buf_desc(k + x.at + i * 512, max(x.bytes - i * 1024, 0)), vk[i], vk[i + 1], vk[i + 2], vk[i + 3], lds + i * 1024);
+  }
+  __device__ __forceinline__ void get_v(Rows x, uint32_t lds) const {
+    if constexpr (N == 2) dma2(buf_desc(v + x.at, x.bytes), vv, vv, lds);
+    else
+#pragma unroll
+      for (int i = 0; i < N; i += 4)
+        dma4(buf_desc(v + x.at + i * 512, max(x.bytes - i * 1024, 0)), vv, vv ^ fv_flip(1), vv, vv ^ fv_flip(1), lds + i * 1024);
+  }
+  // rows row0 .. row0 + 15 of K and V; zeros from row hi on
+  __device__ __forceinline__ void load(const Args& a, int row0, int hi, uint32_t ldsk, uint32_t ldsv) {
+    const Rows x = find(a, row0, hi);
+    get_k(x, ldsk);
+    get_v(x, ldsv);
   }
   // D = 256: a transfer holds 2 rows, so V's piece order takes turns
   static constexpr int fv_flip(int i) { return D == 256 && i ? (2 << 2) * 16 : 0; }
@@ -783,21 +796,22 @@ template <int D, bool Q8 = false> struct Wave {
       }
     }
   }
-  // A tile of listed pages, as codes or as bf16 (lk: K, then V; whole: every query sees all of
-  // it).  Masked weights are 0, but 0 times a NaN is not: `careful` looks for what is not
-  // finite first.
-  __device__ __forceinline__ void listed(const Args& a, lds_char* lk, uint32_t e, int j0, bool whole, bool careful) {
-    const int g = lane_id() >> 5;
-    lds_char* const lv = lk + (Q8 ? W8::TILE : 32 * D * 2);
-    f16_t s[1];
+  // A tile of listed pages (lk: K, then V, as codes or as bf16; whole: every query sees all of
+  // it), first with K, then with V.  Masked weights are 0, but 0 times a NaN is not:
+  // `careful` looks for what is not finite first.
+  __device__ __forceinline__ void listed_k(const lds_char* lk, uint32_t e, f16_t (&s)[1]) const {
     if constexpr (Q8) scores8(lk, e, s);
     else scores<1>(lk, s);
+  }
+  __device__ __forceinline__ float listed_max(const Args& a, f16_t (&s)[1], int j0, bool whole) {
+    const int g = lane_id() >> 5;
     if (!whole)
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         if (j0 + 8 * (i >> 2) + 4 * g + (i & 3) > (i >= 8 ? p1 : p)) s[0][i] = -INFINITY;
-    __builtin_amdgcn_s_setprio(2);
-    const float ms = take_max<1>(a, s);
+    return take_max<1>(a, s);
+  }
+  __device__ __forceinline__ void listed_v(const Args& a, lds_char* lv, uint32_t e, f16_t (&s)[1], float ms, int j0, bool careful) {
     if (careful) {
       if constexpr (Q8) {
         e = without_odd(lv, e, j0);
@@ -813,6 +827,13 @@ template <int D, bool Q8 = false> struct Wave {
     }
     if constexpr (Q8) values8<true>(a, lv, e, s, ms);
     else values<1, true, true>(a, lv, s, ms);
+  }
+  __device__ __forceinline__ void listed(const Args& a, lds_char* lk, uint32_t e, int j0, bool whole, bool careful) {
+    f16_t s[1];
+    listed_k(lk, e, s);
+    __builtin_amdgcn_s_setprio(2);
+    const float ms = listed_max(a, s, j0, whole);
+    listed_v(a, lk + W8::TILE, e, s, ms, j0, careful);
     __builtin_amdgcn_s_setprio(0);
   }
   __device__ __forceinline__ bool finite() const {
@@ -1388,11 +1409,12 @@ __device__ __forceinline__ Listed take_lists(const Args& a, uint32_t slot, int k
 // LIST: a workgroup takes a piece of the pages listed for one (token, key head), which are a
 // sequence of one token to it.
 template <int D, int NW, typename OUT, bool Q8, bool LIST, int QR>
-__global__ __launch_bounds__(NW * 64, Q8 ? 2 : 1) void attn_row_kernel(Args a) {
+__global__ __launch_bounds__(NW * 64, Q8 || LIST ? 2 : 1) void attn_row_kernel(Args a) {
   static_assert(Q8 || QR == 32, "queries of a unit, at most");
   constexpr int R = 32, IMG = R * D * 2, STEP = R * NW, NTHR = NW * 64;
   constexpr int TILE = Q8 ? Raw8<D>::TILE * 2 : 2 * IMG;  // K and V of a tile
-  constexpr int RING = NW * 2 * TILE + (Q8 ? NW * 32 * 8 : 0);  // (and the waves' sums, at the end)
+  constexpr bool ONE = LIST && !Q8;                       // a wave has one tile in LDS, else two
+  constexpr int RING = NW * (ONE ? 1 : 2) * TILE + (Q8 || ONE ? NW * 32 * 8 : 0);  // (and the waves' sums, at the end)
   __shared__ __attribute__((aligned(1024))) char ring[RING];
   __shared__ int64_t found[2];
   __shared__ int sums[NW];
@@ -1476,7 +1498,7 @@ __global__ __launch_bounds__(NW * 64, Q8 ? 2 : 1) void attn_row_kernel(Args a) {
   Shared shared = {0, 0, 0, 0};
 
   constexpr int NT = 4 * (Q8 ? LoaderRaw8<D, NW>::N : Loader<D>::N);  // transfers a tile
-  lds_char* const base = (lds_char*)ring + wave * 2 * TILE;
+  lds_char* const base = (lds_char*)ring + wave * (ONE ? 1 : 2) * TILE;
   for (int seg = 0; (LIST || at < end) && b < a.B; seg = 1) {
     const Seq s = LIST ? Seq{unit.tok0, unit.T, unit.hi} : seq_of(a, b);
     const int steps = LIST ? max((unit.hi + STEP - 1) / STEP, 1) : steps_of(a, s, STEP);
@@ -1556,6 +1578,40 @@ __global__ __launch_bounds__(NW * 64, Q8 ? 2 : 1) void attn_row_kernel(Args a) {
       }
       for (; n < nf; n += NW) w.full8(a, next(n), e);
       for (; n < nt; n += NW) w.part8(a, next(n), e, ord.tile(n) * R);
+    } else if constexpr (LIST) {
+      // Twice as many waves, each with one tile: K's next rows leave when this tile's scores
+      // are formed, V's when its products are, so that another wave of the SIMD works while one waits
+      // (500 tokens of 16 heads on 2 over 32 pages each: 54 us with two tiles for half the waves,
+      // 42 so).
+      Loader<D> ld(a, b, kvh, list);
+      typedef typename Loader<D>::Rows Rows;
+      const uint32_t lk = (uint32_t)(uintptr_t)base, lv = lk + IMG;
+      constexpr int HALF = 2 * Loader<D>::N;  // transfers of K, and of V
+      Rows r0 = {}, r1 = {};
+      auto find = [&](int n) {
+        r0 = ld.find(a, ord.tile(n) * R, x.hi);
+        r1 = ld.find(a, ord.tile(n) * R + 16, x.hi);
+      };
+      auto get_k = [&] { ld.get_k(r0, lk), ld.get_k(r1, lk + 16 * D * 2); };
+      auto get_v = [&] { ld.get_v(r0, lv), ld.get_v(r1, lv + 16 * D * 2); };
+      w.arrived();
+      if (wave < nt) find(wave), get_k(), get_v();
+      for (int n = wave; n < nt; n += NW) {
+        const int t = ord.tile(n);
+        const bool whole = whole_tile(t), more = n + NW < nt;
+        if (more) find(n + NW);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(HALF) : "memory");  // K is here
+        f16_t s1[1];
+        w.listed_k(base, 0, s1);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (more) get_k();
+        const float ms = w.listed_max(a, s1, t * R, whole);
+        if (more) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(HALF) : "memory");  // V is here
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        w.listed_v(a, base + IMG, 0, s1, ms, t * R, careful);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (more) get_v();
+      }
     } else {
       Loader<D> ld(a, b, kvh, list);
       auto issue = [&](int t, int par) {
@@ -1584,11 +1640,6 @@ __global__ __launch_bounds__(NW * 64, Q8 ? 2 : 1) void attn_row_kernel(Args a) {
         w.template full<1, true>(a, k, k + IMG, [] {});
       }
       for (; n < nt; n += NW) {
-        if constexpr (LIST) {
-          const bool whole = whole_tile(ord.tile(n));
-          w.listed(a, next(n), 0, ord.tile(n) * R, whole, careful);
-          continue;
-        }
         lds_char* const k = next(n);
         lds_char* const v = k + IMG;
         f16_t s1[1];
@@ -2020,6 +2071,7 @@ int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
 size_t a256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 constexpr int row_waves(int D) { return D == 256 ? 2 : 4; }  // of attn_row_kernel: two tiles each in LDS
+constexpr int list_waves(int D, bool bits8) { return bits8 ? row_waves(D) : 2 * row_waves(D); }  // over lists
 
 Plan plan(const AttnCall& c) {
   Plan p;
@@ -2209,7 +2261,7 @@ int64_t list_units(const BlockCall& b) {
 // 64 decode steps over 32 pages of 64 rows (128 units): 1 piece 22.0 us, 2 19.6, 4 20.9, 8
 // 25.8; one over 16 pages 14.8, 17.2, 18.1, 17.2.
 int list_pieces(const BlockCall& b) {
-  const int64_t units = list_units(b), hold = b.D == 64 || b.bits8 ? 512 : 256, step = 32 * row_waves(b.D);
+  const int64_t units = list_units(b), hold = b.D == 64 || b.bits8 ? 512 : 256, step = 32 * list_waves(b.D, b.bits8);
   const int64_t steps = cdiv((int64_t)std::min(b.count, b.max_pages) * b.page, step);
   int64_t best = 0;
   int pieces = 1;
@@ -2225,7 +2277,7 @@ size_t list_rows_bytes(const BlockCall& b) {
 }
 
 template <int D, typename OUT, bool Q8> hipError_t launch_lists(const Args& a, int64_t units, hipStream_t stream) {
-  constexpr int NW = row_waves(D), RPB = 256 / (D / 4);
+  constexpr int NW = list_waves(D, Q8), RPB = 256 / (D / 4);
   const dim3 grid((unsigned)(units * a.pieces)), threads(NW * 64);
   const int rows = a.G << a.gshift;
   if (Q8 && rows <= 8) attn_row_kernel<D, NW, OUT, Q8, true, Q8 ? 8 : 32><<<grid, threads, 0, stream>>>(a);
