@@ -33,6 +33,11 @@
 // The cache range of a tile of queries may be cut into nsplit pieces; each
 // writes its unnormalised o, m and l, and attn_join_kernel adds them up.
 // fp32 inputs take attn_f32_kernel, the same tiles on fp32 matrix cores.
+// A cache in 8 bits (Q8) holds bf16 values in half the bytes: an e4m3 code has 4
+// significant bits and its scale is a power of two.  Many queries convert a tile once as it
+// goes into LDS; decode leaves the codes as they are there and converts at the products, 8
+// rows of a column by transposing byte reads, with 16 columns for at most 16 queries.
+// LIST: attn_row_kernel over the pages that each token lists.
 //
 // Reading the cache: 16 consecutive rows lie in one page, so a wave fetches
 // them straight into LDS with one page index and one buffer descriptor that ends
@@ -1167,6 +1172,9 @@ __device__ __forceinline__ int64_t out_row(const Args& a, const Seq& s, int kvh,
 // product of 8192^3 reaches 1226), matrix cores busy 62% of the cycles at the 1.7
 // GHz the card then holds, no bank conflicts.  Head size 64, as much vector work for
 // half the products: 452 us, 900 TFLOP/s; 256, one wave a SIMD: 1574 us, 1030.
+// In 8 bits, the same chunk: 768-798 us over the cards, 4% more than in 16 on the same one
+// (each wave's conversion of 16 rows of the next tile stands behind its products with K; at
+// the tile's start 812 us where so 798).
 template <int D, typename OUT, bool Q8>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a) {
   constexpr int NW = 4, R = 64, IMG = R * D * 2;
@@ -1267,6 +1275,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(Args a
 // run's first and last units may be shared with its neighbours.
 // The lengths live in device memory: every workgroup adds them up itself, and
 // says which shared unit begins in its run.
+// In 8 bits: 64 sequences of 1K to 64K rows 197 us, 5.5 TB/s with the start and the join (tiles
+// by way of registers, converted into LDS: 235 us; 32 columns: 200); two workgroups a CU
+// keep as many bytes on their way.  Waves are ready and wait for the vector memory unit to
+// take their transfers 55% of the time.
 // Bound by HBM: each wave keeps a 16 KB tile on its way (64 KB a CU) while it uses
 // another, without a barrier.  64 sequences of 64K rows, 2 key heads of 128: 707
 // us, 6.1 TB/s (a plain kernel that only reads reaches 7.2); of 1K to 64K rows: 365
@@ -1406,8 +1418,11 @@ __device__ __forceinline__ Listed take_lists(const Args& a, uint32_t slot, int k
   return u;
 }
 
-// LIST: a workgroup takes a piece of the pages listed for one (token, key head), which are a
-// sequence of one token to it.
+// LIST: a workgroup takes a unit of listed pages, or a piece of one.  A decode step of 64
+// sequences, 12 heads on 2, 32 pages of 64 rows each in 8 bits: 19.3 us, half of it HBM's, the rest
+// the lookups before the first rows (list, page, scales) and the join; one of 16 pages in 16
+// bits 14 us.  500 tokens of 16 heads on 2, 32 pages each of 32K rows (4 tokens list 66 of
+// them): 42 us; each token by itself 85 us.
 template <int D, int NW, typename OUT, bool Q8, bool LIST, int QR>
 __global__ __launch_bounds__(NW * 64, Q8 || LIST ? 2 : 1) void attn_row_kernel(Args a) {
   static_assert(Q8 || QR == 32, "queries of a unit, at most");

@@ -220,7 +220,9 @@ template <int D, int NB> struct Means {
 // (rows are tokens, columns pages), one product for each query head, their maximum taken in
 // the accumulators.  A wave keeps the means of 2 x 16 pages in registers, split once, and
 // walks `tiles` tiles of 2 x 16 tokens, the next head's queries on their way while these are
-// used; a workgroup takes 4 times as many pages.  FIGS.
+// used; a workgroup takes 4 times as many pages.  2K tokens of 12 heads on 2 at the end of
+// 64K rows, pages of 64: 26.6-27.6 us with the launch that forms the means (5); the
+// products are 8 of it at the matrix cores' rate, the scores' bytes 3.
 constexpr int PAGES = 128;  // of a workgroup
 
 template <int D>
@@ -335,7 +337,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void block_scores_kernel(Arg
 // Decode (T = 1), bf16: rows are 16 query heads of the one token, columns 16 pages; the
 // maximum over the rows is taken across the lanes.  The one page that holds the token is
 // averaged by the workgroup that scores it, so the step is one launch.  Bound by what it
-// waits for (the length and the page indices, then the means): FIGS.
+// waits for (the length and the page indices, then the means).  64 sequences of up to 64K
+// rows, 12 heads on 2, pages of 64: 14.4-15.3 us a call, 10.5 without the means' bytes (a
+// call's host work).
 template <int D, typename KV>
 __global__ __launch_bounds__(256, D == 64 ? 5 : D == 128 ? 3 : 2) void block_scores_one_kernel(Args a, uint32_t groups) {
   constexpr int STEPS = D / 32, NB = 2;
@@ -496,7 +500,9 @@ __global__ __launch_bounds__(256) void block_scores_f32_kernel(Args a, uint32_t 
 // counts those that reach a candidate (a compare, a scalar bit count).  Once at most 64 are
 // undecided they are gathered, one a lane, and the other steps cost one compare each.  W waves
 // a row; with one the row needs no barrier.  Places are ascending: lane l of wave w has pages
-// (w V + v) 64 + l.  Bound by its chain of steps: FIGS.
+// (w V + v) 64 + l.
+// With at most 64 to select and one wave a row the search is shorter (below): 1 row of 1024
+// pages 4.2 us, 4096 rows 8.0; by the steps over all scores 7.6 and 14.
 __device__ __forceinline__ uint32_t order_of(float x) {
   const uint32_t u = __float_as_uint(x != x ? -INFINITY : x + 0.f);  // (-0 as 0)
   return u & 0x80000000u ? ~u : u | 0x80000000u;

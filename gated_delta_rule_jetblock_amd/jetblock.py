@@ -1029,10 +1029,13 @@ def attn_blocks(q, k_cache, v_cache, page_table, kv_lens, blocks, *, k_scales=No
     shape = AttnShape(B, T, H, Hkv, D, 0, page, max_pages, P, 0, 0, _io_code(q), _code(out_dtype),
                       0 if k_scales is None else CACHE_E4M3, qs, 0, 0, ps)
     if ws is None:
-        ws = torch.empty(attn_blocks_workspace_size(shape, n, packed, count), dtype=torch.uint8, device=q.device)
+        need = attn_blocks_workspace_size(shape, n, packed, count)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
     _launch(di, _lib.jb_attn_blocks, shape, n, _flat(cu_seqlens, "cu_seqlens", B + 1), _flat(kv_lens, "kv_lens", B),
             _flat(page_table, "page_table", B, max_pages), qp, k_cache.data_ptr(), v_cache.data_ptr(),
             None if k_scales is None else k_scales.data_ptr(), None if v_scales is None else v_scales.data_ptr(), ss,
             _flat(blocks, "blocks", *q.shape[:-2], Hkv, count), count, 0.0 if scale is None else float(scale),
-            _flat(o, "o", *q.shape), _flat(lse, "lse", *q.shape[:-1]), ws.data_ptr(), ws.numel())
+            _flat(o, "o", *q.shape), _flat(lse, "lse", *q.shape[:-1]), None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel())
     return {"o": o, "lse": lse}

@@ -551,6 +551,7 @@ jb_status jb_attn_paged8_workspace_size(const jb_attn_shape* shape, int64_t tota
 /*
  * jb_attn_paged8 -- jb_attn_paged over a cache in 8 bits.  bf16 q: the cache's values
  * are bf16 values, and the arithmetic is jb_attn_paged's; fp32 q: fp32 throughout.
+ * workspace: jb_attn_paged8_workspace_size() bytes (NULL if 0), 256-byte aligned.
  */
 jb_status jb_attn_paged8(const jb_attn_shape* shape, int64_t total_tokens, const int32_t* cu_seqlens,
                          const int32_t* kv_lens, const int32_t* page_table, const void* q,
@@ -598,7 +599,8 @@ jb_status jb_attn_blocks_workspace_size(const jb_attn_shape* shape, int64_t tota
  * rows j <= p of the pages in blocks [tokens][Hkv][count] and no others.  An entry counts if
  * it is a page that the token sees and larger than every such entry before it; others (-1,
  * one that comes twice) are passed over, and a token with none gets o = 0 and lse = -inf.
- * The softmax weights are taken as in decode.  shape.window must be 0; max_kv is not used.
+ * The softmax weights are taken as in decode where H / Hkv <= 32.  shape.window must be 0; max_kv
+ * is not used.  workspace: jb_attn_blocks_workspace_size() bytes (NULL if 0), 256-byte aligned.
  */
 jb_status jb_attn_blocks(const jb_attn_shape* shape, int64_t total_tokens, const int32_t* cu_seqlens,
                          const int32_t* kv_lens, const int32_t* page_table, const void* q,

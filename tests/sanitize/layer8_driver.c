@@ -61,8 +61,9 @@ int main(void) {
                       s.flags = bits8 ? JB_CACHE_E4M3 : 0;
                       jb_status st = jb_attn_blocks_workspace_size(&s, total, packed, counts[n], &bytes);
                       EXPECT((good && n < 4) || st != JB_OK, "a shape past the limits was accepted");
-                      if (st == JB_OK && total) {
+                      if (st == JB_OK && total && (f32 || counts[n] > 2048))
                         EXPECT(bytes >= (size_t)total * s.Hkv * (counts[n] + 1) * 4, "workspace %zu holds no lists", bytes);
+                      if (st == JB_OK && total && bytes) {
                         uint8_t* e = bits8 ? p : NULL;
                         st = jb_attn_blocks(&s, total, cu, p, p, p, p, p, e, e, 0, p, counts[n], 0.f, p, p, p, bytes - 1, NULL);
                         EXPECT(st == JB_ERR_WORKSPACE, "short workspace gave %s", jb_status_string(st));

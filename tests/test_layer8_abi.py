@@ -43,8 +43,10 @@ CALLS = {
 CACHED = [n for n in CALLS if n != "jb_block_select"]
 
 
-def call(jb, name, s, total=10, f=1e-6, ws=1 << 40, at=None, value=GOOD, L=0, count=3, first=1, recent=1):
+def call(jb, name, s, total=10, f=1e-6, ws=1 << 40, at=None, value=GOOD, L=0, count=None, first=1, recent=1):
     args = []
+    if count is None:  # (lists of more than 2048 entries need a workspace)
+        count = 3000 if name == "jb_attn_blocks" else 3
     for i, k in enumerate(CALLS[name]):
         args.append({"T": lambda: ctypes.c_int64(total), "f": lambda: ctypes.c_float(f), "w": lambda: ctypes.c_size_t(ws),
                      "s": lambda: P(None), "L": lambda: ctypes.c_int64(L), "c": lambda: ctypes.c_int32(count),
@@ -133,7 +135,10 @@ def test_attention_arguments(jb):
     size = jb.library().jb_attn_blocks_workspace_size
     for flags in (0, jb.CACHE_E4M3):
         s = shape(jb, flags=flags)
-        assert size(ctypes.byref(s), 10, 0, 3, ctypes.byref(n)) == OK and n.value >= 10 * 2 * 4 * 4
+        assert size(ctypes.byref(s), 10, 0, 3, ctypes.byref(n)) == OK and n.value == 0      # one piece of a short list
+        assert size(ctypes.byref(shape(jb, flags=flags, B=1, T=1, max_pages=400)), 1, 0, 300, ctypes.byref(n)) == OK
+        assert n.value >= 2 * 4 * (64 + 2) * 4                                              # pieces of a long one
+        assert size(ctypes.byref(s), 10, 0, 3000, ctypes.byref(n)) == OK and n.value >= 10 * 2 * 3001 * 4
     assert call(jb, "jb_attn_blocks", s, ws=n.value - 1) == WORKSPACE and str(n.value) in jb.last_error()
     assert size(ctypes.byref(s), 10, 0, 3, None) == INVALID
     assert size(ctypes.byref(s), 0, 1, 3, ctypes.byref(n)) == OK and n.value == 0
