@@ -156,6 +156,20 @@ __global__ __launch_bounds__(256) void block_means_kernel(Args a) {
 // the larger of two scores; NaN stays
 __device__ __forceinline__ float larger(float m, float x) { return x > m || x != x ? x : m; }
 
+// A score by plain products (mean: NULL for zeros), where the sum over a mean's parts is NaN:
+// an infinite query times a part that is 0, or the parts of an infinite mean, are NaN
+// where the product itself need not be.  (A call of its own: it is rare, and inline it took
+// the registers of the loops.)
+template <int D> __device__ __attribute__((noinline)) float plain_score(const bf16_t* q, const float* mean, int G) {
+  float best = -INFINITY;
+  for (int h = 0; h < G; ++h) {
+    float x = 0.f;
+    for (int d = 0; d < D; ++d) x = fmaf(__uint_as_float((uint32_t)q[h * D + d] << 16), mean ? mean[d] : 0.f, x);
+    best = h ? larger(best, x) : x;
+  }
+  return best;
+}
+
 // The means of NB x 16 pages as operands: lane (page lane % 16, group g) has d = 8 g + e of
 // every 32, each value as three bf16 parts: hi + mid + lo are its 24 bits, so products with
 // bf16 queries are exact and their sums fp32's.
@@ -163,7 +177,6 @@ __device__ __forceinline__ float larger(float m, float x) { return x > m || x !=
 // other read one row, where an operand's neighbouring lanes are of different rows and cost
 // the vector memory unit a cycle each (a chunk of 2K tokens on 64K rows with the queries
 // read so too: 33 us, of which 24 were that).
-typedef __attribute__((address_space(3))) float4 lds_float4;
 typedef __attribute__((address_space(3))) u4_t lds_u4;
 typedef __attribute__((address_space(3))) char lds_char;
 
@@ -328,7 +341,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void block_scores_kernel(Arg
 #pragma unroll
           for (int n = 0; n < NB; ++n) {
             const int j = j0 + 16 * n + n16;
-            if (j < c.max_pages) out[j] = j <= own ? best[t][n][e] : -INFINITY;
+            if (j >= c.max_pages) continue;
+            float x = j <= own ? best[t][n][e] : -INFINITY;
+            if (x != x) {
+              const int pid = c.page_table[(int64_t)b * c.max_pages + j];
+              x = plain_score<D>((const bf16_t*)c.q + (s.tok0 + i0 + i) * c.q_stride + (int64_t)head * a.G * D,
+                                 pid >= 0 && pid < c.num_pages ? c.means + ((int64_t)pid * c.Hkv + head) * D : nullptr, a.G);
+            }
+            out[j] = x;
           }
       }
   }
@@ -414,8 +434,15 @@ __global__ __launch_bounds__(256, D == 64 ? 5 : D == 128 ? 3 : 2) void block_sco
   }
   // lanes 0 .. 31 write the wave's 32 pages
   const int j = j0 + lane;
-  if (lane < 32 && j < c.max_pages)
-    c.scores[((int64_t)t * c.Hkv + head) * c.max_pages + j] = j <= own ? (lane < 16 ? best[0] : best[1]) : -INFINITY;
+  if (lane < 32 && j < c.max_pages) {
+    float x = j <= own ? (lane < 16 ? best[0] : best[1]) : -INFINITY;
+    if (x != x) {
+      const int page = table[j];
+      const float* mean = page >= 0 && page < c.num_pages ? c.means + ((int64_t)page * c.Hkv + head) * D : nullptr;
+      x = plain_score<D>(q - 8 * g, j == own && formed ? fresh : mean, a.G);
+    }
+    c.scores[((int64_t)t * c.Hkv + head) * c.max_pages + j] = x;
+  }
 }
 
 // The same in fp32: 16 tokens and 16 pages at a time with fp32 products, TM x 16 tokens and

@@ -127,6 +127,46 @@ def test_scores_that_are_not_numbers(jb):
     assert not torch.isfinite(x[1, 1]).any()
 
 
+@pytest.mark.parametrize("new,kv", [([1, 1, 1], [40, 3000, 700]), ([40, 33, 5], [40, 3000, 700])])
+@pytest.mark.parametrize("dtype,D,H,Hkv", [(BF, 64, 4, 2), (BF, 128, 36, 2), (BF, 256, 3, 3), (F32, 64, 4, 2)])
+def test_scores_that_are_infinite(jb, new, kv, dtype, D, H, Hkv):
+    """Infinite queries, keys and means: a score is what the products' sum is, an infinity of its sign
+    or, of both signs or an infinity times 0, NaN.  (Sequence 1 has infinite queries, 2 an infinite key
+    in its own page and means of pages before it.)"""
+    page, G = 16, H // Hkv
+    d, g = inputs(new, kv, H, Hkv, D, page, dtype, 16 if dtype == BF else 32, seed=D + H)
+    first = np.concatenate([[0], np.cumsum(new)])
+    inf = float("inf")
+    d["q"][first[1], 0, 3] = inf                        # head 0 of key head 0
+    d["q"][first[2] - 1, 0, 5], d["q"][first[2] - 1, H - 1, 6] = -inf, inf
+    d["q"][first[2]:, H - G:, 9], d["q"][first[2]:, H - G:, 10] = 0.125, -0.5
+    d["k_cache"][int(d["table"][2, (kv[2] - 1) // page]), 0, 0, 2] = inf
+    means = f64(d["k_cache"]).mean(2)
+    means[int(d["table"][1, 4]), 0, 3] = 0.0            # an infinite query times 0
+    means[int(d["table"][1, 7]), 0, 3] = 0.5            # times a value of one part
+    means[int(d["table"][2, 5]), Hkv - 1, 9] = -inf
+    means[int(d["table"][2, 6]), Hkv - 1, 9:11] = inf, -inf
+    means[int(d["table"][2, 7]), Hkv - 1, 9:11] = inf
+    means[int(d["table"][2, 8]), Hkv - 1, 9] = 3.395e38  # rounds to an infinity in bf16
+    m = torch.from_numpy(means).float().cuda()
+    r = jb.block_scores(d["q"].cuda(), d["k_cache"].cuda(), m, g["table"], g["kv"], cu_seqlens=g["cu"])
+    q, got_m = f64(d["q"]), f64(m)
+    want = np.full((len(q), Hkv, d["table"].shape[1]), -inf)
+    slack = np.zeros_like(want)
+    with np.errstate(invalid="ignore"):
+        for t, b, p in places(new, kv):
+            for h in range(Hkv):
+                for j in range(p // page + 1):
+                    x = q[t, h * G:(h + 1) * G] * got_m[int(d["table"][b, j]), h]
+                    want[t, h, j], slack[t, h, j] = x.sum(1).max(), (3 * D + 2) * 2.0 ** -24 * np.abs(x).sum(1).max()
+    seen = [want[first[i]:first[i + 1]] for i in (1, 2)]
+    assert all(np.isnan(x).any() and np.isposinf(x).any() for x in seen) and (G > 1 or np.isneginf(seen[0][0, 0, :100]).any())
+    got = same_kind(r["scores"], want)
+    fine = np.isfinite(want)
+    assert (np.abs(got[fine] - want[fine]) <= slack[fine]).all()
+
+
+
 # --------------------------------------------------------------- selection
 
 
