@@ -763,6 +763,9 @@ int64_t mean_slots(const BlockCall& c) {
 }
 int64_t score_slots(const BlockCall& c) { return c.packed ? c.total / 32 + c.B : (int64_t)c.B * cdiv(c.T, 32); }
 
+// a step of one token each, in bf16: the means and the scores in one launch
+bool scores_at_once(const BlockCall& c) { return c.scores && c.T == 1 && c.io != IO_F32; }
+
 template <int D, typename KV> hipError_t means(const Args& a, hipStream_t stream) {
   block_means_kernel<D, KV><<<dim3((unsigned)(mean_slots(a.c) * a.c.Hkv)), dim3(256), 0, stream>>>(a);
   return hipGetLastError();
@@ -772,7 +775,7 @@ template <int D> hipError_t scores(const BlockCall& c, hipStream_t stream) {
   Args a = args_of(c);
   const bool f32 = c.io == IO_F32;
   const int64_t groups = cdiv(c.max_pages, PAGES);
-  if (c.scores && c.T == 1 && !f32) {
+  if (scores_at_once(c)) {
     const dim3 grid((unsigned)(c.total * c.Hkv * groups));
     if (c.bits8) block_scores_one_kernel<D, uint8_t><<<grid, dim3(256), 0, stream>>>(a, (uint32_t)groups);
     else block_scores_one_kernel<D, bf16_t><<<grid, dim3(256), 0, stream>>>(a, (uint32_t)groups);
@@ -807,7 +810,8 @@ size_t list_bytes(const BlockCall& c) { return a256((size_t)c.total * c.Hkv * c.
 
 int64_t block_scores_workgroups(const BlockCall& c) {
   const int64_t groups = cdiv(c.max_pages, PAGES);
-  return std::max(mean_slots(c) * c.Hkv, c.scores ? (c.T == 1 ? c.total : score_slots(c)) * c.Hkv * groups : 0);
+  if (scores_at_once(c)) return c.total * c.Hkv * groups;
+  return std::max(mean_slots(c) * c.Hkv, c.scores ? score_slots(c) * c.Hkv * groups : 0);
 }
 
 hipError_t launch_block_scores(const BlockCall& c, hipStream_t stream) {

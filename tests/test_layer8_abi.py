@@ -163,6 +163,10 @@ def test_block_arguments(jb):
     s = shape(jb, B=1, T=1 << 22, H=1, Hkv=1, max_pages=4097)
     assert call(jb, "jb_block_select", s, total=1 << 22) == UNSUPPORTED and "more workgroups" in jb.last_error()
 
+    # one token of 65535 packed sequences, fp32: a sequence has a place of its own even without tokens
+    s = shape(jb, "jb_block_scores", B=65535, T=1, H=1, Hkv=1, max_pages=65536, io_dtype=jb.JB_F32)
+    assert call(jb, "jb_block_scores", s, total=1) == UNSUPPORTED and "more workgroups" in jb.last_error()
+
 
 def test_binding(jb):
     P_, Hkv, page, D = 5, 2, 32, 64
