@@ -800,7 +800,7 @@ AttnCall listed(const BlockCall& c, const AttnCall& attn) {
   AttnCall x = attn;
   x.units = c.Hkv;
   x.B = (int)(c.total * c.Hkv), x.T = 1, x.H = c.H / c.Hkv, x.Hkv = 1, x.total = x.B;
-  x.max_pages = c.count, x.max_kv = (int)std::min<int64_t>((int64_t)c.count << __builtin_ctz((unsigned)c.page), x.max_kv);
+  x.max_pages = c.count, x.max_kv = std::min(c.count, c.max_pages) << __builtin_ctz((unsigned)c.page);
   x.packed = false, x.cu_seqlens = nullptr, x.window = 0;
   return x;
 }

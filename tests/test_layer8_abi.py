@@ -144,6 +144,18 @@ def test_attention_arguments(jb):
     assert size(ctypes.byref(s), 0, 1, 3, ctypes.byref(n)) == OK and n.value == 0
 
 
+def test_max_kv_is_no_part_of_lists(jb):
+    """The workspace of jb_attn_blocks (short lists, long ones, fp32) does not depend on max_kv."""
+    size, n = jb.library().jb_attn_blocks_workspace_size, ctypes.c_size_t(0)
+    for io, count in ((jb.JB_BF16, 300), (jb.JB_BF16, 3000), (jb.JB_F32, 300), (jb.JB_F32, 3000)):
+        got = set()
+        for max_kv in (0, 1, 1 << 20):
+            s = shape(jb, B=1, T=1, page=64, max_pages=4096, num_pages=4096, io_dtype=io, max_kv=max_kv)
+            assert size(ctypes.byref(s), 1, 0, count, ctypes.byref(n)) == OK
+            got.add(n.value)
+        assert len(got) == 1, (io, count, got)
+
+
 def test_block_arguments(jb):
     for name in ("jb_block_scores", "jb_attn_blocks"):
         assert call(jb, name, shape(jb, flags=0)) == INVALID and "must be NULL" in jb.last_error()
