@@ -103,7 +103,8 @@ _lib.jb_block_select.argtypes = [_A, _L] + [_P] * 3 + [ctypes.c_int32] * 3 + [_P
 _lib.jb_attn_blocks_workspace_size.argtypes = [_A, _L, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(_SZ)]
 _lib.jb_attn_blocks.argtypes = [_A, _L] + [_P] * 8 + [_L, _P, ctypes.c_int32, _F] + [_P] * 3 + [_SZ, _P]
 for _f in ("jb_qk_norm_rope_paged8", "jb_attn_paged8_workspace_size", "jb_attn_paged8", "jb_block_scores",
-           "jb_block_select", "jb_attn_blocks_workspace_size", "jb_attn_blocks", "jb_qk_norm_rope", "jb_qk_norm_rope_backward_workspace_size", "jb_qk_norm_rope_backward",
+           "jb_block_select", "jb_attn_blocks_workspace_size", "jb_attn_blocks", "jb_qk_norm_rope",
+           "jb_qk_norm_rope_backward_workspace_size", "jb_qk_norm_rope_backward",
            "jb_qk_norm_rope_paged", "jb_attn_paged_workspace_size", "jb_attn_paged",
            "jb_prefill_workspace_size", "jb_decode_workspace_size", "jb_prefill", "jb_prefill_noalloc",
            "jb_decode_step",
@@ -932,6 +933,13 @@ def attn_paged8(q, k_cache, v_cache, k_scales, v_scales, page_table, kv_lens, *,
     return {"o": o, "lse": lse}
 
 
+def _int32(**values):
+    """The values, which 32 bits hold (ctypes would take others for their low 32 bits)."""
+    for name, x in values.items():
+        if not -1 << 31 <= x < 1 << 31:
+            raise ValueError(f"{name} = {x} is not a 32-bit number")
+
+
 def _cache_of(io, k_cache, k_scales, *v):
     """The dtype groups of a cache in 8 bits (with scales) or of q's type."""
     names = "k_cache v_cache" if v else "k_cache"
@@ -979,6 +987,8 @@ def block_select(scores, kv_lens, count: int, page: int, *, cu_seqlens=None, max
     `count` in all.  Returns int32 [..., Hkv, count], ascending, -1 behind the last."""
     if stream is not None:
         return _on_stream(block_select, locals(), "scores")
+    if (count | page | first | recent) >> 31:
+        _int32(count=count, page=page, first=first, recent=recent)
     di = _device(scores)
     _same(di, (torch.float32, "scores", (scores,)), (torch.int32, "kv_lens cu_seqlens blocks", (kv_lens, cu_seqlens, blocks)),
           first="scores")
@@ -1010,6 +1020,9 @@ def attn_blocks(q, k_cache, v_cache, page_table, kv_lens, blocks, *, k_scales=No
     attn_paged, or a cache in 8 bits with its scales.  Returns dict(o, lse) as attn_paged does."""
     if stream is not None:
         return _on_stream(attn_blocks, locals())
+    count = blocks.shape[-1]
+    if count >> 31:
+        _int32(count=count)
     di, io = _device(q), q.dtype
     out_dtype = out_dtype or (o.dtype if o is not None else io)
     _same(di, *_cache_of(io, k_cache, k_scales, v_cache, v_scales),
@@ -1020,7 +1033,6 @@ def attn_blocks(q, k_cache, v_cache, page_table, kv_lens, blocks, *, k_scales=No
     B, T = _batch(q, cu_seqlens, max_seqlen)
     P, Hkv, page, ps, max_pages = _pages(k_cache, v_cache, page_table, kv_lens, B, D)
     ss = 0 if k_scales is None else _scales(k_scales, v_scales, "k_scales and v_scales", P, Hkv, page)
-    count = blocks.shape[-1]
     if o is None:
         o = _empty(q, out_dtype)
     if lse is None and want_lse:

@@ -200,6 +200,19 @@ def test_binding(jb):
         jb.block_select(torch.zeros(2, 1, 4), torch.zeros(2, dtype=torch.int32), 2, 16)
 
 
+def test_numbers_past_32_bits(jb):
+    """They are refused, not taken for what their low 32 bits are."""
+    scores, kv, big = torch.zeros(2, 1, 4), torch.zeros(2, dtype=torch.int32), (1 << 32) + 16
+    for count, page, first, recent, name in ((big, 16, 1, 1, "count"), (2, big, 1, 1, "page"), (2, 16, 1 << 32, 1, "first"),
+                                             (2, 16, 0, (1 << 32) + 1, "recent"), (2, 16, -(1 << 32), 1, "first")):
+        with pytest.raises(ValueError, match=name):
+            jb.block_select(scores, kv, count, page, first=first, recent=recent)
+    q, c = torch.zeros(2, 1, 64, dtype=torch.bfloat16), torch.zeros(3, 1, 16, 64, dtype=torch.bfloat16)
+    blocks = torch.zeros(1, 1, 1, dtype=torch.int32).expand(2, 1, big)
+    with pytest.raises(ValueError, match="count"):
+        jb.attn_blocks(q, c, c, torch.zeros(2, 3, dtype=torch.int32), kv, blocks)
+
+
 @pytest.mark.parametrize("name", ["qk_norm_rope_paged8", "attn_paged8", "block_scores", "block_select", "attn_blocks"])
 def test_stream_argument_is_taken(jb, monkeypatch, name):
     fn, seen = getattr(jb, name), []
