@@ -837,17 +837,19 @@ E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
 def _scales(scales, other, name: str, P, Hkv, page):
     """Distance between the pages of a cache's scales [pages, Hkv, page / 16] (0: contiguous)."""
-    shape, st = (P, Hkv, page // 16), scales.stride()
-    for t in (scales, other):
-        if t is not None and t.shape != shape:
-            raise ValueError(f"{name}: expected {shape}, got {tuple(t.shape)}")
-    if other is not None and any(n > 1 and a != b for n, a, b in zip(shape, st, other.stride())):
+    n = page // 16
+    shape, st = (P, Hkv, n), scales.stride()
+    if scales.shape != shape or other is not None and other.shape != shape:
+        raise ValueError(f"{name}: expected {shape}, got {tuple((scales if scales.shape != shape else other).shape)}")
+    if other is not None and other.stride() != st and any(m > 1 and a != b for m, a, b in zip(shape, st, other.stride())):
         raise ValueError(f"{name}: expected the strides alike, got {st} and {other.stride()}")
-    if (page > 16 and st[2] != 1) or (Hkv > 1 and st[1] != page // 16):
+    if (n > 1 and st[2] != 1) or (Hkv > 1 and st[1] != n):
         raise ValueError(f"{name}: a page's scales must be contiguous")
-    if P > 1 and st[0] < Hkv * page // 16:
+    if P == 1:
+        return 0
+    if st[0] < Hkv * n:
         raise ValueError(f"{name}: pages overlap (page stride {st[0]})")
-    return st[0] if P > 1 else 0
+    return st[0]
 
 
 def qk_norm_rope_paged8(q, k, v, k_cache, v_cache, k_scales, v_scales, page_table, kv_lens, inv_freq, wq=None, wk=None, *,
