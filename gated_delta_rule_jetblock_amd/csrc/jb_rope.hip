@@ -326,6 +326,69 @@ __global__ __launch_bounds__(256) void rope_kernel(Args a) {
   rope_rows<D, IO, OUT, PAGED, true>(a, blockIdx.x);
 }
 
+// Keys that become codes are formed in 64 bits: a value's error flips its code where the value
+// lies that near to a border, and the errors of fp32 arithmetic (8e-8 rms) flip 2 of a million
+// codes by a whole step, where these flip 0.1 (13K tokens on 2 key heads: 31.4 us, in fp32 29.9).
+//
+// a cos + b sin of 2 pi t.  As in sincos_turn the nearest quarter turn comes off (here a sum's
+// low bits; |t| < 2^48, what lies past that has no angle in 64 bits); it swaps a and b and
+// turns their signs.  The leading terms a + 2 pi x b are in 64 bits, the others, at most 0.3 a and
+// 0.1 b, in fp32: off by 7e-9 of hypot(a, b) rms and 2.5 * 2^-24 at most (roundings of f, y and the
+// two sums; 7e-8 seen).
+template <typename T> __device__ __forceinline__ double turned(T a, T b, double t) {
+  const double up = 6755399441055744., at = fma(4., t, up), x = fma(-0.25, at - up, t);  // up: 1.5 * 2^52
+  const int q = __double2loint(at);
+  const float f = (float)x, y = f * f;
+  const float s = f * y * fmaf(y, fmaf(y, fmaf(y, 42.0586939f, -76.7058598f), 81.6052493f), -41.3417022f);
+  const float c = y * fmaf(y, fmaf(y, fmaf(y, fmaf(y, -26.4262568f, 60.2446414f), -85.4568172f), 64.939394f), -19.7392088f);
+  T u = q & 1 ? b : a, v = q & 1 ? a : b;
+  u = q & 2 ? -u : u;
+  v = (q + 1) & 2 ? -v : v;
+  return fma((double)v, 6.283185307179586 * x, (double)u) + (double)fmaf((float)u, c, (float)v * s);
+}
+
+// x to 24 bits, towards the neighbour whose last bit is set where it lies between two: rounded
+// again to fewer bits it gives what x itself gives
+__device__ __forceinline__ float odd_of(double x) {
+  const int lo = __double2loint(x);
+  return (float)__hiloint2double(__double2hiint(x), (lo & 0xe0000000) | (lo & 0x1fffffff ? 0x20000000 : 0));
+}
+
+// a row's 8 values of this lane: normalised, weighted and turned
+template <int L, typename IO>
+__device__ __forceinline__ void turned_key(const RopeCall& c, const Raw<IO>& x, const Raw<IO>& xp, const float (&w)[8],
+                                           const float (&wp)[8], const float (&f)[8], bool first, int position,
+                                           float (&y)[8]) {
+  double r = 1.;
+  if (c.norm) {
+    double sum = 0.;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fma((double)x.get(e), (double)x.get(e), sum);
+#pragma unroll
+    for (int o = L / 2; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, WAVE);
+    const double m = sum * (1. / (8 * L)) + (double)c.eps;
+    const float q = 1.f / sqrtf((float)m);
+    r = q > 0.f && isfinite(q) ? (double)q * (1.5 - 0.5 * m * (double)q * (double)q) : (double)q;  // a Newton step
+  }
+  const double p = (double)position * 0.15915494309189533577;  // turns per radian
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const double t = p * (double)(c.interleaved ? f[e >> 1] : f[e]);
+    const bool minus = c.interleaved ? !(e & 1) : first;
+    const float we = c.interleaved ? wp[e ^ 1] : wp[e];
+    double z;
+    if constexpr (sizeof(IO) == 2) {  // (16-bit values: their products are exact in fp32)
+      const float b = xp.get(e) * we;
+      z = turned(x.get(e) * w[e], minus ? -b : b, t);
+    } else {
+      const double b = (double)xp.get(e) * (double)we;
+      z = turned((double)x.get(e) * (double)w[e], minus ? -b : b, t);
+    }
+    y[e] = odd_of(r * z);
+    __builtin_amdgcn_sched_barrier(0);  // (values in turn: together they take half as many registers again)
+  }
+}
+
 // Exponent e of the smallest scale 2^(e - 127) with most <= 448 times it, 1 at least:
 // 448 = 1.75 * 2^8, so it is most's exponent less 8, or less 7 where its fraction is over 1.75.
 __device__ __forceinline__ int exponent_for(float most) {
@@ -351,16 +414,16 @@ __device__ __forceinline__ uint2 e4m3_of(const float (&x)[8]) {
 // scales holds: their codes are divided by 2^k (exactly, but for those that fall below the
 // smallest normal code, which are rounded again).  Rows behind the new ones keep their codes.
 // The other workgroups rotate the queries.
-// 32 chunks, 13K tokens of 16 + 2 heads of 128: 28-29 us, 4.3 TB/s; the keys' part by itself
-// would be 18 of that, nearly all the chain of lookups (offsets and length, page index, what
-// the page holds) before a workgroup's first store.  One token: 4.8 us.
+// 32 chunks, 13K tokens of 16 + 2 heads of 128: 30-31 us, 4.1 TB/s; the keys' part by itself
+// would be 18 of that and the sums in 64 bits, nearly all the chain of lookups (offsets and length, page
+// index, what the page holds) before a workgroup's first store.  One token: 5.4 us.
 template <int D, typename IO>
 __global__ __launch_bounds__(256) void rope_append8_kernel(Args a) {
   constexpr int L = D / 8, GROUPS = 256 / L, N = 32 / GROUPS;  // rows at once; times for 16 of K and 16 of V
   const RopeCall& c = a.c;
   const uint32_t cells = (uint32_t)a.cells * (uint32_t)a.kv_heads;
   // the keys' workgroups first, which wait for what they look up (in turn with the queries',
-  // 13K tokens take 30.6 us, so 29.3)
+  // 13K tokens took 30.6 us, so 29.3, with sums in fp32)
   if (blockIdx.x >= cells) {
     rope_rows<D, IO, IO, true, false>(a, blockIdx.x - cells);
     return;
@@ -434,21 +497,11 @@ __global__ __launch_bounds__(256) void rope_append8_kernel(Args a) {
   for (int n = 0; n < N; ++n) {
     const int r = n * GROUPS + group;
     const bool key = r < 16;  // (the same for a wave: 16 rows are a whole number of its lane groups)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[n][e] = x[n].get(e);
     if (key) {
-      float q = 1.f;
-      if (c.norm) {
-        float sum = 0.f;
+      turned_key<L>(c, x[n], others(x[n], c.interleaved, from, 8 * s < c.rot), wk, wkp, f, 8 * s < c.rot / 2, position[n], y[n]);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(y[n][e], y[n][e], sum);
-        q = 1.f / sqrtf(row_sum<L>(sum) * (1.f / D) + c.eps);
-      }
-      const Turn turn = turn_of<D>(c, s, f, position[n]);
-      const Raw<IO> xp = others(x[n], c.interleaved, from, 8 * s < c.rot);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        y[n][e] = q * fmaf(y[n][e], wk[e] * turn.cos[e], xp.get(e) * ((c.interleaved ? wkp[e ^ 1] : wkp[e]) * turn.sin[e]));
+      for (int e = 0; e < 8; ++e) y[n][e] = x[n].get(e);
     }
     float most = 0.f;
 #pragma unroll

@@ -198,6 +198,34 @@ def test_append_not_finite(jb):
     check_append(d, append(jb, d, f), [40], [48], f)
 
 
+@pytest.mark.parametrize("dtype,D,pairs", [(BF, 128, False), (BF, 64, True), (F32, 128, True), (F32, 256, False)])
+def test_append_codes_at_their_borders(jb, dtype, D, pairs):
+    """A key's code is that of its value in 64 bits, but where the value lies nearer to a border than
+    what the append is off by.  Of a cos + b sin the fp32 terms are at most 0.293 a, of y (3 half steps of
+    2^-24) times a sum (2.3) and rounded, and 0.078 b, of f y (5) times a sum (2.5) and rounded twice;
+    their sum, at most 0.37, is rounded once: 0.293 * 6.3 and 0.078 * 9.5 add up to 2 as a root of squares,
+    with 0.37 and what the series leave out (0.04) 2.5 half steps of hypot(a, b).  The rest is in 64
+    bits, and rounding to fp32 in between keeps the side of a border."""
+    print(f"[append8 borders {dtype} D={D} pairs={pairs}]", flush=True)
+    new, kv, Hkv, page = [1000, 1500], [1003, 1700], 2, 64
+    d = append_inputs(new, kv, 2, Hkv, D, page, dtype, seed=D)
+    f = frequencies(D)
+    r = append(jb, d, f, interleaved=pairs)
+    held = ref8.dequantise(codes_of(r["k_cache"]), codes_of(r["k_scales"]))
+    steps = np.repeat(ref8.scale_value(codes_of(r["k_scales"])), 16, -1)[..., None] * np.ones(D)
+    k, at = f64(d["k"]), 0
+    for b, (t, l) in enumerate(zip(new, kv)):
+        table = d["table"][b].tolist()
+        y = ref.norm_rope(k[at:at + t], np.arange(l - t, l), f.numpy(), f64(d["wk"]), interleaved=pairs)
+        got, s = (ref.gather(x, table, l)[l - t:] for x in (held, steps))
+        z = y.reshape(t, Hkv, D // 2, 2) if pairs else y.reshape(t, Hkv, 2, D // 2).swapaxes(-1, -2)
+        size = np.repeat(np.hypot(z[..., 0], z[..., 1])[..., None], 2, -1)
+        size = size.reshape(y.shape) if pairs else size.swapaxes(-1, -2).reshape(y.shape)
+        over = np.abs(got - y) - ref8.half_step(y / s) * s
+        assert (over <= 2.5 * 2.0 ** -24 * size).all(), (b, (over / size).max() * 2 ** 24)
+        at += t
+
+
 def test_append_limits(jb):
     """Tokens behind max_seqlen and rows behind the last sequence are not taken."""
     new, kv = [50, 3], [70, 40]
