@@ -484,42 +484,54 @@ __device__ __forceinline__ void clean_part(lds_char* v, int bytes) {
   }
 }
 
-// The same for a tile of V's codes (e: the tile's exponents): whether one is NaN, NaN to the
-// queries that see its row, and those codes (and scales) as zeros.
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+// The same for a tile of V's codes (e: the tile's exponents): whether one stands for no finite
+// value, what those are to the queries that see their rows, and those codes (and scales) as
+// zeros.  Under exponent e these are the magnitudes from odd_from(e) on: 127 (NaN), from 2^(255 - e) on,
+// which the scale takes to 2^128 (an infinity as bf16), all of them where the scale is NaN.
+__device__ __forceinline__ uint32_t odd_from(uint32_t e) { return e == 255u ? 0u : e < 247u ? 127u : (262u - e) * 8; }
+// bit 7 of each byte of w: its magnitude is `from` at least
+__device__ __forceinline__ uint32_t odd_bytes(uint32_t w, uint32_t from) {
+  return ((w & 0x7f7f7f7fu) + (128u - from) * 0x01010101u) & 0x80808080u;
+}
 template <int D> __device__ __forceinline__ bool odd_codes(const lds_char* v, uint32_t e) {
-  bool odd = ((e >> 8) & 255u) == 255u || e >> 24 == 255u;
+  const uint32_t a = odd_from((e >> 8) & 255u), b = odd_from(e >> 24);
+  bool odd = false;
 #pragma unroll
-  for (int i = lane_id() * 16; i < 32 * D; i += 1024) {
-    const u4_t w = *(const lds_u4*)(v + i);
-    odd |= (nan_codes(w[0]) | nan_codes(w[1]) | nan_codes(w[2]) | nan_codes(w[3])) != 0;
+  for (int i = 0; i < 32 * D; i += 1024) {
+    const u4_t w = *(const lds_u4*)(v + i + lane_id() * 16);
+    const uint32_t from = i < 16 * D ? a : b;
+    odd |= (odd_bytes(w[0], from) | odd_bytes(w[1], from) | odd_bytes(w[2], from) | odd_bytes(w[3], from)) != 0;
   }
   return __any(odd);
 }
-// (COLS queries a wave: o are D COLS / 64 accumulators, in 32 or 16 columns' order)
+// (COLS queries a wave: o are D COLS / 64 accumulators and s COLS / 2 weights, in 32 or 16
+// columns' order)
 template <int D, int COLS>
-__device__ __attribute__((noinline)) void add_odd_codes(float* o, const lds_char* v, uint32_t e, int j0, int p, int p1, int lw) {
+__device__ __attribute__((noinline)) void add_odd_codes(float* o, const float* s, const lds_char* v, uint32_t e, int j0,
+                                                        int p, int p1, int lw) {
   using W = Raw8<D>;
-  const int g = lane_id() / COLS;
+  const int lane = lane_id(), g = lane / COLS;
   for (int r = 0; r < 32; ++r) {
+    // the row's weight, from the lanes that hold it
+    const float w = COLS == 32 ? __shfl(s[(r >> 3) * 4 + (r & 3)], ((r >> 2) & 1) * 32 + lane % 32, WAVE)
+                               : __shfl(s[(r >> 4) * 4 + (r & 3)], ((r >> 2) & 3) * 16 + lane % 16, WAVE);
     if (j0 + r > (r >= 16 ? p1 : p) || j0 + r <= lw) continue;
-    const bool all = (r < 16 ? (e >> 8) & 255u : e >> 24) == 255u;
+    const int from = (int)odd_from(r < 16 ? (e >> 8) & 255u : e >> 24);
     for (int i = 0; i < D * COLS / 64; ++i) {
       const int d = COLS == 32 ? 32 * (i >> 4) + 8 * ((i >> 2) & 3) + 4 * g + (i & 3) : 16 * (i >> 2) + 4 * g + (i & 3);
-      const int code = v[r * D + (((d >> 4) ^ W::f(r & 15)) << 4) + (d & 15)];
-      if (all || (code & 127) == 127) o[i] = NAN;
+      const int code = v[r * D + (((d >> 4) ^ W::f(r & 15)) << 4) + (d & 15)], size = code & 127;
+      if (size >= from) o[i] = fmaf(w, from == 0 || size == 127 ? NAN : code & 128 ? -INFINITY : INFINITY, o[i]);
     }
   }
 }
 template <int D> __device__ __forceinline__ uint32_t clean_codes(lds_char* v, uint32_t e) {
-  const bool a = ((e >> 8) & 255u) == 255u, b = e >> 24 == 255u;
+  const uint32_t a = odd_from((e >> 8) & 255u), b = odd_from(e >> 24);
   for (int i = lane_id() * 4; i < 32 * D; i += 256) {
-    uint32_t w = *(const lds_u32*)(v + i);
-    w &= ~((nan_codes(w) >> 7) * 255u);
-    *(lds_u32*)(v + i) = (i < 16 * D ? a : b) ? 0u : w;
+    const uint32_t w = *(const lds_u32*)(v + i);
+    *(lds_u32*)(v + i) = w & ~((odd_bytes(w, i < 16 * D ? a : b) >> 7) * 255u);
   }
-  if (a) e = (e & 0xffff00ffu) | 127u << 8;
-  if (b) e = (e & 0x00ffffffu) | 127u << 24;
+  if (a == 0) e = (e & 0xffff00ffu) | 127u << 8;
+  if (b == 0) e = (e & 0x00ffffffu) | 127u << 24;
   return e;
 }
 
@@ -802,8 +814,8 @@ template <int D, bool Q8 = false> struct Wave {
     }
   }
   // A tile of listed pages (lk: K, then V, as codes or as bf16; whole: every query sees all of
-  // it), first with K, then with V.  Masked weights are 0, but 0 times a NaN is not:
-  // `careful` looks for what is not finite first.
+  // it), first with K, then with V.  Masked weights are 0, but 0 times an infinity or NaN is
+  // not: `careful` looks for what is not finite first.
   __device__ __forceinline__ void listed_k(const lds_char* lk, uint32_t e, f16_t (&s)[1]) const {
     if constexpr (Q8) scores8(lk, e, s);
     else scores<1>(lk, s);
@@ -818,12 +830,19 @@ template <int D, bool Q8 = false> struct Wave {
   }
   __device__ __forceinline__ void listed_v(const Args& a, lds_char* lv, uint32_t e, f16_t (&s)[1], float ms, int j0, bool careful) {
     if (careful) {
-      if constexpr (Q8) {
-        e = without_odd(lv, e, j0);
-      } else if (odd_part(lv, 32 * D * 2)) {
-        f16_t x[1];
+      auto weighed = [&](f16_t(&x)[1]) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[0][i] = fast_exp2(fmaf(s[0][i], a.scale, -ms));
+      };
+      if constexpr (Q8) {
+        if (odd_codes<D>(lv, e)) {
+          f16_t x[1];
+          weighed(x);
+          e = without_odd(x, lv, e, j0);
+        }
+      } else if (odd_part(lv, 32 * D * 2)) {
+        f16_t x[1];
+        weighed(x);
         odd_values<1>(x, lv, j0);
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         clean_part(lv, 32 * D * 2);
@@ -847,13 +866,14 @@ template <int D, bool Q8 = false> struct Wave {
     for (int i = 0; i < D / 2; ++i) fine &= isfinite(o[i >> 4][i & 15]);
     return fine;
   }
-  // NaN codes of V to the queries that see them, and out of the tile
-  __device__ __forceinline__ uint32_t without_odd(lds_char* v, uint32_t e, int j0) {
-    if (!odd_codes<D>(v, e)) return e;
-    float so[D / 2];
+  // V's codes that stand for no finite value to the queries that see them, and out of the tile
+  __device__ __forceinline__ uint32_t without_odd(const f16_t (&s)[1], lds_char* v, uint32_t e, int j0) {
+    float so[D / 2], ss[16];
 #pragma unroll
     for (int i = 0; i < D / 2; ++i) so[i] = o[i >> 4][i & 15];
-    add_odd_codes<D, 32>(so, v, e, j0, p, p1, lw);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) ss[i] = s[0][i];
+    add_odd_codes<D, 32>(so, ss, v, e, j0, p, p1, lw);
 #pragma unroll
     for (int i = 0; i < D / 2; ++i) o[i >> 4][i & 15] = so[i];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -884,7 +904,7 @@ template <int D, bool Q8 = false> struct Wave {
 #pragma unroll
     for (int k = 0; k < 2; ++k) weights<1>(a, s, ms, k);
     lds_char* const v = lk + W8::TILE;
-    e = without_odd(v, e, j0);
+    if (odd_codes<D>(v, e)) e = without_odd(s, v, e, j0);
     values8<false>(a, v, e, s, 0.f);
   }
 
@@ -1041,11 +1061,11 @@ template <int D, int QR> struct Wave16 {
     }
     weigh(a, s);
     lds_char* const v = lk + W8::TILE;
-    e = without_odd(v, e, j0);
+    if (odd_codes<D>(v, e)) e = without_odd(s, v, e, j0);
     values(v, e, s);
   }
   // A tile of listed pages (whole: every query sees all of it).  Masked weights are 0, but 0
-  // times a NaN is not: `careful` looks for them first.
+  // times an infinity or NaN is not: `careful` looks for them first.
   __device__ __forceinline__ void listed(const Args& a, lds_char* lk, uint32_t e, int j0, bool whole, bool careful) {
     const int g = lane_id() >> 4;
     f4_t s[2];
@@ -1056,7 +1076,7 @@ template <int D, int QR> struct Wave16 {
         if (j0 + 16 * (i >> 2) + 4 * g + (i & 3) > (i >= 4 ? p1 : p)) s[i >> 2][i & 3] = -INFINITY;
     weigh(a, s);
     lds_char* const v = lk + W8::TILE;
-    if (careful) e = without_odd(v, e, j0);
+    if (careful && odd_codes<D>(v, e)) e = without_odd(s, v, e, j0);
     values(v, e, s);
   }
   __device__ __forceinline__ bool finite() const {
@@ -1065,13 +1085,15 @@ template <int D, int QR> struct Wave16 {
     for (int i = 0; i < D / 4; ++i) fine &= isfinite(o[i >> 2][i & 3]);
     return fine;
   }
-  // NaN codes of V to the queries that see them, and out of the tile
-  __device__ __forceinline__ uint32_t without_odd(lds_char* v, uint32_t e, int j0) {
-    if (!odd_codes<D>(v, e)) return e;
-    float so[D / 4];
+  // V's codes that stand for no finite value to the queries that see them, and out of the tile
+  // (QR = 8: to both of a query's columns)
+  __device__ __forceinline__ uint32_t without_odd(const f4_t (&s)[2], lds_char* v, uint32_t e, int j0) {
+    float so[D / 4], ss[8];
 #pragma unroll
     for (int i = 0; i < D / 4; ++i) so[i] = o[i >> 2][i & 3];
-    add_odd_codes<D, 16>(so, v, e, j0, p, p1, lw);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss[i] = s[i >> 2][i & 3];
+    add_odd_codes<D, 16>(so, ss, v, e, j0, p, p1, lw);
 #pragma unroll
     for (int i = 0; i < D / 4; ++i) o[i >> 2][i & 3] = so[i];
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");

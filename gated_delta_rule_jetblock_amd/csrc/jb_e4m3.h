@@ -1,6 +1,7 @@
 // jb_e4m3.h -- values in 8 bits: e4m3 codes (1 sign, 4 exponent and 3 fraction bits, bias
 // 7; largest 448, 0x7f and 0xff NaN, no infinity) times a power-of-two scale that is held as
-// its exponent e: 2^(e - 127), 255 NaN.  A code times a scale is a bf16 value.
+// its exponent e: 2^(e - 127), 255 NaN.  A code times a scale is a bf16 value, but where it
+// is 2^128 or more (scales from 2^120 on), which bf16 and fp32 read as an infinity.
 #pragma once
 
 #include <math.h>
@@ -14,7 +15,7 @@ typedef float e4m3_f2_t __attribute__((ext_vector_type(2)));
 
 // The scale as the conversion to bf16 takes it: it looks at the exponent bits only, and
 // reads all zeros as 2^-127 and all ones as NaN (checked for every code and exponent; what
-// falls below bf16's smallest number is rounded).
+// falls below bf16's smallest number is rounded, what passes its largest is an infinity).
 __device__ __forceinline__ float scale_of(uint32_t e) { return __uint_as_float(e << 23); }
 
 // 8 codes, in order, as bf16

@@ -517,11 +517,12 @@ jb_status jb_attn_paged(const jb_attn_shape* shape, int64_t total_tokens, const 
  * a key head a power of two, held as its exponent:
  *   k_scales, v_scales [num_pages][Hkv][page / 16] uint8: e stands for 2^(e - 127),
  *                      255 for NaN;  a value is its code times its rows' scale
- * (a value below the smallest bf16 number may be rounded to one).  scale_stride: elements
- * between pages of the scales, 0: contiguous.  page_stride counts codes (bytes), a
- * multiple of 16.  A page index outside [0, num_pages) reads as rows of zeros and is
- * not written to, as above; layouts, limits and conventions are those above but for
- * what follows.  The calls over pages take total_tokens Hkv < 2^24 and count page <= 2^30.
+ * (a value below the smallest bf16 number may be rounded to one; one of 2^128 or more reads
+ * as an infinity).  scale_stride: elements between pages of the scales, 0: contiguous.
+ * page_stride counts codes (bytes), a multiple of 16.  A page index outside [0, num_pages)
+ * reads as rows of zeros and is not written to, as above; layouts, limits and conventions
+ * are those above but for what follows.  The calls over pages take total_tokens Hkv < 2^24
+ * and count page <= 2^30.
  * ------------------------------------------------------------------------- */
 
 /* jb_block_scores, jb_attn_blocks: the cache is in 8 bits (else of io_dtype). */
