@@ -523,6 +523,11 @@ __global__ __launch_bounds__(256) void rope_append8_kernel(Args a) {
       const float inv = inverse_scale(e);
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[n][i] *= inv;
+      if (e >= 247) {  // the largest code whose value is less than 2^128, which is no number in fp32 or bf16
+        const float top = 0.9375f * __uint_as_float((uint32_t)(382 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[n][i] = isfinite(y[n][i]) ? fminf(fmaxf(y[n][i], -top), top) : y[n][i];
+      }
       *reinterpret_cast<uint2*>(cache + at + (int64_t)(r & 15) * D) = e4m3_of(y[n]);
     } else if (kept[n] && e != e_was[kv]) {
       const float4 lo = floats_of_e4m3(was[n].x, e_was[kv]), hi = floats_of_e4m3(was[n].y, e_was[kv]);

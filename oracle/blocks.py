@@ -83,7 +83,9 @@ def append(codes, scales, table, kv, fresh, tokens=None):
             for r in old:
                 if e != was:
                     codes[p, h, r % page] = encode(E4M3[codes[p, h, r % page]] * 2.0 ** (was - e))
-            codes[p, h, [r % page for r in new]] = encode(y / scale_value(e))
+            top = 448 if e < 247 else 0.9375 * 2.0 ** (255 - e)  # the last code whose value is less than 2^128
+            z = y / scale_value(e)
+            codes[p, h, [r % page for r in new]] = encode(np.where(np.isfinite(z), np.clip(z, -top, top), z))
             scales[p, h, at // 16] = e
     return margins
 

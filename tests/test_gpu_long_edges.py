@@ -5,8 +5,8 @@ import pytest
 import torch
 
 from oracle import blocks as ref8
-from test_gpu_attn import BF, F32
-from test_gpu_attn8 import E4M3, E8M0, jb  # noqa: F401
+from test_gpu_attn import BF, F32, f64
+from test_gpu_attn8 import E4M3, E8M0, codes_of, equal, frequencies, jb  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +89,38 @@ def test_values_past_the_range(jb, dtype, D, T, H, Hkv, form):
                 assert torch.isfinite(o).all() and (o[seen][..., 5] > 2.0 ** 120).all(), (e, code)
                 d["codes"][1][page, :, row % 16, 5] = 0
             d["scales"][1][page] = 118
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_largest_values_stay_numbers(jb, dtype):
+    """The largest finite keys and values of each type, and those around the last codes' borders, are
+    appended as codes that stand for finite values: of 1.9375 * 2^127 and more the nearest code's value
+    would be 2^128.  In rows of their own, and in 16 rows whose scale in the cache is larger."""
+    H, Hkv, D, page, kv = 2, 1, 64, 16, 40
+    top = torch.finfo(dtype).max
+    sizes = [top, 1.9375 * 2.0 ** 127, 1.9296875 * 2.0 ** 127, 1.875 * 2.0 ** 127, 1.75 * 2.0 ** 127, 2.0 ** 127, 3.0, float("inf")]
+    n = 30  # rows 10 .. 39: 6 of the first 16 share them with rows before, whose scale is 2^123
+    x = torch.tensor(sizes, dtype=torch.float64).to(dtype).repeat(n * D // 8 + 1)[:n * D].view(n, 1, D)
+    x = torch.where(torch.arange(D) % 3 == 0, -x, x)
+    q = torch.zeros(n, H, D, dtype=dtype)
+    cu, lens = torch.tensor([0, n], dtype=torch.int32).cuda(), torch.tensor([kv], dtype=torch.int32).cuda()
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32)
+    caches = [torch.zeros(3, Hkv, page, D, dtype=torch.uint8).cuda().view(E4M3) for _ in range(2)]
+    scales = [torch.full((3, Hkv, 1), 250, dtype=torch.uint8).cuda().view(E8M0) for _ in range(2)]
+    r = jb.qk_norm_rope_paged8(q.cuda(), x.cuda(), x.cuda(), *caches, *scales, table.cuda(), lens, frequencies(D).cuda(),
+                               cu_seqlens=cu, positions=torch.zeros(n, dtype=torch.int32).cuda(), normalize=False)
+    torch.cuda.synchronize()
+    want = np.zeros((3, Hkv, page, D), np.uint8), np.full((3, Hkv, 1), 250, np.uint8)
+    ref8.append(*want, table[0].tolist(), kv, f64(x))
+    assert want[1].ravel().tolist() == [247, 247, 250]
+    for c, s in zip(caches, scales):
+        equal(codes_of(c), want[0])
+        equal(codes_of(s), want[1], nan=256)
+        held = ref8.dequantise(codes_of(c), codes_of(s))
+        held = np.concatenate([held[p, 0] for p in (2, 0, 1)])[10:kv]
+        fine = np.isfinite(f64(x)[:, 0])
+        assert np.isnan(held[~fine]).all() and (np.abs(held[fine]) < 2.0 ** 128).all()
+        # half a step is at most 2^-4 of a value (and 2^-10 of the largest scale, 2^123), the next code
+        # down from 2^128 a whole one: 2^-4 of it
+        assert (np.abs(held - f64(x)[:, 0])[fine] <= 2.0 ** -4 * np.abs(f64(x)[:, 0][fine]) + 2.0 ** 113).all()
+    assert r["k_cache"] is caches[0]
