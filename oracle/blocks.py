@@ -97,7 +97,7 @@ def mean_of(rows):
 
 def scores(q, means):
     """q [T, G, D] of one key head, means [pages, D]: the largest product over G, [T, pages]."""
-    return np.einsum("tgd,pd->tgp", q, means).max(1)
+    return (q @ means.T).max(1)
 
 
 def select(x, own, count, first, recent):
