@@ -1441,10 +1441,11 @@ __device__ __forceinline__ Listed take_lists(const Args& a, uint32_t slot, int k
 }
 
 // LIST: a workgroup takes a unit of listed pages, or a piece of one.  A decode step of 64
-// sequences, 12 heads on 2, 32 pages of 64 rows each in 8 bits: 19.3 us, half of it HBM's, the rest
-// the lookups before the first rows (list, page, scales) and the join; one of 16 pages in 16
-// bits 14 us.  500 tokens of 16 heads on 2, 32 pages each of 32K rows (4 tokens list 66 of
-// them): 42 us; each token by itself 85 us.
+// sequences, 12 heads on 2, 32 pages of 64 rows each in 8 bits: 19.2-20.2 us, half of it HBM's, the
+// rest the lookups before the first rows (list, page, scales) and the join; one of 16 pages in 16
+// bits 14 us.  500 tokens of 16 heads on 2, 32 pages each of 32K rows (4 tokens list 64 of
+// them): 41-44 us; each token by itself 85 us.  Of it 11 us are there with empty lists (launch, merge,
+// join of the waves), the rest are the pages' at 0.5 us each; 32 pages that all tokens list 24 us.
 template <int D, int NW, typename OUT, bool Q8, bool LIST, int QR>
 __global__ __launch_bounds__(NW * 64, Q8 || LIST ? 2 : 1) void attn_row_kernel(Args a) {
   static_assert(Q8 || QR == 32, "queries of a unit, at most");
@@ -2296,7 +2297,14 @@ int64_t list_units(const BlockCall& b) {
 // Pieces of a unit's pages: the rounds of workgroups take the steps of the longest list and
 // some 3 steps' worth of start and end each; a join is worth 3.5 and 2 more for each piece.
 // 64 decode steps over 32 pages of 64 rows (128 units): 1 piece 22.0 us, 2 19.6, 4 20.9, 8
-// 25.8; one over 16 pages 14.8, 17.2, 18.1, 17.2.
+// 25.8; one over 16 pages 14.8, 17.2, 18.1, 17.2.  (Calls, whose second launch costs the host as
+// much as the first.)  In a captured graph, with 1, 2, 4, 8 pieces | by the rule, lists of 32 pages of 64:
+//                     head size 64                      128                              256
+//   64 steps, 8 bits  19.1 15.6 14.4 18.9 | 15.9        22.3 20.2 21.4 26.0 | 20.2       46.6 31.6 30.5 36.9 | 30.5
+//   200 steps         23.5 29.9 31.4 38.9 | 24.1        38.8 44.8 48.4 61.9 | 39.3       79.4 90.0 95.9 107.6 | 79.3
+//   1 step            18.0 13.7 10.9 9.9 | 13.8         20.6 15.6 12.1 10.8 | 15.6       44.5 28.0 18.9 14.8 | 18.9
+//   64 steps, 16 bits 17.2 19.3 23.0 31.5 | 17.4        26.3 28.8 33.4 43.8 | 26.3       46.5 50.3 53.5 64.8 | 50.4
+//   500 tokens        34.0 41.5 55.1 | 34.8 (1, 2, 4)   42.9 55.0 77.1 | 44.1            92.7 61.5 80.8 | 63.1
 int list_pieces(const BlockCall& b) {
   const int64_t units = list_units(b), hold = b.D == 64 || b.bits8 ? 512 : 256, step = 32 * list_waves(b.D, b.bits8);
   const int64_t steps = cdiv((int64_t)std::min(b.count, b.max_pages) * b.page, step);

@@ -235,7 +235,8 @@ template <int D, int NB> struct Means {
 // walks `tiles` tiles of 2 x 16 tokens, the next head's queries on their way while these are
 // used; a workgroup takes 4 times as many pages.  2K tokens of 12 heads on 2 at the end of
 // 64K rows, pages of 64: 26.6-27.6 us with the launch that forms the means (5); the
-// products are 8 of it at the matrix cores' rate, the scores' bytes 3.
+// products are 8 of it at the matrix cores' nominal rate and 15.5 at the one that the library's product
+// reaches, the scores' bytes 3.
 constexpr int PAGES = 128;  // of a workgroup
 
 template <int D>
@@ -357,9 +358,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void block_scores_kernel(Arg
 // Decode (T = 1), bf16: rows are 16 query heads of the one token, columns 16 pages; the
 // maximum over the rows is taken across the lanes.  The one page that holds the token is
 // averaged by the workgroup that scores it, so the step is one launch.  Bound by what it
-// waits for (the length and the page indices, then the means).  64 sequences of up to 64K
-// rows, 12 heads on 2, pages of 64: 14.4-15.3 us a call, 10.5 without the means' bytes (a
-// call's host work).
+// waits for: the length and the page indices, then the means, a wave's 32 pages at once.  64
+// sequences of up to 64K rows, 12 heads on 2, pages of 64 (35 MB): 14.4-15.5 us, as many in a
+// captured graph; all of 64K rows (67 MB) 19.3, 16 of them 7.1.
 template <int D, typename KV>
 __global__ __launch_bounds__(256, D == 64 ? 5 : D == 128 ? 3 : 2) void block_scores_one_kernel(Args a, uint32_t groups) {
   constexpr int STEPS = D / 32, NB = 2;
@@ -787,7 +788,11 @@ template <int D> hipError_t scores(const BlockCall& c, hipStream_t stream) {
   if (f32) {
     block_scores_f32_kernel<D><<<dim3((unsigned)(a.slots * c.Hkv * groups)), dim3(256), 0, stream>>>(a, (uint32_t)groups);
   } else {
-    // tiles a workgroup: as many workgroups as the chip holds, where there are more tiles
+    // Tiles a workgroup: as many workgroups as the chip holds, where there are more tiles.  With
+    // 1, 2, 4 and 8 tiles: 2K tokens at the end of 64K rows, 12 heads on 2 of 128, 32, 28, 36 and 60 us
+    // (the rule takes 2); 4K tokens 54, 47, 43 and 62 (4); heads of 64, 4K tokens 37, 36, 36 and 54 (4);
+    // 8 on 2 of 256, 2K tokens 61, 51, 47 and 74 (4); 4K 114, 93, 84 and 78 (8); 2K on 16K rows 20, 28,
+    // 40 and 68 (1).
     const int64_t all = a.slots * c.Hkv * groups, tiles = std::min<int64_t>(std::max<int64_t>(all / (D == 256 ? 256 : 512), 1), 16);
     block_scores_kernel<D><<<dim3((unsigned)(cdiv(a.slots, tiles) * c.Hkv * groups)), dim3(256), 0, stream>>>(
         a, (uint32_t)groups, (int)tiles);

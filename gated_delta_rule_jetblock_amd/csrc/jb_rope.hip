@@ -328,7 +328,7 @@ __global__ __launch_bounds__(256) void rope_kernel(Args a) {
 
 // Keys that become codes are formed in 64 bits: a value's error flips its code where the value
 // lies that near to a border, and the errors of fp32 arithmetic (8e-8 rms) flip 2 of a million
-// codes by a whole step, where these flip 0.1 (13K tokens on 2 key heads: 31.4 us, in fp32 29.9).
+// codes by a whole step, where these flip 0.1 (13K tokens on 2 key heads, on one card: 31.4 us, in fp32 29.9).
 //
 // a cos + b sin of 2 pi t.  As in sincos_turn the nearest quarter turn comes off (here a sum's
 // low bits; |t| < 2^48, what lies past that has no angle in 64 bits); it swaps a and b and
@@ -422,8 +422,8 @@ __global__ __launch_bounds__(256) void rope_append8_kernel(Args a) {
   constexpr int L = D / 8, GROUPS = 256 / L, N = 32 / GROUPS;  // rows at once; times for 16 of K and 16 of V
   const RopeCall& c = a.c;
   const uint32_t cells = (uint32_t)a.cells * (uint32_t)a.kv_heads;
-  // the keys' workgroups first, which wait for what they look up (in turn with the queries',
-  // 13K tokens took 30.6 us, so 29.3, with sums in fp32)
+  // the keys' workgroups first, which wait for what they look up (13K tokens, with sums in fp32,
+  // on one card: in turn with the queries' 30.6 us, so 29.3)
   if (blockIdx.x >= cells) {
     rope_rows<D, IO, IO, true, false>(a, blockIdx.x - cells);
     return;

@@ -4,9 +4,11 @@ layouts, types and pages, blocks of 16 rows that several calls fill, codes and s
 not numbers, malformed device-side indices, strides, streams and captured graphs.
 
 Bounds.  Values are copied exactly before they are rounded, so V's codes and scales are the
-oracle's bit for bit.  A key is formed in fp32 first: its norm and turn are off by at most TURN
-of the row's largest magnitude (a sum of D squares, a square root, a division, two products and
-a sum: less than 2^-20 with the sine's 1.5e-7), and rounded to a code: half a step more.
+oracle's bit for bit.  A query's norm and turn, in fp32, are off by at most TURN of the row's
+largest magnitude (a sum of D squares, a square root, a division, two products and a sum: less than
+2^-20 with the sine's 1.5e-7).  A key's are in 64 bits where it counts; it is held to half a step of
+its code and twice TURN here, and to its value in 64 bits at the codes' borders below (and in
+test_gpu_long_edges).
 The attention's bounds are test_gpu_attn's, on the values that the cache holds."""
 import numpy as np
 import pytest
