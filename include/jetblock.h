@@ -530,13 +530,14 @@ jb_status jb_attn_paged(const jb_attn_shape* shape, int64_t total_tokens, const 
 
 /*
  * jb_qk_norm_rope_paged8 -- jb_qk_norm_rope_paged into a cache in 8 bits.  The new
- * rows' keys (formed in 64 bits, within 2^-22 of the magnitude of a rotated pair) and values
- * are divided by their 16 rows' scale and rounded once, to the nearest code whose value is
- * less than 2^128, ties to even; infinities and NaN become NaN.  The scale is the smallest
- * 2^k, k >= -126, with 448 * 2^k at least the largest finite magnitude among the call's rows
- * of the 16 - or, where rows before them share the 16, the one in the cache if that is
- * larger; where the scale grows, the codes of those rows are divided by the quotient (and
- * rounded again where they fall below the smallest normal code).  Codes of rows behind the
+ * rows' keys and values are divided by their 16 rows' scale and rounded once, to the
+ * nearest code whose value is less than 2^128, ties to even; infinities and NaN become NaN.
+ * (Keys are formed in 64 bits, within 2^-22 of the magnitude of a rotated pair, where the
+ * mean square and the products with the weights lie in fp32's range.)  The scale is the
+ * smallest 2^k, k >= -126, with 448 * 2^k at least the largest finite magnitude among the
+ * call's rows of the 16 - or, where rows before them share the 16, the one in the cache if
+ * that is larger; where the scale grows, the codes of those rows are divided by the quotient
+ * (and rounded again where they fall below the smallest normal code).  Codes of rows behind the
  * new ones stay as they are, under the new scale.
  */
 jb_status jb_qk_norm_rope_paged8(const jb_attn_shape* shape, int64_t total_tokens, const int32_t* cu_seqlens,
